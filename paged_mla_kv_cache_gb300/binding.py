@@ -1,4 +1,5 @@
-"""Thin ctypes binding of ``libpmg.so`` (declared in ``include/pmg.h``).
+"""Thin ctypes binding of ``libpmg.so`` (declared in ``include/pmg.h`` and
+``include/pmg_mla.h``).
 
 Argument marshalling only: shapes, strides, dtypes and raw pointers are taken
 from torch tensors and passed to the C ABI; every step of the gather runs in
@@ -9,6 +10,10 @@ The call mirrors ops.cp_gather_cache(src_cache, dst, block_table, cu_seq_lens,
 batch_size, seq_starts) of "MLA cache gather scheduled per logical page"
 (prhub.com.cn, vllm PR #51739, section "关键源码片段"), with the dtype pair,
 the FP8 scale, an error flag and the stream made explicit.
+
+plan_step, append, latent_decode and latent_prefill are the operators around
+the gather: a step's pages and slots, the cache write, and the attention over
+the cache (absorbed) or over gathered and expanded entries.
 """
 from __future__ import annotations
 
@@ -34,11 +39,19 @@ FLAG_SEQ_START = 4
 FLAG_CU_ORDER = 8
 FLAG_TIMEOUT = 16
 FLAG_TOKEN = 32
+FLAG_LENGTH = 64
+FLAG_CAPACITY = 128
+FLAG_NO_BLOCKS = 256
+FLAG_POSITION = 512
 
 OPT_FORCE_SIMT = 1
 OPT_FORCE_SCALAR = 2
 OPT_IMPLIED_END = 4
 OPT_EARLY_METADATA = 8
+OPT_ROPE_PAIRS = 1         # append
+OPT_CAUSAL = 1             # latent_prefill
+OPT_FORCE_GENERAL = 2      # latent_decode, latent_prefill
+MAX_ENTRY = 1024           # largest latent_dim + rope_dim of the attention calls
 
 PATH_NAMES = {0: "none", 1: "bulk", 2: "vector", 3: "scalar", 4: "realign"}
 WORKSPACE_INTS = 4
@@ -88,6 +101,21 @@ def load_library() -> ctypes.CDLL:
                                       ctypes.POINTER(i32), ctypes.POINTER(i32)]
         L.pmg_debug_plan.restype = ctypes.c_int
         L.pmg_debug_plan.argtypes = [vp, vp, i32, i64, i32, vp, i64, vp, vp, vp, u32]
+        f32 = ctypes.c_float
+        L.pmg_plan_step.restype = ctypes.c_int
+        L.pmg_plan_step.argtypes = [vp, vp, i32, vp, i64, vp, i64, i64, i32, vp, vp, vp, i64, vp, vp, vp, vp, vp, vp]
+        L.pmg_append.restype = ctypes.c_int
+        L.pmg_append.argtypes = [vp, i64, vp, i64, vp, f32, vp, i64, vp, vp, i64, i32, i32, i32, vp, i64, i64, i64, i32,
+                                 i32, vp, vp, i64, i64, vp, i64, i64, i32, vp, vp, u32]
+        L.pmg_latent_decode.restype = ctypes.c_int
+        L.pmg_latent_decode.argtypes = [vp, i64, i64, i64, vp, i64, i64, i64, vp, i64, vp, i32, i32, i32, i32, i32, i32,
+                                        i32, i32, vp, f32, vp, i64, i64, i64, vp, vp, i64, vp, vp, u32]
+        L.pmg_latent_prefill.restype = ctypes.c_int
+        L.pmg_latent_prefill.argtypes = [vp, i64, i64, vp, i64, i64, vp, i64, vp, i64, i64, vp, vp, i32, i64, i64, i32,
+                                         i32, i32, i32, i32, f32, vp, i64, i64, vp, vp, i64, i64, vp, vp, i64, vp, vp,
+                                         u32]
+        L.pmg_attention_workspace.restype = i64
+        L.pmg_attention_workspace.argtypes = []
         L.pmg_status_string.restype = ctypes.c_char_p
         L.pmg_status_string.argtypes = [ctypes.c_int]
         L.pmg_version.restype = ctypes.c_int
@@ -258,3 +286,236 @@ def debug_plan(cu_seq_lens: torch.Tensor, seq_starts: Optional[torch.Tensor], to
     if st != PMG_OK:
         raise PmgError(st, "pmg_debug_plan")
     return tasks, num
+
+
+# --- the operators around the gather (include/pmg_mla.h) -------------------------
+
+
+def _vector(t: Optional[torch.Tensor], dtype: torch.dtype, n: Optional[int], what: str, optional: bool = False):
+    """Pointer of a contiguous 1-D tensor of n elements (n None: any)."""
+    if t is None:
+        if optional:
+            return None
+        raise ValueError(f"{what} is required")
+    if t.dtype != dtype or t.dim() != 1 or (n is not None and t.shape[0] != n) or not t.is_contiguous():
+        raise ValueError(f"{what} must be {dtype} [{'n' if n is None else n}] and contiguous, got "
+                         f"{t.dtype} {list(t.shape)}")
+    return t.data_ptr()
+
+
+def _scalar(t: Optional[torch.Tensor], dtype: torch.dtype, what: str):
+    if t is None:
+        return None
+    if t.dtype != dtype or t.numel() != 1:
+        raise ValueError(f"{what} must be one {dtype} element")
+    return t.data_ptr()
+
+
+def _unit_last(t: torch.Tensor, dims: int, what: str) -> torch.Tensor:
+    if t.dim() != dims or (t.shape[-1] > 1 and t.stride(-1) != 1):
+        raise ValueError(f"{what} must have {dims} dimensions, the last of stride 1")
+    return t
+
+
+def plan_step(ctx_lens: torch.Tensor, new_lens: torch.Tensor, block_table: torch.Tensor, free_blocks: torch.Tensor,
+              block_size: int, slots: Optional[torch.Tensor], positions: Optional[torch.Tensor],
+              token_to_seq: Optional[torch.Tensor], cu_new: torch.Tensor, seq_lens: torch.Tensor,
+              cu_seq: Optional[torch.Tensor], blocks_taken: Optional[torch.Tensor], num_blocks: int,
+              error_flag: Optional[torch.Tensor] = None, stream=None) -> None:
+    """Block table, slots and positions of one serving step (pmg_plan_step).
+
+    ctx_lens, new_lens  int32 [num_reqs]: tokens in the cache, tokens joining.
+    block_table   int32 [num_reqs, width]: the columns of fresh pages are
+                  filled with ids from free_blocks (int32 [num_free]), in the
+                  order of requests and pages.
+    slots         int64 [max_tokens] or None: block id * block_size + offset
+                  of each new token; -1 without a page and past the last token.
+    positions, token_to_seq  int32 [max_tokens] or None (-1 past the last token).
+    cu_new, cu_seq  int32 [num_reqs + 1]: prefix sums of new and total lengths
+                  (cu_seq is the gather's cu_seq_lens; it may be None).
+    seq_lens      int32 [num_reqs]: total lengths.
+    blocks_taken  int32 [1] or None.
+    """
+    r = ctx_lens.shape[0]
+    i32 = torch.int32
+    given = [t for t in (slots, positions, token_to_seq) if t is not None]
+    tokens = given[0].shape[0] if given else 0
+    st = load_library().pmg_plan_step(
+        _vector(ctx_lens, i32, r, "ctx_lens"), _vector(new_lens, i32, r, "new_lens"), r,
+        _ptr(block_table), _reqs_table(block_table, r), _vector(free_blocks, i32, None, "free_blocks"),
+        free_blocks.shape[0], int(num_blocks), int(block_size), _vector(slots, torch.int64, tokens, "slots", True),
+        _vector(positions, i32, tokens, "positions", True), _vector(token_to_seq, i32, tokens, "token_to_seq", True),
+        tokens, _vector(cu_new, i32, r + 1, "cu_new"), _vector(seq_lens, i32, r, "seq_lens"),
+        _vector(cu_seq, i32, r + 1, "cu_seq", True), _scalar(blocks_taken, i32, "blocks_taken"),
+        _scalar(error_flag, i32, "error_flag"), _stream_handle(stream))
+    if st != PMG_OK:
+        raise PmgError(st, "pmg_plan_step")
+
+
+def _reqs_table(block_table: torch.Tensor, reqs: int) -> int:
+    width = _table_width(block_table)
+    if block_table.shape[0] != reqs:
+        raise ValueError(f"block_table has {block_table.shape[0]} rows for {reqs} requests")
+    return width
+
+
+def append(c_kv: torch.Tensor, k_pe: torch.Tensor, cache: torch.Tensor, slots: torch.Tensor, positions: torch.Tensor,
+           cos_sin: torch.Tensor, norm_weight: Optional[torch.Tensor] = None, eps: float = 1e-6,
+           scale: Optional[torch.Tensor] = None, q_pe: Optional[torch.Tensor] = None,
+           q_out: Optional[torch.Tensor] = None, interleaved: bool = False,
+           error_flag: Optional[torch.Tensor] = None, stream=None) -> None:
+    """Norm, rotate and write the entries of new tokens into the paged cache,
+    and rotate their queries (pmg_append).
+
+    c_kv [tokens, latent], k_pe [tokens, rope] and q_pe [tokens, heads, rope]
+    (bf16, fp16 or fp32, any row strides); cache [num_blocks, block_size,
+    latent + rope] (bf16, fp16, fp32 or e4m3 with `scale`); slots int64 and
+    positions int32 [tokens] as plan_step writes them; cos_sin fp32
+    [num_positions, rope] (cosines, then sines); norm_weight fp32 [latent] or
+    None (no norm). q_out like q_pe (it may be q_pe). interleaved: pairs are
+    neighbours instead of halves apart.
+    """
+    _unit_last(c_kv, 2, "c_kv")
+    _unit_last(k_pe, 2, "k_pe")
+    _unit_last(cache, 3, "cache")
+    t, dv = c_kv.shape
+    dr = k_pe.shape[1]
+    if k_pe.shape[0] != t or cache.shape[2] != dv + dr:
+        raise ValueError(f"c_kv {list(c_kv.shape)}, k_pe {list(k_pe.shape)} and cache {list(cache.shape)} do not fit")
+    if c_kv.dtype not in TORCH_DTYPE_CODES or k_pe.dtype != c_kv.dtype or cache.dtype not in TORCH_DTYPE_CODES:
+        raise ValueError(f"unsupported dtypes {c_kv.dtype}, {k_pe.dtype} -> {cache.dtype}")
+    if cos_sin.dtype != torch.float32 or cos_sin.dim() != 2 or cos_sin.shape[1] != dr or not cos_sin.is_contiguous():
+        raise ValueError(f"cos_sin must be float32 [num_positions, {dr}] and contiguous")
+    heads, qs, os_ = 0, (0, 0), (0, 0)
+    if (q_pe is None) != (q_out is None):
+        raise ValueError("q_pe and q_out go together")
+    if q_pe is not None:
+        _unit_last(q_pe, 3, "q_pe")
+        _unit_last(q_out, 3, "q_out")
+        heads = q_pe.shape[1]
+        if q_pe.shape != (t, heads, dr) or q_out.shape != q_pe.shape or q_pe.dtype != c_kv.dtype or (
+                q_out.dtype != c_kv.dtype):
+            raise ValueError(f"q_pe {list(q_pe.shape)} and q_out {list(q_out.shape)} must be [{t}, heads, {dr}] "
+                             f"of {c_kv.dtype}")
+        qs, os_ = q_pe.stride(), q_out.stride()
+    st = load_library().pmg_append(
+        c_kv.data_ptr(), c_kv.stride(0), k_pe.data_ptr(), k_pe.stride(0),
+        _vector(norm_weight, torch.float32, dv, "norm_weight", True), float(eps), cos_sin.data_ptr(), cos_sin.shape[0],
+        _vector(slots, torch.int64, t, "slots"), _vector(positions, torch.int32, t, "positions"), t, dv, dr,
+        TORCH_DTYPE_CODES[c_kv.dtype], cache.data_ptr(), cache.stride(0), cache.stride(1), cache.shape[0],
+        cache.shape[1], TORCH_DTYPE_CODES[cache.dtype], _scalar(scale, torch.float32, "scale"), _ptr(q_pe), qs[0],
+        qs[1], _ptr(q_out), os_[0], os_[1], heads, _scalar(error_flag, torch.int32, "error_flag"),
+        _stream_handle(stream), OPT_ROPE_PAIRS if interleaved else 0)
+    if st != PMG_OK:
+        raise PmgError(st, "pmg_append")
+
+
+def attention_workspace_bytes() -> int:
+    """Bytes of the workspace of latent_decode and latent_prefill on the
+    current device, for any sizes."""
+    n = load_library().pmg_attention_workspace()
+    if n < 0:
+        raise PmgError(6, "pmg_attention_workspace")
+    return int(n)
+
+
+def new_attention_workspace(device) -> torch.Tensor:
+    """A workspace for latent_decode and latent_prefill. One per stream: calls
+    that may overlap must not share one."""
+    with torch.cuda.device(device):
+        return torch.empty(attention_workspace_bytes(), dtype=torch.uint8, device=device)
+
+
+def latent_decode(q: torch.Tensor, cache: torch.Tensor, block_table: torch.Tensor, seq_lens: torch.Tensor,
+                  out: torch.Tensor, lse: Optional[torch.Tensor] = None, *, sm_scale: float,
+                  scale: Optional[torch.Tensor] = None, workspace: torch.Tensor,
+                  error_flag: Optional[torch.Tensor] = None, stream=None, options: int = 0) -> None:
+    """Absorbed latent attention of q_len new tokens a request over the paged
+    cache (pmg_latent_decode).
+
+    q         [num_reqs, q_len, heads, latent + rope] (bf16, fp16 or fp32)
+    cache     [num_blocks, block_size, latent + rope] of q's dtype, or e4m3
+              with `scale` (fp32 device scalar); the new tokens are in it
+    seq_lens  int32 [num_reqs], lengths with the new tokens: token i of q_len
+              sees the first seq_len - q_len + 1 + i entries
+    out       [num_reqs, q_len, heads, latent] of q's dtype; its last dimension
+              sets what is latent and what is rope
+    lse       fp32 [num_reqs, q_len, heads], contiguous, or None
+    """
+    _unit_last(q, 4, "q")
+    _unit_last(cache, 3, "cache")
+    _unit_last(out, 4, "out")
+    r, q_len, heads, entry = q.shape
+    dv = out.shape[3]
+    if out.shape[:3] != q.shape[:3] or cache.shape[2] != entry or not 1 <= dv <= entry:
+        raise ValueError(f"q {list(q.shape)}, cache {list(cache.shape)} and out {list(out.shape)} do not fit")
+    if q.dtype not in TORCH_DTYPE_CODES or out.dtype != q.dtype or cache.dtype not in TORCH_DTYPE_CODES:
+        raise ValueError(f"unsupported dtypes {q.dtype}, {cache.dtype} -> {out.dtype}")
+    if lse is not None and (lse.dtype != torch.float32 or lse.shape != q.shape[:3] or not lse.is_contiguous()):
+        raise ValueError(f"lse must be float32 {list(q.shape[:3])} and contiguous")
+    qs, os_ = q.stride(), out.stride()
+    st = load_library().pmg_latent_decode(
+        q.data_ptr(), qs[0], qs[1], qs[2], cache.data_ptr(), cache.stride(0), cache.stride(1), cache.shape[0],
+        block_table.data_ptr(), _reqs_table(block_table, r), _vector(seq_lens, torch.int32, r, "seq_lens"), r, q_len,
+        heads, dv, entry - dv, cache.shape[1], TORCH_DTYPE_CODES[q.dtype], TORCH_DTYPE_CODES[cache.dtype],
+        _scalar(scale, torch.float32, "scale"), float(sm_scale), out.data_ptr(), os_[0], os_[1], os_[2], _ptr(lse),
+        workspace.data_ptr(), workspace.numel() * workspace.element_size(),
+        _scalar(error_flag, torch.int32, "error_flag"), _stream_handle(stream), int(options))
+    if st != PMG_OK:
+        raise PmgError(st, "pmg_latent_decode")
+
+
+def latent_prefill(q: torch.Tensor, k_nope: torch.Tensor, k_pe: torch.Tensor, v: torch.Tensor, cu_q: torch.Tensor,
+                   cu_k: torch.Tensor, out: torch.Tensor, lse: Optional[torch.Tensor] = None, *, sm_scale: float,
+                   causal: bool = False, prev_out: Optional[torch.Tensor] = None,
+                   prev_lse: Optional[torch.Tensor] = None, workspace: torch.Tensor,
+                   error_flag: Optional[torch.Tensor] = None, stream=None, options: int = 0) -> None:
+    """Expanded latent attention of a chunk of new tokens (pmg_latent_prefill).
+
+    q       [total_q, heads, nope + rope]; k_nope [total_k, heads, nope]; k_pe
+            [total_k, rope], shared by the heads; v [total_k, heads, v_dim];
+            out [total_q, heads, v_dim]: one dtype (bf16, fp16 or fp32), any
+            strides but the last. Views of one up-projection and of gathered
+            entries are taken as they are.
+    cu_q, cu_k  int32 [num_reqs + 1]: rows of each request.
+    causal  query i of q_len sees the first k_len - q_len + i + 1 keys.
+    lse     fp32 [total_q, heads], contiguous, or None.
+    prev_out, prev_lse  the result over other keys, joined with this one's
+            (they may be out and lse).
+    """
+    _unit_last(q, 3, "q")
+    _unit_last(k_nope, 3, "k_nope")
+    _unit_last(k_pe, 2, "k_pe")
+    _unit_last(v, 3, "v")
+    _unit_last(out, 3, "out")
+    tq, heads, dk = q.shape
+    tk, _, dn = k_nope.shape
+    dr, dv = k_pe.shape[1], v.shape[2]
+    if k_nope.shape[1] != heads or v.shape[:2] != (tk, heads) or k_pe.shape[0] != tk or dn + dr != dk or (
+            out.shape != (tq, heads, dv)):
+        raise ValueError(f"q {list(q.shape)}, k_nope {list(k_nope.shape)}, k_pe {list(k_pe.shape)}, v "
+                         f"{list(v.shape)} and out {list(out.shape)} do not fit")
+    if q.dtype not in TORCH_DTYPE_CODES or any(t.dtype != q.dtype for t in (k_nope, k_pe, v, out)):
+        raise ValueError("q, k_nope, k_pe, v and out must have one supported dtype")
+    if (prev_out is None) != (prev_lse is None):
+        raise ValueError("prev_out and prev_lse go together")
+    ps = (0, 0)
+    if prev_out is not None:
+        _unit_last(prev_out, 3, "prev_out")
+        if prev_out.shape != out.shape or prev_out.dtype != out.dtype:
+            raise ValueError("prev_out must be like out")
+        ps = prev_out.stride()
+    for name, t in (("lse", lse), ("prev_lse", prev_lse)):
+        if t is not None and (t.dtype != torch.float32 or t.shape != (tq, heads) or not t.is_contiguous()):
+            raise ValueError(f"{name} must be float32 [{tq}, {heads}] and contiguous")
+    reqs = cu_q.shape[0] - 1
+    qs, ks, vs, os_ = q.stride(), k_nope.stride(), v.stride(), out.stride()
+    st = load_library().pmg_latent_prefill(
+        q.data_ptr(), qs[0], qs[1], k_nope.data_ptr(), ks[0], ks[1], k_pe.data_ptr(), k_pe.stride(0), v.data_ptr(),
+        vs[0], vs[1], _vector(cu_q, torch.int32, reqs + 1, "cu_q"), _vector(cu_k, torch.int32, reqs + 1, "cu_k"), reqs,
+        tq, tk, heads, dn, dr, dv, TORCH_DTYPE_CODES[q.dtype], float(sm_scale), out.data_ptr(), os_[0], os_[1],
+        _ptr(lse), _ptr(prev_out), ps[0], ps[1], _ptr(prev_lse), workspace.data_ptr(),
+        workspace.numel() * workspace.element_size(), _scalar(error_flag, torch.int32, "error_flag"),
+        _stream_handle(stream), (OPT_CAUSAL if causal else 0) | int(options))
+    if st != PMG_OK:
+        raise PmgError(st, "pmg_latent_prefill")

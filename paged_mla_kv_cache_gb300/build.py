@@ -1,9 +1,9 @@
 """Builds the CUDA library ``libpmg.so`` in-tree with nvcc for sm_103a.
 
-One translation unit (``csrc/pmg_gather.cu``), one ``-gencode``, the CUDA
-runtime linked statically, no fast-math. The library lands in
-``paged_mla_kv_cache_gb300/lib/`` (git-ignored) and is rebuilt when the source
-or the public header is newer than it.
+The translation units of ``csrc/`` are compiled in parallel, with one
+``-gencode``, and linked with the CUDA runtime statically; no fast-math. The
+library lands in ``paged_mla_kv_cache_gb300/lib/`` (git-ignored) and is rebuilt
+when a source or a public header is newer than it.
 """
 from __future__ import annotations
 
@@ -11,10 +11,14 @@ import os
 import shutil
 import subprocess
 
+UNITS = ["mla_plan.cu", "mla_append.cu", "mla_decode.cu", "mla_prefill.cu"]
 PKG_DIR = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(PKG_DIR)
-SRC = os.path.join(PKG_DIR, "csrc", "pmg_gather.cu")
+CSRC = os.path.join(PKG_DIR, "csrc")
+SRC = os.path.join(CSRC, "pmg_gather.cu")
+SOURCES = [SRC] + [os.path.join(CSRC, f) for f in UNITS]
 HEADER = os.path.join(ROOT, "include", "pmg.h")
+HEADERS = [HEADER, os.path.join(ROOT, "include", "pmg_mla.h")]
 LIB_DIR = os.path.join(PKG_DIR, "lib")
 LIB_PATH = os.path.join(LIB_DIR, "libpmg.so")
 
@@ -22,8 +26,8 @@ NVCC_FLAGS = [
     "-gencode", "arch=compute_103a,code=sm_103a",
     "-lineinfo", "-O3", "-std=c++17",
     "-Xcompiler", "-fPIC", "-Xcompiler", "-O2",
-    "-shared", "-cudart", "static",
 ]
+LINK_FLAGS = ["-gencode", "arch=compute_103a,code=sm_103a", "-shared", "-cudart", "static"]
 
 
 def nvcc_path() -> str:
@@ -37,7 +41,8 @@ def needs_build() -> bool:
     if not os.path.exists(LIB_PATH):
         return True
     t = os.path.getmtime(LIB_PATH)
-    return any(os.path.getmtime(f) > t for f in (SRC, HEADER, __file__))
+    shared = [os.path.join(CSRC, f) for f in os.listdir(CSRC) if f.endswith(".cuh")]
+    return any(os.path.getmtime(f) > t for f in (*SOURCES, *HEADERS, *shared, __file__))
 
 
 def build_library(force: bool = False, verbose: bool = False) -> str:
@@ -46,12 +51,24 @@ def build_library(force: bool = False, verbose: bool = False) -> str:
         return LIB_PATH
     os.makedirs(LIB_DIR, exist_ok=True)
     tmp = LIB_PATH + f".tmp{os.getpid()}"
-    cmd = [nvcc_path(), *NVCC_FLAGS, "-I", os.path.join(ROOT, "include"), "-o", tmp, SRC]
-    if verbose:
-        cmd.insert(1, "-Xptxas=-v")
-    res = subprocess.run(cmd, capture_output=True, text=True)
-    if res.returncode != 0:
-        raise RuntimeError(f"nvcc failed ({res.returncode}):\n{' '.join(cmd)}\n{res.stdout}\n{res.stderr}")
+    objects = [f"{tmp}.{i}.o" for i in range(len(SOURCES))]
+    common = [nvcc_path(), *NVCC_FLAGS, *(["-Xptxas=-v"] if verbose else []), "-I", os.path.join(ROOT, "include")]
+    try:
+        jobs = [(cmd, subprocess.Popen(cmd, stdout=subprocess.PIPE, stderr=subprocess.STDOUT, text=True))
+                for cmd in ([*common, "-c", "-o", o, src] for o, src in zip(objects, SOURCES))]
+        for cmd, out, rc in [(cmd, j.communicate()[0], j.returncode) for cmd, j in jobs]:
+            if rc != 0:
+                raise RuntimeError(f"nvcc failed ({rc}):\n{' '.join(cmd)}\n{out}")
+            if verbose:
+                print(out)
+        cmd = [nvcc_path(), *LINK_FLAGS, "-o", tmp, *objects]
+        res = subprocess.run(cmd, capture_output=True, text=True)
+        if res.returncode != 0:
+            raise RuntimeError(f"nvcc failed ({res.returncode}):\n{' '.join(cmd)}\n{res.stdout}\n{res.stderr}")
+    finally:
+        for o in objects:
+            if os.path.exists(o):
+                os.remove(o)
     os.replace(tmp, LIB_PATH)
     return LIB_PATH
 

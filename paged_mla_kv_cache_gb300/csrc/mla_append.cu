@@ -1,0 +1,372 @@
+// Norm, rotation and the write of new entries into the paged cache
+// (pmg_append).
+//
+// Mathematics, for each token: y = c * rsqrt(mean(c^2) + eps) * w over the
+// latent part; every pair (a, b) of the rotated part, of the shared key and of
+// each head's query, goes to (a cos - b sin, b cos + a sin). All in 32 bits,
+// one rounding at the store (an e4m3 cache: y / scale, to nearest even,
+// saturating).
+//
+// Bound by memory: an entry in and out, 2 * rope_dim elements a head, one row
+// of cosines and sines a token. One warp takes either a token's entry (the
+// latent row stays in registers between the sum and the store, so it is read
+// once) or a few heads of a token's queries, for which a lane keeps one set of
+// four cosines and sines in registers and issues all its loads before the
+// first store. Units are four pairs: 16 bytes of 16-bit values where pairs are
+// neighbours, two times 8 bytes where halves are rotated. Rows that are not
+// 16-byte aligned or not whole units take the same warps element by element.
+#include "mla_common.cuh"
+
+namespace pmg_mla {
+namespace {
+
+constexpr int kWarps = 4;
+constexpr int kIters = 4;          // row groups of queries a warp has in flight
+constexpr int kMaxLatentUnits = 4; // units of 8 latent values a lane holds: latent_dim up to 1024
+
+struct AppendParams {
+  const uint8_t* c_kv;
+  int64_t c_stride;
+  const uint8_t* k_pe;
+  int64_t k_stride;
+  const float* weight;
+  float eps;
+  const float* cos_sin;
+  int64_t num_positions;
+  const int64_t* slots;
+  const int32_t* positions;
+  int64_t T;
+  int32_t dv, dr;
+  uint8_t* cache;
+  int64_t blk_stride, tok_stride;
+  int64_t num_blocks;
+  int32_t B;
+  const float* scale;
+  const uint8_t* q;
+  int64_t qt_stride, qh_stride;
+  uint8_t* qo;
+  int64_t ot_stride, oh_stride;
+  int32_t H;
+  int32_t heads_per_task;
+  int32_t tasks_per_token;  // 1 entry + query tasks
+  int32_t pairs;
+  int32_t* err;
+};
+
+// N values (a multiple of 4 bytes in all, aligned to their size up to 16)
+template <class T, int N>
+struct Pack {
+  static constexpr int kBytes = N * static_cast<int>(sizeof(T));
+  static constexpr int kAlign = kBytes < 16 ? kBytes : 16;
+  alignas(kAlign) T v[N];
+};
+
+template <class T, int N>
+__device__ __forceinline__ void load_n(const T* src, float* x) {
+  const Pack<T, N> p = *reinterpret_cast<const Pack<T, N>*>(src);
+#pragma unroll
+  for (int i = 0; i < N; ++i) x[i] = to_f(p.v[i]);
+}
+
+template <class T, int N>
+__device__ __forceinline__ void store_n(T* dst, const float* x) {
+  Pack<T, N> p;
+  if constexpr (sizeof(T) == 1) {
+#pragma unroll
+    for (int i = 0; i < N; i += 2) {
+      const __nv_fp8x2_storage_t two = __nv_cvt_float2_to_fp8x2(make_float2(x[i], x[i + 1]), __NV_SATFINITE, __NV_E4M3);
+      p.v[i].__x = static_cast<__nv_fp8_storage_t>(two & 0xff);
+      p.v[i + 1].__x = static_cast<__nv_fp8_storage_t>(two >> 8);
+    }
+  } else {
+#pragma unroll
+    for (int i = 0; i < N; ++i) p.v[i] = from_f<T>(x[i]);
+  }
+  *reinterpret_cast<Pack<T, N>*>(dst) = p;
+}
+
+// The four pairs of unit u of a row: a and b of each.
+template <class T>
+__device__ __forceinline__ void load_pairs(const T* row, int u, int half, bool pairs, float* a, float* b) {
+  if (pairs) {
+    float x[8];
+    load_n<T, 8>(row + 8 * u, x);
+#pragma unroll
+    for (int i = 0; i < 4; ++i) { a[i] = x[2 * i]; b[i] = x[2 * i + 1]; }
+  } else {
+    load_n<T, 4>(row + 4 * u, a);
+    load_n<T, 4>(row + half + 4 * u, b);
+  }
+}
+
+template <class T>
+__device__ __forceinline__ void store_pairs(T* row, int u, int half, bool pairs, const float* a, const float* b) {
+  if (pairs) {
+    float x[8];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) { x[2 * i] = a[i]; x[2 * i + 1] = b[i]; }
+    store_n<T, 8>(row + 8 * u, x);
+  } else {
+    store_n<T, 4>(row + 4 * u, a);
+    store_n<T, 4>(row + half + 4 * u, b);
+  }
+}
+
+__device__ __forceinline__ void rotate(float& a, float& b, float c, float s) {
+  const float x = a * c - b * s, y = b * c + a * s;
+  a = x;
+  b = y;
+}
+
+__device__ __forceinline__ float warp_sum(float x) {
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) x += __shfl_xor_sync(0xffffffffu, x, o);
+  return x;
+}
+
+template <class TS, class TC, bool kVec>
+__global__ void __launch_bounds__(kWarps * 32) append_kernel(const __grid_constant__ AppendParams p) {
+  pdl_entry();
+  const int lane = threadIdx.x & 31;
+  const int64_t task = static_cast<int64_t>(blockIdx.x) * kWarps + (threadIdx.x >> 5);
+  const int64_t t = task / p.tasks_per_token;
+  if (t >= p.T) return;
+  const int part = static_cast<int>(task - t * p.tasks_per_token);
+  const int half = p.dr >> 1;
+  const bool pairs = p.pairs != 0;
+  const int32_t pos = p.positions[t];
+  const bool turned = pos >= 0 && pos < p.num_positions;
+  const float* cs = p.cos_sin + static_cast<int64_t>(turned ? pos : 0) * p.dr;
+
+  if (part == 0) {
+    const int64_t slot = p.slots[t];
+    if (slot < 0) {
+      if (lane == 0 && pos >= p.num_positions) set_flag(p.err, PMG_FLAG_POSITION);
+      return;
+    }
+    const int64_t block = slot / p.B;
+    if (!turned || block >= p.num_blocks) {
+      if (lane == 0)
+        set_flag(p.err, (turned ? 0 : PMG_FLAG_POSITION) | (block < p.num_blocks ? 0 : PMG_FLAG_PHYS_BLOCK));
+      return;
+    }
+    const TS* c = reinterpret_cast<const TS*>(p.c_kv) + t * p.c_stride;
+    const TS* kp = reinterpret_cast<const TS*>(p.k_pe) + t * p.k_stride;
+    TC* row = reinterpret_cast<TC*>(p.cache) + block * p.blk_stride + (slot - block * p.B) * p.tok_stride;
+    const float scale = sizeof(TC) == 1 && p.scale != nullptr ? *p.scale : 1.0f;
+    const float inv_n = 1.0f / static_cast<float>(p.dv);
+    if constexpr (kVec) {
+      float x[kMaxLatentUnits][8];
+      float a[4], b[4], co[4], si[4];
+      const bool turns = lane * 8 < p.dr;
+      // every load of the token first
+#pragma unroll
+      for (int i = 0; i < kMaxLatentUnits; ++i)
+        if ((lane + 32 * i) * 8 < p.dv) load_n<TS, 8>(c + (lane + 32 * i) * 8, x[i]);
+      if (turns) {
+        load_pairs(kp, lane, half, pairs, a, b);
+        load_n<float, 4>(cs + 4 * lane, co);
+        load_n<float, 4>(cs + half + 4 * lane, si);
+      }
+      float inv = 1.0f;
+      if (p.weight != nullptr) {
+        float sum = 0.0f;
+#pragma unroll
+        for (int i = 0; i < kMaxLatentUnits; ++i)
+          if ((lane + 32 * i) * 8 < p.dv) {
+#pragma unroll
+            for (int k = 0; k < 8; ++k) sum += x[i][k] * x[i][k];
+          }
+        inv = rsqrtf(warp_sum(sum) * inv_n + p.eps);
+      }
+#pragma unroll
+      for (int i = 0; i < kMaxLatentUnits; ++i) {
+        const int at = (lane + 32 * i) * 8;
+        if (at >= p.dv) continue;
+        if (p.weight != nullptr) {
+          float w[8];
+          load_n<float, 4>(p.weight + at, w);
+          load_n<float, 4>(p.weight + at + 4, w + 4);
+#pragma unroll
+          for (int k = 0; k < 8; ++k) x[i][k] = x[i][k] * inv * w[k];
+        }
+        if constexpr (sizeof(TC) == 1) {
+#pragma unroll
+          for (int k = 0; k < 8; ++k) x[i][k] = x[i][k] / scale;
+        }
+        store_n<TC, 8>(row + at, x[i]);
+      }
+      if (turns) {
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+          rotate(a[k], b[k], co[k], si[k]);
+          if constexpr (sizeof(TC) == 1) { a[k] = a[k] / scale; b[k] = b[k] / scale; }
+        }
+        store_pairs(row + p.dv, lane, half, pairs, a, b);
+      }
+    } else {
+      float inv = 1.0f;
+      if (p.weight != nullptr) {
+        float sum = 0.0f;
+        for (int i = lane; i < p.dv; i += 32) {
+          const float v = to_f(c[i]);
+          sum += v * v;
+        }
+        inv = rsqrtf(warp_sum(sum) * inv_n + p.eps);
+      }
+      for (int i = lane; i < p.dv; i += 32) {
+        float v = to_f(c[i]);
+        if (p.weight != nullptr) v = v * inv * p.weight[i];
+        row[i] = from_f<TC>(sizeof(TC) == 1 ? v / scale : v);
+      }
+      for (int i = lane; i < half; i += 32) {
+        const int ia = pairs ? 2 * i : i, ib = pairs ? 2 * i + 1 : i + half;
+        float a = to_f(kp[ia]), b = to_f(kp[ib]);
+        rotate(a, b, cs[i], cs[half + i]);
+        row[p.dv + ia] = from_f<TC>(sizeof(TC) == 1 ? a / scale : a);
+        row[p.dv + ib] = from_f<TC>(sizeof(TC) == 1 ? b / scale : b);
+      }
+    }
+    return;
+  }
+
+  // heads of a token's queries
+  if (!turned) return;  // reported by the entry's warp
+  const int h0 = (part - 1) * p.heads_per_task;
+  const int h1 = min(h0 + p.heads_per_task, p.H);
+  const TS* q = reinterpret_cast<const TS*>(p.q) + t * p.qt_stride;
+  TS* o = reinterpret_cast<TS*>(p.qo) + t * p.ot_stride;
+  if constexpr (kVec) {
+    const int lanes = p.dr >> 3;      // lanes of a row: a divisor of 32
+    const int u = lane & (lanes - 1), step = 32 / lanes;
+    float co[4], si[4];
+    load_n<float, 4>(cs + 4 * u, co);
+    load_n<float, 4>(cs + half + 4 * u, si);
+    float a[kIters][4], b[kIters][4];
+    const int h = h0 + lane / lanes;
+#pragma unroll
+    for (int i = 0; i < kIters; ++i)
+      if (h + i * step < h1) load_pairs(q + (h + i * step) * p.qh_stride, u, half, pairs, a[i], b[i]);
+#pragma unroll
+    for (int i = 0; i < kIters; ++i)
+      if (h + i * step < h1) {
+#pragma unroll
+        for (int k = 0; k < 4; ++k) rotate(a[i][k], b[i][k], co[k], si[k]);
+        store_pairs(o + (h + i * step) * p.oh_stride, u, half, pairs, a[i], b[i]);
+      }
+  } else {
+    for (int h = h0; h < h1; ++h)
+      for (int i = lane; i < half; i += 32) {
+        const int ia = pairs ? 2 * i : i, ib = pairs ? 2 * i + 1 : i + half;
+        float a = to_f(q[h * p.qh_stride + ia]), b = to_f(q[h * p.qh_stride + ib]);
+        rotate(a, b, cs[i], cs[half + i]);
+        o[h * p.oh_stride + ia] = from_f<TS>(a);
+        o[h * p.oh_stride + ib] = from_f<TS>(b);
+      }
+  }
+}
+
+using Kernel = void (*)(const AppendParams);
+
+template <class TS, class TC>
+Kernel pick(bool vec) {
+  return vec ? append_kernel<TS, TC, true> : append_kernel<TS, TC, false>;
+}
+
+template <class TS>
+Kernel pick(int cache_dtype, bool vec) {
+  switch (cache_dtype) {
+    case PMG_BF16: return pick<TS, bf16>(vec);
+    case PMG_FP16: return pick<TS, f16>(vec);
+    case PMG_FP32: return pick<TS, float>(vec);
+    default: return pick<TS, e4m3>(vec);
+  }
+}
+
+}  // namespace
+}  // namespace pmg_mla
+
+extern "C" int pmg_append(const void* c_kv, int64_t c_kv_stride, const void* k_pe, int64_t k_pe_stride,
+                          const float* norm_weight, float eps, const float* cos_sin, int64_t num_positions,
+                          const int64_t* slots, const int32_t* positions, int64_t num_tokens, int32_t latent_dim,
+                          int32_t rope_dim, int32_t src_dtype, void* cache, int64_t cache_block_stride,
+                          int64_t cache_token_stride, int64_t num_blocks, int32_t block_size, int32_t cache_dtype,
+                          const float* scale, const void* q_pe, int64_t q_pe_token_stride, int64_t q_pe_head_stride,
+                          void* q_out, int64_t q_out_token_stride, int64_t q_out_head_stride, int32_t heads,
+                          int32_t* error_flag, void* stream, uint32_t options) {
+  using namespace pmg_mla;
+  const int es = elem_bytes(src_dtype), ec = elem_bytes(cache_dtype);
+  if (es < 2 || ec == 0) return PMG_ERR_DTYPE;
+  if (latent_dim < 1 || rope_dim < 0 || rope_dim % 2 != 0 || num_positions < 0 || num_tokens < 0 || num_blocks < 0 ||
+      block_size < 1 || heads < 0 || !(eps >= 0.0f) || (options & ~PMG_OPT_ROPE_PAIRS))
+    return PMG_ERR_ARG;
+  if (!stride_ok(c_kv_stride) || !stride_ok(k_pe_stride) || !stride_ok(cache_block_stride) ||
+      !stride_ok(cache_token_stride) || !stride_ok(q_pe_token_stride) || !stride_ok(q_pe_head_stride) ||
+      !stride_ok(q_out_token_stride) || !stride_ok(q_out_head_stride))
+    return PMG_ERR_ARG;
+  if (num_tokens > INT32_MAX || num_positions > INT32_MAX || num_blocks > INT32_MAX || latent_dim > (1 << 20) ||
+      rope_dim > (1 << 20) || heads > (1 << 16))
+    return PMG_ERR_UNSUPPORTED;
+  if (num_tokens == 0) return PMG_OK;
+  if (c_kv == nullptr || slots == nullptr || positions == nullptr || (cache == nullptr && num_blocks > 0) ||
+      (rope_dim > 0 && (k_pe == nullptr || (cos_sin == nullptr && num_positions > 0))) ||
+      (heads > 0 && rope_dim > 0 && (q_pe == nullptr || q_out == nullptr)))
+    return PMG_ERR_NULL;
+  if (!aligned(c_kv, es) || !aligned(k_pe, es) || !aligned(norm_weight, 4) || !aligned(cos_sin, 4) ||
+      !aligned(slots, 8) || !aligned(positions, 4) || !aligned(cache, ec) || !aligned(scale, 4) ||
+      !aligned(q_pe, es) || !aligned(q_out, es) || !aligned(error_flag, 4))
+    return PMG_ERR_ALIGN;
+  if (rope_dim == 0) {
+    heads = 0;
+    num_positions = INT32_MAX;  // nothing is looked up
+  }
+  AppendParams p{};
+  p.c_kv = static_cast<const uint8_t*>(c_kv);
+  p.c_stride = c_kv_stride;
+  p.k_pe = static_cast<const uint8_t*>(k_pe);
+  p.k_stride = k_pe_stride;
+  p.weight = norm_weight;
+  p.eps = eps;
+  p.cos_sin = cos_sin;
+  p.num_positions = num_positions;
+  p.slots = slots;
+  p.positions = positions;
+  p.T = num_tokens;
+  p.dv = latent_dim;
+  p.dr = rope_dim;
+  p.cache = static_cast<uint8_t*>(cache);
+  p.blk_stride = cache_block_stride;
+  p.tok_stride = cache_token_stride;
+  p.num_blocks = num_blocks;
+  p.B = block_size;
+  p.scale = scale;
+  p.q = static_cast<const uint8_t*>(q_pe);
+  p.qt_stride = q_pe_token_stride;
+  p.qh_stride = q_pe_head_stride;
+  p.qo = static_cast<uint8_t*>(q_out);
+  p.ot_stride = q_out_token_stride;
+  p.oh_stride = q_out_head_stride;
+  p.H = heads;
+  p.pairs = (options & PMG_OPT_ROPE_PAIRS) ? 1 : 0;
+  p.err = error_flag;
+  // whole units at 16-byte aligned rows (8-byte rows of an e4m3 cache); a row
+  // of queries takes a power of two of lanes
+  auto rows16 = [](const void* base, int bytes, int64_t s0, int64_t s1) {
+    const int n = 8 * bytes < 16 ? 8 * bytes : 16;
+    return aligned(base, n) && s0 * bytes % n == 0 && s1 * bytes % n == 0;
+  };
+  const int lanes = rope_dim / 8;
+  const bool vec = latent_dim % 8 == 0 && latent_dim <= kMaxLatentUnits * 256 && rope_dim % 8 == 0 && rope_dim > 0 &&
+                   lanes <= 32 && (lanes & (lanes - 1)) == 0 && rows16(c_kv, es, c_kv_stride, 0) &&
+                   rows16(k_pe, es, k_pe_stride, 0) && rows16(cache, ec, cache_block_stride, cache_token_stride) &&
+                   aligned(cos_sin, 16) && aligned(norm_weight, 16) &&
+                   (heads == 0 || (rows16(q_pe, es, q_pe_token_stride, q_pe_head_stride) &&
+                                   rows16(q_out, es, q_out_token_stride, q_out_head_stride)));
+  p.heads_per_task = vec ? kIters * (32 / lanes) : 8;
+  p.tasks_per_token = 1 + (heads + p.heads_per_task - 1) / p.heads_per_task;
+  const int64_t ctas = (num_tokens * p.tasks_per_token + kWarps - 1) / kWarps;
+  if (ctas > INT32_MAX) return PMG_ERR_UNSUPPORTED;
+  const Kernel k = src_dtype == PMG_BF16 ? pick<bf16>(cache_dtype, vec)
+                   : src_dtype == PMG_FP16 ? pick<f16>(cache_dtype, vec) : pick<float>(cache_dtype, vec);
+  return launch(k, dim3(static_cast<unsigned>(ctas)), kWarps * 32, 0, stream, p);
+}

@@ -1,0 +1,195 @@
+// What the attention kernels share: how a flat list of work is cut into equal
+// shares, where a share's unfinished rows go, and the kernel body for any
+// sizes.
+//
+// The work of a call is a flat list of equal pieces (a tile of keys for one
+// group of rows), request after request. The list is cut into as many equal
+// shares as there are units (a unit is the CTAs that run one share, one for
+// each group of rows), so long and short requests cost every SM the same. A
+// request that a share covers whole is finished there. One that a cut falls
+// into leaves, from every share that holds a part of it, the unnormalised
+// rows, their running maximum and their sum in the workspace; the share that
+// holds its first piece notes how many shares follow, and the join kernel adds
+// them up in their order, so results do not depend on timing.
+#pragma once
+
+#include "mla_common.cuh"
+
+namespace pmg_mla {
+
+constexpr float kLog2e = 1.4426950408889634f;
+constexpr float kLn2 = 0.6931471805599453f;
+
+// Workspace: one note a CTA, then two slots of unfinished rows a CTA (0: the
+// share began inside the request, 1: the share ended inside it).
+struct JoinNote {
+  int32_t item;   // request (decode) or item (prefill) that begins in this share and goes on, or -1
+  int32_t parts;  // shares that hold it
+};
+constexpr int kNotesPerSm = 4;
+constexpr int64_t kSlotFloats = 256 * 130;  // the largest slot: 256 rows of 128 values, or 64 of 512, and two sums each
+
+struct Workspace {
+  JoinNote* notes;
+  float* slots;
+};
+
+inline int64_t workspace_notes(int sms) { return static_cast<int64_t>(sms) * kNotesPerSm * sizeof(JoinNote); }
+inline int64_t workspace_bytes(int sms) { return (workspace_notes(sms) + 255) / 256 * 256 + 2 * sms * kSlotFloats * 4; }
+inline Workspace workspace_at(void* base, int sms) {
+  uint8_t* b = static_cast<uint8_t*>(base);
+  return {reinterpret_cast<JoinNote*>(b), reinterpret_cast<float*>(b + (workspace_notes(sms) + 255) / 256 * 256)};
+}
+
+struct Share {
+  int64_t begin, end;  // flat pieces
+  int64_t total;
+  int32_t units;       // units that have a share: none of them is empty
+  int32_t item;        // the item that holds `begin`
+  int64_t offset;      // pieces of it before `begin`
+};
+
+// This unit's share of sum over items of pieces(item), found by the whole
+// block. `scratch`: 33 int64, `found`: 2 int64, both shared.
+template <class F>
+__device__ __forceinline__ Share find_share(F pieces, int items, int unit, int units, int64_t* scratch, int64_t* found) {
+  const int nt = blockDim.x, tid = threadIdx.x;
+  Share s;
+  int64_t mine = 0, total = 0;
+  for (int i = tid; i < items; i += nt) mine += pieces(i);
+  int64_t before = block_scan<int64_t>(mine, scratch, total);
+  s.total = total;
+  s.units = static_cast<int32_t>(min(static_cast<int64_t>(units), total));
+  s.begin = unit < s.units ? total * unit / s.units : total;
+  s.end = unit < s.units ? total * (unit + 1) / s.units : total;
+  if (tid == 0) {
+    found[0] = items;
+    found[1] = 0;
+  }
+  __syncthreads();
+  if (items <= nt) {  // `mine` is one item
+    if (before <= s.begin && s.begin < before + mine) {
+      found[0] = tid;
+      found[1] = s.begin - before;
+    }
+  } else {
+    int64_t run = 0;
+    for (int base = 0; base < items; base += nt) {
+      const int64_t x = base + tid < items ? pieces(base + tid) : 0;
+      int64_t sum;
+      const int64_t at = run + block_scan<int64_t>(x, scratch, sum);
+      if (at <= s.begin && s.begin < at + x) {
+        found[0] = base + tid;
+        found[1] = s.begin - at;
+      }
+      run += sum;
+      if (run > s.begin) break;
+    }
+  }
+  __syncthreads();
+  s.item = static_cast<int32_t>(found[0]);
+  s.offset = found[1];
+  return s;
+}
+
+// The unit whose share holds flat piece x.
+__device__ __forceinline__ int unit_of(int64_t x, int64_t total, int units) {
+  int64_t u = x * units / total;
+  while (u + 1 < units && total * (u + 1) / units <= x) ++u;
+  while (u > 0 && total * u / units > x) --u;
+  return static_cast<int>(u);
+}
+
+// ---- the body for any sizes -------------------------------------------------
+
+constexpr int kGenRows = 8;    // rows of one pass: a warp each
+constexpr int kGenKeys = 32;   // keys of a tile: a lane each
+constexpr int kGenThreads = kGenRows * 32;
+constexpr int kGenCols = PMG_MAX_ENTRY / kGenThreads;  // value columns of a thread
+
+struct GenSmem {
+  float* q;      // [kGenRows][E]
+  float* k;      // [kGenKeys][E + 1]
+  float* p;      // [kGenRows][kGenKeys]
+  float* scale;  // [kGenRows]
+};
+
+inline int general_smem(int E) { return (kGenRows * E + kGenKeys * (E + 1) + kGenRows * kGenKeys + kGenRows) * 4; }
+
+__device__ __forceinline__ GenSmem general_smem_at(uint8_t* base, int E) {
+  GenSmem s;
+  s.q = reinterpret_cast<float*>(base);
+  s.k = s.q + kGenRows * E;
+  s.p = s.k + kGenKeys * (E + 1);
+  s.scale = s.p + kGenRows * kGenKeys;
+  return s;
+}
+
+// Keys [j0, j1) for up to 8 rows whose queries are in s.q: one pass with the
+// running maximum m (log2 domain) and sum l of each row, all in 32 bits.
+//   load(j, e): element e of key j, or NaN-free 0;  seen(row, j);
+//   value(j - tile, j, d): element d of the value of key j (only called where some row sees j)
+template <class Load, class Seen, class Value>
+__device__ __forceinline__ void general_rows(const GenSmem& s, int E, int dv, int64_t j0, int64_t j1, float sm_log2,
+                                             Load load, Seen seen, Value value, float (&acc)[kGenRows][kGenCols],
+                                             float& m, float& l) {
+  const int tid = threadIdx.x, lane = tid & 31, row = tid >> 5;
+#pragma unroll
+  for (int r = 0; r < kGenRows; ++r)
+#pragma unroll
+    for (int c = 0; c < kGenCols; ++c) acc[r][c] = 0.0f;
+  m = -INFINITY;
+  l = 0.0f;
+  for (int64_t t = j0; t < j1; t += kGenKeys) {
+    const int n = static_cast<int>(min(static_cast<int64_t>(kGenKeys), j1 - t));
+    __syncthreads();
+    for (int j = row; j < kGenKeys; j += kGenRows)
+      for (int e = lane; e < E; e += 32) s.k[j * (E + 1) + e] = j < n ? load(t + j, e) : 0.0f;
+    __syncthreads();
+    const bool mine = lane < n && seen(row, t + lane);
+    float x = 0.0f;
+    for (int e = 0; e < E; ++e) x += s.q[row * E + e] * s.k[lane * (E + 1) + e];
+    x = mine ? x * sm_log2 : -INFINITY;
+    float top = x;
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
+    const float next = fmaxf(m, top);
+    const float base = next == -INFINITY ? 0.0f : next;
+    const float w = mine ? exp2f(x - base) : 0.0f;
+    float sum = w;
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
+    const float keep = m == -INFINITY ? 0.0f : exp2f(m - base);
+    l = l * keep + sum;
+    m = next;
+    s.p[row * kGenKeys + lane] = w;
+    if (lane == 0) s.scale[row] = keep;
+    __syncthreads();
+#pragma unroll
+    for (int r = 0; r < kGenRows; ++r)
+#pragma unroll
+      for (int c = 0; c < kGenCols; ++c) acc[r][c] *= s.scale[r];
+    for (int j = 0; j < n; ++j) {
+      float w8[kGenRows];
+      bool any = false;
+#pragma unroll
+      for (int r = 0; r < kGenRows; ++r) {
+        w8[r] = s.p[r * kGenKeys + j];
+        any |= w8[r] != 0.0f;
+      }
+      if (!any) continue;
+#pragma unroll
+      for (int c = 0; c < kGenCols; ++c) {
+        const int d = tid + c * kGenThreads;
+        if (d < dv) {
+          const float v = value(j, t + j, d);
+#pragma unroll
+          for (int r = 0; r < kGenRows; ++r)
+            if (w8[r] != 0.0f) acc[r][c] += w8[r] * v;
+        }
+      }
+    }
+  }
+}
+
+}  // namespace pmg_mla
