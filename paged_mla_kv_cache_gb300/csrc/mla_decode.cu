@@ -8,6 +8,7 @@
 #include <algorithm>
 
 #include "mla_decode.cuh"
+#include "mla_decode_tc.cuh"
 
 namespace pmg_mla {
 namespace {
@@ -271,18 +272,22 @@ extern "C" int pmg_latent_decode(const void* q, int64_t q_req_stride, int64_t q_
   p.ws = workspace_at(workspace, sms);
   p.err = error_flag;
   const int rows = q_len * heads;
-  p.rows_per_group = std::min(rows, kGenRows);
-  p.groups = (rows + p.rows_per_group - 1) / p.rows_per_group;
-  // as many shares as fill the SMs; more groups than that run whole requests
-  p.units = std::max(1, sms / p.groups);
-  p.slot_floats = (static_cast<int64_t>(p.rows_per_group) * (p.dv + 2) + 3) / 4 * 4;
-  const int E = p.dv + p.dr;
-  const Kernel k = general_kernel(q_dtype, cache_dtype);
-  st = allow_smem(reinterpret_cast<const void*>(k), general_smem(PMG_MAX_ENTRY));
-  if (st != PMG_OK) return st;
-  const unsigned ctas = static_cast<unsigned>(p.units) * p.groups;
-  st = launch(k, dim3(ctas), kGenThreads, general_smem(E), stream, p);
+  if (!(options & PMG_OPT_FORCE_GENERAL) && decode_tc_takes(p, q_dtype, cache_dtype)) {
+    st = decode_tc(p, q_dtype, cache_dtype, sms, stream);
+  } else {
+    p.rows_per_group = std::min(rows, kGenRows);
+    p.groups = (rows + p.rows_per_group - 1) / p.rows_per_group;
+    // as many shares as fill the SMs; more groups than that run whole requests
+    p.units = std::max(1, sms / p.groups);
+    p.slot_floats = (static_cast<int64_t>(p.rows_per_group) * (p.dv + 2) + 3) / 4 * 4;
+    const int E = p.dv + p.dr;
+    const Kernel k = general_kernel(q_dtype, cache_dtype);
+    st = allow_smem(reinterpret_cast<const void*>(k), general_smem(PMG_MAX_ENTRY));
+    if (st != PMG_OK) return st;
+    st = launch(k, dim3(static_cast<unsigned>(p.units) * p.groups), kGenThreads, general_smem(E), stream, p);
+  }
   if (st != PMG_OK || p.units == 1) return st;
+  const unsigned ctas = static_cast<unsigned>(p.units) * p.groups;
   const Kernel join = q_dtype == PMG_BF16 ? decode_join_kernel<bf16>
                       : q_dtype == PMG_FP16 ? decode_join_kernel<f16> : decode_join_kernel<float>;
   return launch(join, dim3(ctas, static_cast<unsigned>(p.rows_per_group)), kJoinThreads, 0, stream, p);

@@ -27,6 +27,7 @@ struct DecodeParams {
   int32_t* err;
   int32_t rows_per_group, groups, units;
   int64_t slot_floats;
+  int32_t out_pairs;  // rows of out begin at 4 bytes
 };
 
 struct DecodeLen {

@@ -54,7 +54,7 @@ def rotate(x, cs, pairs):
 
 def attend(q, k, v, seen, sm_scale):
     """One head group: q [n, e], k [m, e], v [m, d], seen [n, m], all 64 bits. Returns out, lse, and what bounds the
-    errors: sum p|v| and the largest sum |q k| sm_scale of a seen key."""
+    errors: sum p|v|, the largest sum |q k| sm_scale of a seen key, and the largest p times sum |v| of seen keys."""
     s = q @ k.T * sm_scale
     mag = (q.abs() @ k.abs().T * sm_scale).masked_fill(~seen, 0.0)
     s = s.masked_fill(~seen, -math.inf)
@@ -62,7 +62,8 @@ def attend(q, k, v, seen, sm_scale):
     p = torch.exp(s - torch.where(lse == -math.inf, 0.0, lse)[:, None])
     worst = mag.amax(1) if mag.shape[1] else torch.zeros_like(lse)
     v = torch.where(seen.any(0)[:, None], v, 0.0)
-    return p @ v, lse, p @ v.abs(), worst
+    flat = (p.amax(1)[:, None] if p.shape[1] else 0.0) * (seen.double() @ v.abs())
+    return p @ v, lse, p @ v.abs(), worst, flat
 
 
 def decode(q, cache, table, lens, dv, sm_scale, factor=1.0):
@@ -71,7 +72,7 @@ def decode(q, cache, table, lens, dv, sm_scale, factor=1.0):
     B = cache.shape[1]
     out = torch.zeros(R, n, H, dv, dtype=torch.float64, device=q.device)
     lse = torch.full((R, n, H), -math.inf, dtype=torch.float64, device=q.device)
-    pv, worst = torch.zeros_like(out), torch.zeros_like(lse)
+    pv, worst, flat = torch.zeros_like(out), torch.zeros_like(lse), torch.zeros_like(out)
     for r in range(R):
         length = max(int(lens[r]), 0)
         m = min(length, table.shape[1] * B)
@@ -85,8 +86,9 @@ def decode(q, cache, table, lens, dv, sm_scale, factor=1.0):
         place = torch.arange(m, device=q.device)
         for i in range(n):
             seen = (ok & (place < length - n + 1 + i))[None].expand(H, m)
-            out[r, i], lse[r, i], pv[r, i], worst[r, i] = attend(q[r, i].double(), kv, kv[:, :dv], seen, sm_scale)
-    return out, lse, pv, worst
+            out[r, i], lse[r, i], pv[r, i], worst[r, i], flat[r, i] = attend(q[r, i].double(), kv, kv[:, :dv], seen,
+                                                                             sm_scale)
+    return out, lse, pv, worst, flat
 
 
 def prefill(q, k, pe, v, cu_q, cu_k, sm_scale, causal, prev_out=None, prev_lse=None):
@@ -103,8 +105,8 @@ def prefill(q, k, pe, v, cu_q, cu_k, sm_scale, causal, prev_out=None, prev_lse=N
             seen = seen.tril((d - c) - (b - a))
         for h in range(H):
             key = torch.cat([k[c:d, h], pe[c:d]], 1).double()
-            out[a:b, h], lse[a:b, h], pv[a:b, h], worst[a:b, h] = attend(q[a:b, h].double(), key, v[c:d, h].double(),
-                                                                       seen, sm_scale)
+            out[a:b, h], lse[a:b, h], pv[a:b, h], worst[a:b, h], _ = attend(q[a:b, h].double(), key,
+                                                                          v[c:d, h].double(), seen, sm_scale)
     if prev_lse is not None:
         both = torch.logaddexp(lse, prev_lse.double())
         x = torch.where(both == -math.inf, 0.0, both)
@@ -114,9 +116,10 @@ def prefill(q, k, pe, v, cu_q, cu_k, sm_scale, causal, prev_out=None, prev_lse=N
     return out, lse, pv, worst
 
 
-def check_attention(got, got_lse, want, want_lse, pv, worst, entry, weights_u, extra=0.0):
+def check_attention(got, got_lse, want, want_lse, pv, worst, entry, weights_u, extra=0.0, weights_abs=0.0):
     """Scores are sums of `entry` products in 32 bits (`extra`: a further bound on them), so each weight is off by a
-    factor within exp(2 ds); weights are rounded with unit weights_u for the second product, sums of values in 32 bits
+    factor within exp(2 ds); weights are rounded with unit weights_u for the second product (weights_abs: and by a step
+    below it, already times the magnitudes it meets), sums of values in 32 bits
     (2^-18 of the magnitudes covers 64 additions in a row), and the result is rounded to its own type."""
     ds = (entry + 64) * 2.0 ** -24 * worst + extra
     finite = want_lse != -math.inf
@@ -125,7 +128,7 @@ def check_attention(got, got_lse, want, want_lse, pv, worst, entry, weights_u, e
     bound = (ds + 2.0 ** -20 * (4 + want_lse.abs()))[finite]
     assert (err <= bound).all(), f"lse off by {err.max():.3g}, {(err / bound).max():.3g} of its bound"
     err = (got.double() - want).abs()
-    bound = U[got.dtype] * want.abs() + (2 * ds[..., None] + weights_u + 2.0 ** -18) * pv * 1.01 + 1e-30
+    bound = U[got.dtype] * want.abs() + (2 * ds[..., None] + weights_u + 2.0 ** -18) * pv * 1.01 + weights_abs + 1e-30
     if got.dtype == torch.float16:
         bound = bound + 2.0 ** -25
     assert not got.isnan().any(), "NaN"

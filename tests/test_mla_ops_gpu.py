@@ -212,7 +212,7 @@ def decode_case(lens, heads, q_len, src, cdt, block, dv=512, dr=64, stride=None,
     return q, cache, i32(table), i32(lens), (torch.tensor([scale], device=DEV) if cdt == FP8 else None)
 
 
-def run_decode(case, ws, dv=512, options=0, sm=None, weights_u=None, flag=0, extra=0.0):
+def run_decode(case, ws, dv=512, options=0, sm=None, weights_u=None, flag=0):
     q, cache, table, lens, sc = case
     sm = 1.0 / math.sqrt(192) if sm is None else sm
     out = torch.full(q.shape[:3] + (dv,), 7.0, dtype=q.dtype, device=DEV)
@@ -222,9 +222,16 @@ def run_decode(case, ws, dv=512, options=0, sm=None, weights_u=None, flag=0, ext
                           options=options)
     torch.cuda.synchronize()
     assert int(err) == flag
-    want, wl, pv, worst = ref.decode(q, cache, table, lens, dv, sm, 1.0 if sc is None else float(sc))
-    u = ref.U[q.dtype] if weights_u is None else weights_u
-    ref.check_attention(out, lse, want, wl, pv, worst, q.shape[3], u, extra)
+    f = 1.0 if sc is None else float(sc)
+    want, wl, pv, worst, flat = ref.decode(q, cache, table, lens, dv, sm, f)
+    u, extra, below = ref.U[q.dtype] if weights_u is None else weights_u, 0.0, 0.0
+    if cache.dtype == FP8 and options == 0:
+        # weights of two e4m3 parts: 2^-8 of their value, and half a subnormal step (2^-10) at 2^6; queries of parts
+        # that hold all their bits but those below 2 * 2^-10 where the largest is at least 224
+        u, below = 2.0 ** -8, 2.0 ** -16 * flat
+        size = cache.double().nan_to_num(0).abs().sum(2).max() * f
+        extra = sm * 2.0 ** -16.8 * q.double().abs().amax(3) * size
+    ref.check_attention(out, lse, want, wl, pv, worst, q.shape[3], u, extra, below)
     return out, lse
 
 
