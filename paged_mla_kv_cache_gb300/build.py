@@ -11,7 +11,8 @@ import os
 import shutil
 import subprocess
 
-UNITS = ["mla_plan.cu", "mla_append.cu", "mla_decode.cu", "mla_decode_tc.cu", "mla_prefill.cu"]
+UNITS = ["mla_plan.cu", "mla_append.cu", "mla_decode.cu", "mla_decode_tc.cu", "mla_prefill.cu",
+         "mla_prefill_tc.cu"]
 PKG_DIR = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(PKG_DIR)
 CSRC = os.path.join(PKG_DIR, "csrc")

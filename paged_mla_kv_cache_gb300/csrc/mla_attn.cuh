@@ -23,8 +23,9 @@ constexpr float kLn2 = 0.6931471805599453f;
 // Workspace: one note a CTA, then two slots of unfinished rows a CTA (0: the
 // share began inside the request, 1: the share ended inside it).
 struct JoinNote {
-  int32_t item;   // request (decode) or item (prefill) that begins in this share and goes on, or -1
-  int32_t parts;  // shares that hold it
+  int32_t item;         // request that begins in this share and goes on in the next, or -1
+  int32_t parts;        // shares that hold it
+  int32_t head, tile;   // prefill: which of the request's row tiles
 };
 constexpr int kNotesPerSm = 4;
 constexpr int64_t kSlotFloats = 256 * 130;  // the largest slot: 256 rows of 128 values, or 64 of 512, and two sums each

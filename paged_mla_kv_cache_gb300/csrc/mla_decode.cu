@@ -32,7 +32,7 @@ __global__ void __launch_bounds__(kGenThreads) decode_general_kernel(const __gri
   const int g0 = group * p.rows_per_group;
   const int n_rows = min(p.rows_per_group, rows - g0);
   const float scale = sizeof(TC) == 1 && p.scale != nullptr ? *p.scale : 1.0f;
-  JoinNote note{-1, 0};
+  JoinNote note{-1, 0, 0, 0};
   int bad = 0;
   int64_t at = share.begin;
   int64_t tile = share.offset;

@@ -459,7 +459,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     constexpr float kBase = kFp8 ? 6.0f : 0.0f;
     const int token = warp * 16 + (lane & 15);       // M = 64: 16 rows in each quarter of the lanes
     const uint32_t lanes = static_cast<uint32_t>(warp * 32) << 16;
-    JoinNote note{-1, 0};
+    JoinNote note{-1, 0, 0, 0};
     int64_t t = 0;
     bool alive = true;
     bool more = it.next();

@@ -8,6 +8,7 @@
 #include <algorithm>
 
 #include "mla_prefill.cuh"
+#include "mla_prefill_tc.cuh"
 
 namespace pmg_mla {
 namespace {
@@ -171,6 +172,7 @@ extern "C" int pmg_latent_prefill(const void* q, int64_t q_token_stride, int64_t
   p.ws = workspace_at(workspace, sms);
   p.err = error_flag;
   p.causal = (options & PMG_OPT_CAUSAL) ? 1 : 0;
+  if (!(options & PMG_OPT_FORCE_GENERAL) && prefill_tc_takes(p, dtype)) return prefill_tc(p, dtype, sms, stream);
   const int E = p.dn + p.dr;
   const Kernel k = dtype == PMG_BF16 ? prefill_general_kernel<bf16>
                    : dtype == PMG_FP16 ? prefill_general_kernel<f16> : prefill_general_kernel<float>;

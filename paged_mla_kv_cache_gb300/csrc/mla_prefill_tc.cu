@@ -1,0 +1,666 @@
+// Expanded latent attention on the fifth-generation tensor core: 128 + 64 key
+// values, 128 values a head, 16-bit types.
+//
+// Mathematics. An item is 256 query rows of one head: two halves of 128 rows.
+// For a block of 128 keys, S = Q K^T (128 x 128 over 192) for each half, P =
+// 2^(S - ref), O += P V. S and O stay in tensor memory (2 x 128 + 2 x 128
+// columns: all of it); P is written over S as 16-bit values and is read from
+// there by the second product.
+//
+// Bound: the tensor core. A block costs a half 768 + 512 clocks of products
+// against about 128 exponentials a thread, and the halves take turns: while
+// one half's softmax runs, the other half's products do. The rotated key part
+// is loaded once a token (not once a head) straight from the gathered rows.
+//
+// Roles: warps 0-3 and 4-7 are the softmax and epilogue of a half each (a row
+// a thread, so no maximum or sum ever crosses threads); warp 8 loads; warp 9
+// issues products; warp 10 clears value rows past the end of a request, which
+// may hold anything while their weights are 0; warp 11 fills up the warpgroup.
+//
+// A row's reference follows its maximum only when a score passes it by 2^8, so
+// the accumulator is rescaled in the first blocks at most. Work is cut into
+// equal shares of blocks over the whole call (see mla_attn.cuh): causal
+// triangles, short and long requests cost every SM the same, and a chunk of
+// few rows over a long context uses them all.
+#include <string.h>
+
+#include <algorithm>
+#include <type_traits>
+
+#include "mla_prefill_tc.cuh"
+#include "mla_sm103.cuh"
+
+namespace pmg_mla {
+namespace {
+
+constexpr int kThreads = 384;
+// registers of a thread: 12 warps are launched with 168, then the last 4 give some to the first 8
+constexpr int kRegsUp = 208, kRegsDown = 80;
+static_assert(8 * kRegsUp + 4 * kRegsDown <= 12 * 168, "the shares add up to the launch's");
+constexpr int kRows = 256, kHalf = 128, kBlock = 128;
+constexpr int kNope = 128, kRope = 64, kVal = 128;
+constexpr int kPiece = 128 * 128;        // 128 rows of 128 bytes
+constexpr int kSlots = 8;                // key and value pieces in flight: 3 + 2 a block
+constexpr int kQAt = 0;                  // two halves of three pieces
+constexpr int kSlotAt = 6 * kPiece;
+constexpr int kMiscAt = kSlotAt + kSlots * kPiece;
+constexpr int kMisc = 1024;
+constexpr int kBytes = kMiscAt + kMisc + 1024;
+static_assert(kBytes <= 232448, "fits");
+constexpr int kSlotRow = kVal;           // floats of a row in a join slot, its two sums behind all rows
+
+struct Misc {
+  uint64_t full[kSlots], empty[kSlots];
+  uint64_t q_full, q_empty, s_full[2], p_full[2], o_done[2], dirty, clean;
+  int64_t scratch[33], found[2];
+  uint32_t tmem;
+  int32_t stop;
+};
+static_assert(sizeof(Misc) <= kMisc, "Misc fits");
+
+// keys that row tile t of a request sees at most
+__device__ __forceinline__ int keys_of(const PrefillReq& x, int t, int causal) {
+  if (!causal) return x.lk;
+  const int64_t end = min(static_cast<int64_t>(x.lq), static_cast<int64_t>(t + 1) * kRows);
+  return static_cast<int>(max(static_cast<int64_t>(0), min(static_cast<int64_t>(x.lk), x.lk - x.lq + end)));
+}
+__device__ __forceinline__ int blocks_of(int keys) { return keys > 0 ? (keys + kBlock - 1) / kBlock : 1; }
+__device__ __forceinline__ int tiles_of(const PrefillReq& x) { return (x.lq + kRows - 1) / kRows; }
+
+// blocks of one head of a request
+__device__ __forceinline__ int64_t head_pieces(const PrefillReq& x, int causal) {
+  const int n = tiles_of(x);
+  if (!causal) return static_cast<int64_t>(n) * blocks_of(x.lk);
+  int64_t s = 0;
+  for (int t = 0; t < n; ++t) s += blocks_of(keys_of(x, t, causal));
+  return s;
+}
+
+// Walks the items of a share: (request, head, row tile), blocks [b0, b0 + n) of nb.
+struct Items {
+  const PrefillParams* p;
+  int64_t at, end;
+  int r, head, tile;
+  PrefillReq x;
+  int nb, b0, n;
+  int act[2];   // blocks that each half takes part in (of the item's nb)
+  int keys;     // keys of the item
+  bool begun;
+
+  __device__ Items(const PrefillParams& p_, const Share& s) : p(&p_), at(s.begin), end(s.end) {
+    r = s.item;
+    head = tile = nb = b0 = n = keys = 0;
+    begun = false;
+    if (at < end) {
+      x = prefill_req(*p, r);
+      const int64_t per = head_pieces(x, p->causal);
+      head = static_cast<int>(s.offset / per);
+      int64_t left = s.offset % per;
+      while (left >= blocks_of(keys_of(x, tile, p->causal))) left -= blocks_of(keys_of(x, tile++, p->causal));
+      b0 = static_cast<int>(left);
+    }
+  }
+  __device__ bool next() {
+    if (at >= end) return false;
+    if (begun) {
+      b0 = 0;
+      if (++tile >= tiles_of(x)) {
+        tile = 0;
+        if (++head >= p->H) {
+          head = 0;
+          do x = prefill_req(*p, ++r); while (x.lq == 0);
+        }
+      }
+    }
+    begun = true;
+    keys = keys_of(x, tile, p->causal);
+    nb = blocks_of(keys);
+    n = static_cast<int>(min(static_cast<int64_t>(nb - b0), end - at));
+    at += n;
+    // the first half's last row may see fewer keys; the second half may not exist
+    const int rows = x.lq - tile * kRows;
+    int k0 = keys;
+    if (p->causal && rows > kHalf)
+      k0 = max(0, min(x.lk, x.lk - x.lq + tile * kRows + kHalf));
+    act[0] = k0 > 0 ? (k0 + kBlock - 1) / kBlock : 0;
+    act[1] = rows > kHalf && keys > 0 ? nb : 0;
+    return true;
+  }
+  __device__ int64_t piece() const { return at - n; }
+  // blocks of this share that half h takes part in: [b0, last(h))
+  __device__ int last(int h) const { return min(b0 + n, act[h]); }
+};
+
+template <class T>
+__global__ void __launch_bounds__(kThreads, 1)
+    prefill_tc_kernel(const __grid_constant__ PrefillParams p, const __grid_constant__ CUtensorMap map_q,
+                      const __grid_constant__ CUtensorMap map_k, const __grid_constant__ CUtensorMap map_pe,
+                      const __grid_constant__ CUtensorMap map_v) {
+  extern __shared__ uint8_t raw[];
+  uint8_t* smem = raw + ((1024 - (smem_u32(raw) & 1023)) & 1023);
+  Misc& mi = *reinterpret_cast<Misc*>(smem + kMiscAt);
+  const uint32_t base = smem_u32(smem);
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+
+  if (tid == 0) {
+    for (int i = 0; i < kSlots; ++i) {
+      mbar_init(smem_u32(&mi.full[i]), 1);
+      mbar_init(smem_u32(&mi.empty[i]), 1);
+    }
+    mbar_init(smem_u32(&mi.q_full), 1);
+    mbar_init(smem_u32(&mi.q_empty), 1);
+    mbar_init(smem_u32(&mi.dirty), 1);
+    mbar_init(smem_u32(&mi.clean), 1);
+    for (int h = 0; h < 2; ++h) {
+      mbar_init(smem_u32(&mi.s_full[h]), 1);
+      mbar_init(smem_u32(&mi.p_full[h]), 4);
+      mbar_init(smem_u32(&mi.o_done[h]), 1);
+    }
+    mi.stop = 0;
+    mbar_fence_init();
+    tma_prefetch(&map_q);
+    tma_prefetch(&map_k);
+    tma_prefetch(&map_pe);
+    tma_prefetch(&map_v);
+  }
+  if (warp == 9) tmem_alloc(smem_u32(&mi.tmem), 512);
+  pdl_entry();
+
+  const int unit = blockIdx.x;
+  auto pieces = [&](int r) -> int64_t {
+    const PrefillReq x = prefill_req(p, r);
+    return x.lq > 0 ? head_pieces(x, p.causal) * p.H : 0;
+  };
+  const Share share = find_share(pieces, p.R, unit, p.units, mi.scratch, mi.found);
+  tmem_fence_before();
+  __syncthreads();
+  tmem_fence_after();
+  const uint32_t tmem = mi.tmem;  // S of the halves at columns 0 and 128, O at 256 and 384
+  volatile int* stop = &mi.stop;
+  constexpr int kFmt = std::is_same<T, bf16>::value ? 1 : 0;
+  constexpr uint32_t kIdescS = umma_idesc(kFmt, 0, 0, 128, kBlock);
+  constexpr uint32_t kIdescO = umma_idesc(kFmt, 0, 1, 128, kVal);
+
+  if (warp >= 8) {
+    regs_down<kRegsDown>();
+    if (warp == 8) {
+      // ---- loads ----
+      int bad = 0;
+      if (unit == 0)
+        for (int i = lane; i < p.R; i += 32) bad |= prefill_req(p, i).bad;
+      set_flag(p.err, bad);
+      if (lane == 0) {
+        Items it(p, share);
+        int slot = 0, phase = 0, items = 0;
+        bool alive = true;
+        auto piece = [&](const CUtensorMap* map, int c, int head, int row) {
+          if (!alive) return;
+          if (!mbar_wait(smem_u32(&mi.empty[slot]), phase ^ 1, stop)) {
+            alive = false;
+            return;
+          }
+          const uint32_t full = smem_u32(&mi.full[slot]);
+          mbar_expect(full, kPiece);
+          tma_load_3d(base + kSlotAt + slot * kPiece, map, full, c, head, row);
+          if (++slot == kSlots) {
+            slot = 0;
+            phase ^= 1;
+          }
+        };
+        while (alive && it.next()) {
+          if (it.keys == 0) continue;
+          if (!mbar_wait(smem_u32(&mi.q_empty), (items & 1) ^ 1, stop)) break;
+          ++items;
+          const int halves = it.act[1] > 0 ? 2 : 1;
+          const uint32_t q_full = smem_u32(&mi.q_full);
+          mbar_expect(q_full, halves * 3 * kPiece);
+          for (int h = 0; h < halves; ++h)
+            for (int c = 0; c < 3; ++c)
+              tma_load_3d(base + kQAt + (3 * h + c) * kPiece, &map_q, q_full, 64 * c, it.head,
+                          it.x.q0 + it.tile * kRows + h * kHalf);
+          for (int b = it.b0; b < it.b0 + it.n && alive; ++b) {
+            const int row = it.x.k0 + b * kBlock;
+            piece(&map_k, 0, it.head, row);
+            piece(&map_k, 64, it.head, row);
+            piece(&map_pe, 0, 0, row);
+            piece(&map_v, 0, it.head, row);
+            piece(&map_v, 64, it.head, row);
+          }
+        }
+        if (*stop != 0) {  // copies in flight land before the CTA ends
+          int never = 0;
+          for (int i = 0; i < kSlots; ++i) mbar_wait(smem_u32(&mi.full[i]), i < slot ? phase : phase ^ 1, &never);
+          if (items > 0) mbar_wait(smem_u32(&mi.q_full), (items - 1) & 1, &never);
+        }
+      }
+      __syncwarp();
+    } else if (warp == 9) {
+      // ---- products ----
+      if (lane == 0) {
+        Items it(p, share);
+        bool alive = true;
+        auto wait = [&](uint64_t& bar, int parity) {
+          if (alive && !mbar_wait(smem_u32(&bar), parity, stop)) alive = false;
+          return alive;
+        };
+        auto advance = [&]() {
+          bool more = it.next();
+          while (more && it.keys == 0) more = it.next();
+          return more;
+        };
+        int items = 0, cleans = 0;
+        // piece c of step st in the ring: 5 pieces a step (counted modulo 2^32, a multiple of the ring)
+        auto slot_of = [](uint32_t st, uint32_t c) { return (5 * st + c) & (kSlots - 1); };
+        auto phase_of = [](uint32_t st, uint32_t c) { return static_cast<int>((5 * st + c) / kSlots & 1); };
+        // S of half h for the block of step st
+        auto scores = [&](int h, uint32_t st) {
+#pragma unroll 1
+          for (uint32_t c = 0; c < 3; ++c) {
+            const uint64_t qa = umma_desc(base + kQAt + (3 * h + c) * kPiece, 16, 1024);
+            const uint64_t ka = umma_desc(base + kSlotAt + slot_of(st, c) * kPiece, 16, 1024);
+#pragma unroll
+            for (int k = 0; k < 4; ++k)  // 32 bytes of K each
+              umma_ss<false>(tmem + h * kBlock, qa + 2 * k, ka + 2 * k, kIdescS, c > 0 || k > 0);
+          }
+          umma_commit(smem_u32(&mi.s_full[0]) + 8 * h);
+        };
+        auto values = [&](int h, uint32_t st, bool first) {
+          // the two 64-value pieces of V are two slots, which may wrap around the ring: a product of 64 each then
+          const uint64_t v0 = umma_desc(base + kSlotAt + slot_of(st, 3) * kPiece, kPiece, 1024);
+          const uint64_t v1 = umma_desc(base + kSlotAt + slot_of(st, 4) * kPiece, kPiece, 1024);
+          const uint32_t d = tmem + 256 + h * kVal, w = tmem + h * kBlock;
+          if (slot_of(st, 4) != 0) {
+#pragma unroll
+            for (int k = 0; k < 8; ++k) umma_ts(d, w + 8 * k, v0 + 128 * k, kIdescO, !first || k > 0);
+          } else {
+            constexpr uint32_t kIdescHalf = umma_idesc(kFmt, 0, 1, 128, 64);
+#pragma unroll 1
+            for (int k = 0; k < 8; ++k) {
+              umma_ts(d, w + 8 * k, v0 + 128 * k, kIdescHalf, !first || k > 0);
+              umma_ts(d + 64, w + 8 * k, v1 + 128 * k, kIdescHalf, !first || k > 0);
+            }
+          }
+          umma_commit(smem_u32(&mi.o_done[0]) + 8 * h);
+        };
+        auto wait_pieces = [&](uint32_t st, uint32_t c0, uint32_t c1) {
+#pragma unroll 1
+          for (uint32_t c = c0; c < c1 && alive; ++c)
+            if (!mbar_wait(smem_u32(&mi.full[0]) + 8 * slot_of(st, c), phase_of(st, c), stop)) alive = false;
+          return alive;
+        };
+        auto free_pieces = [&](uint32_t st, uint32_t c0, uint32_t c1) {
+#pragma unroll 1
+          for (uint32_t c = c0; c < c1; ++c) umma_commit(smem_u32(&mi.empty[0]) + 8 * slot_of(st, c));
+        };
+        uint32_t step = 0;                  // blocks begun
+        uint32_t taken = 0;                 // parity of the weights taken, a bit a half
+        uint32_t any = 0;                   // halves that have taken any
+        while (alive && advance()) {
+          if (!wait(mi.q_full, items & 1)) break;
+          ++items;
+          const int end = it.b0 + it.n;
+          const bool partial_end = end == it.nb && it.x.lk - (end - 1) * kBlock < kBlock;  // warp 10's rule
+          const int last0 = it.last(0), last1 = it.last(1);
+#pragma unroll 1
+          for (int b = it.b0; b < end && alive; ++b, ++step) {
+            if (b == it.b0) {
+              if (!wait_pieces(step, 0, 3)) break;
+              tmem_fence_after();
+#pragma unroll 1
+              for (int h = 0; h < 2; ++h)
+                if (b < (h ? last1 : last0)) scores(h, step);
+              free_pieces(step, 0, 3);
+              if (b + 1 == end) umma_commit(smem_u32(&mi.q_empty));
+            }
+            bool have_v = false, have_k = false;
+#pragma unroll 1
+            for (int h = 0; h < 2; ++h) {
+              const int last = h ? last1 : last0;
+              if (b < last) {
+                if (!have_v) {
+                  if (!wait_pieces(step, 3, 5)) break;
+                  if (partial_end && b + 1 == end) {
+                    mbar_arrive(smem_u32(&mi.dirty));
+                    if (!wait(mi.clean, cleans++ & 1)) break;
+                  }
+                  have_v = true;
+                }
+                if (alive && !mbar_wait(smem_u32(&mi.p_full[0]) + 8 * h, taken >> h & 1, stop)) alive = false;
+                if (!alive) break;
+                taken ^= 1u << h;
+                any |= 1u << h;
+                tmem_fence_after();
+                values(h, step, b == it.b0);
+              }
+              if (b + 1 < last) {
+                if (!have_k) {
+                  if (!wait_pieces(step + 1, 0, 3)) break;
+                  tmem_fence_after();
+                  have_k = true;
+                }
+                scores(h, step + 1);
+              }
+            }
+            if (!alive) break;
+            free_pieces(step, 3, 5);
+            if (b + 1 < end) {
+              free_pieces(step + 1, 0, 3);
+              if (b + 2 == end) umma_commit(smem_u32(&mi.q_empty));
+            }
+          }
+        }
+        if (!alive) {
+          // what was issued ends before the CTA does
+          int never = 0;
+          for (int h = 0; h < 2; ++h)
+            if (any >> h & 1) mbar_wait(smem_u32(&mi.o_done[0]) + 8 * h, (taken >> h & 1) ^ 1, &never);
+        }
+      }
+      __syncwarp();
+    } else if (warp == 10) {
+      // ---- value rows past a request's end ----
+      Items it(p, share);
+      int64_t step = 0;
+      int cleans = 0;
+      bool alive = true;
+      while (alive && it.next()) {
+        if (it.keys == 0) continue;
+        step += it.n;
+        const int end = it.b0 + it.n;
+        const int first = it.x.lk - (end - 1) * kBlock;  // rows of the last block that belong to the request
+        if (end != it.nb || first >= kBlock) continue;
+        if (lane == 0) alive = mbar_wait(smem_u32(&mi.dirty), cleans & 1, stop);  // the block is there
+        alive = __shfl_sync(0xffffffffu, static_cast<int>(alive), 0) != 0;
+        if (!alive) break;
+        ++cleans;
+        for (int c = 3; c < 5; ++c) {
+          const int slot = static_cast<int>((5 * (step - 1) + c) % kSlots);
+          uint4* at = reinterpret_cast<uint4*>(smem + kSlotAt + slot * kPiece + first * 128);
+          for (int i = lane; i < (kBlock - first) * 8; i += 32) at[i] = make_uint4(0, 0, 0, 0);
+        }
+        fence_async_smem();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(smem_u32(&mi.clean));
+      }
+    }
+  } else {
+    regs_up<kRegsUp>();
+    // ---- softmax and epilogue of half h: thread = row ----
+    const int h = warp >> 2;
+    const int row = tid & 127;
+    const uint32_t lanes = static_cast<uint32_t>((warp & 3) * 32) << 16;
+    const uint32_t s_at = tmem + h * kBlock + lanes, o_at = tmem + 256 + h * kVal + lanes;
+    const float sc = p.sm_scale * kLog2e;
+    constexpr float kSlack = 8.0f;
+    JoinNote note{-1, 0, 0, 0};
+    Items it(p, share);
+    int count = 0;  // blocks taken part in
+    bool alive = true;
+    while (alive && it.next()) {
+      const int i0 = it.tile * kRows + h * kHalf;        // first row of this half within the request
+      const int64_t i = i0 + row;
+      const int limit = p.causal ? static_cast<int>(max(static_cast<int64_t>(0), min(static_cast<int64_t>(it.x.lk), it.x.lk - it.x.lq + 1 + i)))
+                                 : it.x.lk;               // keys this row sees
+      // the fewest keys any row of this warp sees
+      const int low = __reduce_min_sync(0xffffffffu, limit);
+      float ref = -INFINITY, l = 0.0f;
+      const int last = it.last(h);
+      for (int b = it.b0; b < last; ++b, ++count) {
+        if (!mbar_wait(smem_u32(&mi.s_full[h]), count & 1, stop)) alive = false;
+        alive = __all_sync(0xffffffffu, alive);
+        if (!alive) break;
+        tmem_fence_after();
+        uint32_t raw_s[128];
+#pragma unroll
+        for (int c = 0; c < 4; ++c) tmem_ld32(s_at + 32 * c, raw_s + 32 * c);
+        tmem_wait_ld();
+        tmem_pin<128>(raw_s);
+        float* s = reinterpret_cast<float*>(raw_s);
+        const int j0 = b * kBlock;
+        if (j0 + kBlock > low) {
+#pragma unroll
+          for (int k = 0; k < 128; ++k)
+            if (j0 + k >= limit) s[k] = -INFINITY;
+        }
+        float m4[4] = {s[0], s[1], s[2], s[3]};
+#pragma unroll
+        for (int k = 4; k < 128; ++k) m4[k & 3] = fmaxf(m4[k & 3], s[k]);
+        const float top = fmaxf(fmaxf(m4[0], m4[1]), fmaxf(m4[2], m4[3])) * sc;
+        if (__any_sync(0xffffffffu, top > ref + kSlack)) {
+          float a = 1.0f;
+          if (top > ref) {
+            a = ref == -INFINITY ? 0.0f : ex2(ref - top);
+            ref = top;
+          }
+          l *= a;
+          if (b > it.b0) {
+            if (!mbar_wait(smem_u32(&mi.o_done[h]), (count - 1) & 1, stop)) alive = false;
+            __syncwarp();
+            tmem_fence_after();
+#pragma unroll 1
+            for (int c = 0; c < kVal; c += 16) {
+              uint32_t o[16];
+              tmem_ld16(o_at + c, o);
+              tmem_wait_ld();
+              tmem_pin<16>(o);
+#pragma unroll
+              for (int k = 0; k < 16; ++k) o[k] = __float_as_uint(__uint_as_float(o[k]) * a);
+              tmem_st16(o_at + c, o);
+            }
+          }
+        }
+        const float r = ref == -INFINITY ? 0.0f : ref;
+        float sum[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+#pragma unroll
+        for (int c = 0; c < 4; ++c) {
+          uint32_t w[16];
+#pragma unroll
+          for (int k = 0; k < 16; ++k) {
+            const float x = ex2(fmaf(s[32 * c + 2 * k], sc, -r)), y = ex2(fmaf(s[32 * c + 2 * k + 1], sc, -r));
+            sum[(2 * k) & 3] += x;
+            sum[(2 * k + 1) & 3] += y;
+            w[k] = pack2<T>(x, y);
+          }
+          tmem_st16(s_at + 16 * c, w);
+        }
+        l += (sum[0] + sum[1]) + (sum[2] + sum[3]);
+        tmem_wait_st();
+        tmem_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(smem_u32(&mi.p_full[h]));
+      }
+      if (!alive) break;
+
+      // epilogue
+      const bool whole = it.b0 == 0 && it.n == it.nb;
+      const bool some = last > it.b0;
+      if (some) {
+        if (!mbar_wait(smem_u32(&mi.o_done[h]), (count - 1) & 1, stop)) alive = false;
+        alive = __all_sync(0xffffffffu, alive);
+        if (!alive) break;
+        tmem_fence_after();
+      }
+      const bool mine = i < it.x.lq;
+      if (!whole && it.b0 == 0 && tid == 0) {
+        note.item = it.r;
+        note.head = it.head;
+        note.tile = it.tile;
+        note.parts = unit_of(it.piece() + it.nb - 1, share.total, share.units) - unit + 1;
+      }
+      float* slot = p.ws.slots + (static_cast<int64_t>(unit) * 2 + (it.b0 == 0 ? 1 : 0)) * kSlotFloats;
+      const int64_t t = it.x.q0 + i;
+      float now = l > 0.0f ? 1.0f / l : 0.0f, before = 0.0f;
+      if (whole && mine) {
+        float lse = l > 0.0f ? (ref + log2f(l)) * kLn2 : -INFINITY;
+        if (p.prev_lse != nullptr) {
+          const Joined g = join_state(lse, p.prev_lse[t * p.H + it.head]);
+          now *= g.now;
+          before = g.before;
+          lse = g.lse;
+        }
+        if (p.lse != nullptr) p.lse[t * p.H + it.head] = lse;
+      } else if (!whole) {
+        float* ml = slot + kRows * kSlotRow + 2 * (h * kHalf + row);
+        ml[0] = ref;
+        ml[1] = l;
+      }
+      __syncwarp();
+#pragma unroll 1
+      for (int c = 0; c < kVal; c += 16) {
+        uint32_t o[16];
+        __syncwarp();
+        if (some) {
+          tmem_ld16(o_at + c, o);
+          tmem_wait_ld();
+          tmem_pin<16>(o);
+        } else {
+#pragma unroll
+          for (int k = 0; k < 16; ++k) o[k] = 0;
+        }
+        if (!mine) continue;
+        if (whole) {
+          float y[16];
+#pragma unroll
+          for (int k = 0; k < 16; ++k) y[k] = __uint_as_float(o[k]) * now;
+          if (before != 0.0f) {
+            const uint4* prev = reinterpret_cast<const uint4*>(static_cast<const T*>(p.prev) + t * p.pt_stride +
+                                                               it.head * p.ph_stride + c);
+#pragma unroll
+            for (int q = 0; q < 2; ++q) {
+              const uint4 v = prev[q];
+              const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+              for (int k = 0; k < 8; ++k) {
+                T e;
+                const unsigned short bits = static_cast<unsigned short>(k & 1 ? w[k >> 1] >> 16 : w[k >> 1] & 0xffff);
+                memcpy(&e, &bits, 2);
+                y[8 * q + k] += before * to_f(e);
+              }
+            }
+          }
+          uint4* out = reinterpret_cast<uint4*>(static_cast<T*>(p.out) + t * p.ot_stride + it.head * p.oh_stride + c);
+          out[0] = make_uint4(pack2<T>(y[0], y[1]), pack2<T>(y[2], y[3]), pack2<T>(y[4], y[5]), pack2<T>(y[6], y[7]));
+          out[1] = make_uint4(pack2<T>(y[8], y[9]), pack2<T>(y[10], y[11]), pack2<T>(y[12], y[13]), pack2<T>(y[14], y[15]));
+        } else {
+          float4* at = reinterpret_cast<float4*>(slot + (h * kHalf + row) * kSlotRow + c);
+#pragma unroll
+          for (int k = 0; k < 4; ++k)
+            at[k] = make_float4(__uint_as_float(o[4 * k]), __uint_as_float(o[4 * k + 1]), __uint_as_float(o[4 * k + 2]),
+                                __uint_as_float(o[4 * k + 3]));
+        }
+      }
+      tmem_fence_before();
+    }
+    if (tid == 0) p.ws.notes[unit] = note;
+    if (tid == 0 && *stop != 0) set_flag(p.err, PMG_FLAG_TIMEOUT);
+  }
+  tmem_fence_before();
+  __syncthreads();
+  tmem_fence_after();
+  if (warp == 9) tmem_free(tmem, 512);
+}
+
+// The join: a warp a row, four columns a lane, parts in the order of the shares.
+constexpr int kJoinRows = 8;
+
+template <class T>
+__global__ void __launch_bounds__(kJoinRows * 32) prefill_join_kernel(const __grid_constant__ PrefillParams p) {
+  pdl_entry();
+  const JoinNote note = p.ws.notes[blockIdx.x];
+  if (note.item < 0) return;
+  const PrefillReq x = prefill_req(p, note.item);
+  const int row = blockIdx.y * kJoinRows + (threadIdx.x >> 5), lane = threadIdx.x & 31;
+  const int i = note.tile * kRows + row;
+  if (i >= x.lq) return;
+  auto slot_of = [&](int k) {
+    return p.ws.slots + (static_cast<int64_t>(blockIdx.x + k) * 2 + (k == 0 ? 1 : 0)) * kSlotFloats;
+  };
+  const int ml = kRows * kSlotRow + 2 * row;
+  float top = -INFINITY;
+  for (int k = lane; k < note.parts; k += 32) top = fmaxf(top, slot_of(k)[ml]);
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
+  float l = 0.0f;
+  float4 a = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+#pragma unroll 4
+  for (int k = 0; k < note.parts; ++k) {
+    const float* slot = slot_of(k);
+    const float m = slot[ml];
+    const float w = m == -INFINITY ? 0.0f : exp2f(m - top);
+    l += w * slot[ml + 1];
+    const float4 v = *reinterpret_cast<const float4*>(slot + row * kSlotRow + 4 * lane);
+    if (w != 0.0f) {  // a part in which the row saw nothing may have no values
+      a.x += w * v.x;
+      a.y += w * v.y;
+      a.z += w * v.z;
+      a.w += w * v.w;
+    }
+  }
+  const int64_t t = static_cast<int64_t>(x.q0) + i;
+  float lse = l > 0.0f ? (top + log2f(l)) * kLn2 : -INFINITY;
+  float now = l > 0.0f ? 1.0f / l : 0.0f, before = 0.0f;
+  if (p.prev_lse != nullptr) {
+    const Joined g = join_state(lse, p.prev_lse[t * p.H + note.head]);
+    now *= g.now;
+    before = g.before;
+    lse = g.lse;
+  }
+  __syncwarp();  // every lane has read prev_lse, which lse may be
+  if (lane == 0 && p.lse != nullptr) p.lse[t * p.H + note.head] = lse;
+  float y[4] = {a.x * now, a.y * now, a.z * now, a.w * now};
+  if (before != 0.0f) {
+    const T* prev = static_cast<const T*>(p.prev) + t * p.pt_stride + note.head * p.ph_stride + 4 * lane;
+#pragma unroll
+    for (int k = 0; k < 4; ++k) y[k] += before * to_f(prev[k]);
+  }
+  T* out = static_cast<T*>(p.out) + t * p.ot_stride + note.head * p.oh_stride + 4 * lane;
+  *reinterpret_cast<uint2*>(out) = make_uint2(pack2<T>(y[0], y[1]), pack2<T>(y[2], y[3]));
+}
+
+template <class T>
+int run(const PrefillParams& p, const CUtensorMap* maps, void* stream) {
+  auto k = prefill_tc_kernel<T>;
+  int st = allow_smem(reinterpret_cast<const void*>(k), kBytes);
+  if (st != PMG_OK) return st;
+  st = launch(k, dim3(static_cast<unsigned>(p.units)), kThreads, kBytes, stream, p, maps[0], maps[1], maps[2], maps[3]);
+  if (st != PMG_OK) return st;
+  return launch(prefill_join_kernel<T>, dim3(static_cast<unsigned>(p.units), kRows / kJoinRows), kJoinRows * 32, 0,
+                stream, p);
+}
+
+}  // namespace
+
+bool prefill_tc_takes(const PrefillParams& p, int dtype) {
+  auto rows = [](const void* base, int64_t s0, int64_t s1) {
+    return aligned(base, 16) && s0 % 8 == 0 && s1 % 8 == 0 && s0 * 2 < (int64_t{1} << 40) && s1 * 2 < (int64_t{1} << 40);
+  };
+  return p.dn == kNope && p.dr == kRope && p.dv == kVal && (dtype == PMG_BF16 || dtype == PMG_FP16) && p.Tk > 0 &&
+         p.sm_scale > 0.0f && rows(p.q, p.qt_stride, p.qh_stride) && rows(p.k, p.kt_stride, p.kh_stride) &&
+         rows(p.pe, p.pe_stride, 0) && rows(p.v, p.vt_stride, p.vh_stride) && rows(p.out, p.ot_stride, p.oh_stride) &&
+         (p.prev == nullptr || rows(p.prev, p.pt_stride, p.ph_stride)) &&
+         // a stride of 0 (one row for all) has no tensor map
+         (p.qt_stride > 0 || p.Tq == 1) && (p.qh_stride > 0 || p.H == 1) && (p.kt_stride > 0 || p.Tk == 1) &&
+         (p.kh_stride > 0 || p.H == 1) && (p.vt_stride > 0 || p.Tk == 1) && (p.vh_stride > 0 || p.H == 1) &&
+         (p.pe_stride > 0 || p.Tk == 1);
+}
+
+int prefill_tc(PrefillParams& p, int dtype, int sms, void* stream) {
+  p.units = sms;
+  const CUtensorMapDataType type = dtype == PMG_BF16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT16;
+  CUtensorMap maps[4];
+  auto map = [&](CUtensorMap* m, const void* at, int dim, int heads, int rows, int64_t head_stride, int64_t row_stride) {
+    // the stride of a dimension of one is not used; it has to be a valid one all the same
+    const uint64_t s1 = heads > 1 ? static_cast<uint64_t>(head_stride) * 2 : 512;
+    const uint64_t s2 = rows > 1 ? static_cast<uint64_t>(row_stride) * 2 : 512;
+    return tensor_map(m, type, at, static_cast<uint64_t>(dim), static_cast<uint64_t>(heads), static_cast<uint64_t>(rows),
+                      s1, s2, 64, 1, 128);
+  };
+  int st = map(&maps[0], p.q, kNope + kRope, p.H, p.Tq, p.qh_stride, p.qt_stride);
+  if (st == PMG_OK) st = map(&maps[1], p.k, kNope, p.H, p.Tk, p.kh_stride, p.kt_stride);
+  if (st == PMG_OK) st = map(&maps[2], p.pe, kRope, 1, p.Tk, 0, p.pe_stride);
+  if (st == PMG_OK) st = map(&maps[3], p.v, kVal, p.H, p.Tk, p.vh_stride, p.vt_stride);
+  if (st != PMG_OK) return st;
+  return dtype == PMG_BF16 ? run<bf16>(p, maps, stream) : run<f16>(p, maps, stream);
+}
+
+}  // namespace pmg_mla

@@ -60,22 +60,20 @@ __device__ __forceinline__ uint64_t now_ns() {
 // all its roles), reports PMG_FLAG_TIMEOUT and ends in order.
 constexpr uint64_t kWaitNs = 2000000000ull;
 
-__device__ __noinline__ bool mbar_wait_slow(uint32_t bar, int parity, volatile int* stop) {
+// (inlined: a call would spill what the waiting thread holds in registers)
+__device__ __forceinline__ bool mbar_wait(uint32_t bar, int parity, volatile int* stop) {
+  if (mbar_try(bar, parity)) return true;
   const uint64_t t0 = now_ns();
-  for (;;) {
 #pragma unroll 1
-    for (int i = 0; i < 64; ++i)
-      if (mbar_try(bar, parity)) return true;
+  for (int i = 0;; ++i) {
+    if (mbar_try(bar, parity)) return true;
+    if ((i & 63) != 63) continue;
     if (*stop != 0) return false;
     if (now_ns() - t0 > kWaitNs) {
       *stop = 1;
       return false;
     }
   }
-}
-__device__ __forceinline__ bool mbar_wait(uint32_t bar, int parity, volatile int* stop) {
-  if (mbar_try(bar, parity)) return true;
-  return mbar_wait_slow(bar, parity, stop);
 }
 
 // ---- proxies, named barriers --------------------------------------------------
@@ -99,6 +97,16 @@ __device__ __forceinline__ bool named_any(int id, bool x) {
       : "r"(static_cast<uint32_t>(x)), "r"(id), "n"(kThreads)
       : "memory");
   return any != 0;
+}
+
+// Registers of a warpgroup's threads from here on; the shares add up to no more than the launch's.
+template <int kRegs>
+__device__ __forceinline__ void regs_down() {
+  asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kRegs));
+}
+template <int kRegs>
+__device__ __forceinline__ void regs_up() {
+  asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kRegs));
 }
 
 // ---- TMA ----------------------------------------------------------------------
