@@ -215,14 +215,15 @@ __device__ __forceinline__ void load_queries(const DecodeParams& p, int b, int g
 
 template <class TQ, int kParts, int N>
 __global__ void __launch_bounds__(kThreads, 1)
-    decode_tc_kernel(const __grid_constant__ DecodeParams p, const __grid_constant__ CUtensorMap map, int box_rows) {
+    decode_tc_kernel(const __grid_constant__ DecodeParams p, const __grid_constant__ CUtensorMap map,
+                     const __grid_constant__ CUtensorMap rope_map, int box_rows) {
   using L = Lay<kParts, N>;
   constexpr bool kFp8 = kParts > 1;
   extern __shared__ uint8_t raw[];
   uint8_t* smem = raw + ((1024 - (smem_u32(raw) & 1023)) & 1023);
   Misc& mi = *reinterpret_cast<Misc*>(smem + L::kMiscAt);
   const uint32_t base = smem_u32(smem);
-  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  const int tid = threadIdx.x, warp = __shfl_sync(0xffffffffu, tid >> 5, 0), lane = tid & 31;
   constexpr int kColumns = N == 16 ? 128 : N == 32 ? 256 : 512;  // 2 S and 4 O accumulators of N columns
 
   // before the previous kernel's results are needed
@@ -245,6 +246,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     mi.stop = 0;
     mbar_fence_init();
     tma_prefetch(&map);
+    tma_prefetch(&rope_map);
   }
   if (warp == 5) tmem_alloc(smem_u32(&mi.tmem), kColumns);
   pdl_entry();
@@ -267,6 +269,8 @@ __global__ void __launch_bounds__(kThreads, 1)
     int64_t t = 0;
     int bad = 0;
     bool alive = true;
+    const uint32_t full = smem_u32(&mi.full[0]), empty = smem_u32(&mi.empty[0]);
+    const uint32_t rope_full = smem_u32(&mi.rope_full[0]), rope_empty = smem_u32(&mi.rope_empty[0]);
     const int segs = kDecodeTile / box_rows;  // boxes of a tile along its rows: 1, 2, 4 or 8
     while (alive && it.next()) {
       if (lane == 0) bad |= decode_len(p, it.b).bad;
@@ -298,34 +302,37 @@ __global__ void __launch_bounds__(kThreads, 1)
           if (left < 64) m &= (1ull << left) - 1;
           mi.mask[t & 7] = m;
         }
+        const uint32_t bytes = static_cast<uint32_t>(n_boxes * box_rows * 128);
 #pragma unroll 1
-        for (int m = 0; m < 5; ++m) {
-          const bool rope = m == 4;
-          const uint32_t full = smem_u32(rope ? &mi.rope_full[rslot] : &mi.full[slot]);
-          const uint32_t empty = smem_u32(rope ? &mi.rope_empty[rslot] : &mi.empty[slot]);
-          const uint32_t dst = base + (rope ? L::kRopeAt + rslot * L::kPiece : L::kSlotAt + slot * L::kSlot);
-          const int pieces = rope ? 1 : L::kPieces;
-          bool ok = true;
-          if (lane == 0) ok = mbar_wait(empty, (rope ? rphase : phase) ^ 1, stop);
-          ok = __shfl_sync(0xffffffffu, ok, 0);
-          if (!ok) {
-            alive = false;
-            break;
+        for (int m = 0; m < 4; ++m) {
+          alive = mbar_wait_warp(empty + 8 * slot, phase ^ 1, stop);
+          if (!alive) break;
+          const uint32_t dst = base + L::kSlotAt + slot * L::kSlot;
+          if (elect_one()) mbar_expect(full + 8 * slot, bytes * L::kPieces);
+          for (int s = 0; s < n_boxes; ++s) {
+            const int sid = __shfl_sync(0xffffffffu, id, s), srow = __shfl_sync(0xffffffffu, row, s);
+            // boxes of fewer rows than a slot has leave gaps between their pieces: a copy a piece
+            if (box_rows == kDecodeTile) {
+              if (elect_one()) tma_load_4d(dst, &map, full + 8 * slot, 0, srow, m * L::kPieces, sid);
+            } else if (elect_one()) {
+#pragma unroll
+              for (int c = 0; c < L::kPieces; ++c)
+                tma_load_4d(dst + c * L::kPiece + s * box_rows * 128, &map, full + 8 * slot, 0, srow, m * L::kPieces + c, sid);
+            }
           }
-          if (lane == 0) mbar_expect(full, static_cast<uint32_t>(n_boxes * box_rows * 128 * pieces));
-          __syncwarp();
-          const int seg = lane / pieces, piece = lane % pieces;
-          const int sid = __shfl_sync(0xffffffffu, id, seg & 31), srow = __shfl_sync(0xffffffffu, row, seg & 31);
-          if (seg < n_boxes) {
-            const int x = rope ? kLatent : (m * L::kPieces + piece) * (kFp8 ? 128 : 64);
-            tma_load_3d(dst + piece * L::kPiece + seg * box_rows * 128, &map, full, x, srow, sid);
-          }
-          if (rope) {
-            if (++rslot == L::kRopeSlots) { rslot = 0; rphase ^= 1; }
-          } else {
-            if (++slot == L::kSlots) { slot = 0; phase ^= 1; }
-          }
+          if (++slot == L::kSlots) { slot = 0; phase ^= 1; }
         }
+        if (!alive) break;
+        alive = mbar_wait_warp(rope_empty + 8 * rslot, rphase ^ 1, stop);
+        if (!alive) break;
+        if (elect_one()) mbar_expect(rope_full + 8 * rslot, bytes);
+        for (int s = 0; s < n_boxes; ++s) {
+          const int sid = __shfl_sync(0xffffffffu, id, s), srow = __shfl_sync(0xffffffffu, row, s);
+          if (elect_one())
+            tma_load_3d(base + L::kRopeAt + rslot * L::kPiece + s * box_rows * 128, &rope_map, rope_full + 8 * rslot, kLatent,
+                        srow, sid);
+        }
+        if (++rslot == L::kRopeSlots) { rslot = 0; rphase ^= 1; }
       }
     }
     set_flag(p.err, bad);
@@ -339,112 +346,122 @@ __global__ void __launch_bounds__(kThreads, 1)
     __syncwarp();
   } else if (warp == 5) {
     // ---- products ----
-    if (lane == 0) {
-      Items qi(p, share), vi(p, share);
-      auto advance = [](Items& it) {
-        bool more = it.next();
-        while (more && it.len == 0) more = it.next();
-        return more;
-      };
-      bool q_more = advance(qi), v_more = advance(vi);
-      int q_tile = 0, q_part = 0, v_tile = 0;     // within the items
-      int q_item = 0;                             // items begun, for the queries' barrier
-      int64_t qt = 0, vt = 0;                     // tiles issued
-      int qslot = 0, qphase = 0, rslot = 0, rphase = 0, vslot = 0;
-      uint64_t t0 = 0;
-      int idle = 0;
-      bool alive = true;
-      while (alive && (q_more || v_more)) {
-        bool progress = false;
-        if (v_more && vt < qt && mbar_test(smem_u32(&mi.p_full), static_cast<int>(vt & 1))) {
-          tmem_fence_after();
-          const uint32_t pa = base + L::kPAt;
-#pragma unroll 1
-          for (int m = 0; m < 4; ++m) {
-            const uint32_t va = base + L::kSlotAt + vslot * L::kSlot;
+    Items qi(p, share), vi(p, share);
+    auto advance = [](Items& it) {
+      bool more = it.next();
+      while (more && it.len == 0) more = it.next();
+      return more;
+    };
+    const uint32_t full = smem_u32(&mi.full[0]), empty = smem_u32(&mi.empty[0]);
+    const uint32_t rope_full = smem_u32(&mi.rope_full[0]), rope_empty = smem_u32(&mi.rope_empty[0]);
+    const uint32_t s_full = smem_u32(&mi.s_full[0]), s_free = smem_u32(&mi.s_free[0]);
+    bool q_more = advance(qi), v_more = advance(vi);
+    int q_tile = 0, q_part = 0, v_tile = 0;     // within the items
+    int q_item = 0;                             // items begun, for the queries' barrier
+    uint32_t qt = 0, vt = 0;                    // tiles issued
+    int qslot = 0, qphase = 0, rslot = 0, rphase = 0, vslot = 0;
+    uint64_t t0 = 0;
+    int idle = 0;
+    bool alive = true;
+    // whichever product has its operands: O of a tile once its weights are there, parts of S up to two tiles ahead
+    while (alive && (q_more || v_more)) {
+      bool progress = false;
+      if (v_more && vt != qt && mbar_test_warp(smem_u32(&mi.p_full), vt & 1)) {
+        tmem_fence_after();
+        const bool first = v_tile == 0;
+#pragma unroll
+        for (int m = 0; m < 4; ++m) {
+          if (elect_one()) {
+            const uint64_t va = umma_desc(base + L::kSlotAt + vslot * L::kSlot, L::kPiece, 1024);
+            const uint64_t pa = umma_desc(base + L::kPAt, L::kPiece, 1024);
             const uint32_t d = tmem + (2 + m) * N;
 #pragma unroll
             for (int k = 0; k < (kFp8 ? 2 : 4); ++k) {
-              const uint32_t step = k * (kFp8 ? 32 : 16) * 128;
-              const uint64_t a = umma_desc(va + step, L::kPiece, 1024);
-              umma_ss<kFp8>(d, a, umma_desc(pa + step, L::kPiece, 1024), kIdescO, v_tile > 0 || k > 0);
-              if constexpr (kFp8)
-                umma_ss<kFp8>(d, a, umma_desc(pa + L::kPiece + step, L::kPiece, 1024), kIdescO, true);
+              const uint32_t step = k * (kFp8 ? 32 : 16) * 8;  // rows of 128 bytes, in units of 16
+              umma_ss<kFp8>(d, va + step, pa + step, kIdescO, !first || k > 0);
+              if constexpr (kFp8) umma_ss<kFp8>(d, va + step, pa + step + L::kPiece / 16, kIdescO, true);
             }
-            umma_commit(smem_u32(&mi.empty[vslot]));
-            if (++vslot == L::kSlots) vslot = 0;
+            umma_commit(empty + 8 * vslot);
+            if (m == 3) umma_commit(smem_u32(&mi.pv_done));
           }
-          umma_commit(smem_u32(&mi.pv_done));
-          ++vt;
-          if (++v_tile == vi.n) {
-            v_tile = 0;
-            v_more = advance(vi);
+          __syncwarp();
+          if (++vslot == L::kSlots) vslot = 0;
+        }
+        ++vt;
+        if (++v_tile == vi.n) {
+          v_tile = 0;
+          v_more = advance(vi);
+        }
+        progress = true;
+      }
+      if (q_more && qt - vt < 2) {
+        const uint32_t buf = qt & 1;
+        bool ready = true;
+        if (q_part == 0) {
+          if (qt >= 2) ready = mbar_test_warp(s_free + 8 * buf, ((qt >> 1) + 1) & 1);
+          if (ready && q_tile == 0) ready = mbar_test_warp(smem_u32(&mi.q_full), q_item & 1);
+        }
+        if (ready)
+          ready = q_part < 4 ? mbar_test_warp(full + 8 * qslot, qphase) : mbar_test_warp(rope_full + 8 * rslot, rphase);
+        if (ready) {
+          tmem_fence_after();
+          const uint32_t d = tmem + buf * N;
+          if (q_part < 4) {
+            if (elect_one()) {
+#pragma unroll
+              for (int c = 0; c < L::kPieces; ++c) {
+                const uint64_t ka = umma_desc(base + L::kSlotAt + qslot * L::kSlot + c * L::kPiece, 16, 1024);
+                const uint64_t qa = umma_desc(base + L::kQAt + (q_part * L::kPieces + c) * (N * 128), 16, 1024);
+#pragma unroll
+                for (int k = 0; k < 4; ++k)  // 32 bytes of K each
+#pragma unroll
+                  for (int x = 0; x < kParts; ++x)
+                    umma_ss<kFp8>(d, ka + 2 * k, qa + 2 * k + x * (5 * N * 8), kIdescS,
+                                  q_part > 0 || c > 0 || k > 0 || x > 0);
+              }
+            }
+            __syncwarp();
+            ++q_part;
+            if (++qslot == L::kSlots) { qslot = 0; qphase ^= 1; }
+          } else {
+            if (elect_one()) {
+              const uint64_t ka = umma_desc(base + L::kRopeAt + rslot * L::kPiece, 16, 1024);
+              const uint64_t qa = umma_desc(base + L::kQAt + 4 * L::kPieces * (N * 128), 16, 1024);
+#pragma unroll
+              for (int k = 0; k < (kFp8 ? 2 : 4); ++k)
+#pragma unroll
+                for (int x = 0; x < kParts; ++x)
+                  umma_ss<kFp8>(d, ka + 2 * k, qa + 2 * k + x * (5 * N * 8), kIdescS, true);
+              umma_commit(rope_empty + 8 * rslot);
+              umma_commit(s_full + 8 * buf);
+            }
+            __syncwarp();
+            if (++rslot == L::kRopeSlots) { rslot = 0; rphase ^= 1; }
+            q_part = 0;
+            ++qt;
+            if (q_tile == 0) ++q_item;
+            if (++q_tile == qi.n) {
+              q_tile = 0;
+              q_more = advance(qi);
+            }
           }
           progress = true;
         }
-        if (q_more && qt < vt + 2) {
-          const int buf = static_cast<int>(qt & 1);
-          bool ready = true;
-          if (q_part == 0) {
-            if (qt >= 2) ready = mbar_test(smem_u32(&mi.s_free[buf]), static_cast<int>((qt >> 1) + 1) & 1);
-            if (ready && q_tile == 0) ready = mbar_test(smem_u32(&mi.q_full), q_item & 1);
-          }
-          if (ready)
-            ready = q_part < 4 ? mbar_test(smem_u32(&mi.full[qslot]), qphase)
-                               : mbar_test(smem_u32(&mi.rope_full[rslot]), rphase);
-          if (ready) {
-            tmem_fence_after();
-            const uint32_t d = tmem + buf * N;
-            const uint32_t ka = base + (q_part < 4 ? L::kSlotAt + qslot * L::kSlot : L::kRopeAt + rslot * L::kPiece);
-            const int pieces = q_part < 4 ? L::kPieces : 1;
-            const int steps = kFp8 && q_part == 4 ? 2 : 4;  // 32 bytes of K each
-#pragma unroll 1
-            for (int c = 0; c < pieces; ++c) {
-              const uint32_t qa = base + L::kQAt + (q_part * L::kPieces + c) * (N * 128);
-#pragma unroll 1
-              for (int k = 0; k < steps; ++k) {
-                const uint64_t a = umma_desc(ka + c * L::kPiece + k * 32, 16, 1024);
-                umma_ss<kFp8>(d, a, umma_desc(qa + k * 32, 16, 1024), kIdescS, q_part > 0 || c > 0 || k > 0);
-#pragma unroll
-                for (int x = 1; x < kParts; ++x)
-                  umma_ss<kFp8>(d, a, umma_desc(qa + x * (5 * N * 128) + k * 32, 16, 1024), kIdescS, true);
-              }
-            }
-            if (q_part < 4) {
-              ++q_part;
-              if (++qslot == L::kSlots) { qslot = 0; qphase ^= 1; }
-            } else {
-              umma_commit(smem_u32(&mi.rope_empty[rslot]));
-              umma_commit(smem_u32(&mi.s_full[buf]));
-              if (++rslot == L::kRopeSlots) { rslot = 0; rphase ^= 1; }
-              q_part = 0;
-              ++qt;
-              if (q_tile == 0) ++q_item;
-              if (++q_tile == qi.n) {
-                q_tile = 0;
-                q_more = advance(qi);
-              }
-            }
-            progress = true;
-          }
-        }
-        if (progress) {
-          idle = 0;
-        } else if (++idle >= 256) {
-          idle = 0;
-          if (t0 == 0) t0 = now_ns();
-          if (*stop != 0) alive = false;
-          else if (now_ns() - t0 > kWaitNs) {
-            *stop = 1;
-            alive = false;
-          }
-        }
-        if (progress) t0 = 0;
       }
-      if (!alive) {  // what was issued ends before the CTA does
-        int never = 0;
-        if (vt > 0) mbar_wait(smem_u32(&mi.pv_done), static_cast<int>((vt - 1) & 1), &never);
+      if (progress) {
+        idle = 0;
+        t0 = 0;
+      } else if (++idle >= 256) {
+        idle = 0;
+        const uint64_t now = now_ns();
+        if (t0 == 0) t0 = now;
+        if (now - t0 > kWaitNs) *stop = 1;
+        alive = __all_sync(0xffffffffu, *stop == 0) != 0;
       }
+    }
+    if (!alive && vt > 0) {  // what was issued ends before the CTA does
+      int never = 0;
+      mbar_wait(smem_u32(&mi.pv_done), static_cast<int>((vt - 1) & 1), &never);
     }
     __syncwarp();
   } else {
@@ -753,20 +770,25 @@ __global__ void __launch_bounds__(kThreads, 1)
   if (warp == 5) tmem_free(tmem, kColumns);
 }
 
+struct Maps {
+  CUtensorMap latent, rope;
+};
+
 template <class TQ, int kParts, int N>
-int run(const DecodeParams& p, const CUtensorMap& map, int box_rows, void* stream) {
+int run(const DecodeParams& p, const Maps& maps, int box_rows, void* stream) {
   auto k = decode_tc_kernel<TQ, kParts, N>;
   constexpr int kBytes = Lay<kParts, N>::kBytes;
   const int st = allow_smem(reinterpret_cast<const void*>(k), kBytes);
   if (st != PMG_OK) return st;
-  return launch(k, dim3(static_cast<unsigned>(p.units) * p.groups), kThreads, kBytes, stream, p, map, box_rows);
+  return launch(k, dim3(static_cast<unsigned>(p.units) * p.groups), kThreads, kBytes, stream, p, maps.latent, maps.rope,
+                box_rows);
 }
 
 template <class TQ, int kParts>
-int run(const DecodeParams& p, const CUtensorMap& map, int box_rows, void* stream) {
-  if (p.rows_per_group <= 16) return run<TQ, kParts, 16>(p, map, box_rows, stream);
-  if (p.rows_per_group <= 32) return run<TQ, kParts, 32>(p, map, box_rows, stream);
-  return run<TQ, kParts, 64>(p, map, box_rows, stream);
+int run(const DecodeParams& p, const Maps& maps, int box_rows, void* stream) {
+  if (p.rows_per_group <= 16) return run<TQ, kParts, 16>(p, maps, box_rows, stream);
+  if (p.rows_per_group <= 32) return run<TQ, kParts, 32>(p, maps, box_rows, stream);
+  return run<TQ, kParts, 64>(p, maps, box_rows, stream);
 }
 
 int gcd(int a, int b) { return b == 0 ? a : gcd(b, a % b); }
@@ -793,16 +815,22 @@ int decode_tc(DecodeParams& p, int q_dtype, int cache_dtype, int sms, void* stre
   const bool fp8 = cache_dtype == PMG_FP8_E4M3;
   const int ec = elem_bytes(cache_dtype);
   const int box_rows = gcd(p.B, kDecodeTile);
-  CUtensorMap map;
   const CUtensorMapDataType type = fp8 ? CU_TENSOR_MAP_DATA_TYPE_UINT8
                                    : q_dtype == PMG_BF16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16
                                                          : CU_TENSOR_MAP_DATA_TYPE_FLOAT16;
-  const int st = tensor_map(&map, type, p.cache, kEntry, static_cast<uint64_t>(p.B), static_cast<uint64_t>(p.num_blocks),
-                            static_cast<uint64_t>(p.tok_stride) * ec, static_cast<uint64_t>(p.blk_stride) * ec,
-                            fp8 ? 128 : 64, static_cast<uint32_t>(box_rows), 1);
+  const uint64_t page = static_cast<uint64_t>(p.B), blocks = static_cast<uint64_t>(p.num_blocks);
+  const uint64_t row_stride = static_cast<uint64_t>(p.tok_stride) * ec, blk_stride = static_cast<uint64_t>(p.blk_stride) * ec;
+  const uint32_t piece = 128 / ec, box = static_cast<uint32_t>(box_rows);  // elements of 128 bytes
+  Maps maps;
+  // the latent part as pieces of 128 bytes; the rotated part from the whole row (an e4m3 one is half a piece, and what
+  // lies past the row reads as 0)
+  int st = tensor_map<4>(&maps.latent, type, p.cache, {piece, page, kLatent / piece, blocks},
+                         {row_stride, 128, blk_stride}, {piece, box, box_rows == kDecodeTile && !fp8 ? 2u : 1u, 1});
+  if (st == PMG_OK)
+    st = tensor_map<3>(&maps.rope, type, p.cache, {kEntry, page, blocks}, {row_stride, blk_stride}, {piece, box, 1});
   if (st != PMG_OK) return st;
-  if (q_dtype == PMG_BF16) return fp8 ? run<bf16, 2>(p, map, box_rows, stream) : run<bf16, 1>(p, map, box_rows, stream);
-  return fp8 ? run<f16, 3>(p, map, box_rows, stream) : run<f16, 1>(p, map, box_rows, stream);
+  if (q_dtype == PMG_BF16) return fp8 ? run<bf16, 2>(p, maps, box_rows, stream) : run<bf16, 1>(p, maps, box_rows, stream);
+  return fp8 ? run<f16, 3>(p, maps, box_rows, stream) : run<f16, 1>(p, maps, box_rows, stream);
 }
 
 }  // namespace pmg_mla

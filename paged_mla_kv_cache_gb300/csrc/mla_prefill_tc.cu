@@ -140,7 +140,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   uint8_t* smem = raw + ((1024 - (smem_u32(raw) & 1023)) & 1023);
   Misc& mi = *reinterpret_cast<Misc*>(smem + kMiscAt);
   const uint32_t base = smem_u32(smem);
-  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  const int tid = threadIdx.x, warp = __shfl_sync(0xffffffffu, tid >> 5, 0), lane = tid & 31;
 
   if (tid == 0) {
     for (int i = 0; i < kSlots; ++i) {
@@ -189,28 +189,29 @@ __global__ void __launch_bounds__(kThreads, 1)
       if (unit == 0)
         for (int i = lane; i < p.R; i += 32) bad |= prefill_req(p, i).bad;
       set_flag(p.err, bad);
-      if (lane == 0) {
-        Items it(p, share);
-        int slot = 0, phase = 0, items = 0;
-        bool alive = true;
-        auto piece = [&](const CUtensorMap* map, int c, int head, int row) {
-          if (!alive) return;
-          if (!mbar_wait(smem_u32(&mi.empty[slot]), phase ^ 1, stop)) {
-            alive = false;
-            return;
-          }
-          const uint32_t full = smem_u32(&mi.full[slot]);
+      Items it(p, share);
+      int slot = 0, phase = 0, items = 0;
+      bool alive = true;
+      auto piece = [&](const CUtensorMap* map, int c, int head, int row) {
+        if (!alive) return;
+        alive = mbar_wait_warp(smem_u32(&mi.empty[0]) + 8 * slot, phase ^ 1, stop);
+        if (!alive) return;
+        if (elect_one()) {
+          const uint32_t full = smem_u32(&mi.full[0]) + 8 * slot;
           mbar_expect(full, kPiece);
           tma_load_3d(base + kSlotAt + slot * kPiece, map, full, c, head, row);
-          if (++slot == kSlots) {
-            slot = 0;
-            phase ^= 1;
-          }
-        };
-        while (alive && it.next()) {
-          if (it.keys == 0) continue;
-          if (!mbar_wait(smem_u32(&mi.q_empty), (items & 1) ^ 1, stop)) break;
-          ++items;
+        }
+        if (++slot == kSlots) {
+          slot = 0;
+          phase ^= 1;
+        }
+      };
+      while (alive && it.next()) {
+        if (it.keys == 0) continue;
+        alive = mbar_wait_warp(smem_u32(&mi.q_empty), (items & 1) ^ 1, stop);
+        if (!alive) break;
+        ++items;
+        if (elect_one()) {
           const int halves = it.act[1] > 0 ? 2 : 1;
           const uint32_t q_full = smem_u32(&mi.q_full);
           mbar_expect(q_full, halves * 3 * kPiece);
@@ -218,43 +219,44 @@ __global__ void __launch_bounds__(kThreads, 1)
             for (int c = 0; c < 3; ++c)
               tma_load_3d(base + kQAt + (3 * h + c) * kPiece, &map_q, q_full, 64 * c, it.head,
                           it.x.q0 + it.tile * kRows + h * kHalf);
-          for (int b = it.b0; b < it.b0 + it.n && alive; ++b) {
-            const int row = it.x.k0 + b * kBlock;
-            piece(&map_k, 0, it.head, row);
-            piece(&map_k, 64, it.head, row);
-            piece(&map_pe, 0, 0, row);
-            piece(&map_v, 0, it.head, row);
-            piece(&map_v, 64, it.head, row);
-          }
         }
-        if (*stop != 0) {  // copies in flight land before the CTA ends
-          int never = 0;
-          for (int i = 0; i < kSlots; ++i) mbar_wait(smem_u32(&mi.full[i]), i < slot ? phase : phase ^ 1, &never);
-          if (items > 0) mbar_wait(smem_u32(&mi.q_full), (items - 1) & 1, &never);
+        __syncwarp();
+        for (int b = it.b0; b < it.b0 + it.n && alive; ++b) {
+          const int row = it.x.k0 + b * kBlock;
+          piece(&map_k, 0, it.head, row);
+          piece(&map_k, 64, it.head, row);
+          piece(&map_pe, 0, 0, row);
+          piece(&map_v, 0, it.head, row);
+          piece(&map_v, 64, it.head, row);
         }
+      }
+      if (!alive) {  // copies in flight land before the CTA ends
+        int never = 0;
+        for (int i = 0; i < kSlots; ++i) mbar_wait(smem_u32(&mi.full[i]), i < slot ? phase : phase ^ 1, &never);
+        if (items > 0) mbar_wait(smem_u32(&mi.q_full), (items - 1) & 1, &never);
       }
       __syncwarp();
     } else if (warp == 9) {
       // ---- products ----
-      if (lane == 0) {
-        Items it(p, share);
-        bool alive = true;
-        auto wait = [&](uint64_t& bar, int parity) {
-          if (alive && !mbar_wait(smem_u32(&bar), parity, stop)) alive = false;
-          return alive;
-        };
-        auto advance = [&]() {
-          bool more = it.next();
-          while (more && it.keys == 0) more = it.next();
-          return more;
-        };
-        int items = 0, cleans = 0;
-        // piece c of step st in the ring: 5 pieces a step (counted modulo 2^32, a multiple of the ring)
-        auto slot_of = [](uint32_t st, uint32_t c) { return (5 * st + c) & (kSlots - 1); };
-        auto phase_of = [](uint32_t st, uint32_t c) { return static_cast<int>((5 * st + c) / kSlots & 1); };
-        // S of half h for the block of step st
-        auto scores = [&](int h, uint32_t st) {
-#pragma unroll 1
+      Items it(p, share);
+      bool alive = true;
+      auto wait = [&](uint32_t bar, int parity) {
+        alive = alive && mbar_wait_warp(bar, parity, stop);
+        return alive;
+      };
+      const uint32_t full = smem_u32(&mi.full[0]), empty = smem_u32(&mi.empty[0]), s_full = smem_u32(&mi.s_full[0]),
+                     p_full = smem_u32(&mi.p_full[0]), o_done = smem_u32(&mi.o_done[0]);
+      // piece c of step st in the ring: 5 pieces a step (counted modulo 2^32, a multiple of the ring)
+      auto slot_of = [](uint32_t st, uint32_t c) { return (5 * st + c) & (kSlots - 1); };
+      auto phase_of = [](uint32_t st, uint32_t c) { return static_cast<int>((5 * st + c) / kSlots & 1); };
+      auto wait_pieces = [&](uint32_t st, uint32_t c0, uint32_t c1) {
+        for (uint32_t c = c0; c < c1; ++c) wait(full + 8 * slot_of(st, c), phase_of(st, c));
+        return alive;
+      };
+      // S of half h for the block of step st
+      auto scores = [&](int h, uint32_t st) {
+        if (elect_one()) {
+#pragma unroll
           for (uint32_t c = 0; c < 3; ++c) {
             const uint64_t qa = umma_desc(base + kQAt + (3 * h + c) * kPiece, 16, 1024);
             const uint64_t ka = umma_desc(base + kSlotAt + slot_of(st, c) * kPiece, 16, 1024);
@@ -262,99 +264,93 @@ __global__ void __launch_bounds__(kThreads, 1)
             for (int k = 0; k < 4; ++k)  // 32 bytes of K each
               umma_ss<false>(tmem + h * kBlock, qa + 2 * k, ka + 2 * k, kIdescS, c > 0 || k > 0);
           }
-          umma_commit(smem_u32(&mi.s_full[0]) + 8 * h);
-        };
-        auto values = [&](int h, uint32_t st, bool first) {
-          // the two 64-value pieces of V are two slots, which may wrap around the ring: a product of 64 each then
+          umma_commit(s_full + 8 * h);
+        }
+        __syncwarp();
+      };
+      auto values = [&](int h, uint32_t st, bool first) {
+        // the two 64-value pieces of V are two slots, which may wrap around the ring: a product of 64 each then
+        const uint32_t d = tmem + 256 + h * kVal, w = tmem + h * kBlock;
+        const bool wraps = slot_of(st, 4) == 0;
+        if (elect_one()) {
           const uint64_t v0 = umma_desc(base + kSlotAt + slot_of(st, 3) * kPiece, kPiece, 1024);
           const uint64_t v1 = umma_desc(base + kSlotAt + slot_of(st, 4) * kPiece, kPiece, 1024);
-          const uint32_t d = tmem + 256 + h * kVal, w = tmem + h * kBlock;
-          if (slot_of(st, 4) != 0) {
+          if (!wraps) {
 #pragma unroll
             for (int k = 0; k < 8; ++k) umma_ts(d, w + 8 * k, v0 + 128 * k, kIdescO, !first || k > 0);
           } else {
             constexpr uint32_t kIdescHalf = umma_idesc(kFmt, 0, 1, 128, 64);
-#pragma unroll 1
+#pragma unroll
             for (int k = 0; k < 8; ++k) {
               umma_ts(d, w + 8 * k, v0 + 128 * k, kIdescHalf, !first || k > 0);
               umma_ts(d + 64, w + 8 * k, v1 + 128 * k, kIdescHalf, !first || k > 0);
             }
           }
-          umma_commit(smem_u32(&mi.o_done[0]) + 8 * h);
-        };
-        auto wait_pieces = [&](uint32_t st, uint32_t c0, uint32_t c1) {
-#pragma unroll 1
-          for (uint32_t c = c0; c < c1 && alive; ++c)
-            if (!mbar_wait(smem_u32(&mi.full[0]) + 8 * slot_of(st, c), phase_of(st, c), stop)) alive = false;
-          return alive;
-        };
-        auto free_pieces = [&](uint32_t st, uint32_t c0, uint32_t c1) {
-#pragma unroll 1
-          for (uint32_t c = c0; c < c1; ++c) umma_commit(smem_u32(&mi.empty[0]) + 8 * slot_of(st, c));
-        };
-        uint32_t step = 0;                  // blocks begun
-        uint32_t taken = 0;                 // parity of the weights taken, a bit a half
-        uint32_t any = 0;                   // halves that have taken any
-        while (alive && advance()) {
-          if (!wait(mi.q_full, items & 1)) break;
-          ++items;
-          const int end = it.b0 + it.n;
-          const bool partial_end = end == it.nb && it.x.lk - (end - 1) * kBlock < kBlock;  // warp 10's rule
-          const int last0 = it.last(0), last1 = it.last(1);
-#pragma unroll 1
-          for (int b = it.b0; b < end && alive; ++b, ++step) {
-            if (b == it.b0) {
-              if (!wait_pieces(step, 0, 3)) break;
+          umma_commit(o_done + 8 * h);
+        }
+        __syncwarp();
+      };
+      // frees pieces [c0, c1) of a step, and the queries after their last product
+      auto free_pieces = [&](uint32_t st, uint32_t c0, uint32_t c1, bool queries) {
+        if (elect_one()) {
+          for (uint32_t c = c0; c < c1; ++c) umma_commit(empty + 8 * slot_of(st, c));
+          if (queries) umma_commit(smem_u32(&mi.q_empty));
+        }
+        __syncwarp();
+      };
+      int items = 0, cleans = 0;
+      uint32_t step = 0;   // blocks begun
+      uint32_t taken = 0;  // parity of the weights taken, a bit a half
+      uint32_t any = 0;    // halves that have taken any
+      while (alive && it.next()) {
+        if (it.keys == 0) continue;
+        if (!wait(smem_u32(&mi.q_full), items & 1)) break;
+        ++items;
+        const int end = it.b0 + it.n;
+        const bool partial_end = end == it.nb && it.x.lk - (end - 1) * kBlock < kBlock;  // warp 10's rule
+        const int last0 = it.last(0), last1 = it.last(1);
+        for (int b = it.b0; b < end && alive; ++b, ++step) {
+          if (b == it.b0) {
+            if (!wait_pieces(step, 0, 3)) break;
+            tmem_fence_after();
+            if (b < last0) scores(0, step);
+            if (b < last1) scores(1, step);
+            free_pieces(step, 0, 3, b + 1 == end);
+          }
+          if (!wait_pieces(step, 3, 5)) break;
+          if (partial_end && b + 1 == end) {
+            if (elect_one()) mbar_arrive(smem_u32(&mi.dirty));
+            if (!wait(smem_u32(&mi.clean), cleans++ & 1)) break;
+          }
+          bool have_k = false;
+#pragma unroll
+          for (int h = 0; h < 2; ++h) {
+            const int last = h ? last1 : last0;
+            if (alive && b < last && wait(p_full + 8 * h, taken >> h & 1)) {
+              taken ^= 1u << h;
+              any |= 1u << h;
               tmem_fence_after();
-#pragma unroll 1
-              for (int h = 0; h < 2; ++h)
-                if (b < (h ? last1 : last0)) scores(h, step);
-              free_pieces(step, 0, 3);
-              if (b + 1 == end) umma_commit(smem_u32(&mi.q_empty));
+              values(h, step, b == it.b0);
             }
-            bool have_v = false, have_k = false;
-#pragma unroll 1
-            for (int h = 0; h < 2; ++h) {
-              const int last = h ? last1 : last0;
-              if (b < last) {
-                if (!have_v) {
-                  if (!wait_pieces(step, 3, 5)) break;
-                  if (partial_end && b + 1 == end) {
-                    mbar_arrive(smem_u32(&mi.dirty));
-                    if (!wait(mi.clean, cleans++ & 1)) break;
-                  }
-                  have_v = true;
-                }
-                if (alive && !mbar_wait(smem_u32(&mi.p_full[0]) + 8 * h, taken >> h & 1, stop)) alive = false;
-                if (!alive) break;
-                taken ^= 1u << h;
-                any |= 1u << h;
+            if (alive && b + 1 < last) {
+              if (!have_k) {
+                wait_pieces(step + 1, 0, 3);
                 tmem_fence_after();
-                values(h, step, b == it.b0);
+                have_k = true;
               }
-              if (b + 1 < last) {
-                if (!have_k) {
-                  if (!wait_pieces(step + 1, 0, 3)) break;
-                  tmem_fence_after();
-                  have_k = true;
-                }
-                scores(h, step + 1);
-              }
-            }
-            if (!alive) break;
-            free_pieces(step, 3, 5);
-            if (b + 1 < end) {
-              free_pieces(step + 1, 0, 3);
-              if (b + 2 == end) umma_commit(smem_u32(&mi.q_empty));
+              if (alive) scores(h, step + 1);
             }
           }
+          if (!alive) break;
+          free_pieces(step, 3, 5, false);
+          if (b + 1 < end) free_pieces(step + 1, 0, 3, b + 2 == end);
         }
-        if (!alive) {
-          // what was issued ends before the CTA does
-          int never = 0;
-          for (int h = 0; h < 2; ++h)
-            if (any >> h & 1) mbar_wait(smem_u32(&mi.o_done[0]) + 8 * h, (taken >> h & 1) ^ 1, &never);
-        }
+      }
+      if (!alive) {
+        // what was issued ends before the CTA does
+        int never = 0;
+        for (int h = 0; h < 2; ++h)
+          if (any >> h & 1) mbar_wait(o_done + 8 * h, (taken >> h & 1) ^ 1, &never);
       }
       __syncwarp();
     } else if (warp == 10) {
@@ -652,8 +648,8 @@ int prefill_tc(PrefillParams& p, int dtype, int sms, void* stream) {
     // the stride of a dimension of one is not used; it has to be a valid one all the same
     const uint64_t s1 = heads > 1 ? static_cast<uint64_t>(head_stride) * 2 : 512;
     const uint64_t s2 = rows > 1 ? static_cast<uint64_t>(row_stride) * 2 : 512;
-    return tensor_map(m, type, at, static_cast<uint64_t>(dim), static_cast<uint64_t>(heads), static_cast<uint64_t>(rows),
-                      s1, s2, 64, 1, 128);
+    return tensor_map<3>(m, type, at, {static_cast<uint64_t>(dim), static_cast<uint64_t>(heads), static_cast<uint64_t>(rows)},
+                         {s1, s2}, {64, 1, 128});
   };
   int st = map(&maps[0], p.q, kNope + kRope, p.H, p.Tq, p.qh_stride, p.qt_stride);
   if (st == PMG_OK) st = map(&maps[1], p.k, kNope, p.H, p.Tk, p.kh_stride, p.kt_stride);

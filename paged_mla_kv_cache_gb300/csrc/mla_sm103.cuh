@@ -76,6 +76,27 @@ __device__ __forceinline__ bool mbar_wait(uint32_t bar, int parity, volatile int
   }
 }
 
+// One lane of a converged warp. The roles that issue copies and products run
+// with all their lanes and let the elected one issue: addresses and
+// descriptors then stay in uniform registers, which these instructions read (a
+// role run by a single lane took about 170 clocks a product instead).
+__device__ __forceinline__ bool elect_one() {
+  uint32_t leader;
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "elect.sync _|p, 0xffffffff;\n\t"
+      "selp.u32 %0, 1, 0, p;\n\t}"
+      : "=r"(leader));
+  return leader != 0;
+}
+// The same answer for all lanes.
+__device__ __forceinline__ bool mbar_wait_warp(uint32_t bar, int parity, volatile int* stop) {
+  return __all_sync(0xffffffffu, mbar_wait(bar, parity, stop)) != 0;
+}
+__device__ __forceinline__ bool mbar_test_warp(uint32_t bar, int parity) {
+  return __all_sync(0xffffffffu, mbar_test(bar, parity)) != 0;
+}
+
 // ---- proxies, named barriers --------------------------------------------------
 
 // orders this thread's shared-memory writes before later reads by TMA and the tensor core
@@ -119,6 +140,15 @@ __device__ __forceinline__ void tma_load_3d(uint32_t dst, const CUtensorMap* map
       "cp.async.bulk.tensor.3d.shared::cta.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%3, %4, %5}], [%2];" ::"r"(
           dst),
       "l"(map), "r"(bar), "r"(x), "r"(y), "r"(z)
+      : "memory");
+}
+
+__device__ __forceinline__ void tma_load_4d(uint32_t dst, const CUtensorMap* map, uint32_t bar, int x, int y, int z,
+                                            int w) {
+  asm volatile(
+      "cp.async.bulk.tensor.4d.shared::cta.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%3, %4, %5, %6}], "
+      "[%2];" ::"r"(dst),
+      "l"(map), "r"(bar), "r"(x), "r"(y), "r"(z), "r"(w)
       : "memory");
 }
 
@@ -271,15 +301,22 @@ inline EncodeTiled encode_tiled() {
   return fn;
 }
 
-// A 3-d map with the 128-byte swizzle: dims and box in elements, innermost
-// first, strides in bytes of the two outer dimensions. Reads outside give 0.
-inline int tensor_map(CUtensorMap* map, CUtensorMapDataType type, const void* base, uint64_t d0, uint64_t d1,
-                      uint64_t d2, uint64_t s1, uint64_t s2, uint32_t b0, uint32_t b1, uint32_t b2) {
+// A map with the 128-byte swizzle: dims and box in elements, innermost first,
+// strides in bytes of the outer dimensions. Reads outside give 0.
+template <int kDims>
+inline int tensor_map(CUtensorMap* map, CUtensorMapDataType type, const void* base, const uint64_t (&dims)[kDims],
+                      const uint64_t (&strides)[kDims - 1], const uint32_t (&box)[kDims]) {
   const EncodeTiled fn = encode_tiled();
   if (fn == nullptr) return PMG_ERR_CUDA;
-  const cuuint64_t dims[3] = {d0, d1, d2}, strides[2] = {s1, s2};
-  const cuuint32_t box[3] = {b0, b1, b2}, steps[3] = {1, 1, 1};
-  return fn(map, type, 3, const_cast<void*>(base), dims, strides, box, steps, CU_TENSOR_MAP_INTERLEAVE_NONE,
+  cuuint64_t d[kDims], s[kDims - 1];
+  cuuint32_t b[kDims], steps[kDims];
+  for (int i = 0; i < kDims; ++i) {
+    d[i] = dims[i];
+    b[i] = box[i];
+    steps[i] = 1;
+    if (i > 0) s[i - 1] = strides[i - 1];
+  }
+  return fn(map, type, kDims, const_cast<void*>(base), d, s, b, steps, CU_TENSOR_MAP_INTERLEAVE_NONE,
             CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
             CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS
              ? PMG_OK
