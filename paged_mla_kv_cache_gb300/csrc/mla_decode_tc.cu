@@ -74,51 +74,62 @@ struct Lay {
   static constexpr int kRopeAt = kSlotAt + kSlots * kSlot;
   static constexpr int kMiscAt = kRopeAt + kRopeSlots * kPiece;
   static constexpr int kBytes = kMiscAt + kMisc + 1024;
-  static_assert(kTiles >= 2 && kBytes <= kSmemMax, "two tiles in flight");
+  static_assert(kTiles >= 2 && kRopeSlots <= 8 && kBytes <= kSmemMax, "two tiles in flight, notes for all");
 };
 
-struct Misc {
-  uint64_t full[24], empty[24], rope_full[8], rope_empty[8];
-  uint64_t s_full[2], s_free[2], p_full, pv_done, q_full;
-  uint64_t mask[8];        // entries of a tile that exist, by tile & 7
-  int64_t scratch[33], found[2];
-  float ref[64], factor[64], alpha[64];  // of each row: reference, what a raw score is multiplied by, rescaling
-  int32_t step[64];                      // of each row: which of the new tokens it belongs to
+template <int kSlots, int kRopeSlots, int N>
+struct MiscOf {
+  uint64_t full[kSlots], empty[kSlots], rope_full[kRopeSlots], rope_empty[kRopeSlots];
+  uint64_t s_full[2], s_free[2], p_full, pv_done, q_full, end;
+  uint64_t mask[8];      // entries of a tile that exist, by tile & 7
+  union {
+    struct {
+      int64_t scratch[33], found[2];  // while the share is looked up
+    };
+    float warp_sums[4 * N];
+  };
+  float factor[N];       // of each row: what a raw score is multiplied by
+  union {
+    float alpha[N];      // what its sums are multiplied by as its reference moves
+    float inv[N];        // what its result is multiplied by
+  };
+  uint8_t step[N];       // which of the group's new tokens it belongs to
   uint32_t tmem;
-  int32_t stop;
+  int32_t stop, never;
 };
-static_assert(sizeof(Misc) <= 2048, "Misc fits");
 
-// Walks the requests of a share.
+// Walks the requests of a share. The next request's length is loaded one step
+// early.
 struct Items {
   const DecodeParams* p;
   int64_t at, end;
   int b;
-  int64_t tile, tiles;
-  int n;      // tiles of this share
-  int len;    // keys of the request
+  int tile, tiles;  // first tile of this share, tiles of the request
+  int n;            // tiles of this share
+  int len;          // keys of the request
   int full_len;
+  DecodeLen ahead;
   __device__ Items(const DecodeParams& p_, const Share& s) : p(&p_), at(s.begin), end(s.end), b(s.item - 1) {
-    tile = s.offset;
-    tiles = n = len = full_len = 0;
-    first_ = true;
+    tile = tiles = n = len = full_len = 0;
+    if (at < end) ahead = decode_len(*p, s.item);
+    first_ = static_cast<int>(s.offset);
   }
   __device__ bool next() {
     if (at >= end) return false;
     ++b;
-    if (!first_) tile = 0;
-    first_ = false;
-    const DecodeLen l = decode_len(*p, b);
-    len = l.use;
-    full_len = l.full;
+    tile = first_;
+    first_ = 0;
+    len = ahead.use;
+    full_len = ahead.full;
+    if (b + 1 < p->R) ahead = decode_len(*p, b + 1);
     tiles = len > 0 ? (len + kDecodeTile - 1) / kDecodeTile : 1;
-    n = static_cast<int>(min(tiles - tile, end - at));
+    n = static_cast<int>(min(static_cast<int64_t>(tiles - tile), end - at));
     at += n;
     return true;
   }
   __device__ int64_t piece() const { return at - n; }
  private:
-  bool first_;
+  int first_;
 };
 
 // The next e4m3 part of two values, packed low first; what is left of them
@@ -139,7 +150,7 @@ __device__ __forceinline__ float half_of(uint32_t two, int i, f16) {
 
 // One row group's queries into shared memory, K-major. A warp takes every
 // fourth row.
-template <class TQ, int kParts, int N>
+template <class TQ, int kParts, int N, class Misc>
 __device__ __forceinline__ void load_queries(const DecodeParams& p, int b, int g0, int n_rows, uint8_t* q_smem,
                                              Misc& mi, float factor) {
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -221,6 +232,8 @@ __global__ void __launch_bounds__(kThreads, 1)
   constexpr bool kFp8 = kParts > 1;
   extern __shared__ uint8_t raw[];
   uint8_t* smem = raw + ((1024 - (smem_u32(raw) & 1023)) & 1023);
+  using Misc = MiscOf<L::kSlots, L::kRopeSlots, N>;
+  static_assert(sizeof(Misc) <= L::kMisc, "fits");
   Misc& mi = *reinterpret_cast<Misc*>(smem + L::kMiscAt);
   const uint32_t base = smem_u32(smem);
   const int tid = threadIdx.x, warp = __shfl_sync(0xffffffffu, tid >> 5, 0), lane = tid & 31;
@@ -243,7 +256,8 @@ __global__ void __launch_bounds__(kThreads, 1)
     mbar_init(smem_u32(&mi.p_full), 4);
     mbar_init(smem_u32(&mi.pv_done), 1);
     mbar_init(smem_u32(&mi.q_full), 4);
-    mi.stop = 0;
+    mi.stop = mi.never = 0;
+    mbar_init(smem_u32(&mi.end), 1);
     mbar_fence_init();
     tma_prefetch(&map);
     tma_prefetch(&rope_map);
@@ -257,7 +271,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   __syncthreads();
   tmem_fence_after();
   const uint32_t tmem = mi.tmem;
-  volatile int* stop = &mi.stop;
+  const uint32_t stop = smem_u32(&mi.stop);
   constexpr int kFmt = kFp8 ? 0 : (sizeof(TQ) == 2 && std::is_same<TQ, bf16>::value ? 1 : 0);
   constexpr uint32_t kIdescS = umma_idesc(kFmt, 0, 0, 64, N);
   constexpr uint32_t kIdescO = umma_idesc(kFmt, 1, 1, 128, N);
@@ -266,7 +280,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     // ---- loads ----
     Items it(p, share);
     int slot = 0, phase = 0, rslot = 0, rphase = 0;
-    int64_t t = 0;
+    uint32_t t = 0;
     int bad = 0;
     bool alive = true;
     const uint32_t full = smem_u32(&mi.full[0]), empty = smem_u32(&mi.empty[0]);
@@ -277,7 +291,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       if (it.len == 0) continue;
       const int32_t* table = p.bt + static_cast<int64_t>(it.b) * p.bt_stride;
       for (int i = 0; i < it.n && alive; ++i, ++t) {
-        const int j0 = static_cast<int>(it.tile + i) * kDecodeTile;
+        const int j0 = (it.tile + i) * kDecodeTile;
         // lane s < segs looks up the page of box s
         const int j = j0 + lane * box_rows;
         const bool in = lane < segs && j < it.len;
@@ -305,7 +319,8 @@ __global__ void __launch_bounds__(kThreads, 1)
         const uint32_t bytes = static_cast<uint32_t>(n_boxes * box_rows * 128);
 #pragma unroll 1
         for (int m = 0; m < 4; ++m) {
-          alive = mbar_wait_warp(empty + 8 * slot, phase ^ 1, stop);
+          mbar_wait(empty + 8 * slot, phase ^ 1, stop);
+          alive = !stopped(stop);
           if (!alive) break;
           const uint32_t dst = base + L::kSlotAt + slot * L::kSlot;
           if (elect_one()) mbar_expect(full + 8 * slot, bytes * L::kPieces);
@@ -323,7 +338,8 @@ __global__ void __launch_bounds__(kThreads, 1)
           if (++slot == L::kSlots) { slot = 0; phase ^= 1; }
         }
         if (!alive) break;
-        alive = mbar_wait_warp(rope_empty + 8 * rslot, rphase ^ 1, stop);
+        mbar_wait(rope_empty + 8 * rslot, rphase ^ 1, stop);
+        alive = !stopped(stop);
         if (!alive) break;
         if (elect_one()) mbar_expect(rope_full + 8 * rslot, bytes);
         for (int s = 0; s < n_boxes; ++s) {
@@ -336,14 +352,12 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
     }
     set_flag(p.err, bad);
-    // copies that nobody will use any more still have to land before the CTA ends
-    if (!alive && lane == 0) {
-      int never = 0;
-      for (int i = 0; i < L::kSlots; ++i) mbar_wait(smem_u32(&mi.full[i]), (i < slot ? phase : phase ^ 1), &never);
-      for (int i = 0; i < L::kRopeSlots; ++i)
-        mbar_wait(smem_u32(&mi.rope_full[i]), (i < rslot ? rphase : rphase ^ 1), &never);
+    // after a timeout, copies in flight land before the CTA ends (`never` is not set: these waits run on)
+    if (!alive) {
+      const uint32_t never = smem_u32(&mi.never);
+      for (int i = 0; i < L::kSlots; ++i) mbar_wait(full + 8 * i, i < slot ? phase : phase ^ 1, never);
+      for (int i = 0; i < L::kRopeSlots; ++i) mbar_wait(rope_full + 8 * i, i < rslot ? rphase : rphase ^ 1, never);
     }
-    __syncwarp();
   } else if (warp == 5) {
     // ---- products ----
     Items qi(p, share), vi(p, share);
@@ -356,114 +370,98 @@ __global__ void __launch_bounds__(kThreads, 1)
     const uint32_t rope_full = smem_u32(&mi.rope_full[0]), rope_empty = smem_u32(&mi.rope_empty[0]);
     const uint32_t s_full = smem_u32(&mi.s_full[0]), s_free = smem_u32(&mi.s_free[0]);
     bool q_more = advance(qi), v_more = advance(vi);
-    int q_tile = 0, q_part = 0, v_tile = 0;     // within the items
-    int q_item = 0;                             // items begun, for the queries' barrier
+    int q_tile = 0, v_tile = 0;                 // within the items
+    uint32_t q_item = 0;                        // items begun, for the queries' barrier
     uint32_t qt = 0, vt = 0;                    // tiles issued
     int qslot = 0, qphase = 0, rslot = 0, rphase = 0, vslot = 0;
-    uint64_t t0 = 0;
-    int idle = 0;
-    bool alive = true;
-    // whichever product has its operands: O of a tile once its weights are there, parts of S up to two tiles ahead
-    while (alive && (q_more || v_more)) {
-      bool progress = false;
-      if (v_more && vt != qt && mbar_test_warp(smem_u32(&mi.p_full), vt & 1)) {
+    const uint32_t p_full = smem_u32(&mi.p_full);
+    // O of the oldest tile
+    auto values = [&]() {
+      tmem_fence_after();
+      const uint32_t leader = elect_one();
+      const uint64_t pa = umma_desc(base + L::kPAt, L::kPiece, 1024);
+      const bool first = v_tile == 0;
+#pragma unroll
+      for (int m = 0; m < 4; ++m) {
+        const uint64_t va = umma_desc(base + L::kSlotAt + vslot * L::kSlot, L::kPiece, 1024);
+        const uint32_t d = tmem + (2 + m) * N;
+#pragma unroll
+        for (int k = 0; k < (kFp8 ? 2 : 4); ++k) {
+          const uint32_t step = k * (kFp8 ? 32 : 16) * 8;  // rows of 128 bytes, in units of 16
+          umma_ss<kFp8>(leader, d, va + step, pa + step, kIdescO, !first || k > 0);
+          if constexpr (kFp8) umma_ss<kFp8>(leader, d, va + step, pa + step + L::kPiece / 16, kIdescO, true);
+        }
+        umma_commit(leader, empty + 8 * vslot);
+        if (++vslot == L::kSlots) vslot = 0;
+      }
+      umma_commit(leader, smem_u32(&mi.pv_done));
+      ++vt;
+      if (++v_tile == vi.n) {
+        v_tile = 0;
+        v_more = advance(vi);
+      }
+    };
+    // Parts of S of a tile as they arrive; O of the tile before it as soon as its weights are there.
+    while (q_more) {
+      const uint32_t buf = qt & 1, d = tmem + buf * N;
+      if (qt >= 2) mbar_wait(s_free + 8 * buf, ((qt >> 1) + 1) & 1, stop);
+      if (q_tile == 0) {
+        // these queries come after the last product with the ones before
+        while (vt != qt && mbar_wait_either(p_full, vt & 1, smem_u32(&mi.q_full), q_item & 1, stop)) values();
+        mbar_wait(smem_u32(&mi.q_full), q_item & 1, stop);
+        ++q_item;
+      }
+#pragma unroll 1
+      for (int part = 0; part < 4; ++part) {
+        if (vt != qt && mbar_wait_either(p_full, vt & 1, full + 8 * qslot, qphase, stop)) values();
+        mbar_wait(full + 8 * qslot, qphase, stop);
         tmem_fence_after();
-        const bool first = v_tile == 0;
+        const uint32_t leader = elect_one();
 #pragma unroll
-        for (int m = 0; m < 4; ++m) {
-          if (elect_one()) {
-            const uint64_t va = umma_desc(base + L::kSlotAt + vslot * L::kSlot, L::kPiece, 1024);
-            const uint64_t pa = umma_desc(base + L::kPAt, L::kPiece, 1024);
-            const uint32_t d = tmem + (2 + m) * N;
+        for (int c = 0; c < L::kPieces; ++c) {
+          const uint64_t ka = umma_desc(base + L::kSlotAt + qslot * L::kSlot + c * L::kPiece, 16, 1024);
+          const uint64_t qa = umma_desc(base + L::kQAt + (part * L::kPieces + c) * (N * 128), 16, 1024);
 #pragma unroll
-            for (int k = 0; k < (kFp8 ? 2 : 4); ++k) {
-              const uint32_t step = k * (kFp8 ? 32 : 16) * 8;  // rows of 128 bytes, in units of 16
-              umma_ss<kFp8>(d, va + step, pa + step, kIdescO, !first || k > 0);
-              if constexpr (kFp8) umma_ss<kFp8>(d, va + step, pa + step + L::kPiece / 16, kIdescO, true);
-            }
-            umma_commit(empty + 8 * vslot);
-            if (m == 3) umma_commit(smem_u32(&mi.pv_done));
-          }
-          __syncwarp();
-          if (++vslot == L::kSlots) vslot = 0;
+          for (int k = 0; k < 4; ++k)  // 32 bytes of K each
+#pragma unroll
+            for (int x = 0; x < kParts; ++x)
+              umma_ss<kFp8>(leader, d, ka + 2 * k, qa + 2 * k + x * (5 * N * 8), kIdescS,
+                            part > 0 || c > 0 || k > 0 || x > 0);
         }
-        ++vt;
-        if (++v_tile == vi.n) {
-          v_tile = 0;
-          v_more = advance(vi);
-        }
-        progress = true;
+        if (++qslot == L::kSlots) { qslot = 0; qphase ^= 1; }
       }
-      if (q_more && qt - vt < 2) {
-        const uint32_t buf = qt & 1;
-        bool ready = true;
-        if (q_part == 0) {
-          if (qt >= 2) ready = mbar_test_warp(s_free + 8 * buf, ((qt >> 1) + 1) & 1);
-          if (ready && q_tile == 0) ready = mbar_test_warp(smem_u32(&mi.q_full), q_item & 1);
-        }
-        if (ready)
-          ready = q_part < 4 ? mbar_test_warp(full + 8 * qslot, qphase) : mbar_test_warp(rope_full + 8 * rslot, rphase);
-        if (ready) {
-          tmem_fence_after();
-          const uint32_t d = tmem + buf * N;
-          if (q_part < 4) {
-            if (elect_one()) {
+      if (vt != qt && mbar_wait_either(p_full, vt & 1, rope_full + 8 * rslot, rphase, stop)) values();
+      mbar_wait(rope_full + 8 * rslot, rphase, stop);
+      tmem_fence_after();
+      const uint32_t leader = elect_one();
+      const uint64_t ka = umma_desc(base + L::kRopeAt + rslot * L::kPiece, 16, 1024);
+      const uint64_t qa = umma_desc(base + L::kQAt + 4 * L::kPieces * (N * 128), 16, 1024);
 #pragma unroll
-              for (int c = 0; c < L::kPieces; ++c) {
-                const uint64_t ka = umma_desc(base + L::kSlotAt + qslot * L::kSlot + c * L::kPiece, 16, 1024);
-                const uint64_t qa = umma_desc(base + L::kQAt + (q_part * L::kPieces + c) * (N * 128), 16, 1024);
+      for (int k = 0; k < (kFp8 ? 2 : 4); ++k)
 #pragma unroll
-                for (int k = 0; k < 4; ++k)  // 32 bytes of K each
-#pragma unroll
-                  for (int x = 0; x < kParts; ++x)
-                    umma_ss<kFp8>(d, ka + 2 * k, qa + 2 * k + x * (5 * N * 8), kIdescS,
-                                  q_part > 0 || c > 0 || k > 0 || x > 0);
-              }
-            }
-            __syncwarp();
-            ++q_part;
-            if (++qslot == L::kSlots) { qslot = 0; qphase ^= 1; }
-          } else {
-            if (elect_one()) {
-              const uint64_t ka = umma_desc(base + L::kRopeAt + rslot * L::kPiece, 16, 1024);
-              const uint64_t qa = umma_desc(base + L::kQAt + 4 * L::kPieces * (N * 128), 16, 1024);
-#pragma unroll
-              for (int k = 0; k < (kFp8 ? 2 : 4); ++k)
-#pragma unroll
-                for (int x = 0; x < kParts; ++x)
-                  umma_ss<kFp8>(d, ka + 2 * k, qa + 2 * k + x * (5 * N * 8), kIdescS, true);
-              umma_commit(rope_empty + 8 * rslot);
-              umma_commit(s_full + 8 * buf);
-            }
-            __syncwarp();
-            if (++rslot == L::kRopeSlots) { rslot = 0; rphase ^= 1; }
-            q_part = 0;
-            ++qt;
-            if (q_tile == 0) ++q_item;
-            if (++q_tile == qi.n) {
-              q_tile = 0;
-              q_more = advance(qi);
-            }
-          }
-          progress = true;
-        }
+        for (int x = 0; x < kParts; ++x)
+          umma_ss<kFp8>(leader, d, ka + 2 * k, qa + 2 * k + x * (5 * N * 8), kIdescS, true);
+      umma_commit(leader, rope_empty + 8 * rslot);
+      umma_commit(leader, s_full + 8 * buf);
+      if (++rslot == L::kRopeSlots) { rslot = 0; rphase ^= 1; }
+      ++qt;
+      if (++q_tile == qi.n) {
+        q_tile = 0;
+        q_more = advance(qi);
       }
-      if (progress) {
-        idle = 0;
-        t0 = 0;
-      } else if (++idle >= 256) {
-        idle = 0;
-        const uint64_t now = now_ns();
-        if (t0 == 0) t0 = now;
-        if (now - t0 > kWaitNs) *stop = 1;
-        alive = __all_sync(0xffffffffu, *stop == 0) != 0;
+      // at most two tiles' scores are ahead of the weights
+      if (qt - vt == 2) {
+        mbar_wait(p_full, vt & 1, stop);
+        values();
       }
     }
-    if (!alive && vt > 0) {  // what was issued ends before the CTA does
-      int never = 0;
-      mbar_wait(smem_u32(&mi.pv_done), static_cast<int>((vt - 1) & 1), &never);
+    while (v_more) {
+      mbar_wait(p_full, vt & 1, stop);
+      values();
     }
-    __syncwarp();
+    // everything issued ends before the tensor memory is given back
+    umma_commit(elect_one(), smem_u32(&mi.end));
+    mbar_wait(smem_u32(&mi.end), 0, smem_u32(&mi.never));
   } else {
     // ---- softmax and epilogue ----
     Items it(p, share);
@@ -474,11 +472,14 @@ __global__ void __launch_bounds__(kThreads, 1)
     const float factor = p.sm_scale * kLog2e * kv_scale;
     constexpr float kSlack = kFp8 ? 2.5f : 8.0f;     // weights up to 2^(kBase + kSlack) <= 448
     constexpr float kBase = kFp8 ? 6.0f : 0.0f;
-    const int token = warp * 16 + (lane & 15);       // M = 64: 16 rows in each quarter of the lanes
     const uint32_t lanes = static_cast<uint32_t>(warp * 32) << 16;
+    // Scores (M = 64: 16 rows in each quarter of the lanes) are read so that this thread has entries tok and tok + 8
+    // of the tile, and of every 8 columns 2 c and 2 c + 1.
+    constexpr int kG = N / 8;
+    const int c = lane & 3, tok = warp * 16 + (lane >> 2);
     JoinNote note{-1, 0, 0, 0};
-    int64_t t = 0;
-    bool alive = true;
+    uint32_t t = 0;                 // tiles of the share
+    uint32_t slot0 = 0, phase0 = 0; // slot of the tile's first part, its phase
     bool more = it.next();
     // queries of the first request that has any keys
     auto queries = [&](const Items& x) {
@@ -487,102 +488,100 @@ __global__ void __launch_bounds__(kThreads, 1)
       __syncwarp();
       if (lane == 0) mbar_arrive(smem_u32(&mi.q_full));
     };
-    if (tid < N) mi.step[tid] = (g0 + tid) / p.H;
+    const int step0 = g0 / p.H;  // the group's first new token
+    if (tid < N) mi.step[tid] = static_cast<uint8_t>((g0 + tid) / p.H - step0);
+    // where row h of the group is in a request's output
+    auto out_at = [&](int h) {
+      const int step = step0 + mi.step[h];
+      return step * p.ot_stride + (g0 + h - step * p.H) * p.oh_stride;
+    };
     bool loaded = false;  // whether the queries of `it` are in place
-    while (alive && more) {
+    while (more) {
       if (it.len > 0 && !loaded) queries(it);
       Items ahead = it;
       const bool more_ahead = ahead.next();
-      float l[N];
-#pragma unroll
-      for (int h = 0; h < N; ++h) l[h] = 0.0f;
       const int n = it.len > 0 ? it.n : 0;
-      named_sync<kSoft>(1);  // everybody is done with the last request's references
-      if (tid < N) mi.ref[tid] = -INFINITY;
-      named_sync<kSoft>(1);  // and the queries' factors are there
+      named_sync<kSoft>(1);  // the queries' factors are there, and everybody is done with the last request's sums
+      float ref[2 * kG], l[2 * kG], f[2 * kG];  // of columns 8 g + 2 c and the next
+#pragma unroll
+      for (int i = 0; i < 2 * kG; ++i) {
+        ref[i] = -INFINITY;
+        l[i] = 0.0f;
+        f[i] = kFp8 ? mi.factor[(i >> 1) * 8 + 2 * c + (i & 1)] : factor;
+      }
       for (int i = 0; i < n; ++i, ++t) {
-        const int buf = static_cast<int>(t & 1);
-        if (!mbar_wait(smem_u32(&mi.s_full[buf]), static_cast<int>(t >> 1) & 1, stop)) alive = false;
-        const int64_t j0 = (it.tile + i) * kDecodeTile;
+        const uint32_t buf = t & 1;
+        const int j0 = (it.tile + i) * kDecodeTile;
         // the loading warp's note of the tile is ordered by its first slot's barrier
-        if (alive && !mbar_wait(smem_u32(&mi.full[static_cast<int>((4 * t) % L::kSlots)]),
-                                static_cast<int>((4 * t) / L::kSlots) & 1, stop))
-          alive = false;
-        if (named_any<kSoft>(2, !alive)) {
-          alive = false;
-          break;
-        }
-        tmem_fence_after();
-        const uint64_t mask = mi.mask[t & 7];
+        mbar_wait(smem_u32(&mi.full[0]) + 8 * slot0, phase0, stop);
+        mbar_wait(smem_u32(&mi.s_full[0]) + 8 * buf, t >> 1 & 1, stop);
         __syncwarp();
-        uint32_t raw_s[N];
-        if constexpr (N == 16) tmem_ld16(tmem + buf * N + lanes, raw_s);
-        else if constexpr (N == 32) tmem_ld32(tmem + buf * N + lanes, raw_s);
-        else {
-          tmem_ld32(tmem + buf * N + lanes, raw_s);
-          tmem_ld32(tmem + buf * N + 32 + lanes, raw_s + 32);
-        }
+        tmem_fence_after();
+        uint32_t raw_s[4 * kG];
+        tmem_ld_rows16(tmem + buf * N + lanes, raw_s);
+        const uint64_t mask = mi.mask[t & 7] >> tok;
+        const bool in0 = mask & 1, in1 = mask >> 8 & 1;
         tmem_wait_ld();
-        tmem_pin<N>(raw_s);
+        tmem_pin<4 * kG>(raw_s);
         tmem_fence_before();
         __syncwarp();
-        if (lane == 0) mbar_arrive(smem_u32(&mi.s_free[buf]));
-        float s[N];
-        const bool there = lane < 16 && (mask >> token & 1) != 0;
-        const int j = static_cast<int>(j0) + token;
-        const bool edge = j0 + kDecodeTile > it.full_len - p.q_len + 1;  // some row does not see the whole tile
+        if (lane == 0) mbar_arrive(smem_u32(&mi.s_free[0]) + 8 * buf);
+        float* s = reinterpret_cast<float*>(raw_s);
+        const bool all = __all_sync(0xffffffffu, in0 && in1);
+        // some row does not see the whole tile for its place among the new tokens
+        const bool edge = p.q_len > 1 && j0 + kDecodeTile > it.full_len - p.q_len + 1;
+        if (!all || edge) {
+          const int first = it.full_len - p.q_len + 1 + step0 - j0 - tok;  // of row 0's token: entries tok + k < first are seen
+#pragma unroll
+          for (int g = 0; g < kG; ++g)
+#pragma unroll
+            for (int k = 0; k < 4; ++k) {
+              const int step = edge ? mi.step[8 * g + 2 * c + (k & 1)] : 0;
+              const bool seen = (k < 2 ? in0 : in1) && (!edge || (k < 2 ? 0 : 8) < first + step);
+              // an unseen score is -inf whatever its entry holds (factors are not negative; 0 makes a NaN, cleared below)
+              if (!seen) s[4 * g + k] = -INFINITY;
+            }
+        }
+        // scores less the references; -inf less -inf only where nothing was seen yet, which raises nothing
+        float x[4 * kG];
         float over = -INFINITY;
 #pragma unroll
-        for (int h = 0; h < N; h += 4) {
-          const float4 f = kFp8 ? *reinterpret_cast<const float4*>(&mi.factor[h]) : make_float4(factor, factor, factor, factor);
-          const float4 r = *reinterpret_cast<const float4*>(&mi.ref[h]);
-          s[h] = there ? __uint_as_float(raw_s[h]) * f.x : -INFINITY;
-          s[h + 1] = there ? __uint_as_float(raw_s[h + 1]) * f.y : -INFINITY;
-          s[h + 2] = there ? __uint_as_float(raw_s[h + 2]) * f.z : -INFINITY;
-          s[h + 3] = there ? __uint_as_float(raw_s[h + 3]) * f.w : -INFINITY;
-          if (!edge) {
-            over = fmaxf(over, fmaxf(fmaxf(s[h] - r.x, s[h + 1] - r.y), fmaxf(s[h + 2] - r.z, s[h + 3] - r.w)));
-          }
-        }
-        if (edge) {
+        for (int g = 0; g < kG; ++g)
 #pragma unroll
-          for (int h = 0; h < N; ++h) {
-            if (j >= it.full_len - p.q_len + 1 + mi.step[h]) s[h] = -INFINITY;
-            // (-inf) - (-inf) is no excess
-            if (s[h] != -INFINITY) over = fmaxf(over, s[h] - mi.ref[h]);
+          for (int k = 0; k < 4; ++k) {
+            const float y = s[4 * g + k] == -INFINITY ? -INFINITY : fmaf(s[4 * g + k], f[2 * g + (k & 1)], -ref[2 * g + (k & 1)]);
+            x[4 * g + k] = y;
+            over = fmaxf(over, y);
           }
-        } else if (!there) {
-          over = -INFINITY;
-        }
         const bool raise = named_any<kSoft>(2, over > kBase + kSlack);
         if (raise) {
           // maximum of every row over the tile's entries
           float* part = reinterpret_cast<float*>(smem + L::kPAt);  // free once the last tile's product is done
-          if (t > 0 && !mbar_wait(smem_u32(&mi.pv_done), static_cast<int>(t - 1) & 1, stop)) alive = false;
+          if (t > 0) mbar_wait(smem_u32(&mi.pv_done), (t - 1) & 1, stop);
+          __syncwarp();
           tmem_fence_after();
 #pragma unroll
-          for (int h = 0; h < N; ++h) {
-            float top = s[h];
+          for (int k = 0; k < 2 * kG; ++k) {
+            const float a = s[4 * (k >> 1) + (k & 1)], b = s[4 * (k >> 1) + (k & 1) + 2];
+            float top = fmaxf(a == -INFINITY ? a : a * f[k], b == -INFINITY ? b : b * f[k]);
 #pragma unroll
-            for (int o = 8; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
-            if (lane == 0) part[warp * N + h] = top;
+            for (int o = 16; o >= 4; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
+            if (lane < 4) part[warp * N + (k >> 1) * 8 + 2 * c + (k & 1)] = top;
           }
           named_sync<kSoft>(1);
-          if (tid < N) {
-            const float top = fmaxf(fmaxf(part[tid], part[N + tid]), fmaxf(part[2 * N + tid], part[3 * N + tid]));
-            const float old = mi.ref[tid];
-            float next = old, a = 1.0f;
-            if (top - kBase > old) {  // where the tile raises it at all
-              next = top - kBase;
-              a = old == -INFINITY ? 0.0f : ex2(old - next);
+#pragma unroll
+          for (int k = 0; k < 2 * kG; ++k) {
+            const int col = (k >> 1) * 8 + 2 * c + (k & 1);
+            const float top = fmaxf(fmaxf(part[col], part[N + col]), fmaxf(part[2 * N + col], part[3 * N + col])) - kBase;
+            float a = 1.0f;
+            if (top > ref[k]) {  // where the tile raises it at all
+              a = ref[k] == -INFINITY ? 0.0f : ex2(ref[k] - top);
+              ref[k] = top;
+              l[k] *= a;
             }
-            mi.ref[tid] = next;
-            mi.alpha[tid] = a;
+            if (tid < 4) mi.alpha[col] = a;
           }
-          named_sync<kSoft>(1);
-#pragma unroll
-          for (int h = 0; h < N; ++h) l[h] *= mi.alpha[h];
-          __syncwarp();
+          named_sync<kSoft>(1);  // (also: the maxima's place is where the weights go)
           if (i > 0) {
 #pragma unroll 1
             for (int m = 0; m < 4; ++m) {
@@ -601,126 +600,106 @@ __global__ void __launch_bounds__(kThreads, 1)
             tmem_wait_st();
             tmem_fence_before();
           }
+#pragma unroll
+          for (int g = 0; g < kG; ++g)
+#pragma unroll
+            for (int k = 0; k < 4; ++k)
+              x[4 * g + k] = s[4 * g + k] == -INFINITY ? -INFINITY : fmaf(s[4 * g + k], f[2 * g + (k & 1)], -ref[2 * g + (k & 1)]);
         }
         // weights
 #pragma unroll
-        for (int h = 0; h < N; h += 4) {
-          const float4 r = *reinterpret_cast<const float4*>(&mi.ref[h]);
-          const float rr[4] = {r.x, r.y, r.z, r.w};
+        for (int g = 0; g < kG; ++g)
 #pragma unroll
           for (int k = 0; k < 4; ++k) {
-            s[h + k] = s[h + k] == -INFINITY ? 0.0f : ex2(s[h + k] - rr[k]);
-            l[h + k] += s[h + k];
+            x[4 * g + k] = ex2(x[4 * g + k]);
+            l[2 * g + (k & 1)] += x[4 * g + k];
           }
-        }
         // the last tile's product has read its weights
-        if (t > 0 && !mbar_wait(smem_u32(&mi.pv_done), static_cast<int>(t - 1) & 1, stop)) alive = false;
+        if (t > 0) mbar_wait(smem_u32(&mi.pv_done), (t - 1) & 1, stop);
         // values past the end of the request may be anything: their weights are 0, so must they be
-        const int64_t valid = it.len - j0;
-        if (valid < kDecodeTile) {
-          const int first = static_cast<int>(valid);
-          for (int m = 0; m < 4; ++m) {
-            uint8_t* at = smem + L::kSlotAt + static_cast<int>((4 * t + m) % L::kSlots) * L::kSlot;
-            for (int x = tid; x < (kDecodeTile - first) * 8 * L::kPieces; x += kSoft) {
-              const int piece = x / ((kDecodeTile - first) * 8), y = x % ((kDecodeTile - first) * 8);
-              *reinterpret_cast<uint4*>(at + piece * L::kPiece + (first + y / 8) * 128 + (y % 8) * 16) =
-                  make_uint4(0, 0, 0, 0);
+        const int first = it.len - j0;
+        if (first < kDecodeTile) {
+          for (uint32_t m = 0; m < 4; ++m) {
+            const uint32_t sl = slot0 + m < L::kSlots ? slot0 + m : slot0 + m - L::kSlots;
+            uint4* at = reinterpret_cast<uint4*>(smem + L::kSlotAt + sl * L::kSlot + first * 128);
+            for (int y = tid; y < (kDecodeTile - first) * 8; y += kSoft) {
+#pragma unroll
+              for (int q = 0; q < L::kPieces; ++q) at[q * (L::kPiece / 16) + y] = make_uint4(0, 0, 0, 0);
             }
           }
         }
-        if (raise) named_sync<kSoft>(1);  // the maxima's place is where the weights go
-        if (lane < 16) {
-          uint8_t* row = smem + L::kPAt + token * 128;
-          if constexpr (!kFp8) {
 #pragma unroll
-            for (int u = 0; u < N / 8; ++u)
-              *reinterpret_cast<uint4*>(row + ((u ^ (token & 7)) << 4)) =
-                  make_uint4(pack2<TQ>(s[8 * u], s[8 * u + 1]), pack2<TQ>(s[8 * u + 2], s[8 * u + 3]),
-                             pack2<TQ>(s[8 * u + 4], s[8 * u + 5]), pack2<TQ>(s[8 * u + 6], s[8 * u + 7]));
-          } else {
+        for (int h = 0; h < 2; ++h) {
+          uint8_t* row = smem + L::kPAt + (tok + 8 * h) * 128;
 #pragma unroll
-            for (int u = 0; u < N / 16; ++u) {
-              const int at = (u ^ (token & 7)) << 4;
+          for (int g = 0; g < kG; ++g) {
+            float a = x[4 * g + 2 * h], b = x[4 * g + 2 * h + 1];
+            if constexpr (!kFp8) {
+              *reinterpret_cast<uint32_t*>(row + ((g ^ (tok & 7)) << 4) + 4 * c) = pack2<TQ>(a, b);
+            } else {
+              uint8_t* at = row + (((g >> 1) ^ (tok & 7)) << 4) + (g & 1) * 8 + 2 * c;
 #pragma unroll
-              for (int c = 0; c < 2; ++c) {
-                uint32_t y[8];
-#pragma unroll
-                for (int k = 0; k < 8; ++k) y[k] = part2(s[16 * u + 2 * k], s[16 * u + 2 * k + 1]);
-                *reinterpret_cast<uint4*>(row + c * L::kPiece + at) =
-                    make_uint4(y[0] | y[1] << 16, y[2] | y[3] << 16, y[4] | y[5] << 16, y[6] | y[7] << 16);
-              }
+              for (int q = 0; q < 2; ++q) *reinterpret_cast<uint16_t*>(at + q * L::kPiece) = static_cast<uint16_t>(part2(a, b));
             }
           }
         }
         fence_async_smem();
         __syncwarp();
         if (lane == 0) mbar_arrive(smem_u32(&mi.p_full));
-      }
-      if (!alive) break;
-
-      // sums of every row over the lanes, then over the warps
-      const bool whole = it.tile == 0 && it.n == it.tiles;
-      float* sums = mi.alpha;
-      named_sync<kSoft>(1);
-      if (tid < N) sums[tid] = 0.0f;
-      named_sync<kSoft>(1);
-#pragma unroll
-      for (int h = 0; h < N; ++h) {
-        float x = l[h];
-#pragma unroll
-        for (int o = 8; o > 0; o >>= 1) x += __shfl_xor_sync(0xffffffffu, x, o);
-        l[h] = x;
-      }
-      for (int w = 0; w < 4; ++w) {  // in a fixed order
-        if (warp == w && lane == 0) {
-#pragma unroll
-          for (int h = 0; h < N; ++h) sums[h] += l[h];
+        slot0 += 4;
+        if (slot0 >= L::kSlots) {
+          slot0 -= L::kSlots;
+          phase0 ^= 1;
         }
-        named_sync<kSoft>(1);
+      }
+
+      // sums of every row over the lanes, then over the warps in their order
+      const bool whole = it.tile == 0 && it.n == it.tiles;
+#pragma unroll
+      for (int k = 0; k < 2 * kG; ++k) {
+#pragma unroll
+        for (int o = 16; o >= 4; o >>= 1) l[k] += __shfl_xor_sync(0xffffffffu, l[k], o);
+        if (lane < 4) mi.warp_sums[warp * N + (k >> 1) * 8 + 2 * c + (k & 1)] = l[k];
+      }
+      named_sync<kSoft>(1);
+      auto sum_of = [&](int h) {
+        return (mi.warp_sums[h] + mi.warp_sums[N + h]) + (mi.warp_sums[2 * N + h] + mi.warp_sums[3 * N + h]);
+      };
+      if (tid < N) mi.inv[tid] = sum_of(tid) > 0.0f ? kv_scale / sum_of(tid) : 0.0f;
+      float* slot = p.ws.slots + (static_cast<int64_t>(blockIdx.x) * 2 + (it.tile == 0 ? 1 : 0)) * p.slot_floats;
+      if (tid < 4) {  // these four have all references
+#pragma unroll
+        for (int k = 0; k < 2 * kG; ++k) {
+          const int h = (k >> 1) * 8 + 2 * c + (k & 1);
+          if (h < n_rows) {
+            const float sum = sum_of(h);
+            if (!whole) *reinterpret_cast<float2*>(slot + p.rows_per_group * kLatent + 2 * h) = make_float2(ref[k], sum);
+            else if (p.lse != nullptr)
+              p.lse[static_cast<int64_t>(it.b) * rows + g0 + h] = sum > 0.0f ? (ref[k] + log2f(sum)) * kLn2 : -INFINITY;
+          }
+        }
       }
       // the next request's queries, while the last product runs
       loaded = false;
-      float my_ref = 0.0f, my_sum = 0.0f;
-      if (tid < N) {
-        my_ref = mi.ref[tid];
-        my_sum = sums[tid];
-      }
       if (more_ahead && ahead.len > 0) {
         queries(ahead);
         loaded = true;
       }
-      float* slot = p.ws.slots + (static_cast<int64_t>(blockIdx.x) * 2 + (it.tile == 0 ? 1 : 0)) * p.slot_floats;
       if (!whole && it.tile == 0 && tid == 0) {
         note.item = it.b;
         note.parts = unit_of(it.piece() + it.tiles - 1, share.total, share.units) - unit + 1;
       }
-      if (tid < n_rows) {
-        const int rr = g0 + tid;
-        if (whole) {
-          if (p.lse != nullptr)
-            p.lse[static_cast<int64_t>(it.b) * rows + rr] =
-                my_sum > 0.0f ? (my_ref + log2f(my_sum)) * kLn2 : -INFINITY;
-        } else {
-          float* ml = slot + p.rows_per_group * kLatent + 2 * tid;
-          ml[0] = my_ref;
-          ml[1] = my_sum;
-        }
-      }
-      if (n > 0) {
-        if (!mbar_wait(smem_u32(&mi.pv_done), static_cast<int>(t - 1) & 1, stop)) alive = false;
-        if (named_any<kSoft>(2, !alive)) {
-          alive = false;
-          break;
-        }
-        tmem_fence_after();
-      }
-      __syncwarp();
+      if (n > 0) mbar_wait(smem_u32(&mi.pv_done), (t - 1) & 1, stop);
+      named_sync<kSoft>(1);  // the sums
+      tmem_fence_after();
+      TQ* out = static_cast<TQ*>(p.out) + it.b * p.or_stride;
 #pragma unroll 1
       for (int m = 0; m < 4; ++m) {
         const int d = m * 128 + warp * 32 + lane;
 #pragma unroll 1
-        for (int h0 = 0; h0 < N; h0 += 16) {
+        for (int h0 = 0; h0 < N && h0 < n_rows; h0 += 16) {
           uint32_t o[16];
+          __syncwarp();
           if (n > 0) {
             tmem_ld16(tmem + (2 + m) * N + h0 + lanes, o);
             tmem_wait_ld();
@@ -732,22 +711,16 @@ __global__ void __launch_bounds__(kThreads, 1)
           if (whole) {
 #pragma unroll
             for (int k = 0; k < 16; k += 2) {
-              // even lanes write row k, odd lanes row k + 1, two neighbours' values each
-              const float la = sums[h0 + k], lb = sums[h0 + k + 1];
-              const float a = __uint_as_float(o[k]) * (la > 0.0f ? kv_scale / la : 0.0f);
-              const float b = __uint_as_float(o[k + 1]) * (lb > 0.0f ? kv_scale / lb : 0.0f);
-              auto out_at = [&](int h) {
-                const int rr = g0 + h;
-                return static_cast<TQ*>(p.out) + it.b * p.or_stride + (rr / p.H) * p.ot_stride + (rr % p.H) * p.oh_stride;
-              };
+              const float a = __uint_as_float(o[k]) * mi.inv[h0 + k], b = __uint_as_float(o[k + 1]) * mi.inv[h0 + k + 1];
               if (p.out_pairs) {
+                // even lanes write row k, odd lanes row k + 1, two neighbours' values each
                 const float other = __shfl_xor_sync(0xffffffffu, lane & 1 ? a : b, 1);
                 const int h = h0 + k + (lane & 1);
                 if (h < n_rows)
-                  *reinterpret_cast<uint32_t*>(out_at(h) + (d & ~1)) = lane & 1 ? pack2<TQ>(other, b) : pack2<TQ>(a, other);
+                  *reinterpret_cast<uint32_t*>(out + out_at(h) + (d & ~1)) = lane & 1 ? pack2<TQ>(other, b) : pack2<TQ>(a, other);
               } else {
-                if (h0 + k < n_rows) out_at(h0 + k)[d] = from_f<TQ>(a);
-                if (h0 + k + 1 < n_rows) out_at(h0 + k + 1)[d] = from_f<TQ>(b);
+                if (h0 + k < n_rows) out[out_at(h0 + k) + d] = from_f<TQ>(a);
+                if (h0 + k + 1 < n_rows) out[out_at(h0 + k + 1) + d] = from_f<TQ>(b);
               }
             }
           } else {
@@ -762,7 +735,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       more = more_ahead;
     }
     if (tid == 0 && p.units > 1) p.ws.notes[blockIdx.x] = note;
-    if (tid == 0 && *stop != 0) set_flag(p.err, PMG_FLAG_TIMEOUT);
+    if (stopped(stop) && tid == 0) set_flag(p.err, PMG_FLAG_TIMEOUT);
   }
   tmem_fence_before();
   __syncthreads();

@@ -50,11 +50,11 @@ static_assert(kBytes <= 232448, "fits");
 constexpr int kSlotRow = kVal;           // floats of a row in a join slot, its two sums behind all rows
 
 struct Misc {
-  uint64_t full[kSlots], empty[kSlots];
-  uint64_t q_full, q_empty, s_full[2], p_full[2], o_done[2], dirty, clean;
+  uint64_t k_full[2], v_full[2], k_empty[2], v_empty[2];  // of a block's key and value pieces, by the block's parity
+  uint64_t q_full, q_empty, s_full[2], p_full[4], o_done[2], dirty, clean, end;
   int64_t scratch[33], found[2];
   uint32_t tmem;
-  int32_t stop;
+  int32_t stop, never;
 };
 static_assert(sizeof(Misc) <= kMisc, "Misc fits");
 
@@ -143,20 +143,24 @@ __global__ void __launch_bounds__(kThreads, 1)
   const int tid = threadIdx.x, warp = __shfl_sync(0xffffffffu, tid >> 5, 0), lane = tid & 31;
 
   if (tid == 0) {
-    for (int i = 0; i < kSlots; ++i) {
-      mbar_init(smem_u32(&mi.full[i]), 1);
-      mbar_init(smem_u32(&mi.empty[i]), 1);
+    for (int i = 0; i < 2; ++i) {
+      mbar_init(smem_u32(&mi.k_full[i]), 1);
+      mbar_init(smem_u32(&mi.v_full[i]), 1);
+      mbar_init(smem_u32(&mi.k_empty[i]), 1);
+      mbar_init(smem_u32(&mi.v_empty[i]), 1);
     }
     mbar_init(smem_u32(&mi.q_full), 1);
     mbar_init(smem_u32(&mi.q_empty), 1);
     mbar_init(smem_u32(&mi.dirty), 1);
     mbar_init(smem_u32(&mi.clean), 1);
+    mbar_init(smem_u32(&mi.end), 1);
     for (int h = 0; h < 2; ++h) {
       mbar_init(smem_u32(&mi.s_full[h]), 1);
-      mbar_init(smem_u32(&mi.p_full[h]), 4);
+      mbar_init(smem_u32(&mi.p_full[2 * h]), 4);
+      mbar_init(smem_u32(&mi.p_full[2 * h + 1]), 4);
       mbar_init(smem_u32(&mi.o_done[h]), 1);
     }
-    mi.stop = 0;
+    mi.stop = mi.never = 0;
     mbar_fence_init();
     tma_prefetch(&map_q);
     tma_prefetch(&map_k);
@@ -176,7 +180,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   __syncthreads();
   tmem_fence_after();
   const uint32_t tmem = mi.tmem;  // S of the halves at columns 0 and 128, O at 256 and 384
-  volatile int* stop = &mi.stop;
+  const uint32_t stop = smem_u32(&mi.stop);
   constexpr int kFmt = std::is_same<T, bf16>::value ? 1 : 0;
   constexpr uint32_t kIdescS = umma_idesc(kFmt, 0, 0, 128, kBlock);
   constexpr uint32_t kIdescO = umma_idesc(kFmt, 0, 1, 128, kVal);
@@ -190,26 +194,24 @@ __global__ void __launch_bounds__(kThreads, 1)
         for (int i = lane; i < p.R; i += 32) bad |= prefill_req(p, i).bad;
       set_flag(p.err, bad);
       Items it(p, share);
-      int slot = 0, phase = 0, items = 0;
-      bool alive = true;
-      auto piece = [&](const CUtensorMap* map, int c, int head, int row) {
-        if (!alive) return;
-        alive = mbar_wait_warp(smem_u32(&mi.empty[0]) + 8 * slot, phase ^ 1, stop);
-        if (!alive) return;
-        if (elect_one()) {
-          const uint32_t full = smem_u32(&mi.full[0]) + 8 * slot;
-          mbar_expect(full, kPiece);
-          tma_load_3d(base + kSlotAt + slot * kPiece, map, full, c, head, row);
-        }
-        if (++slot == kSlots) {
-          slot = 0;
-          phase ^= 1;
-        }
+      uint32_t items = 0, step = 0;
+      const uint32_t k_full = smem_u32(&mi.k_full[0]), v_full = smem_u32(&mi.v_full[0]),
+                     k_empty = smem_u32(&mi.k_empty[0]), v_empty = smem_u32(&mi.v_empty[0]);
+      // Piece c of block st goes to slot (5 st + c) % 8, where piece c + 2 of block st - 2 was (or c - 3 of st - 1).
+      auto wait_old = [&](uint32_t empty, uint32_t back) {
+        if (step >= back) mbar_wait(empty + 8 * ((step - back) & 1), (step - back) >> 1 & 1, stop);
+        return !stopped(stop);
       };
+      auto piece = [&](const CUtensorMap* map, uint32_t full, uint32_t c, int x, int head, int row) {
+        if (elect_one())
+          tma_load_3d(base + kSlotAt + ((5 * step + c) & (kSlots - 1)) * kPiece, map, full + 8 * (step & 1), x, head, row);
+        __syncwarp();
+      };
+      bool alive = true;
       while (alive && it.next()) {
         if (it.keys == 0) continue;
-        alive = mbar_wait_warp(smem_u32(&mi.q_empty), (items & 1) ^ 1, stop);
-        if (!alive) break;
+        if (items > 0) mbar_wait(smem_u32(&mi.q_empty), (items - 1) & 1, stop);
+        if (stopped(stop)) break;
         ++items;
         if (elect_one()) {
           const int halves = it.act[1] > 0 ? 2 : 1;
@@ -221,154 +223,146 @@ __global__ void __launch_bounds__(kThreads, 1)
                           it.x.q0 + it.tile * kRows + h * kHalf);
         }
         __syncwarp();
-        for (int b = it.b0; b < it.b0 + it.n && alive; ++b) {
+        for (int b = it.b0; b < it.b0 + it.n; ++b, ++step) {
           const int row = it.x.k0 + b * kBlock;
-          piece(&map_k, 0, it.head, row);
-          piece(&map_k, 64, it.head, row);
-          piece(&map_pe, 0, 0, row);
-          piece(&map_v, 0, it.head, row);
-          piece(&map_v, 64, it.head, row);
+          // the pieces of a group share a barrier but come as soon as their own slots are free
+          alive = wait_old(k_empty, 2);
+          if (!alive) break;
+          if (elect_one()) mbar_expect(k_full + 8 * (step & 1), 3 * kPiece);
+          __syncwarp();
+          piece(&map_k, k_full, 0, 0, it.head, row);
+          wait_old(v_empty, 2);
+          piece(&map_k, k_full, 1, 64, it.head, row);
+          piece(&map_pe, k_full, 2, 0, 0, row);
+          alive = wait_old(k_empty, 1);
+          if (!alive) {
+            ++step;
+            break;
+          }
+          if (elect_one()) mbar_expect(v_full + 8 * (step & 1), 2 * kPiece);
+          __syncwarp();
+          piece(&map_v, v_full, 3, 0, it.head, row);
+          piece(&map_v, v_full, 4, 64, it.head, row);
         }
       }
-      if (!alive) {  // copies in flight land before the CTA ends
-        int never = 0;
-        for (int i = 0; i < kSlots; ++i) mbar_wait(smem_u32(&mi.full[i]), i < slot ? phase : phase ^ 1, &never);
-        if (items > 0) mbar_wait(smem_u32(&mi.q_full), (items - 1) & 1, &never);
+      // after a timeout, copies in flight land before the CTA ends (`never` is not set: these waits run on)
+      if (stopped(stop)) {
+        const uint32_t never = smem_u32(&mi.never);
+        for (uint32_t i = 1; i <= 2 && i <= step; ++i) {
+          mbar_wait(k_full + 8 * ((step - i) & 1), (step - i) >> 1 & 1, never);
+          mbar_wait(v_full + 8 * ((step - i) & 1), (step - i) >> 1 & 1, never);
+        }
+        if (items > 0) mbar_wait(smem_u32(&mi.q_full), (items - 1) & 1, never);
       }
-      __syncwarp();
     } else if (warp == 9) {
       // ---- products ----
       Items it(p, share);
-      bool alive = true;
-      auto wait = [&](uint32_t bar, int parity) {
-        alive = alive && mbar_wait_warp(bar, parity, stop);
-        return alive;
-      };
-      const uint32_t full = smem_u32(&mi.full[0]), empty = smem_u32(&mi.empty[0]), s_full = smem_u32(&mi.s_full[0]),
+      const uint32_t k_full = smem_u32(&mi.k_full[0]), v_full = smem_u32(&mi.v_full[0]), k_empty = smem_u32(&mi.k_empty[0]),
+                     v_empty = smem_u32(&mi.v_empty[0]), s_full = smem_u32(&mi.s_full[0]),
                      p_full = smem_u32(&mi.p_full[0]), o_done = smem_u32(&mi.o_done[0]);
       // piece c of step st in the ring: 5 pieces a step (counted modulo 2^32, a multiple of the ring)
       auto slot_of = [](uint32_t st, uint32_t c) { return (5 * st + c) & (kSlots - 1); };
-      auto phase_of = [](uint32_t st, uint32_t c) { return static_cast<int>((5 * st + c) / kSlots & 1); };
-      auto wait_pieces = [&](uint32_t st, uint32_t c0, uint32_t c1) {
-        for (uint32_t c = c0; c < c1; ++c) wait(full + 8 * slot_of(st, c), phase_of(st, c));
-        return alive;
-      };
+      auto wait_block = [&](uint32_t full, uint32_t st) { mbar_wait(full + 8 * (st & 1), st >> 1 & 1, stop); };
       // S of half h for the block of step st
       auto scores = [&](int h, uint32_t st) {
-        if (elect_one()) {
+        const uint32_t leader = elect_one();
 #pragma unroll
-          for (uint32_t c = 0; c < 3; ++c) {
-            const uint64_t qa = umma_desc(base + kQAt + (3 * h + c) * kPiece, 16, 1024);
-            const uint64_t ka = umma_desc(base + kSlotAt + slot_of(st, c) * kPiece, 16, 1024);
+        for (uint32_t c = 0; c < 3; ++c) {
+          const uint64_t qa = umma_desc(base + kQAt + (3 * h + c) * kPiece, 16, 1024);
+          const uint64_t ka = umma_desc(base + kSlotAt + slot_of(st, c) * kPiece, 16, 1024);
 #pragma unroll
-            for (int k = 0; k < 4; ++k)  // 32 bytes of K each
-              umma_ss<false>(tmem + h * kBlock, qa + 2 * k, ka + 2 * k, kIdescS, c > 0 || k > 0);
-          }
-          umma_commit(s_full + 8 * h);
+          for (int k = 0; k < 4; ++k)  // 32 bytes of K each
+            umma_ss<false>(leader, tmem + h * kBlock, qa + 2 * k, ka + 2 * k, kIdescS, c > 0 || k > 0);
         }
-        __syncwarp();
+        umma_commit(leader, s_full + 8 * h);
       };
-      auto values = [&](int h, uint32_t st, bool first) {
+      // O of half h: the products with keys 64 w to 64 w + 63 of the block
+      auto values = [&](int h, int w, uint32_t st, bool first) {
         // the two 64-value pieces of V are two slots, which may wrap around the ring: a product of 64 each then
-        const uint32_t d = tmem + 256 + h * kVal, w = tmem + h * kBlock;
-        const bool wraps = slot_of(st, 4) == 0;
-        if (elect_one()) {
-          const uint64_t v0 = umma_desc(base + kSlotAt + slot_of(st, 3) * kPiece, kPiece, 1024);
-          const uint64_t v1 = umma_desc(base + kSlotAt + slot_of(st, 4) * kPiece, kPiece, 1024);
-          if (!wraps) {
+        const uint32_t leader = elect_one();
+        const uint32_t d = tmem + 256 + h * kVal, a = tmem + h * kBlock + 32 * w;
+        const uint64_t v0 = umma_desc(base + kSlotAt + slot_of(st, 3) * kPiece + w * 8192, kPiece, 1024);
+        if (slot_of(st, 4) != 0) {
 #pragma unroll
-            for (int k = 0; k < 8; ++k) umma_ts(d, w + 8 * k, v0 + 128 * k, kIdescO, !first || k > 0);
-          } else {
-            constexpr uint32_t kIdescHalf = umma_idesc(kFmt, 0, 1, 128, 64);
+          for (int k = 0; k < 4; ++k) umma_ts(leader, d, a + 8 * k, v0 + 128 * k, kIdescO, !first || w > 0 || k > 0);
+        } else {
+          const uint64_t v1 = umma_desc(base + kSlotAt + w * 8192, kPiece, 1024);
+          constexpr uint32_t kIdescHalf = umma_idesc(kFmt, 0, 1, 128, 64);
 #pragma unroll
-            for (int k = 0; k < 8; ++k) {
-              umma_ts(d, w + 8 * k, v0 + 128 * k, kIdescHalf, !first || k > 0);
-              umma_ts(d + 64, w + 8 * k, v1 + 128 * k, kIdescHalf, !first || k > 0);
-            }
+          for (int k = 0; k < 4; ++k) {
+            umma_ts(leader, d, a + 8 * k, v0 + 128 * k, kIdescHalf, !first || w > 0 || k > 0);
+            umma_ts(leader, d + 64, a + 8 * k, v1 + 128 * k, kIdescHalf, !first || w > 0 || k > 0);
           }
-          umma_commit(o_done + 8 * h);
         }
-        __syncwarp();
+        if (w == 1) umma_commit(leader, o_done + 8 * h);
       };
-      // frees pieces [c0, c1) of a step, and the queries after their last product
-      auto free_pieces = [&](uint32_t st, uint32_t c0, uint32_t c1, bool queries) {
-        if (elect_one()) {
-          for (uint32_t c = c0; c < c1; ++c) umma_commit(empty + 8 * slot_of(st, c));
-          if (queries) umma_commit(smem_u32(&mi.q_empty));
-        }
-        __syncwarp();
-      };
-      int items = 0, cleans = 0;
+      uint32_t items = 0, cleans = 0;
       uint32_t step = 0;   // blocks begun
       uint32_t taken = 0;  // parity of the weights taken, a bit a half
-      uint32_t any = 0;    // halves that have taken any
-      while (alive && it.next()) {
+      while (it.next()) {
         if (it.keys == 0) continue;
-        if (!wait(smem_u32(&mi.q_full), items & 1)) break;
-        ++items;
+        mbar_wait(smem_u32(&mi.q_full), items++ & 1, stop);
         const int end = it.b0 + it.n;
         const bool partial_end = end == it.nb && it.x.lk - (end - 1) * kBlock < kBlock;  // warp 10's rule
         const int last0 = it.last(0), last1 = it.last(1);
-        for (int b = it.b0; b < end && alive; ++b, ++step) {
-          if (b == it.b0) {
-            if (!wait_pieces(step, 0, 3)) break;
-            tmem_fence_after();
-            if (b < last0) scores(0, step);
-            if (b < last1) scores(1, step);
-            free_pieces(step, 0, 3, b + 1 == end);
-          }
-          if (!wait_pieces(step, 3, 5)) break;
-          if (partial_end && b + 1 == end) {
+        wait_block(k_full, step);
+        tmem_fence_after();
+        if (it.b0 < last0) scores(0, step);
+        if (it.b0 < last1) scores(1, step);
+        {
+          const uint32_t leader = elect_one();
+          umma_commit(leader, k_empty + 8 * (step & 1));
+          if (it.n == 1) umma_commit(leader, smem_u32(&mi.q_empty));
+        }
+        for (int b = it.b0; b < end; ++b, ++step) {
+          const bool more = b + 1 < end;
+          wait_block(v_full, step);
+          if (!more && partial_end) {
             if (elect_one()) mbar_arrive(smem_u32(&mi.dirty));
-            if (!wait(smem_u32(&mi.clean), cleans++ & 1)) break;
+            __syncwarp();
+            mbar_wait(smem_u32(&mi.clean), cleans++ & 1, stop);
           }
-          bool have_k = false;
 #pragma unroll
           for (int h = 0; h < 2; ++h) {
             const int last = h ? last1 : last0;
-            if (alive && b < last && wait(p_full + 8 * h, taken >> h & 1)) {
-              taken ^= 1u << h;
-              any |= 1u << h;
+            if (b < last) {
+              mbar_wait(p_full + 16 * h, taken >> h & 1, stop);
               tmem_fence_after();
-              values(h, step, b == it.b0);
+              values(h, 0, step, b == it.b0);
+              mbar_wait(p_full + 16 * h + 8, taken >> h & 1, stop);
+              tmem_fence_after();
+              values(h, 1, step, b == it.b0);
+              taken ^= 1u << h;
             }
-            if (alive && b + 1 < last) {
-              if (!have_k) {
-                wait_pieces(step + 1, 0, 3);
-                tmem_fence_after();
-                have_k = true;
-              }
-              if (alive) scores(h, step + 1);
+            if (h == 0 && more) {
+              wait_block(k_full, step + 1);
+              tmem_fence_after();
             }
+            if (b + 1 < last) scores(h, step + 1);
           }
-          if (!alive) break;
-          free_pieces(step, 3, 5, false);
-          if (b + 1 < end) free_pieces(step + 1, 0, 3, b + 2 == end);
+          const uint32_t leader = elect_one();
+          umma_commit(leader, v_empty + 8 * (step & 1));
+          if (more) {
+            umma_commit(leader, k_empty + 8 * ((step + 1) & 1));
+            if (b + 2 == end) umma_commit(leader, smem_u32(&mi.q_empty));
+          }
         }
       }
-      if (!alive) {
-        // what was issued ends before the CTA does
-        int never = 0;
-        for (int h = 0; h < 2; ++h)
-          if (any >> h & 1) mbar_wait(o_done + 8 * h, (taken >> h & 1) ^ 1, &never);
-      }
-      __syncwarp();
+      // everything issued ends before the tensor memory is given back
+      umma_commit(elect_one(), smem_u32(&mi.end));
+      mbar_wait(smem_u32(&mi.end), 0, smem_u32(&mi.never));
     } else if (warp == 10) {
       // ---- value rows past a request's end ----
       Items it(p, share);
       int64_t step = 0;
-      int cleans = 0;
-      bool alive = true;
-      while (alive && it.next()) {
+      uint32_t cleans = 0;
+      while (it.next()) {
         if (it.keys == 0) continue;
         step += it.n;
         const int end = it.b0 + it.n;
         const int first = it.x.lk - (end - 1) * kBlock;  // rows of the last block that belong to the request
         if (end != it.nb || first >= kBlock) continue;
-        if (lane == 0) alive = mbar_wait(smem_u32(&mi.dirty), cleans & 1, stop);  // the block is there
-        alive = __shfl_sync(0xffffffffu, static_cast<int>(alive), 0) != 0;
-        if (!alive) break;
-        ++cleans;
+        mbar_wait(smem_u32(&mi.dirty), cleans++ & 1, stop);  // the block is there
         for (int c = 3; c < 5; ++c) {
           const int slot = static_cast<int>((5 * (step - 1) + c) % kSlots);
           uint4* at = reinterpret_cast<uint4*>(smem + kSlotAt + slot * kPiece + first * 128);
@@ -390,9 +384,8 @@ __global__ void __launch_bounds__(kThreads, 1)
     constexpr float kSlack = 8.0f;
     JoinNote note{-1, 0, 0, 0};
     Items it(p, share);
-    int count = 0;  // blocks taken part in
-    bool alive = true;
-    while (alive && it.next()) {
+    uint32_t count = 0;  // blocks taken part in
+    while (it.next()) {
       const int i0 = it.tile * kRows + h * kHalf;        // first row of this half within the request
       const int64_t i = i0 + row;
       const int limit = p.causal ? static_cast<int>(max(static_cast<int64_t>(0), min(static_cast<int64_t>(it.x.lk), it.x.lk - it.x.lq + 1 + i)))
@@ -402,9 +395,8 @@ __global__ void __launch_bounds__(kThreads, 1)
       float ref = -INFINITY, l = 0.0f;
       const int last = it.last(h);
       for (int b = it.b0; b < last; ++b, ++count) {
-        if (!mbar_wait(smem_u32(&mi.s_full[h]), count & 1, stop)) alive = false;
-        alive = __all_sync(0xffffffffu, alive);
-        if (!alive) break;
+        mbar_wait(smem_u32(&mi.s_full[h]), count & 1, stop);
+        __syncwarp();
         tmem_fence_after();
         uint32_t raw_s[128];
 #pragma unroll
@@ -418,10 +410,12 @@ __global__ void __launch_bounds__(kThreads, 1)
           for (int k = 0; k < 128; ++k)
             if (j0 + k >= limit) s[k] = -INFINITY;
         }
-        float m4[4] = {s[0], s[1], s[2], s[3]};
+        float m4[4];
 #pragma unroll
-        for (int k = 4; k < 128; ++k) m4[k & 3] = fmaxf(m4[k & 3], s[k]);
-        const float top = fmaxf(fmaxf(m4[0], m4[1]), fmaxf(m4[2], m4[3])) * sc;
+        for (int c = 0; c < 4; ++c) m4[c] = max3(s[3 * c], s[3 * c + 1], s[3 * c + 2]);
+#pragma unroll
+        for (int k = 12; k < 128; k += 2) m4[(k >> 1) & 3] = max3(m4[(k >> 1) & 3], s[k], s[k + 1]);
+        const float top = fmaxf(max3(m4[0], m4[1], m4[2]), m4[3]) * sc;
         if (__any_sync(0xffffffffu, top > ref + kSlack)) {
           float a = 1.0f;
           if (top > ref) {
@@ -430,7 +424,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           }
           l *= a;
           if (b > it.b0) {
-            if (!mbar_wait(smem_u32(&mi.o_done[h]), (count - 1) & 1, stop)) alive = false;
+            mbar_wait(smem_u32(&mi.o_done[h]), (count - 1) & 1, stop);
             __syncwarp();
             tmem_fence_after();
 #pragma unroll 1
@@ -446,34 +440,36 @@ __global__ void __launch_bounds__(kThreads, 1)
           }
         }
         const float r = ref == -INFINITY ? 0.0f : ref;
-        float sum[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+        const float2 sc2 = make_float2(sc, sc), r2 = make_float2(-r, -r);
+        float2 sum[2] = {make_float2(0.0f, 0.0f), make_float2(0.0f, 0.0f)};
 #pragma unroll
         for (int c = 0; c < 4; ++c) {
           uint32_t w[16];
 #pragma unroll
           for (int k = 0; k < 16; ++k) {
-            const float x = ex2(fmaf(s[32 * c + 2 * k], sc, -r)), y = ex2(fmaf(s[32 * c + 2 * k + 1], sc, -r));
-            sum[(2 * k) & 3] += x;
-            sum[(2 * k + 1) & 3] += y;
-            w[k] = pack2<T>(x, y);
+            float2 x = fma2(make_float2(s[32 * c + 2 * k], s[32 * c + 2 * k + 1]), sc2, r2);
+            x = make_float2(ex2(x.x), ex2(x.y));
+            sum[k & 1] = add2(sum[k & 1], x);
+            w[k] = pack2<T>(x.x, x.y);
           }
           tmem_st16(s_at + 16 * c, w);
+          if (c & 1) {  // 64 keys' weights are there: their products may begin
+            tmem_wait_st();
+            tmem_fence_before();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(smem_u32(&mi.p_full[2 * h + (c >> 1)]));
+          }
         }
-        l += (sum[0] + sum[1]) + (sum[2] + sum[3]);
-        tmem_wait_st();
-        tmem_fence_before();
-        __syncwarp();
-        if (lane == 0) mbar_arrive(smem_u32(&mi.p_full[h]));
+        sum[0] = add2(sum[0], sum[1]);
+        l += sum[0].x + sum[0].y;
       }
-      if (!alive) break;
 
       // epilogue
       const bool whole = it.b0 == 0 && it.n == it.nb;
       const bool some = last > it.b0;
       if (some) {
-        if (!mbar_wait(smem_u32(&mi.o_done[h]), (count - 1) & 1, stop)) alive = false;
-        alive = __all_sync(0xffffffffu, alive);
-        if (!alive) break;
+        mbar_wait(smem_u32(&mi.o_done[h]), (count - 1) & 1, stop);
+        __syncwarp();
         tmem_fence_after();
       }
       const bool mine = i < it.x.lq;
@@ -548,7 +544,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       tmem_fence_before();
     }
     if (tid == 0) p.ws.notes[unit] = note;
-    if (tid == 0 && *stop != 0) set_flag(p.err, PMG_FLAG_TIMEOUT);
+    if (stopped(stop) && tid == 0) set_flag(p.err, PMG_FLAG_TIMEOUT);
   }
   tmem_fence_before();
   __syncthreads();

@@ -27,74 +27,95 @@ __device__ __forceinline__ void mbar_arrive(uint32_t bar) {
 __device__ __forceinline__ void mbar_expect(uint32_t bar, uint32_t bytes) {
   asm volatile("mbarrier.arrive.expect_tx.shared::cta.b64 _, [%0], %1;" ::"r"(bar), "r"(bytes) : "memory");
 }
-__device__ __forceinline__ bool mbar_test(uint32_t bar, int parity) {
-  uint32_t ok;
+// Every wait is bounded: after two seconds it gives up and sets `stop`, a word
+// of shared memory that makes all later waits of the CTA return at once. Roles
+// then run their (finite) loops to the end over whatever is there, the loading
+// role issues nothing more, and the CTA reports PMG_FLAG_TIMEOUT. One block of
+// instructions with no result: nothing of the waiting role's own control flow
+// depends on it.
+__device__ __forceinline__ void mbar_wait(uint32_t bar, uint32_t parity, uint32_t stop) {
   asm volatile(
-      "{\n\t.reg .pred p;\n\t"
+      "{\n\t"
+      ".reg .pred p;\n\t"
+      ".reg .b32 s;\n\t"
+      ".reg .b64 t0, t1;\n\t"
+      "mbarrier.try_wait.parity.shared::cta.b64 p, [%0], %1;\n\t"
+      "@p bra DONE%=;\n\t"
+      "mov.u64 t0, %%globaltimer;\n\t"
+      "AGAIN%=:\n\t"
+      "mbarrier.try_wait.parity.shared::cta.b64 p, [%0], %1;\n\t"
+      "@p bra DONE%=;\n\t"
+      "ld.volatile.shared.b32 s, [%2];\n\t"
+      "setp.ne.b32 p, s, 0;\n\t"
+      "@p bra DONE%=;\n\t"
+      "mov.u64 t1, %%globaltimer;\n\t"
+      "sub.u64 t1, t1, t0;\n\t"
+      "setp.lt.u64 p, t1, 2000000000;\n\t"
+      "@p bra AGAIN%=;\n\t"
+      "mov.b32 s, 1;\n\t"
+      "st.volatile.shared.b32 [%2], s;\n\t"
+      "DONE%=:\n\t"
+      "}" ::"r"(bar),
+      "r"(parity), "r"(stop)
+      : "memory");
+}
+// Waits for either of two; whether the first is there.
+__device__ __forceinline__ bool mbar_wait_either(uint32_t bar_a, uint32_t parity_a, uint32_t bar_b, uint32_t parity_b,
+                                                 uint32_t stop) {
+  uint32_t first;
+  asm volatile(
+      "{\n\t"
+      ".reg .pred p;\n\t"
+      ".reg .b32 s;\n\t"
+      ".reg .b64 t0, t1;\n\t"
+      "mov.b32 %0, 1;\n\t"
       "mbarrier.test_wait.parity.shared::cta.b64 p, [%1], %2;\n\t"
-      "selp.u32 %0, 1, 0, p;\n\t}"
-      : "=r"(ok)
-      : "r"(bar), "r"(parity)
+      "@p bra DONE%=;\n\t"
+      "mov.b32 %0, 0;\n\t"
+      "mbarrier.test_wait.parity.shared::cta.b64 p, [%3], %4;\n\t"
+      "@p bra DONE%=;\n\t"
+      "mov.u64 t0, %%globaltimer;\n\t"
+      "AGAIN%=:\n\t"
+      "mov.b32 %0, 1;\n\t"
+      "mbarrier.test_wait.parity.shared::cta.b64 p, [%1], %2;\n\t"
+      "@p bra DONE%=;\n\t"
+      "mov.b32 %0, 0;\n\t"
+      "mbarrier.test_wait.parity.shared::cta.b64 p, [%3], %4;\n\t"
+      "@p bra DONE%=;\n\t"
+      "ld.volatile.shared.b32 s, [%5];\n\t"
+      "setp.ne.b32 p, s, 0;\n\t"
+      "@p bra DONE%=;\n\t"
+      "mov.u64 t1, %%globaltimer;\n\t"
+      "sub.u64 t1, t1, t0;\n\t"
+      "setp.lt.u64 p, t1, 2000000000;\n\t"
+      "@p bra AGAIN%=;\n\t"
+      "mov.b32 s, 1;\n\t"
+      "st.volatile.shared.b32 [%5], s;\n\t"
+      "DONE%=:\n\t"
+      "}"
+      : "=&r"(first)
+      : "r"(bar_a), "r"(parity_a), "r"(bar_b), "r"(parity_b), "r"(stop)
       : "memory");
-  return ok != 0;
+  return __shfl_sync(0xffffffffu, first, 0) != 0;
 }
-__device__ __forceinline__ bool mbar_try(uint32_t bar, int parity) {
-  uint32_t ok;
-  asm volatile(
-      "{\n\t.reg .pred p;\n\t"
-      "mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2;\n\t"
-      "selp.u32 %0, 1, 0, p;\n\t}"
-      : "=r"(ok)
-      : "r"(bar), "r"(parity)
-      : "memory");
-  return ok != 0;
-}
-
-__device__ __forceinline__ uint64_t now_ns() {
-  uint64_t t;
-  asm volatile("mov.u64 %0, %%globaltimer;" : "=l"(t));
-  return t;
-}
-
-// Every wait is bounded: after two seconds the CTA gives up (`stop` is set for
-// all its roles), reports PMG_FLAG_TIMEOUT and ends in order.
-constexpr uint64_t kWaitNs = 2000000000ull;
-
-// (inlined: a call would spill what the waiting thread holds in registers)
-__device__ __forceinline__ bool mbar_wait(uint32_t bar, int parity, volatile int* stop) {
-  if (mbar_try(bar, parity)) return true;
-  const uint64_t t0 = now_ns();
-#pragma unroll 1
-  for (int i = 0;; ++i) {
-    if (mbar_try(bar, parity)) return true;
-    if ((i & 63) != 63) continue;
-    if (*stop != 0) return false;
-    if (now_ns() - t0 > kWaitNs) {
-      *stop = 1;
-      return false;
-    }
-  }
+__device__ __forceinline__ bool stopped(uint32_t stop) {
+  uint32_t s;
+  asm volatile("ld.volatile.shared.b32 %0, [%1];" : "=r"(s) : "r"(stop) : "memory");
+  return __shfl_sync(0xffffffffu, s, 0) != 0;
 }
 
 // One lane of a converged warp. The roles that issue copies and products run
 // with all their lanes and let the elected one issue: addresses and
 // descriptors then stay in uniform registers, which these instructions read (a
 // role run by a single lane took about 170 clocks a product instead).
-__device__ __forceinline__ bool elect_one() {
+__device__ __forceinline__ uint32_t elect_one() {
   uint32_t leader;
   asm volatile(
       "{\n\t.reg .pred p;\n\t"
       "elect.sync _|p, 0xffffffff;\n\t"
       "selp.u32 %0, 1, 0, p;\n\t}"
       : "=r"(leader));
-  return leader != 0;
-}
-// The same answer for all lanes.
-__device__ __forceinline__ bool mbar_wait_warp(uint32_t bar, int parity, volatile int* stop) {
-  return __all_sync(0xffffffffu, mbar_wait(bar, parity, stop)) != 0;
-}
-__device__ __forceinline__ bool mbar_test_warp(uint32_t bar, int parity) {
-  return __all_sync(0xffffffffu, mbar_test(bar, parity)) != 0;
+  return leader;
 }
 
 // ---- proxies, named barriers --------------------------------------------------
@@ -173,33 +194,39 @@ __host__ __device__ constexpr uint32_t umma_idesc(int fmt, int a_mn, int b_mn, i
          (static_cast<uint32_t>(n >> 3) << 17) | (static_cast<uint32_t>(m >> 4) << 24);
 }
 
+// Products are run by a whole converged warp, with `leader` (elect_one) as the
+// instruction's own predicate: 28 clocks each against 41 inside a branch of the
+// elected lane (64 x 16 x 16 products back to back).
 template <bool kFp8>
-__device__ __forceinline__ void umma_ss(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, bool add) {
+__device__ __forceinline__ void umma_ss(uint32_t leader, uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, bool add) {
   if constexpr (kFp8) {
     asm volatile(
-        "{\n\t.reg .pred p;\n\tsetp.ne.u32 p, %4, 0;\n\t"
-        "tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], %1, %2, %3, p;\n\t}" ::"r"(d),
-        "l"(a), "l"(b), "r"(idesc), "r"(static_cast<uint32_t>(add))
+        "{\n\t.reg .pred p, q;\n\tsetp.ne.u32 p, %4, 0;\n\tsetp.ne.u32 q, %5, 0;\n\t"
+        "@q tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], %1, %2, %3, p;\n\t}" ::"r"(d),
+        "l"(a), "l"(b), "r"(idesc), "r"(static_cast<uint32_t>(add)), "r"(leader)
         : "memory");
   } else {
     asm volatile(
-        "{\n\t.reg .pred p;\n\tsetp.ne.u32 p, %4, 0;\n\t"
-        "tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(d),
-        "l"(a), "l"(b), "r"(idesc), "r"(static_cast<uint32_t>(add))
+        "{\n\t.reg .pred p, q;\n\tsetp.ne.u32 p, %4, 0;\n\tsetp.ne.u32 q, %5, 0;\n\t"
+        "@q tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(d),
+        "l"(a), "l"(b), "r"(idesc), "r"(static_cast<uint32_t>(add)), "r"(leader)
         : "memory");
   }
 }
 // A from tensor memory
-__device__ __forceinline__ void umma_ts(uint32_t d, uint32_t a, uint64_t b, uint32_t idesc, bool add) {
+__device__ __forceinline__ void umma_ts(uint32_t leader, uint32_t d, uint32_t a, uint64_t b, uint32_t idesc, bool add) {
   asm volatile(
-      "{\n\t.reg .pred p;\n\tsetp.ne.u32 p, %4, 0;\n\t"
-      "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d),
-      "r"(a), "l"(b), "r"(idesc), "r"(static_cast<uint32_t>(add))
+      "{\n\t.reg .pred p, q;\n\tsetp.ne.u32 p, %4, 0;\n\tsetp.ne.u32 q, %5, 0;\n\t"
+      "@q tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d),
+      "r"(a), "l"(b), "r"(idesc), "r"(static_cast<uint32_t>(add)), "r"(leader)
       : "memory");
 }
 // arrives on the barrier when every product issued so far by this thread is done
-__device__ __forceinline__ void umma_commit(uint32_t bar) {
-  asm volatile("tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(bar) : "memory");
+__device__ __forceinline__ void umma_commit(uint32_t leader, uint32_t bar) {
+  asm volatile(
+      "{\n\t.reg .pred q;\n\tsetp.ne.u32 q, %1, 0;\n\t"
+      "@q tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];\n\t}" ::"r"(bar), "r"(leader)
+      : "memory");
 }
 
 __device__ __forceinline__ void tmem_alloc(uint32_t smem_slot, int columns) {
@@ -241,6 +268,32 @@ __device__ __forceinline__ void tmem_ld32(uint32_t addr, uint32_t* r) {
         "=r"(r[25]), "=r"(r[26]), "=r"(r[27]), "=r"(r[28]), "=r"(r[29]), "=r"(r[30]), "=r"(r[31])
       : "r"(addr));
 }
+// 16 lanes and 8 N columns, spread over a warp: of columns 8 g + 2 (lane & 3)
+// and the next, values 4 g and 4 g + 1 are row lane >> 2, 4 g + 2 and 4 g + 3
+// row (lane >> 2) + 8.
+__device__ __forceinline__ void tmem_ld_rows16(uint32_t addr, uint32_t (&r)[8]) {
+  asm volatile("tcgen05.ld.sync.aligned.16x256b.x2.b32 {%0, %1, %2, %3, %4, %5, %6, %7}, [%8];"
+               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7])
+               : "r"(addr));
+}
+__device__ __forceinline__ void tmem_ld_rows16(uint32_t addr, uint32_t (&r)[16]) {
+  asm volatile(
+      "tcgen05.ld.sync.aligned.16x256b.x4.b32 {%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15}, "
+      "[%16];"
+      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]), "=r"(r[8]),
+        "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15])
+      : "r"(addr));
+}
+__device__ __forceinline__ void tmem_ld_rows16(uint32_t addr, uint32_t (&r)[32]) {
+  asm volatile(
+      "tcgen05.ld.sync.aligned.16x256b.x8.b32 {%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, "
+      "%16, %17, %18, %19, %20, %21, %22, %23, %24, %25, %26, %27, %28, %29, %30, %31}, [%32];"
+      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]), "=r"(r[8]),
+        "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15]), "=r"(r[16]),
+        "=r"(r[17]), "=r"(r[18]), "=r"(r[19]), "=r"(r[20]), "=r"(r[21]), "=r"(r[22]), "=r"(r[23]), "=r"(r[24]),
+        "=r"(r[25]), "=r"(r[26]), "=r"(r[27]), "=r"(r[28]), "=r"(r[29]), "=r"(r[30]), "=r"(r[31])
+      : "r"(addr));
+}
 __device__ __forceinline__ void tmem_st16(uint32_t addr, const uint32_t* r) {
   asm volatile(
       "tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, "
@@ -264,6 +317,33 @@ __device__ __forceinline__ float ex2(float x) {
   float y;
   asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
   return y;
+}
+
+// three-input maximum, and two fused or plain operations an instruction
+__device__ __forceinline__ float max3(float a, float b, float c) {
+  float y;
+  asm("max.f32 %0, %1, %2, %3;" : "=f"(y) : "f"(a), "f"(b), "f"(c));
+  return y;
+}
+__device__ __forceinline__ uint64_t bits2(float2 a) {
+  uint64_t r;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(a.x), "f"(a.y));
+  return r;
+}
+__device__ __forceinline__ float2 from_bits2(uint64_t r) {
+  float2 a;
+  asm("mov.b64 {%0, %1}, %2;" : "=f"(a.x), "=f"(a.y) : "l"(r));
+  return a;
+}
+__device__ __forceinline__ float2 fma2(float2 a, float2 b, float2 c) {
+  uint64_t r;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(bits2(a)), "l"(bits2(b)), "l"(bits2(c)));
+  return from_bits2(r);
+}
+__device__ __forceinline__ float2 add2(float2 a, float2 b) {
+  uint64_t r;
+  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(bits2(a)), "l"(bits2(b)));
+  return from_bits2(r);
 }
 
 // two values, the first in the low half
