@@ -3,13 +3,14 @@
 // sizes.
 //
 // The work of a call is a flat list of equal pieces (a tile of keys for one
-// group of rows), request after request. The list is cut into as many equal
-// shares as there are units (a unit is the CTAs that run one share, one for
-// each group of rows), so long and short requests cost every SM the same. A
-// request that a share covers whole is finished there. One that a cut falls
+// group of rows), request after request, with a few idle pieces before each
+// request for what its beginning and end cost. The list is cut into as many
+// equal shares as there are units (a unit is the CTAs that run one share, one
+// for each group of rows), so long and short requests cost every SM the same.
+// A request that a share covers whole is finished there. One that a cut falls
 // into leaves, from every share that holds a part of it, the unnormalised
 // rows, their running maximum and their sum in the workspace; the share that
-// holds its first piece notes how many shares follow, and the join kernel adds
+// holds its first tile notes how many shares follow, and the join kernel adds
 // them up in their order, so results do not depend on timing.
 #pragma once
 
@@ -99,6 +100,129 @@ __device__ __forceinline__ int unit_of(int64_t x, int64_t total, int units) {
   while (u + 1 < units && total * (u + 1) / units <= x) ++u;
   while (u > 0 && total * u / units > x) --u;
   return static_cast<int>(u);
+}
+
+// ---- the join -----------------------------------------------------------------
+
+// Sums of the rows that shares cut. Work is one warp for each row and 128
+// columns where a request lies in a few shares, and a whole CTA (its warps take
+// the shares in turn) where it lies in many: a request cut into a hundred
+// parts and a hundred requests cut in two both fill the SMs in one wave.
+//   part i of a note by CTA c is in the slots of CTA c + i * stride;
+//   valid(note, c, row): whether the row exists;
+//   emit(note, c, row, d, sums, top, l): columns d to d + 3 of the unnormalised
+//   row (to be multiplied by 1 / l), its reference and sum. d is lane * 4 + 128 k:
+//   whoever has d == 0 writes the log sum.
+constexpr int kJoinThreads = 256;
+constexpr int kJoinWarps = kJoinThreads / 32;
+constexpr int kJoinFew = 8;        // parts that one warp adds up
+constexpr int kJoinNotes = 512;    // notes at most (a unit has more than one share only while CTAs fit the SMs)
+constexpr int kJoinCtasPerSm = 4;
+
+template <class Valid, class Emit>
+__device__ __forceinline__ void join_rows(const Workspace& ws, int notes, int stride, int rows, int dv,
+                                          int64_t slot_floats, Valid valid, Emit emit) {
+  __shared__ int16_t few[kJoinNotes], many[kJoinNotes];
+  __shared__ int n_few, n_many;
+  __shared__ float4 sums[kJoinThreads];
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  // the notes in their order, the same in every CTA: it decides who does what
+  if (warp == 0) {
+    int a = 0, b = 0;
+    for (int i0 = 0; i0 < notes; i0 += 32) {
+      const int i = i0 + lane;
+      const JoinNote note = i < notes ? ws.notes[i] : JoinNote{-1, 0, 0, 0};
+      const bool one = note.item >= 0 && note.parts <= kJoinFew, other = note.item >= 0 && !one;
+      const uint32_t ones = __ballot_sync(0xffffffffu, one), others = __ballot_sync(0xffffffffu, other);
+      const uint32_t below = (1u << lane) - 1;
+      if (one) few[a + __popc(ones & below)] = static_cast<int16_t>(i);
+      if (other) many[b + __popc(others & below)] = static_cast<int16_t>(i);
+      a += __popc(ones);
+      b += __popc(others);
+    }
+    if (lane == 0) {
+      n_few = a;
+      n_many = b;
+    }
+  }
+  __syncthreads();
+  if (n_few + n_many == 0) return;
+  const int quarters = (dv + 127) / 128;
+  const bool vec = dv % 4 == 0;
+  auto slot_of = [&](int cta, int i) {  // part 0 is the noting share's own end, the others begin their shares
+    return ws.slots + ((cta + static_cast<int64_t>(i) * stride) * 2 + (i == 0 ? 1 : 0)) * slot_floats;
+  };
+  // adds parts i0, i0 + step, ... of a row's columns d to d + 3 under the reference `top`
+  auto add = [&](int cta, int row, int d, int i0, int parts, int step, float top, float4& a, float& l) {
+    const int64_t ml = static_cast<int64_t>(rows) * dv + 2 * row;
+#pragma unroll 4
+    for (int i = i0; i < parts; i += step) {
+      const float* slot = slot_of(cta, i);
+      const float m = slot[ml], part_l = slot[ml + 1];
+      const float* o = slot + static_cast<int64_t>(row) * dv + d;
+      float4 x = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+      if (vec) {
+        if (d < dv) x = *reinterpret_cast<const float4*>(o);
+      } else {
+        if (d < dv) x.x = o[0];
+        if (d + 1 < dv) x.y = o[1];
+        if (d + 2 < dv) x.z = o[2];
+        if (d + 3 < dv) x.w = o[3];
+      }
+      if (m == -INFINITY) continue;  // the row saw nothing there, and may have no values
+      const float w = exp2f(m - top);
+      l += w * part_l;
+      a.x += w * x.x;
+      a.y += w * x.y;
+      a.z += w * x.z;
+      a.w += w * x.w;
+    }
+  };
+  auto top_of = [&](int cta, int row, int parts) {
+    const int64_t ml = static_cast<int64_t>(rows) * dv + 2 * row;
+    float top = -INFINITY;
+    for (int i = lane; i < parts; i += 32) top = fmaxf(top, slot_of(cta, i)[ml]);
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
+    return top;
+  };
+  for (int x = blockIdx.x * kJoinWarps + warp; x < n_few * rows * quarters; x += gridDim.x * kJoinWarps) {
+    const int cta = few[x / (rows * quarters)], row = x / quarters % rows, d = x % quarters * 128 + lane * 4;
+    const JoinNote note = ws.notes[cta];
+    if (!valid(note, cta, row)) continue;
+    const float top = top_of(cta, row, note.parts);
+    float4 a = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+    float l = 0.0f;
+    add(cta, row, d, 0, note.parts, 1, top, a, l);
+    __syncwarp();
+    if (d < dv) emit(note, cta, row, d, a, top, l);
+  }
+  for (int x = blockIdx.x; x < n_many * rows * quarters; x += gridDim.x) {
+    const int cta = many[x / (rows * quarters)], row = x / quarters % rows, d = x % quarters * 128 + lane * 4;
+    const JoinNote note = ws.notes[cta];
+    if (!valid(note, cta, row)) continue;  // the same for the whole CTA
+    const float top = top_of(cta, row, note.parts);
+    float4 a = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+    float l = 0.0f;
+    add(cta, row, d, warp, note.parts, kJoinWarps, top, a, l);
+    __shared__ float sums_l[kJoinWarps];
+    sums[tid] = a;
+    if (lane == 0) sums_l[warp] = l;
+    __syncthreads();
+    if (warp == 0) {
+#pragma unroll
+      for (int k = 1; k < kJoinWarps; ++k) {
+        const float4 y = sums[k * 32 + lane];
+        a.x += y.x;
+        a.y += y.y;
+        a.z += y.z;
+        a.w += y.w;
+        l += sums_l[k];
+      }
+      if (d < dv) emit(note, cta, row, d, a, top, l);
+    }
+    __syncthreads();
+  }
 }
 
 // ---- the body for any sizes -------------------------------------------------

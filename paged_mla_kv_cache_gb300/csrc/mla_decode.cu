@@ -107,87 +107,25 @@ __global__ void __launch_bounds__(kGenThreads) decode_general_kernel(const __gri
   set_flag(p.err, bad);
 }
 
-// The join: rows of a request that shares cut, added up in the order of the
-// shares. A CTA takes one row of one note; its threads take columns, and
-// quarters of the parts, four columns at a time.
-constexpr int kJoinThreads = 512;
-
 template <class TQ>
 __global__ void __launch_bounds__(kJoinThreads) decode_join_kernel(const __grid_constant__ DecodeParams p) {
-  __shared__ float4 sums[kJoinThreads];
   pdl_entry();
-  const JoinNote note = p.ws.notes[blockIdx.x];
-  if (note.item < 0) return;
-  const int group = blockIdx.x % p.groups, row = blockIdx.y;
-  const int rows = p.q_len * p.H, rr = group * p.rows_per_group + row;
-  if (rr >= rows) return;
-  const int64_t mlat = static_cast<int64_t>(p.rows_per_group) * p.dv + 2 * row;
-  auto slot_of = [&](int i) {  // part 0 is the noting share's own end, the others begin their shares
-    const int64_t cta = blockIdx.x + static_cast<int64_t>(i) * p.groups;
-    return p.ws.slots + (cta * 2 + (i == 0 ? 1 : 0)) * p.slot_floats;
-  };
-  float top = -INFINITY;
-  for (int i = threadIdx.x & 31; i < note.parts; i += 32) top = fmaxf(top, slot_of(i)[mlat]);
+  const int rows = p.q_len * p.H;
+  auto row_of = [&](int cta, int row) { return cta % p.groups * p.rows_per_group + row; };
+  join_rows(
+      p.ws, p.units * p.groups, p.groups, p.rows_per_group, p.dv, p.slot_floats,
+      [&](const JoinNote&, int cta, int row) { return row_of(cta, row) < rows; },
+      [&](const JoinNote& note, int cta, int row, int d, const float4& a, float top, float l) {
+        const int rr = row_of(cta, row);
+        const float inv = l > 0.0f ? 1.0f / l : 0.0f;
+        if (d == 0 && p.lse != nullptr)
+          p.lse[static_cast<int64_t>(note.item) * rows + rr] = l > 0.0f ? (top + log2f(l)) * kLn2 : -INFINITY;
+        TQ* out = static_cast<TQ*>(p.out) + note.item * p.or_stride + (rr / p.H) * p.ot_stride + (rr % p.H) * p.oh_stride + d;
+        const float y[4] = {a.x * inv, a.y * inv, a.z * inv, a.w * inv};
 #pragma unroll
-  for (int o = 16; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
-  float l = 0.0f;
-  for (int i = threadIdx.x & 31; i < note.parts; i += 32) {
-    const float* ml = slot_of(i) + mlat;
-    if (ml[0] != -INFINITY) l += ml[1] * exp2f(ml[0] - top);
-  }
-#pragma unroll
-  for (int o = 16; o > 0; o >>= 1) l += __shfl_xor_sync(0xffffffffu, l, o);
-  const float inv = l > 0.0f ? 1.0f / l : 0.0f;
-  if (threadIdx.x == 0 && p.lse != nullptr)
-    p.lse[static_cast<int64_t>(note.item) * rows + rr] = l > 0.0f ? (top + log2f(l)) * kLn2 : -INFINITY;
-  TQ* out = reinterpret_cast<TQ*>(p.out) + note.item * p.or_stride + (rr / p.H) * p.ot_stride + (rr % p.H) * p.oh_stride;
-  constexpr int kLanes = kJoinThreads / 4;
-  const int quarter = threadIdx.x / kLanes, lane = threadIdx.x % kLanes;
-  const int i0 = note.parts * quarter / 4, i1 = note.parts * (quarter + 1) / 4;
-  const bool vec = p.dv % 4 == 0;
-  for (int d0 = 0; d0 < p.dv; d0 += kLanes * 4) {
-    const int d = d0 + lane * 4;
-    float4 a = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-    if (d < p.dv) {
-#pragma unroll 8
-      for (int i = i0; i < i1; ++i) {
-        const float* slot = slot_of(i);
-        const float m = slot[mlat];
-        const float w = m == -INFINITY ? 0.0f : exp2f(m - top);
-        const float* o = slot + static_cast<int64_t>(row) * p.dv + d;
-        float4 x = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-        if (vec) {
-          x = *reinterpret_cast<const float4*>(o);
-        } else {
-          x.x = o[0];
-          if (d + 1 < p.dv) x.y = o[1];
-          if (d + 2 < p.dv) x.z = o[2];
-          if (d + 3 < p.dv) x.w = o[3];
-        }
-        a.x += w * x.x;
-        a.y += w * x.y;
-        a.z += w * x.z;
-        a.w += w * x.w;
-      }
-    }
-    __syncthreads();
-    sums[threadIdx.x] = a;
-    __syncthreads();
-    if (quarter == 0 && d < p.dv) {
-#pragma unroll
-      for (int k = 1; k < 4; ++k) {
-        const float4 x = sums[k * kLanes + lane];
-        a.x += x.x;
-        a.y += x.y;
-        a.z += x.z;
-        a.w += x.w;
-      }
-      const float y[4] = {a.x * inv, a.y * inv, a.z * inv, a.w * inv};
-#pragma unroll
-      for (int k = 0; k < 4; ++k)
-        if (d + k < p.dv) out[d + k] = from_f<TQ>(y[k]);
-    }
-  }
+        for (int k = 0; k < 4; ++k)
+          if (d + k < p.dv) out[k] = from_f<TQ>(y[k]);
+      });
 }
 
 using Kernel = void (*)(const DecodeParams);
@@ -287,8 +225,7 @@ extern "C" int pmg_latent_decode(const void* q, int64_t q_req_stride, int64_t q_
     st = launch(k, dim3(static_cast<unsigned>(p.units) * p.groups), kGenThreads, general_smem(E), stream, p);
   }
   if (st != PMG_OK || p.units == 1) return st;
-  const unsigned ctas = static_cast<unsigned>(p.units) * p.groups;
   const Kernel join = q_dtype == PMG_BF16 ? decode_join_kernel<bf16>
                       : q_dtype == PMG_FP16 ? decode_join_kernel<f16> : decode_join_kernel<float>;
-  return launch(join, dim3(ctas, static_cast<unsigned>(p.rows_per_group)), kJoinThreads, 0, stream, p);
+  return launch(join, dim3(static_cast<unsigned>(kJoinCtasPerSm * sms)), kJoinThreads, 0, stream, p);
 }

@@ -53,7 +53,7 @@ __device__ __forceinline__ DecodeLen decode_len(const DecodeParams& p, int b) {
   return l;
 }
 
-// Pieces of a request; an empty one has a piece too, which writes its rows.
+// Tiles of a request; an empty one has a piece too, which writes its rows.
 __device__ __forceinline__ int64_t decode_tiles(const DecodeParams& p, int b) {
   const int64_t n = decode_len(p, b).use;
   return n > 0 ? (n + kDecodeTile - 1) / kDecodeTile : 1;

@@ -98,38 +98,52 @@ struct MiscOf {
   int32_t stop, never;
 };
 
+// Pieces of a request of `len` keys: its tiles and kItemCost idle ones for its
+// beginning and end (queries, first reference, epilogue). An empty request has
+// one, which writes its rows.
+constexpr int kItemCost = 4;
+__device__ __forceinline__ int tiles_of(int len) { return (len + kDecodeTile - 1) / kDecodeTile; }
+__device__ __forceinline__ int pieces_of(int len) { return len > 0 ? kItemCost + tiles_of(len) : 1; }
+
 // Walks the requests of a share. The next request's length is loaded one step
 // early.
 struct Items {
   const DecodeParams* p;
   int64_t at, end;
+  int64_t first;    // the request's first piece
   int b;
   int tile, tiles;  // first tile of this share, tiles of the request
   int n;            // tiles of this share
   int len;          // keys of the request
   int full_len;
+  int skip;         // pieces of the request before this share
   DecodeLen ahead;
   __device__ Items(const DecodeParams& p_, const Share& s) : p(&p_), at(s.begin), end(s.end), b(s.item - 1) {
     tile = tiles = n = len = full_len = 0;
+    first = 0;
+    skip = static_cast<int>(s.offset);
     if (at < end) ahead = decode_len(*p, s.item);
-    first_ = static_cast<int>(s.offset);
   }
+  // the next request of which this share has tiles, or that is empty
   __device__ bool next() {
-    if (at >= end) return false;
-    ++b;
-    tile = first_;
-    first_ = 0;
-    len = ahead.use;
-    full_len = ahead.full;
-    if (b + 1 < p->R) ahead = decode_len(*p, b + 1);
-    tiles = len > 0 ? (len + kDecodeTile - 1) / kDecodeTile : 1;
-    n = static_cast<int>(min(static_cast<int64_t>(tiles - tile), end - at));
-    at += n;
+    do {
+      if (at >= end) return false;
+      ++b;
+      len = ahead.use;
+      full_len = ahead.full;
+      if (b + 1 < p->R) ahead = decode_len(*p, b + 1);
+      tiles = tiles_of(len);
+      first = at - skip;
+      const int take = static_cast<int>(min(static_cast<int64_t>(pieces_of(len) - skip), end - at));
+      tile = max(0, skip - kItemCost);
+      n = max(0, skip + take - kItemCost) - tile;
+      at += take;
+      skip = 0;
+    } while (n == 0 && len > 0);
     return true;
   }
-  __device__ int64_t piece() const { return at - n; }
- private:
-  int first_;
+  // the piece of the request's last tile
+  __device__ int64_t last_piece() const { return first + kItemCost + tiles - 1; }
 };
 
 // The next e4m3 part of two values, packed low first; what is left of them
@@ -149,45 +163,49 @@ __device__ __forceinline__ float half_of(uint32_t two, int i, f16) {
 }
 
 // One row group's queries into shared memory, K-major. A warp takes every
-// fourth row.
+// fourth row, several rows' loads in flight; the rows are then converted one at
+// a time by one copy of the code.
 template <class TQ, int kParts, int N, class Misc>
 __device__ __forceinline__ void load_queries(const DecodeParams& p, int b, int g0, int n_rows, uint8_t* q_smem,
                                              Misc& mi, float factor) {
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   constexpr int kUnits = kEntry / 8;  // 16 bytes each
-  constexpr int kBatch = 4;
+  constexpr int kBatch = N < 32 ? N / 4 : 8;  // rows of a warp in flight
 #pragma unroll 1
   for (int r0 = warp; r0 < N; r0 += 4 * kBatch) {
     uint4 x[kBatch][3];
 #pragma unroll
     for (int i = 0; i < kBatch; ++i) {
-      const int r = r0 + 4 * i;
-      if (r < N) {
-        const int rr = g0 + r;
-        const uint4* src = reinterpret_cast<const uint4*>(static_cast<const TQ*>(p.q) + b * p.qr_stride +
-                                                          (rr / p.H) * p.qt_stride + (rr % p.H) * p.qh_stride);
+      const int r = r0 + 4 * i, rr = g0 + min(r, n_rows - 1);
+      const uint4* src = reinterpret_cast<const uint4*>(static_cast<const TQ*>(p.q) + b * p.qr_stride +
+                                                        (rr / p.H) * p.qt_stride + (rr % p.H) * p.qh_stride);
 #pragma unroll
-        for (int k = 0; k < 3; ++k)
-          x[i][k] = r < n_rows && lane + 32 * k < kUnits ? src[lane + 32 * k] : make_uint4(0, 0, 0, 0);
-      }
+      for (int k = 0; k < 3; ++k)
+        x[i][k] = r < n_rows && lane + 32 * k < kUnits ? src[lane + 32 * k] : make_uint4(0, 0, 0, 0);
     }
-#pragma unroll
+#pragma unroll 1
     for (int i = 0; i < kBatch; ++i) {
       const int r = r0 + 4 * i;
-      if (r >= N) continue;
+      uint4 y[3] = {x[0][0], x[0][1], x[0][2]};
+#pragma unroll
+      for (int j = 1; j < kBatch; ++j)
+        if (i == j) {
+          y[0] = x[j][0];
+          y[1] = x[j][1];
+          y[2] = x[j][2];
+        }
       if constexpr (kParts == 1) {
         if (lane == 0) mi.factor[r] = factor;
 #pragma unroll
         for (int k = 0; k < 3; ++k) {
           const int u = lane + 32 * k;
-          if (u < kUnits)
-            *reinterpret_cast<uint4*>(q_smem + (u >> 3) * (N * 128) + r * 128 + (((u & 7) ^ (r & 7)) << 4)) = x[i][k];
+          if (u < kUnits) *reinterpret_cast<uint4*>(q_smem + (u >> 3) * (N * 128) + r * 128 + (((u & 7) ^ (r & 7)) << 4)) = y[k];
         }
       } else {
         float top = 0.0f;
 #pragma unroll
         for (int k = 0; k < 3; ++k) {
-          const uint32_t w[4] = {x[i][k].x, x[i][k].y, x[i][k].z, x[i][k].w};
+          const uint32_t w[4] = {y[k].x, y[k].y, y[k].z, y[k].w};
 #pragma unroll
           for (int j = 0; j < 8; ++j) top = fmaxf(top, fabsf(half_of(w[j >> 1], j & 1, TQ())));
         }
@@ -201,21 +219,22 @@ __device__ __forceinline__ void load_queries(const DecodeParams& p, int b, int g
           scale = ldexpf(1.0f, (m < 0.875f ? 9 : 8) - e);
         }
         if (lane == 0) mi.factor[r] = factor / scale;
-#pragma unroll
+#pragma unroll 1
         for (int k = 0; k < 3; ++k) {
           const int u = lane + 32 * k;  // 8 values: 8 bytes of each part
           if (u < kUnits) {
-            const uint32_t w[4] = {x[i][k].x, x[i][k].y, x[i][k].z, x[i][k].w};
+            const uint4 z = k == 0 ? y[0] : k == 1 ? y[1] : y[2];
+            const uint32_t w[4] = {z.x, z.y, z.z, z.w};
             float v[8];
 #pragma unroll
             for (int j = 0; j < 8; ++j) v[j] = half_of(w[j >> 1], j & 1, TQ()) * scale;
             uint8_t* dst = q_smem + (u >> 4) * (N * 128) + r * 128 + ((((u & 15) >> 1) ^ (r & 7)) << 4) + (u & 1) * 8;
 #pragma unroll
             for (int c = 0; c < kParts; ++c) {
-              uint32_t y[4];
+              uint32_t q[4];
 #pragma unroll
-              for (int j = 0; j < 4; ++j) y[j] = part2(v[2 * j], v[2 * j + 1]);
-              *reinterpret_cast<uint2*>(dst + c * (5 * N * 128)) = make_uint2(y[0] | y[1] << 16, y[2] | y[3] << 16);
+              for (int j = 0; j < 4; ++j) q[j] = part2(v[2 * j], v[2 * j + 1]);
+              *reinterpret_cast<uint2*>(dst + c * (5 * N * 128)) = make_uint2(q[0] | q[1] << 16, q[2] | q[3] << 16);
             }
           }
         }
@@ -266,7 +285,8 @@ __global__ void __launch_bounds__(kThreads, 1)
   pdl_entry();
 
   const int unit = blockIdx.x / p.groups, group = blockIdx.x % p.groups;
-  const Share share = find_share([&](int b) { return decode_tiles(p, b); }, p.R, unit, p.units, mi.scratch, mi.found);
+  const Share share = find_share([&](int b) -> int64_t { return pieces_of(decode_len(p, b).use); }, p.R, unit, p.units,
+                                 mi.scratch, mi.found);
   tmem_fence_before();
   __syncthreads();
   tmem_fence_after();
@@ -290,17 +310,19 @@ __global__ void __launch_bounds__(kThreads, 1)
       if (lane == 0) bad |= decode_len(p, it.b).bad;
       if (it.len == 0) continue;
       const int32_t* table = p.bt + static_cast<int64_t>(it.b) * p.bt_stride;
-      for (int i = 0; i < it.n && alive; ++i, ++t) {
+      // lane s < segs looks up the page of box s, one tile ahead of its use
+      auto page_of = [&](int j) {
+        return lane < segs && j < it.len ? table[static_cast<uint32_t>(j) / static_cast<uint32_t>(p.B)] : -1;
+      };
+      int j = it.tile * kDecodeTile + lane * box_rows;
+      int next_id = page_of(j);
+#pragma unroll 1
+      for (int i = 0; i < it.n; ++i, ++t, j += kDecodeTile) {
         const int j0 = (it.tile + i) * kDecodeTile;
-        // lane s < segs looks up the page of box s
-        const int j = j0 + lane * box_rows;
         const bool in = lane < segs && j < it.len;
-        int id = -1, row = 0;
-        if (in) {
-          const uint32_t page = static_cast<uint32_t>(j) / static_cast<uint32_t>(p.B);
-          id = table[page];
-          row = j - static_cast<int>(page) * p.B;
-        }
+        int id = next_id;
+        const int row = static_cast<int>(static_cast<uint32_t>(j) % static_cast<uint32_t>(p.B));
+        next_id = i + 1 < it.n ? page_of(j + kDecodeTile) : -1;
         const bool good = id >= 0 && id < p.num_blocks;
         if (in && !good) {
           bad |= PMG_FLAG_PHYS_BLOCK;
@@ -317,36 +339,46 @@ __global__ void __launch_bounds__(kThreads, 1)
           mi.mask[t & 7] = m;
         }
         const uint32_t bytes = static_cast<uint32_t>(n_boxes * box_rows * 128);
+        const int id0 = __shfl_sync(0xffffffffu, id, 0), row0 = __shfl_sync(0xffffffffu, row, 0);
+        if (stopped(stop)) {
+          alive = false;
+          break;
+        }
 #pragma unroll 1
         for (int m = 0; m < 4; ++m) {
           mbar_wait(empty + 8 * slot, phase ^ 1, stop);
-          alive = !stopped(stop);
-          if (!alive) break;
-          const uint32_t dst = base + L::kSlotAt + slot * L::kSlot;
-          if (elect_one()) mbar_expect(full + 8 * slot, bytes * L::kPieces);
-          for (int s = 0; s < n_boxes; ++s) {
-            const int sid = __shfl_sync(0xffffffffu, id, s), srow = __shfl_sync(0xffffffffu, row, s);
+          const uint32_t dst = base + L::kSlotAt + slot * L::kSlot, bar = full + 8 * slot;
+          if (n_boxes == 1 && box_rows == kDecodeTile) {
+            if (elect_one()) {
+              mbar_expect(bar, L::kSlot);
+              tma_load_4d(dst, &map, bar, 0, row0, m * L::kPieces, id0);
+            }
+          } else {
             // boxes of fewer rows than a slot has leave gaps between their pieces: a copy a piece
-            if (box_rows == kDecodeTile) {
-              if (elect_one()) tma_load_4d(dst, &map, full + 8 * slot, 0, srow, m * L::kPieces, sid);
-            } else if (elect_one()) {
+            if (elect_one()) mbar_expect(bar, bytes * L::kPieces);
+#pragma unroll 1
+            for (int s = 0; s < n_boxes; ++s) {
+              const int sid = __shfl_sync(0xffffffffu, id, s), srow = __shfl_sync(0xffffffffu, row, s);
+              if (elect_one()) {
 #pragma unroll
-              for (int c = 0; c < L::kPieces; ++c)
-                tma_load_4d(dst + c * L::kPiece + s * box_rows * 128, &map, full + 8 * slot, 0, srow, m * L::kPieces + c, sid);
+                for (int c = 0; c < L::kPieces; ++c)
+                  tma_load_4d(dst + c * L::kPiece + s * box_rows * 128, &map, bar, 0, srow, m * L::kPieces + c, sid);
+              }
             }
           }
+          __syncwarp();
           if (++slot == L::kSlots) { slot = 0; phase ^= 1; }
         }
-        if (!alive) break;
         mbar_wait(rope_empty + 8 * rslot, rphase ^ 1, stop);
-        alive = !stopped(stop);
-        if (!alive) break;
         if (elect_one()) mbar_expect(rope_full + 8 * rslot, bytes);
+        __syncwarp();
+#pragma unroll 1
         for (int s = 0; s < n_boxes; ++s) {
           const int sid = __shfl_sync(0xffffffffu, id, s), srow = __shfl_sync(0xffffffffu, row, s);
           if (elect_one())
             tma_load_3d(base + L::kRopeAt + rslot * L::kPiece + s * box_rows * 128, &rope_map, rope_full + 8 * rslot, kLatent,
                         srow, sid);
+          __syncwarp();
         }
         if (++rslot == L::kRopeSlots) { rslot = 0; rphase ^= 1; }
       }
@@ -378,89 +410,102 @@ __global__ void __launch_bounds__(kThreads, 1)
     // O of the oldest tile
     auto values = [&]() {
       tmem_fence_after();
-      const uint32_t leader = elect_one();
-      const uint64_t pa = umma_desc(base + L::kPAt, L::kPiece, 1024);
       const bool first = v_tile == 0;
+      if (elect_one()) {
+        const uint64_t pa = umma_desc(base + L::kPAt, L::kPiece, 1024);
+        int at = vslot;
 #pragma unroll
-      for (int m = 0; m < 4; ++m) {
-        const uint64_t va = umma_desc(base + L::kSlotAt + vslot * L::kSlot, L::kPiece, 1024);
-        const uint32_t d = tmem + (2 + m) * N;
+        for (int m = 0; m < 4; ++m) {
+          const uint64_t va = umma_desc(base + L::kSlotAt + at * L::kSlot, L::kPiece, 1024);
+          const uint32_t d = tmem + (2 + m) * N;
 #pragma unroll
-        for (int k = 0; k < (kFp8 ? 2 : 4); ++k) {
-          const uint32_t step = k * (kFp8 ? 32 : 16) * 8;  // rows of 128 bytes, in units of 16
-          umma_ss<kFp8>(leader, d, va + step, pa + step, kIdescO, !first || k > 0);
-          if constexpr (kFp8) umma_ss<kFp8>(leader, d, va + step, pa + step + L::kPiece / 16, kIdescO, true);
+          for (int k = 0; k < (kFp8 ? 2 : 4); ++k) {
+            const uint32_t step = k * (kFp8 ? 32 : 16) * 8;  // rows of 128 bytes, in units of 16
+            umma_ss<kFp8>(d, va + step, pa + step, kIdescO, !first || k > 0);
+            if constexpr (kFp8) umma_ss<kFp8>(d, va + step, pa + step + L::kPiece / 16, kIdescO, true);
+          }
+          umma_commit(empty + 8 * at);
+          if (++at == L::kSlots) at = 0;
         }
-        umma_commit(leader, empty + 8 * vslot);
-        if (++vslot == L::kSlots) vslot = 0;
+        umma_commit(smem_u32(&mi.pv_done));
       }
-      umma_commit(leader, smem_u32(&mi.pv_done));
+      __syncwarp();
+      vslot = vslot + 4 < L::kSlots ? vslot + 4 : vslot + 4 - L::kSlots;
       ++vt;
       if (++v_tile == vi.n) {
         v_tile = 0;
         v_more = advance(vi);
       }
     };
-    // Parts of S of a tile as they arrive; O of the tile before it as soon as its weights are there.
-    while (q_more) {
-      const uint32_t buf = qt & 1, d = tmem + buf * N;
-      if (qt >= 2) mbar_wait(s_free + 8 * buf, ((qt >> 1) + 1) & 1, stop);
-      if (q_tile == 0) {
-        // these queries come after the last product with the ones before
-        while (vt != qt && mbar_wait_either(p_full, vt & 1, smem_u32(&mi.q_full), q_item & 1, stop)) values();
-        mbar_wait(smem_u32(&mi.q_full), q_item & 1, stop);
-        ++q_item;
+    // Parts of S of a tile as they arrive (the rotated part last); O of the tile before it as soon as its weights are
+    // there, and before a third tile's scores. One loop, so that this role's code stays small.
+    int part = 0;
+    while (q_more || v_more) {
+      const uint32_t buf = qt & 1;
+      if (q_more && part == 0 && qt - vt < 2) {
+        if (qt >= 2) mbar_wait(s_free + 8 * buf, ((qt >> 1) + 1) & 1, stop);
       }
-#pragma unroll 1
-      for (int part = 0; part < 4; ++part) {
-        if (vt != qt && mbar_wait_either(p_full, vt & 1, full + 8 * qslot, qphase, stop)) values();
+      // what the next part of S waits for: its slot, or the queries of a new request
+      const bool new_item = part == 0 && q_tile == 0;
+      const uint32_t bar = new_item ? smem_u32(&mi.q_full) : part < 4 ? full + 8 * qslot : rope_full + 8 * rslot;
+      const uint32_t parity = new_item ? q_item & 1 : part < 4 ? qphase : rphase;
+      if (vt != qt) {
+        bool ready = true;
+        if (!q_more || qt - vt == 2) mbar_wait(p_full, vt & 1, stop);
+        else ready = mbar_wait_either(p_full, vt & 1, bar, parity, stop);
+        if (ready) {
+          values();
+          continue;
+        }
+      }
+      if (new_item) mbar_wait(bar, parity, stop);
+      const uint32_t d = tmem + buf * N;
+      if (part < 4) {
         mbar_wait(full + 8 * qslot, qphase, stop);
         tmem_fence_after();
-        const uint32_t leader = elect_one();
+        if (elect_one()) {
 #pragma unroll
-        for (int c = 0; c < L::kPieces; ++c) {
-          const uint64_t ka = umma_desc(base + L::kSlotAt + qslot * L::kSlot + c * L::kPiece, 16, 1024);
-          const uint64_t qa = umma_desc(base + L::kQAt + (part * L::kPieces + c) * (N * 128), 16, 1024);
+          for (int c = 0; c < L::kPieces; ++c) {
+            const uint64_t ka = umma_desc(base + L::kSlotAt + qslot * L::kSlot + c * L::kPiece, 16, 1024);
+            const uint64_t qa = umma_desc(base + L::kQAt + (part * L::kPieces + c) * (N * 128), 16, 1024);
 #pragma unroll
-          for (int k = 0; k < 4; ++k)  // 32 bytes of K each
+            for (int k = 0; k < 4; ++k)  // 32 bytes of K each
+#pragma unroll
+              for (int x = 0; x < kParts; ++x)
+                umma_ss<kFp8>(d, ka + 2 * k, qa + 2 * k + x * (5 * N * 8), kIdescS, part > 0 || c > 0 || k > 0 || x > 0);
+          }
+        }
+        __syncwarp();
+        if (++qslot == L::kSlots) { qslot = 0; qphase ^= 1; }
+        ++part;
+      } else {
+        mbar_wait(rope_full + 8 * rslot, rphase, stop);
+        tmem_fence_after();
+        if (elect_one()) {
+          const uint64_t ka = umma_desc(base + L::kRopeAt + rslot * L::kPiece, 16, 1024);
+          const uint64_t qa = umma_desc(base + L::kQAt + 4 * L::kPieces * (N * 128), 16, 1024);
+#pragma unroll
+          for (int k = 0; k < (kFp8 ? 2 : 4); ++k)
 #pragma unroll
             for (int x = 0; x < kParts; ++x)
-              umma_ss<kFp8>(leader, d, ka + 2 * k, qa + 2 * k + x * (5 * N * 8), kIdescS,
-                            part > 0 || c > 0 || k > 0 || x > 0);
+              umma_ss<kFp8>(d, ka + 2 * k, qa + 2 * k + x * (5 * N * 8), kIdescS, true);
+          umma_commit(rope_empty + 8 * rslot);
+          umma_commit(s_full + 8 * buf);
         }
-        if (++qslot == L::kSlots) { qslot = 0; qphase ^= 1; }
+        __syncwarp();
+        if (++rslot == L::kRopeSlots) { rslot = 0; rphase ^= 1; }
+        part = 0;
+        ++qt;
+        if (q_tile == 0) ++q_item;
+        if (++q_tile == qi.n) {
+          q_tile = 0;
+          q_more = advance(qi);
+        }
       }
-      if (vt != qt && mbar_wait_either(p_full, vt & 1, rope_full + 8 * rslot, rphase, stop)) values();
-      mbar_wait(rope_full + 8 * rslot, rphase, stop);
-      tmem_fence_after();
-      const uint32_t leader = elect_one();
-      const uint64_t ka = umma_desc(base + L::kRopeAt + rslot * L::kPiece, 16, 1024);
-      const uint64_t qa = umma_desc(base + L::kQAt + 4 * L::kPieces * (N * 128), 16, 1024);
-#pragma unroll
-      for (int k = 0; k < (kFp8 ? 2 : 4); ++k)
-#pragma unroll
-        for (int x = 0; x < kParts; ++x)
-          umma_ss<kFp8>(leader, d, ka + 2 * k, qa + 2 * k + x * (5 * N * 8), kIdescS, true);
-      umma_commit(leader, rope_empty + 8 * rslot);
-      umma_commit(leader, s_full + 8 * buf);
-      if (++rslot == L::kRopeSlots) { rslot = 0; rphase ^= 1; }
-      ++qt;
-      if (++q_tile == qi.n) {
-        q_tile = 0;
-        q_more = advance(qi);
-      }
-      // at most two tiles' scores are ahead of the weights
-      if (qt - vt == 2) {
-        mbar_wait(p_full, vt & 1, stop);
-        values();
-      }
-    }
-    while (v_more) {
-      mbar_wait(p_full, vt & 1, stop);
-      values();
     }
     // everything issued ends before the tensor memory is given back
-    umma_commit(elect_one(), smem_u32(&mi.end));
+    if (elect_one()) umma_commit(smem_u32(&mi.end));
+    __syncwarp();
     mbar_wait(smem_u32(&mi.end), 0, smem_u32(&mi.never));
   } else {
     // ---- softmax and epilogue ----
@@ -480,14 +525,6 @@ __global__ void __launch_bounds__(kThreads, 1)
     JoinNote note{-1, 0, 0, 0};
     uint32_t t = 0;                 // tiles of the share
     uint32_t slot0 = 0, phase0 = 0; // slot of the tile's first part, its phase
-    bool more = it.next();
-    // queries of the first request that has any keys
-    auto queries = [&](const Items& x) {
-      load_queries<TQ, kParts, N>(p, x.b, g0, n_rows, smem + L::kQAt, mi, factor);
-      fence_async_smem();
-      __syncwarp();
-      if (lane == 0) mbar_arrive(smem_u32(&mi.q_full));
-    };
     const int step0 = g0 / p.H;  // the group's first new token
     if (tid < N) mi.step[tid] = static_cast<uint8_t>((g0 + tid) / p.H - step0);
     // where row h of the group is in a request's output
@@ -495,12 +532,76 @@ __global__ void __launch_bounds__(kThreads, 1)
       const int step = step0 + mi.step[h];
       return step * p.ot_stride + (g0 + h - step * p.H) * p.oh_stride;
     };
-    bool loaded = false;  // whether the queries of `it` are in place
-    while (more) {
-      if (it.len > 0 && !loaded) queries(it);
-      Items ahead = it;
-      const bool more_ahead = ahead.next();
-      const int n = it.len > 0 ? it.n : 0;
+    // For each request: its queries, then the epilogue of the request before (whose last product runs meanwhile), then
+    // its tiles.
+    bool more = it.next();
+    int prev_b = -1, prev_n = 0;
+    bool prev_whole = false;
+    float* prev_slot = nullptr;
+    for (;;) {
+      if (more && it.len > 0) {
+        load_queries<TQ, kParts, N>(p, it.b, g0, n_rows, smem + L::kQAt, mi, factor);
+        fence_async_smem();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(smem_u32(&mi.q_full));
+      }
+      if (prev_b >= 0) {
+        if (prev_n > 0) mbar_wait(smem_u32(&mi.pv_done), (t - 1) & 1, stop);
+        tmem_fence_after();
+        TQ* out = static_cast<TQ*>(p.out) + prev_b * p.or_stride;
+        const int d = warp * 32 + lane;  // and 128 further for each m
+#pragma unroll 1
+        for (int h0 = 0; h0 < n_rows; h0 += 16) {
+          uint32_t o[4][16];
+          __syncwarp();
+          if (prev_n > 0) {
+#pragma unroll
+            for (int m = 0; m < 4; ++m) tmem_ld16(tmem + (2 + m) * N + h0 + lanes, o[m]);
+            tmem_wait_ld();
+#pragma unroll
+            for (int m = 0; m < 4; ++m) tmem_pin<16>(o[m]);
+          } else {
+#pragma unroll
+            for (int m = 0; m < 4; ++m)
+#pragma unroll
+              for (int k = 0; k < 16; ++k) o[m][k] = 0;
+          }
+          if (!prev_whole) {
+            float* at = prev_slot + h0 * kLatent + d;
+#pragma unroll
+            for (int k = 0; k < 16; ++k)
+              if (h0 + k < n_rows) {
+#pragma unroll
+                for (int m = 0; m < 4; ++m) at[k * kLatent + m * 128] = __uint_as_float(o[m][k]) * kv_scale;
+              }
+          } else {
+#pragma unroll
+            for (int k = 0; k < 16; k += 2) {
+              // even lanes write row k, odd lanes row k + 1, two neighbours' values each
+              const int h = h0 + k + (lane & 1);
+              const float ia = mi.inv[h0 + k], ib = mi.inv[h0 + k + 1];
+              TQ* at = out + out_at(min(h, n_rows - 1)) + (d & ~1);
+#pragma unroll
+              for (int m = 0; m < 4; ++m) {
+                const float a = __uint_as_float(o[m][k]) * ia, b = __uint_as_float(o[m][k + 1]) * ib;
+                const float other = __shfl_xor_sync(0xffffffffu, lane & 1 ? a : b, 1);
+                const uint32_t two = lane & 1 ? pack2<TQ>(other, b) : pack2<TQ>(a, other);
+                if (h < n_rows) {
+                  if (p.out_pairs) {
+                    *reinterpret_cast<uint32_t*>(at + m * 128) = two;
+                  } else {
+                    reinterpret_cast<uint16_t*>(at + m * 128)[0] = static_cast<uint16_t>(two);
+                    reinterpret_cast<uint16_t*>(at + m * 128)[1] = static_cast<uint16_t>(two >> 16);
+                  }
+                }
+              }
+            }
+          }
+        }
+        tmem_fence_before();
+      }
+      if (!more) break;
+      const int n = it.n;
       named_sync<kSoft>(1);  // the queries' factors are there, and everybody is done with the last request's sums
       float ref[2 * kG], l[2 * kG], f[2 * kG];  // of columns 8 g + 2 c and the next
 #pragma unroll
@@ -654,7 +755,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
 
       // sums of every row over the lanes, then over the warps in their order
-      const bool whole = it.tile == 0 && it.n == it.tiles;
+      const bool whole = it.n == it.tiles;  // (an empty request too)
 #pragma unroll
       for (int k = 0; k < 2 * kG; ++k) {
 #pragma unroll
@@ -679,60 +780,16 @@ __global__ void __launch_bounds__(kThreads, 1)
           }
         }
       }
-      // the next request's queries, while the last product runs
-      loaded = false;
-      if (more_ahead && ahead.len > 0) {
-        queries(ahead);
-        loaded = true;
-      }
       if (!whole && it.tile == 0 && tid == 0) {
         note.item = it.b;
-        note.parts = unit_of(it.piece() + it.tiles - 1, share.total, share.units) - unit + 1;
+        note.parts = unit_of(it.last_piece(), share.total, share.units) - unit + 1;
       }
-      if (n > 0) mbar_wait(smem_u32(&mi.pv_done), (t - 1) & 1, stop);
-      named_sync<kSoft>(1);  // the sums
-      tmem_fence_after();
-      TQ* out = static_cast<TQ*>(p.out) + it.b * p.or_stride;
-#pragma unroll 1
-      for (int m = 0; m < 4; ++m) {
-        const int d = m * 128 + warp * 32 + lane;
-#pragma unroll 1
-        for (int h0 = 0; h0 < N && h0 < n_rows; h0 += 16) {
-          uint32_t o[16];
-          __syncwarp();
-          if (n > 0) {
-            tmem_ld16(tmem + (2 + m) * N + h0 + lanes, o);
-            tmem_wait_ld();
-            tmem_pin<16>(o);
-          } else {
-#pragma unroll
-            for (int k = 0; k < 16; ++k) o[k] = 0;
-          }
-          if (whole) {
-#pragma unroll
-            for (int k = 0; k < 16; k += 2) {
-              const float a = __uint_as_float(o[k]) * mi.inv[h0 + k], b = __uint_as_float(o[k + 1]) * mi.inv[h0 + k + 1];
-              if (p.out_pairs) {
-                // even lanes write row k, odd lanes row k + 1, two neighbours' values each
-                const float other = __shfl_xor_sync(0xffffffffu, lane & 1 ? a : b, 1);
-                const int h = h0 + k + (lane & 1);
-                if (h < n_rows)
-                  *reinterpret_cast<uint32_t*>(out + out_at(h) + (d & ~1)) = lane & 1 ? pack2<TQ>(other, b) : pack2<TQ>(a, other);
-              } else {
-                if (h0 + k < n_rows) out[out_at(h0 + k) + d] = from_f<TQ>(a);
-                if (h0 + k + 1 < n_rows) out[out_at(h0 + k + 1) + d] = from_f<TQ>(b);
-              }
-            }
-          } else {
-#pragma unroll
-            for (int k = 0; k < 16; ++k)
-              if (h0 + k < n_rows) slot[(h0 + k) * kLatent + d] = __uint_as_float(o[k]) * kv_scale;
-          }
-        }
-      }
-      tmem_fence_before();
-      it = ahead;
-      more = more_ahead;
+      named_sync<kSoft>(1);  // the rows' factors are there for the epilogue
+      prev_b = it.b;
+      prev_n = n;
+      prev_whole = whole;
+      prev_slot = slot;
+      more = it.next();
     }
     if (tid == 0 && p.units > 1) p.ws.notes[blockIdx.x] = note;
     if (stopped(stop) && tid == 0) set_flag(p.err, PMG_FLAG_TIMEOUT);

@@ -64,14 +64,16 @@ __device__ __forceinline__ int keys_of(const PrefillReq& x, int t, int causal) {
   const int64_t end = min(static_cast<int64_t>(x.lq), static_cast<int64_t>(t + 1) * kRows);
   return static_cast<int>(max(static_cast<int64_t>(0), min(static_cast<int64_t>(x.lk), x.lk - x.lq + end)));
 }
+constexpr int kItemCost = 1;  // what an item's beginning and end cost, in blocks
 __device__ __forceinline__ int blocks_of(int keys) { return keys > 0 ? (keys + kBlock - 1) / kBlock : 1; }
 __device__ __forceinline__ int tiles_of(const PrefillReq& x) { return (x.lq + kRows - 1) / kRows; }
 
-// blocks of one head of a request
+// pieces of one head of a request
 __device__ __forceinline__ int64_t head_pieces(const PrefillReq& x, int causal) {
   const int n = tiles_of(x);
-  if (!causal) return static_cast<int64_t>(n) * blocks_of(x.lk);
-  int64_t s = 0;
+  if (!causal) return static_cast<int64_t>(n) * (kItemCost + blocks_of(x.lk));
+  int64_t s = static_cast<int64_t>(n) * kItemCost;
+#pragma unroll 1
   for (int t = 0; t < n; ++t) s += blocks_of(keys_of(x, t, causal));
   return s;
 }
@@ -85,38 +87,50 @@ struct Items {
   int nb, b0, n;
   int act[2];   // blocks that each half takes part in (of the item's nb)
   int keys;     // keys of the item
+  int skip;     // pieces of the item before this share
+  int64_t first;  // its first piece
   bool begun;
 
   __device__ Items(const PrefillParams& p_, const Share& s) : p(&p_), at(s.begin), end(s.end) {
     r = s.item;
     head = tile = nb = b0 = n = keys = 0;
+    skip = 0;
     begun = false;
     if (at < end) {
       x = prefill_req(*p, r);
       const int64_t per = head_pieces(x, p->causal);
       head = static_cast<int>(s.offset / per);
-      int64_t left = s.offset % per;
-      while (left >= blocks_of(keys_of(x, tile, p->causal))) left -= blocks_of(keys_of(x, tile++, p->causal));
-      b0 = static_cast<int>(left);
+      int64_t left = s.offset - head * per;
+      for (;;) {
+        const int here = kItemCost + blocks_of(keys_of(x, tile, p->causal));
+        if (left < here) break;
+        left -= here;
+        ++tile;
+      }
+      skip = static_cast<int>(left);
     }
   }
+  // the next item of which this share has blocks
   __device__ bool next() {
-    if (at >= end) return false;
-    if (begun) {
-      b0 = 0;
-      if (++tile >= tiles_of(x)) {
+    do {
+      if (at >= end) return false;
+      if (begun && ++tile >= tiles_of(x)) {
         tile = 0;
         if (++head >= p->H) {
           head = 0;
           do x = prefill_req(*p, ++r); while (x.lq == 0);
         }
       }
-    }
-    begun = true;
-    keys = keys_of(x, tile, p->causal);
-    nb = blocks_of(keys);
-    n = static_cast<int>(min(static_cast<int64_t>(nb - b0), end - at));
-    at += n;
+      begun = true;
+      keys = keys_of(x, tile, p->causal);
+      nb = blocks_of(keys);
+      first = at - skip;
+      const int take = static_cast<int>(min(static_cast<int64_t>(kItemCost + nb - skip), end - at));
+      b0 = max(0, skip - kItemCost);
+      n = max(0, skip + take - kItemCost) - b0;
+      at += take;
+      skip = 0;
+    } while (n == 0);
     // the first half's last row may see fewer keys; the second half may not exist
     const int rows = x.lq - tile * kRows;
     int k0 = keys;
@@ -126,7 +140,8 @@ struct Items {
     act[1] = rows > kHalf && keys > 0 ? nb : 0;
     return true;
   }
-  __device__ int64_t piece() const { return at - n; }
+  // the piece of the item's last block
+  __device__ int64_t last_piece() const { return first + kItemCost + nb - 1; }
   // blocks of this share that half h takes part in: [b0, last(h))
   __device__ int last(int h) const { return min(b0 + n, act[h]); }
 };
@@ -179,7 +194,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   tmem_fence_before();
   __syncthreads();
   tmem_fence_after();
-  const uint32_t tmem = mi.tmem;  // S of the halves at columns 0 and 128, O at 256 and 384
+  const uint32_t tmem = static_cast<uint32_t>(uniform(static_cast<int>(mi.tmem)));  // S of the halves at columns 0 and 128, O at 256 and 384
   const uint32_t stop = smem_u32(&mi.stop);
   constexpr int kFmt = std::is_same<T, bf16>::value ? 1 : 0;
   constexpr uint32_t kIdescS = umma_idesc(kFmt, 0, 0, 128, kBlock);
@@ -265,56 +280,63 @@ __global__ void __launch_bounds__(kThreads, 1)
       auto wait_block = [&](uint32_t full, uint32_t st) { mbar_wait(full + 8 * (st & 1), st >> 1 & 1, stop); };
       // S of half h for the block of step st
       auto scores = [&](int h, uint32_t st) {
-        const uint32_t leader = elect_one();
+        if (elect_one()) {
 #pragma unroll
-        for (uint32_t c = 0; c < 3; ++c) {
-          const uint64_t qa = umma_desc(base + kQAt + (3 * h + c) * kPiece, 16, 1024);
-          const uint64_t ka = umma_desc(base + kSlotAt + slot_of(st, c) * kPiece, 16, 1024);
+          for (uint32_t c = 0; c < 3; ++c) {
+            const uint64_t qa = umma_desc(base + kQAt + (3 * h + c) * kPiece, 16, 1024);
+            const uint64_t ka = umma_desc(base + kSlotAt + slot_of(st, c) * kPiece, 16, 1024);
 #pragma unroll
-          for (int k = 0; k < 4; ++k)  // 32 bytes of K each
-            umma_ss<false>(leader, tmem + h * kBlock, qa + 2 * k, ka + 2 * k, kIdescS, c > 0 || k > 0);
+            for (int k = 0; k < 4; ++k)  // 32 bytes of K each
+              umma_ss<false>(tmem + h * kBlock, qa + 2 * k, ka + 2 * k, kIdescS, c > 0 || k > 0);
+          }
+          umma_commit(s_full + 8 * h);
         }
-        umma_commit(leader, s_full + 8 * h);
+        __syncwarp();
       };
       // O of half h: the products with keys 64 w to 64 w + 63 of the block
       auto values = [&](int h, int w, uint32_t st, bool first) {
         // the two 64-value pieces of V are two slots, which may wrap around the ring: a product of 64 each then
-        const uint32_t leader = elect_one();
         const uint32_t d = tmem + 256 + h * kVal, a = tmem + h * kBlock + 32 * w;
         const uint64_t v0 = umma_desc(base + kSlotAt + slot_of(st, 3) * kPiece + w * 8192, kPiece, 1024);
         if (slot_of(st, 4) != 0) {
+          if (elect_one()) {
 #pragma unroll
-          for (int k = 0; k < 4; ++k) umma_ts(leader, d, a + 8 * k, v0 + 128 * k, kIdescO, !first || w > 0 || k > 0);
+            for (int k = 0; k < 4; ++k) umma_ts(d, a + 8 * k, v0 + 128 * k, kIdescO, !first || w > 0 || k > 0);
+            if (w == 1) umma_commit(o_done + 8 * h);
+          }
         } else {
           const uint64_t v1 = umma_desc(base + kSlotAt + w * 8192, kPiece, 1024);
           constexpr uint32_t kIdescHalf = umma_idesc(kFmt, 0, 1, 128, 64);
+          if (elect_one()) {
 #pragma unroll
-          for (int k = 0; k < 4; ++k) {
-            umma_ts(leader, d, a + 8 * k, v0 + 128 * k, kIdescHalf, !first || w > 0 || k > 0);
-            umma_ts(leader, d + 64, a + 8 * k, v1 + 128 * k, kIdescHalf, !first || w > 0 || k > 0);
+            for (int k = 0; k < 4; ++k) {
+              umma_ts(d, a + 8 * k, v0 + 128 * k, kIdescHalf, !first || w > 0 || k > 0);
+              umma_ts(d + 64, a + 8 * k, v1 + 128 * k, kIdescHalf, !first || w > 0 || k > 0);
+            }
+            if (w == 1) umma_commit(o_done + 8 * h);
           }
         }
-        if (w == 1) umma_commit(leader, o_done + 8 * h);
+        __syncwarp();
       };
       uint32_t items = 0, cleans = 0;
       uint32_t step = 0;   // blocks begun
       uint32_t taken = 0;  // parity of the weights taken, a bit a half
-      while (it.next()) {
-        if (it.keys == 0) continue;
+      while (uniform(it.next())) {
+        if (uniform(it.keys) == 0) continue;
         mbar_wait(smem_u32(&mi.q_full), items++ & 1, stop);
-        const int end = it.b0 + it.n;
-        const bool partial_end = end == it.nb && it.x.lk - (end - 1) * kBlock < kBlock;  // warp 10's rule
-        const int last0 = it.last(0), last1 = it.last(1);
+        const int end = uniform(it.b0 + it.n), begin = uniform(it.b0);
+        const bool partial_end = uniform(end == it.nb && it.x.lk - (end - 1) * kBlock < kBlock);  // warp 10's rule
+        const int last0 = uniform(it.last(0)), last1 = uniform(it.last(1));
         wait_block(k_full, step);
         tmem_fence_after();
-        if (it.b0 < last0) scores(0, step);
-        if (it.b0 < last1) scores(1, step);
-        {
-          const uint32_t leader = elect_one();
-          umma_commit(leader, k_empty + 8 * (step & 1));
-          if (it.n == 1) umma_commit(leader, smem_u32(&mi.q_empty));
+        if (begin < last0) scores(0, step);
+        if (begin < last1) scores(1, step);
+        if (elect_one()) {
+          umma_commit(k_empty + 8 * (step & 1));
+          if (begin + 1 == end) umma_commit(smem_u32(&mi.q_empty));
         }
-        for (int b = it.b0; b < end; ++b, ++step) {
+        __syncwarp();
+        for (int b = begin; b < end; ++b, ++step) {
           const bool more = b + 1 < end;
           wait_block(v_full, step);
           if (!more && partial_end) {
@@ -328,10 +350,10 @@ __global__ void __launch_bounds__(kThreads, 1)
             if (b < last) {
               mbar_wait(p_full + 16 * h, taken >> h & 1, stop);
               tmem_fence_after();
-              values(h, 0, step, b == it.b0);
+              values(h, 0, step, b == begin);
               mbar_wait(p_full + 16 * h + 8, taken >> h & 1, stop);
               tmem_fence_after();
-              values(h, 1, step, b == it.b0);
+              values(h, 1, step, b == begin);
               taken ^= 1u << h;
             }
             if (h == 0 && more) {
@@ -340,16 +362,17 @@ __global__ void __launch_bounds__(kThreads, 1)
             }
             if (b + 1 < last) scores(h, step + 1);
           }
-          const uint32_t leader = elect_one();
-          umma_commit(leader, v_empty + 8 * (step & 1));
-          if (more) {
-            umma_commit(leader, k_empty + 8 * ((step + 1) & 1));
-            if (b + 2 == end) umma_commit(leader, smem_u32(&mi.q_empty));
+          if (elect_one()) {
+            umma_commit(v_empty + 8 * (step & 1));
+            if (more) umma_commit(k_empty + 8 * ((step + 1) & 1));
+            if (b + 2 == end) umma_commit(smem_u32(&mi.q_empty));
           }
+          __syncwarp();
         }
       }
       // everything issued ends before the tensor memory is given back
-      umma_commit(elect_one(), smem_u32(&mi.end));
+      if (elect_one()) umma_commit(smem_u32(&mi.end));
+      __syncwarp();
       mbar_wait(smem_u32(&mi.end), 0, smem_u32(&mi.never));
     } else if (warp == 10) {
       // ---- value rows past a request's end ----
@@ -477,7 +500,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         note.item = it.r;
         note.head = it.head;
         note.tile = it.tile;
-        note.parts = unit_of(it.piece() + it.nb - 1, share.total, share.units) - unit + 1;
+        note.parts = unit_of(it.last_piece(), share.total, share.units) - unit + 1;
       }
       float* slot = p.ws.slots + (static_cast<int64_t>(unit) * 2 + (it.b0 == 0 ? 1 : 0)) * kSlotFloats;
       const int64_t t = it.x.q0 + i;
@@ -552,61 +575,33 @@ __global__ void __launch_bounds__(kThreads, 1)
   if (warp == 9) tmem_free(tmem, 512);
 }
 
-// The join: a warp a row, four columns a lane, parts in the order of the shares.
-constexpr int kJoinRows = 8;
-
 template <class T>
-__global__ void __launch_bounds__(kJoinRows * 32) prefill_join_kernel(const __grid_constant__ PrefillParams p) {
+__global__ void __launch_bounds__(kJoinThreads) prefill_join_kernel(const __grid_constant__ PrefillParams p) {
   pdl_entry();
-  const JoinNote note = p.ws.notes[blockIdx.x];
-  if (note.item < 0) return;
-  const PrefillReq x = prefill_req(p, note.item);
-  const int row = blockIdx.y * kJoinRows + (threadIdx.x >> 5), lane = threadIdx.x & 31;
-  const int i = note.tile * kRows + row;
-  if (i >= x.lq) return;
-  auto slot_of = [&](int k) {
-    return p.ws.slots + (static_cast<int64_t>(blockIdx.x + k) * 2 + (k == 0 ? 1 : 0)) * kSlotFloats;
-  };
-  const int ml = kRows * kSlotRow + 2 * row;
-  float top = -INFINITY;
-  for (int k = lane; k < note.parts; k += 32) top = fmaxf(top, slot_of(k)[ml]);
+  join_rows(
+      p.ws, p.units, 1, kRows, kVal, kSlotFloats,
+      [&](const JoinNote& note, int, int row) { return note.tile * kRows + row < prefill_req(p, note.item).lq; },
+      [&](const JoinNote& note, int, int row, int d, const float4& a, float top, float l) {
+        const int64_t t = static_cast<int64_t>(prefill_req(p, note.item).q0) + note.tile * kRows + row;
+        float lse = l > 0.0f ? (top + log2f(l)) * kLn2 : -INFINITY;
+        float now = l > 0.0f ? 1.0f / l : 0.0f, before = 0.0f;
+        if (p.prev_lse != nullptr) {
+          const Joined g = join_state(lse, p.prev_lse[t * p.H + note.head]);
+          now *= g.now;
+          before = g.before;
+          lse = g.lse;
+        }
+        __syncwarp();  // every lane has read prev_lse, which lse may be
+        if (d == 0 && p.lse != nullptr) p.lse[t * p.H + note.head] = lse;
+        float y[4] = {a.x * now, a.y * now, a.z * now, a.w * now};
+        if (before != 0.0f) {
+          const T* prev = static_cast<const T*>(p.prev) + t * p.pt_stride + note.head * p.ph_stride + d;
 #pragma unroll
-  for (int o = 16; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
-  float l = 0.0f;
-  float4 a = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-#pragma unroll 4
-  for (int k = 0; k < note.parts; ++k) {
-    const float* slot = slot_of(k);
-    const float m = slot[ml];
-    const float w = m == -INFINITY ? 0.0f : exp2f(m - top);
-    l += w * slot[ml + 1];
-    const float4 v = *reinterpret_cast<const float4*>(slot + row * kSlotRow + 4 * lane);
-    if (w != 0.0f) {  // a part in which the row saw nothing may have no values
-      a.x += w * v.x;
-      a.y += w * v.y;
-      a.z += w * v.z;
-      a.w += w * v.w;
-    }
-  }
-  const int64_t t = static_cast<int64_t>(x.q0) + i;
-  float lse = l > 0.0f ? (top + log2f(l)) * kLn2 : -INFINITY;
-  float now = l > 0.0f ? 1.0f / l : 0.0f, before = 0.0f;
-  if (p.prev_lse != nullptr) {
-    const Joined g = join_state(lse, p.prev_lse[t * p.H + note.head]);
-    now *= g.now;
-    before = g.before;
-    lse = g.lse;
-  }
-  __syncwarp();  // every lane has read prev_lse, which lse may be
-  if (lane == 0 && p.lse != nullptr) p.lse[t * p.H + note.head] = lse;
-  float y[4] = {a.x * now, a.y * now, a.z * now, a.w * now};
-  if (before != 0.0f) {
-    const T* prev = static_cast<const T*>(p.prev) + t * p.pt_stride + note.head * p.ph_stride + 4 * lane;
-#pragma unroll
-    for (int k = 0; k < 4; ++k) y[k] += before * to_f(prev[k]);
-  }
-  T* out = static_cast<T*>(p.out) + t * p.ot_stride + note.head * p.oh_stride + 4 * lane;
-  *reinterpret_cast<uint2*>(out) = make_uint2(pack2<T>(y[0], y[1]), pack2<T>(y[2], y[3]));
+          for (int k = 0; k < 4; ++k) y[k] += before * to_f(prev[k]);
+        }
+        T* out = static_cast<T*>(p.out) + t * p.ot_stride + note.head * p.oh_stride + d;
+        *reinterpret_cast<uint2*>(out) = make_uint2(pack2<T>(y[0], y[1]), pack2<T>(y[2], y[3]));
+      });
 }
 
 template <class T>
@@ -616,8 +611,7 @@ int run(const PrefillParams& p, const CUtensorMap* maps, void* stream) {
   if (st != PMG_OK) return st;
   st = launch(k, dim3(static_cast<unsigned>(p.units)), kThreads, kBytes, stream, p, maps[0], maps[1], maps[2], maps[3]);
   if (st != PMG_OK) return st;
-  return launch(prefill_join_kernel<T>, dim3(static_cast<unsigned>(p.units), kRows / kJoinRows), kJoinRows * 32, 0,
-                stream, p);
+  return launch(prefill_join_kernel<T>, dim3(static_cast<unsigned>(kJoinCtasPerSm * p.units)), kJoinThreads, 0, stream, p);
 }
 
 }  // namespace

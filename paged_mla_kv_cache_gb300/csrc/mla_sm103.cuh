@@ -108,15 +108,19 @@ __device__ __forceinline__ bool stopped(uint32_t stop) {
 // with all their lanes and let the elected one issue: addresses and
 // descriptors then stay in uniform registers, which these instructions read (a
 // role run by a single lane took about 170 clocks a product instead).
-__device__ __forceinline__ uint32_t elect_one() {
+__device__ __forceinline__ bool elect_one() {
   uint32_t leader;
   asm volatile(
       "{\n\t.reg .pred p;\n\t"
       "elect.sync _|p, 0xffffffff;\n\t"
       "selp.u32 %0, 1, 0, p;\n\t}"
       : "=r"(leader));
-  return leader;
+  return leader != 0;
 }
+
+// A value that is the same in all lanes, in a uniform register: loop bounds and
+// choices made of such values keep the issuing roles' control flow uniform.
+__device__ __forceinline__ int uniform(int x) { return static_cast<int>(__reduce_or_sync(0xffffffffu, static_cast<unsigned>(x))); }
 
 // ---- proxies, named barriers --------------------------------------------------
 
@@ -194,39 +198,37 @@ __host__ __device__ constexpr uint32_t umma_idesc(int fmt, int a_mn, int b_mn, i
          (static_cast<uint32_t>(n >> 3) << 17) | (static_cast<uint32_t>(m >> 4) << 24);
 }
 
-// Products are run by a whole converged warp, with `leader` (elect_one) as the
-// instruction's own predicate: 28 clocks each against 41 inside a branch of the
-// elected lane (64 x 16 x 16 products back to back).
+// Called by one thread, in a branch of elect_one() around a run of products:
+// the compiler then knows the branch has one thread and emits three
+// instructions a product. With the election as the instruction's own predicate
+// it is four times the code, and the issuing warp waits for instructions.
 template <bool kFp8>
-__device__ __forceinline__ void umma_ss(uint32_t leader, uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, bool add) {
+__device__ __forceinline__ void umma_ss(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, bool add) {
   if constexpr (kFp8) {
     asm volatile(
-        "{\n\t.reg .pred p, q;\n\tsetp.ne.u32 p, %4, 0;\n\tsetp.ne.u32 q, %5, 0;\n\t"
-        "@q tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], %1, %2, %3, p;\n\t}" ::"r"(d),
-        "l"(a), "l"(b), "r"(idesc), "r"(static_cast<uint32_t>(add)), "r"(leader)
+        "{\n\t.reg .pred p;\n\tsetp.ne.u32 p, %4, 0;\n\t"
+        "tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], %1, %2, %3, p;\n\t}" ::"r"(d),
+        "l"(a), "l"(b), "r"(idesc), "r"(static_cast<uint32_t>(add))
         : "memory");
   } else {
     asm volatile(
-        "{\n\t.reg .pred p, q;\n\tsetp.ne.u32 p, %4, 0;\n\tsetp.ne.u32 q, %5, 0;\n\t"
-        "@q tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(d),
-        "l"(a), "l"(b), "r"(idesc), "r"(static_cast<uint32_t>(add)), "r"(leader)
+        "{\n\t.reg .pred p;\n\tsetp.ne.u32 p, %4, 0;\n\t"
+        "tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(d),
+        "l"(a), "l"(b), "r"(idesc), "r"(static_cast<uint32_t>(add))
         : "memory");
   }
 }
 // A from tensor memory
-__device__ __forceinline__ void umma_ts(uint32_t leader, uint32_t d, uint32_t a, uint64_t b, uint32_t idesc, bool add) {
+__device__ __forceinline__ void umma_ts(uint32_t d, uint32_t a, uint64_t b, uint32_t idesc, bool add) {
   asm volatile(
-      "{\n\t.reg .pred p, q;\n\tsetp.ne.u32 p, %4, 0;\n\tsetp.ne.u32 q, %5, 0;\n\t"
-      "@q tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d),
-      "r"(a), "l"(b), "r"(idesc), "r"(static_cast<uint32_t>(add)), "r"(leader)
+      "{\n\t.reg .pred p;\n\tsetp.ne.u32 p, %4, 0;\n\t"
+      "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d),
+      "r"(a), "l"(b), "r"(idesc), "r"(static_cast<uint32_t>(add))
       : "memory");
 }
 // arrives on the barrier when every product issued so far by this thread is done
-__device__ __forceinline__ void umma_commit(uint32_t leader, uint32_t bar) {
-  asm volatile(
-      "{\n\t.reg .pred q;\n\tsetp.ne.u32 q, %1, 0;\n\t"
-      "@q tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];\n\t}" ::"r"(bar), "r"(leader)
-      : "memory");
+__device__ __forceinline__ void umma_commit(uint32_t bar) {
+  asm volatile("tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(bar) : "memory");
 }
 
 __device__ __forceinline__ void tmem_alloc(uint32_t smem_slot, int columns) {
