@@ -28,6 +28,7 @@ struct DecodeParams {
   int32_t rows_per_group, groups, units;
   int64_t slot_floats;
   int32_t out_pairs;  // rows of out begin at 4 bytes
+  int32_t q_tma;      // heads of a query box (0: queries are loaded and converted by the softmax warps)
 };
 
 struct DecodeLen {

@@ -34,8 +34,10 @@
 // parts that is as many instructions as the 16-bit products at half the bytes.
 // Queries are first scaled by a power of two for each row that puts its
 // largest value in [224, 448); what is lost is below a step of 2^-9, 2^-16.8 of
-// the largest. Weights are taken at 2^6, where that step is 2^-15 of the
-// reference weight.
+// the largest. Weights are kept below 2^8.5: a request's first tile sets its
+// largest weights to 2^4, which leaves room for the maximum to grow as more
+// entries come, later corrections to 2^6; the step is 2^-13 to 2^-17 of the
+// largest weight.
 #include <algorithm>
 #include <type_traits>
 
@@ -80,7 +82,7 @@ struct Lay {
 template <int kSlots, int kRopeSlots, int N>
 struct MiscOf {
   uint64_t full[kSlots], empty[kSlots], rope_full[kRopeSlots], rope_empty[kRopeSlots];
-  uint64_t s_full[2], s_free[2], p_full, pv_done, q_full, end;
+  uint64_t s_full[2], s_free[2], p_full, pv_done, q_full, q_empty, end;
   uint64_t mask[8];      // entries of a tile that exist, by tile & 7
   union {
     struct {
@@ -146,17 +148,6 @@ struct Items {
   __device__ int64_t last_piece() const { return first + kItemCost + tiles - 1; }
 };
 
-// The next e4m3 part of two values, packed low first; what is left of them
-// stays in a and b. Rounded to 4 significant bits by Dekker's multiplication
-// with 2^20 + 1, each step rounded by itself (no fused multiply-add).
-__device__ __forceinline__ uint32_t part2(float& a, float& b) {
-  const float ca = __fmul_rn(a, 1048577.0f), cb = __fmul_rn(b, 1048577.0f);
-  const float ha = __fsub_rn(ca, __fsub_rn(ca, a)), hb = __fsub_rn(cb, __fsub_rn(cb, b));
-  a -= ha;
-  b -= hb;
-  return __nv_cvt_float2_to_fp8x2(make_float2(ha, hb), __NV_SATFINITE, __NV_E4M3);
-}
-
 __device__ __forceinline__ float half_of(uint32_t two, int i, bf16) { return __uint_as_float(i ? two & 0xffff0000u : two << 16); }
 __device__ __forceinline__ float half_of(uint32_t two, int i, f16) {
   return __half2float(__ushort_as_half(static_cast<unsigned short>(i ? two >> 16 : two & 0xffff)));
@@ -202,38 +193,34 @@ __device__ __forceinline__ void load_queries(const DecodeParams& p, int b, int g
           if (u < kUnits) *reinterpret_cast<uint4*>(q_smem + (u >> 3) * (N * 128) + r * 128 + (((u & 7) ^ (r & 7)) << 4)) = y[k];
         }
       } else {
-        float top = 0.0f;
+        // largest magnitude: 16-bit floats without their signs are ordered as whole numbers
+        uint32_t top2 = 0;
 #pragma unroll
         for (int k = 0; k < 3; ++k) {
           const uint32_t w[4] = {y[k].x, y[k].y, y[k].z, y[k].w};
 #pragma unroll
-          for (int j = 0; j < 8; ++j) top = fmaxf(top, fabsf(half_of(w[j >> 1], j & 1, TQ())));
+          for (int j = 0; j < 4; ++j) top2 = __vmaxu2(top2, w[j] & 0x7fff7fffu);
         }
+        const uint32_t top16 = __reduce_max_sync(0xffffffffu, max(top2 & 0xffff, top2 >> 16));
+        const uint32_t top = __float_as_uint(half_of(top16, 0, TQ()));
+        // 2^e * top in [224, 448), 224 = 1.75 * 2^7, with 2^e and its inverse normal numbers
+        int e = 135 - static_cast<int>(top >> 23) - ((top & 0x7fffff) >= 0x600000 ? 1 : 0);
+        e = top == 0 ? 0 : max(-126, min(126, e));
+        const float scale = __uint_as_float(static_cast<uint32_t>(127 + e) << 23);
+        if (lane == 0) mi.factor[r] = factor * __uint_as_float(static_cast<uint32_t>(127 - e) << 23);
 #pragma unroll
-        for (int o = 16; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
-        // 2^e * top in [224, 448): 224 = 1.75 * 2^7
-        float scale = 1.0f;
-        if (top > 0.0f && top < INFINITY) {
-          int e = 0;
-          const float m = frexpf(top, &e);  // top = m 2^e, m in [0.5, 1)
-          scale = ldexpf(1.0f, (m < 0.875f ? 9 : 8) - e);
-        }
-        if (lane == 0) mi.factor[r] = factor / scale;
-#pragma unroll 1
         for (int k = 0; k < 3; ++k) {
           const int u = lane + 32 * k;  // 8 values: 8 bytes of each part
           if (u < kUnits) {
-            const uint4 z = k == 0 ? y[0] : k == 1 ? y[1] : y[2];
-            const uint32_t w[4] = {z.x, z.y, z.z, z.w};
-            float v[8];
+            uint32_t v[4] = {y[k].x, y[k].y, y[k].z, y[k].w};
 #pragma unroll
-            for (int j = 0; j < 8; ++j) v[j] = half_of(w[j >> 1], j & 1, TQ()) * scale;
+            for (int j = 0; j < 4; ++j) v[j] = pack2<f16>(half_of(v[j], 0, TQ()) * scale, half_of(v[j], 1, TQ()) * scale);
             uint8_t* dst = q_smem + (u >> 4) * (N * 128) + r * 128 + ((((u & 15) >> 1) ^ (r & 7)) << 4) + (u & 1) * 8;
 #pragma unroll
             for (int c = 0; c < kParts; ++c) {
               uint32_t q[4];
 #pragma unroll
-              for (int j = 0; j < 4; ++j) q[j] = part2(v[2 * j], v[2 * j + 1]);
+              for (int j = 0; j < 4; ++j) q[j] = e4m3_part(v[j]);
               *reinterpret_cast<uint2*>(dst + c * (5 * N * 128)) = make_uint2(q[0] | q[1] << 16, q[2] | q[3] << 16);
             }
           }
@@ -246,7 +233,8 @@ __device__ __forceinline__ void load_queries(const DecodeParams& p, int b, int g
 template <class TQ, int kParts, int N>
 __global__ void __launch_bounds__(kThreads, 1)
     decode_tc_kernel(const __grid_constant__ DecodeParams p, const __grid_constant__ CUtensorMap map,
-                     const __grid_constant__ CUtensorMap rope_map, int box_rows) {
+                     const __grid_constant__ CUtensorMap rope_map, const __grid_constant__ CUtensorMap q_map,
+                     int box_rows) {
   using L = Lay<kParts, N>;
   constexpr bool kFp8 = kParts > 1;
   extern __shared__ uint8_t raw[];
@@ -274,12 +262,14 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
     mbar_init(smem_u32(&mi.p_full), 4);
     mbar_init(smem_u32(&mi.pv_done), 1);
-    mbar_init(smem_u32(&mi.q_full), 4);
+    mbar_init(smem_u32(&mi.q_full), p.q_tma ? 1 : 4);
+    mbar_init(smem_u32(&mi.q_empty), 1);
     mi.stop = mi.never = 0;
     mbar_init(smem_u32(&mi.end), 1);
     mbar_fence_init();
     tma_prefetch(&map);
     tma_prefetch(&rope_map);
+    if (p.q_tma) tma_prefetch(&q_map);
   }
   if (warp == 5) tmem_alloc(smem_u32(&mi.tmem), kColumns);
   pdl_entry();
@@ -305,6 +295,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     bool alive = true;
     const uint32_t full = smem_u32(&mi.full[0]), empty = smem_u32(&mi.empty[0]);
     const uint32_t rope_full = smem_u32(&mi.rope_full[0]), rope_empty = smem_u32(&mi.rope_empty[0]);
+    uint32_t items = 0;
     const int segs = kDecodeTile / box_rows;  // boxes of a tile along its rows: 1, 2, 4 or 8
     while (alive && it.next()) {
       if (lane == 0) bad |= decode_len(p, it.b).bad;
@@ -340,6 +331,17 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
         const uint32_t bytes = static_cast<uint32_t>(n_boxes * box_rows * 128);
         const int id0 = __shfl_sync(0xffffffffu, id, 0), row0 = __shfl_sync(0xffffffffu, row, 0);
+        if (box_rows == kDecodeTile && group == 0 && i + 1 < it.n) {
+          // the next tile on its way into L2 while this one waits for slots
+          const int next0 = __shfl_sync(0xffffffffu, next_id, 0);
+          const int next_row = static_cast<int>(static_cast<uint32_t>(j0 + kDecodeTile) % static_cast<uint32_t>(p.B));
+          if (next0 >= 0 && next0 < p.num_blocks && elect_one()) {
+#pragma unroll 1
+            for (int m = 0; m < 4; ++m) tma_prefetch_4d(&map, 0, next_row, m * L::kPieces, next0);
+            tma_prefetch_3d(&rope_map, kLatent, next_row, next0);
+          }
+          __syncwarp();
+        }
         if (stopped(stop)) {
           alive = false;
           break;
@@ -381,9 +383,24 @@ __global__ void __launch_bounds__(kThreads, 1)
           __syncwarp();
         }
         if (++rslot == L::kRopeSlots) { rslot = 0; rphase ^= 1; }
+        if (i == 0 && p.q_tma) {
+          // the request's queries, once the products with the ones before are done
+          if (items > 0) mbar_wait(smem_u32(&mi.q_empty), (items - 1) & 1, stop);
+          ++items;
+          if (elect_one()) {
+            const int g0 = group * p.rows_per_group;
+            const uint32_t bar = smem_u32(&mi.q_full);
+            mbar_expect(bar, static_cast<uint32_t>(p.rows_per_group) * kEntry * 2);
+#pragma unroll 1
+            for (int c = 0; c < 9; ++c)
+              tma_load_4d(base + L::kQAt + c * (N * 128), &q_map, bar, 64 * c, g0 % p.H, g0 / p.H, it.b);
+          }
+          __syncwarp();
+        }
       }
     }
     set_flag(p.err, bad);
+    if (!alive && items > 0) mbar_wait(smem_u32(&mi.q_full), (items - 1) & 1, smem_u32(&mi.never));
     // after a timeout, copies in flight land before the CTA ends (`never` is not set: these waits run on)
     if (!alive) {
       const uint32_t never = smem_u32(&mi.never);
@@ -491,6 +508,7 @@ __global__ void __launch_bounds__(kThreads, 1)
               umma_ss<kFp8>(d, ka + 2 * k, qa + 2 * k + x * (5 * N * 8), kIdescS, true);
           umma_commit(rope_empty + 8 * rslot);
           umma_commit(s_full + 8 * buf);
+          if (p.q_tma && q_tile + 1 == qi.n) umma_commit(smem_u32(&mi.q_empty));
         }
         __syncwarp();
         if (++rslot == L::kRopeSlots) { rslot = 0; rphase ^= 1; }
@@ -515,8 +533,8 @@ __global__ void __launch_bounds__(kThreads, 1)
     const int n_rows = min(p.rows_per_group, rows - g0);
     const float kv_scale = kFp8 && p.scale != nullptr ? *p.scale : 1.0f;
     const float factor = p.sm_scale * kLog2e * kv_scale;
-    constexpr float kSlack = kFp8 ? 2.5f : 8.0f;     // weights up to 2^(kBase + kSlack) <= 448
-    constexpr float kBase = kFp8 ? 6.0f : 0.0f;
+    constexpr float kCap = kFp8 ? 8.5f : 8.0f;       // weights stay below 2^kCap
+    constexpr float kFirst = kFp8 ? 4.0f : 0.0f, kLater = kFp8 ? 6.0f : 0.0f;  // where a new reference puts the largest
     const uint32_t lanes = static_cast<uint32_t>(warp * 32) << 16;
     // Scores (M = 64: 16 rows in each quarter of the lanes) are read so that this thread has entries tok and tok + 8
     // of the tile, and of every 8 columns 2 c and 2 c + 1.
@@ -534,12 +552,21 @@ __global__ void __launch_bounds__(kThreads, 1)
     };
     // For each request: its queries, then the epilogue of the request before (whose last product runs meanwhile), then
     // its tiles.
+    if (p.q_tma) {
+      // rows that no copy fills: 0
+      for (int i = tid; i < 9 * (N - p.rows_per_group) * 8; i += kSoft) {
+        const int c = i / ((N - p.rows_per_group) * 8), y = i % ((N - p.rows_per_group) * 8);
+        *reinterpret_cast<uint4*>(smem + L::kQAt + c * (N * 128) + p.rows_per_group * 128 + y * 16) = make_uint4(0, 0, 0, 0);
+      }
+      fence_async_smem();
+      named_sync<kSoft>(1);
+    }
     bool more = it.next();
     int prev_b = -1, prev_n = 0;
     bool prev_whole = false;
     float* prev_slot = nullptr;
     for (;;) {
-      if (more && it.len > 0) {
+      if (more && it.len > 0 && !p.q_tma) {
         load_queries<TQ, kParts, N>(p, it.b, g0, n_rows, smem + L::kQAt, mi, factor);
         fence_async_smem();
         __syncwarp();
@@ -654,7 +681,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             x[4 * g + k] = y;
             over = fmaxf(over, y);
           }
-        const bool raise = named_any<kSoft>(2, over > kBase + kSlack);
+        const bool raise = named_any<kSoft>(2, over > kCap);
         if (raise) {
           // maximum of every row over the tile's entries
           float* part = reinterpret_cast<float*>(smem + L::kPAt);  // free once the last tile's product is done
@@ -673,7 +700,8 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
           for (int k = 0; k < 2 * kG; ++k) {
             const int col = (k >> 1) * 8 + 2 * c + (k & 1);
-            const float top = fmaxf(fmaxf(part[col], part[N + col]), fmaxf(part[2 * N + col], part[3 * N + col])) - kBase;
+            const float top = fmaxf(fmaxf(part[col], part[N + col]), fmaxf(part[2 * N + col], part[3 * N + col])) -
+                              (ref[k] == -INFINITY ? kFirst : kLater);
             float a = 1.0f;
             if (top > ref[k]) {  // where the tile raises it at all
               a = ref[k] == -INFINITY ? 0.0f : ex2(ref[k] - top);
@@ -734,13 +762,14 @@ __global__ void __launch_bounds__(kThreads, 1)
           uint8_t* row = smem + L::kPAt + (tok + 8 * h) * 128;
 #pragma unroll
           for (int g = 0; g < kG; ++g) {
-            float a = x[4 * g + 2 * h], b = x[4 * g + 2 * h + 1];
+            const float a = x[4 * g + 2 * h], b = x[4 * g + 2 * h + 1];
             if constexpr (!kFp8) {
               *reinterpret_cast<uint32_t*>(row + ((g ^ (tok & 7)) << 4) + 4 * c) = pack2<TQ>(a, b);
             } else {
               uint8_t* at = row + (((g >> 1) ^ (tok & 7)) << 4) + (g & 1) * 8 + 2 * c;
+              uint32_t two = pack2<f16>(a, b);
 #pragma unroll
-              for (int q = 0; q < 2; ++q) *reinterpret_cast<uint16_t*>(at + q * L::kPiece) = static_cast<uint16_t>(part2(a, b));
+              for (int q = 0; q < 2; ++q) *reinterpret_cast<uint16_t*>(at + q * L::kPiece) = static_cast<uint16_t>(e4m3_part(two));
             }
           }
         }
@@ -762,22 +791,20 @@ __global__ void __launch_bounds__(kThreads, 1)
         for (int o = 16; o >= 4; o >>= 1) l[k] += __shfl_xor_sync(0xffffffffu, l[k], o);
         if (lane < 4) mi.warp_sums[warp * N + (k >> 1) * 8 + 2 * c + (k & 1)] = l[k];
       }
-      named_sync<kSoft>(1);
-      auto sum_of = [&](int h) {
-        return (mi.warp_sums[h] + mi.warp_sums[N + h]) + (mi.warp_sums[2 * N + h] + mi.warp_sums[3 * N + h]);
-      };
-      if (tid < N) mi.inv[tid] = sum_of(tid) > 0.0f ? kv_scale / sum_of(tid) : 0.0f;
-      float* slot = p.ws.slots + (static_cast<int64_t>(blockIdx.x) * 2 + (it.tile == 0 ? 1 : 0)) * p.slot_floats;
-      if (tid < 4) {  // these four have all references
+      if (tid < 4) {  // these four have all references; the factors are in registers by now
 #pragma unroll
-        for (int k = 0; k < 2 * kG; ++k) {
-          const int h = (k >> 1) * 8 + 2 * c + (k & 1);
-          if (h < n_rows) {
-            const float sum = sum_of(h);
-            if (!whole) *reinterpret_cast<float2*>(slot + p.rows_per_group * kLatent + 2 * h) = make_float2(ref[k], sum);
-            else if (p.lse != nullptr)
-              p.lse[static_cast<int64_t>(it.b) * rows + g0 + h] = sum > 0.0f ? (ref[k] + log2f(sum)) * kLn2 : -INFINITY;
-          }
+        for (int k = 0; k < 2 * kG; ++k) mi.factor[(k >> 1) * 8 + 2 * c + (k & 1)] = ref[k];
+      }
+      named_sync<kSoft>(1);
+      float* slot = p.ws.slots + (static_cast<int64_t>(blockIdx.x) * 2 + (it.tile == 0 ? 1 : 0)) * p.slot_floats;
+      if (tid < N) {
+        const float sum = (mi.warp_sums[tid] + mi.warp_sums[N + tid]) + (mi.warp_sums[2 * N + tid] + mi.warp_sums[3 * N + tid]);
+        const float r = mi.factor[tid];
+        mi.inv[tid] = sum > 0.0f ? kv_scale / sum : 0.0f;
+        if (tid < n_rows) {
+          if (!whole) *reinterpret_cast<float2*>(slot + p.rows_per_group * kLatent + 2 * tid) = make_float2(r, sum);
+          else if (p.lse != nullptr)
+            p.lse[static_cast<int64_t>(it.b) * rows + g0 + tid] = sum > 0.0f ? (r + log2f(sum)) * kLn2 : -INFINITY;
         }
       }
       if (!whole && it.tile == 0 && tid == 0) {
@@ -801,7 +828,7 @@ __global__ void __launch_bounds__(kThreads, 1)
 }
 
 struct Maps {
-  CUtensorMap latent, rope;
+  CUtensorMap latent, rope, q;
 };
 
 template <class TQ, int kParts, int N>
@@ -811,7 +838,7 @@ int run(const DecodeParams& p, const Maps& maps, int box_rows, void* stream) {
   const int st = allow_smem(reinterpret_cast<const void*>(k), kBytes);
   if (st != PMG_OK) return st;
   return launch(k, dim3(static_cast<unsigned>(p.units) * p.groups), kThreads, kBytes, stream, p, maps.latent, maps.rope,
-                box_rows);
+                maps.q, box_rows);
 }
 
 template <class TQ, int kParts>
@@ -831,7 +858,8 @@ bool decode_tc_takes(const DecodeParams& p, int q_dtype, int cache_dtype) {
          p.num_blocks > 0 && p.tok_stride > 0 && p.blk_stride > 0 && aligned(p.cache, 16) &&
          p.tok_stride * ec % 16 == 0 && p.blk_stride * ec % 16 == 0 && p.blk_stride * ec < (int64_t{1} << 40) &&
          p.tok_stride * ec < (int64_t{1} << 40) && aligned(p.q, 16) && p.qr_stride % 8 == 0 && p.qt_stride % 8 == 0 &&
-         p.qh_stride % 8 == 0;
+         p.qh_stride % 8 == 0 && p.qr_stride < (int64_t{1} << 38) && p.qt_stride < (int64_t{1} << 38) &&
+         p.qh_stride < (int64_t{1} << 38);
 }
 
 int decode_tc(DecodeParams& p, int q_dtype, int cache_dtype, int sms, void* stream) {
@@ -859,6 +887,21 @@ int decode_tc(DecodeParams& p, int q_dtype, int cache_dtype, int sms, void* stre
   if (st == PMG_OK)
     st = tensor_map<3>(&maps.rope, type, p.cache, {kEntry, page, blocks}, {row_stride, blk_stride}, {piece, box, 1});
   if (st != PMG_OK) return st;
+  // queries of a 16-bit cache: whole boxes of heads and tokens, where a group is one
+  const int rpg = p.rows_per_group, heads = std::min(p.H, rpg);
+  p.q_tma = 0;
+  maps.q = maps.rope;
+  if (!fp8 && p.H % heads == 0 && rpg % heads == 0 && (p.qh_stride > 0 || p.H == 1) && (p.qt_stride > 0 || p.q_len == 1) &&
+      (p.qr_stride > 0 || p.R == 1)) {
+    // the stride of a dimension of one is not used; it has to be a valid one all the same
+    const uint64_t s1 = p.H > 1 ? p.qh_stride * 2 : kEntry * 2, s2 = p.q_len > 1 ? p.qt_stride * 2 : kEntry * 2,
+                   s3 = p.R > 1 ? p.qr_stride * 2 : kEntry * 2;
+    st = tensor_map<4>(&maps.q, type, p.q,
+                       {kEntry, static_cast<uint64_t>(p.H), static_cast<uint64_t>(p.q_len), static_cast<uint64_t>(p.R)},
+                       {s1, s2, s3}, {64, static_cast<uint32_t>(heads), static_cast<uint32_t>(rpg / heads), 1});
+    if (st != PMG_OK) return st;
+    p.q_tma = heads;
+  }
   if (q_dtype == PMG_BF16) return fp8 ? run<bf16, 2>(p, maps, box_rows, stream) : run<bf16, 1>(p, maps, box_rows, stream);
   return fp8 ? run<f16, 3>(p, maps, box_rows, stream) : run<f16, 1>(p, maps, box_rows, stream);
 }

@@ -177,6 +177,17 @@ __device__ __forceinline__ void tma_load_4d(uint32_t dst, const CUtensorMap* map
       : "memory");
 }
 
+// a tile on its way into L2 only
+__device__ __forceinline__ void tma_prefetch_4d(const CUtensorMap* map, int x, int y, int z, int w) {
+  asm volatile("cp.async.bulk.prefetch.tensor.4d.L2.global.tile [%0, {%1, %2, %3, %4}];" ::"l"(map), "r"(x), "r"(y),
+               "r"(z), "r"(w)
+               : "memory");
+}
+__device__ __forceinline__ void tma_prefetch_3d(const CUtensorMap* map, int x, int y, int z) {
+  asm volatile("cp.async.bulk.prefetch.tensor.3d.L2.global.tile [%0, {%1, %2, %3}];" ::"l"(map), "r"(x), "r"(y), "r"(z)
+               : "memory");
+}
+
 // ---- tensor core ----------------------------------------------------------------
 
 // Shared-memory operand tiles are rows of 128 bytes with the 128-byte swizzle
@@ -362,6 +373,17 @@ __device__ __forceinline__ uint32_t pack2<f16>(float a, float b) {
   uint32_t r;
   asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(b), "f"(a));
   return r;
+}
+
+// The next e4m3 part of two values held as f16x2 (each below 448), packed low
+// first; what is left of them, exactly, stays in x.
+__device__ __forceinline__ uint32_t e4m3_part(uint32_t& x) {
+  uint16_t two;
+  uint32_t back;
+  asm("cvt.rn.satfinite.e4m3x2.f16x2 %0, %1;" : "=h"(two) : "r"(x));
+  asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(back) : "h"(two));
+  asm("sub.rn.f16x2 %0, %0, %1;" : "+r"(x) : "r"(back));
+  return two;
 }
 
 // ---- host: tensor maps ------------------------------------------------------------
