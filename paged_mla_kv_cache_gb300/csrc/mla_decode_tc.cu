@@ -81,7 +81,7 @@ struct Lay {
 
 template <int kSlots, int kRopeSlots, int N>
 struct MiscOf {
-  uint64_t full[kSlots], empty[kSlots], rope_full[kRopeSlots], rope_empty[kRopeSlots];
+  uint64_t full[kRopeSlots], rope_empty[kRopeSlots], empty[kSlots];  // a tile is full as a whole, by its rope slot
   uint64_t s_full[2], s_free[2], p_full, pv_done, q_full, q_empty, end;
   uint64_t mask[8];      // entries of a tile that exist, by tile & 7
   union {
@@ -248,12 +248,9 @@ __global__ void __launch_bounds__(kThreads, 1)
 
   // before the previous kernel's results are needed
   if (tid == 0) {
-    for (int i = 0; i < L::kSlots; ++i) {
-      mbar_init(smem_u32(&mi.full[i]), 1);
-      mbar_init(smem_u32(&mi.empty[i]), 1);
-    }
+    for (int i = 0; i < L::kSlots; ++i) mbar_init(smem_u32(&mi.empty[i]), 1);
     for (int i = 0; i < L::kRopeSlots; ++i) {
-      mbar_init(smem_u32(&mi.rope_full[i]), 1);
+      mbar_init(smem_u32(&mi.full[i]), 1);
       mbar_init(smem_u32(&mi.rope_empty[i]), 1);
     }
     for (int i = 0; i < 2; ++i) {
@@ -293,8 +290,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     uint32_t t = 0;
     int bad = 0;
     bool alive = true;
-    const uint32_t full = smem_u32(&mi.full[0]), empty = smem_u32(&mi.empty[0]);
-    const uint32_t rope_full = smem_u32(&mi.rope_full[0]), rope_empty = smem_u32(&mi.rope_empty[0]);
+    const uint32_t full = smem_u32(&mi.full[0]), empty = smem_u32(&mi.empty[0]), rope_empty = smem_u32(&mi.rope_empty[0]);
     uint32_t items = 0;
     const int segs = kDecodeTile / box_rows;  // boxes of a tile along its rows: 1, 2, 4 or 8
     while (alive && it.next()) {
@@ -346,18 +342,32 @@ __global__ void __launch_bounds__(kThreads, 1)
           alive = false;
           break;
         }
+        // the rotated part's slot, free since the tile's scores two tiles ago, brings the tile's barrier
+        const uint32_t bar = full + 8 * rslot;
+        mbar_wait(rope_empty + 8 * rslot, rphase ^ 1, stop);
+        if (elect_one()) mbar_expect(bar, bytes * (4 * L::kPieces + 1));
+        __syncwarp();
+        const bool one_box = n_boxes == 1 && box_rows == kDecodeTile;
+        if (one_box) {
+          if (elect_one()) tma_load_3d(base + L::kRopeAt + rslot * L::kPiece, &rope_map, bar, kLatent, row0, id0);
+          __syncwarp();
+        } else {
+#pragma unroll 1
+          for (int s = 0; s < n_boxes; ++s) {
+            const int sid = __shfl_sync(0xffffffffu, id, s), srow = __shfl_sync(0xffffffffu, row, s);
+            if (elect_one())
+              tma_load_3d(base + L::kRopeAt + rslot * L::kPiece + s * box_rows * 128, &rope_map, bar, kLatent, srow, sid);
+            __syncwarp();
+          }
+        }
 #pragma unroll 1
         for (int m = 0; m < 4; ++m) {
           mbar_wait(empty + 8 * slot, phase ^ 1, stop);
-          const uint32_t dst = base + L::kSlotAt + slot * L::kSlot, bar = full + 8 * slot;
-          if (n_boxes == 1 && box_rows == kDecodeTile) {
-            if (elect_one()) {
-              mbar_expect(bar, L::kSlot);
-              tma_load_4d(dst, &map, bar, 0, row0, m * L::kPieces, id0);
-            }
+          const uint32_t dst = base + L::kSlotAt + slot * L::kSlot;
+          if (one_box) {
+            if (elect_one()) tma_load_4d(dst, &map, bar, 0, row0, m * L::kPieces, id0);
           } else {
             // boxes of fewer rows than a slot has leave gaps between their pieces: a copy a piece
-            if (elect_one()) mbar_expect(bar, bytes * L::kPieces);
 #pragma unroll 1
             for (int s = 0; s < n_boxes; ++s) {
               const int sid = __shfl_sync(0xffffffffu, id, s), srow = __shfl_sync(0xffffffffu, row, s);
@@ -370,17 +380,6 @@ __global__ void __launch_bounds__(kThreads, 1)
           }
           __syncwarp();
           if (++slot == L::kSlots) { slot = 0; phase ^= 1; }
-        }
-        mbar_wait(rope_empty + 8 * rslot, rphase ^ 1, stop);
-        if (elect_one()) mbar_expect(rope_full + 8 * rslot, bytes);
-        __syncwarp();
-#pragma unroll 1
-        for (int s = 0; s < n_boxes; ++s) {
-          const int sid = __shfl_sync(0xffffffffu, id, s), srow = __shfl_sync(0xffffffffu, row, s);
-          if (elect_one())
-            tma_load_3d(base + L::kRopeAt + rslot * L::kPiece + s * box_rows * 128, &rope_map, rope_full + 8 * rslot, kLatent,
-                        srow, sid);
-          __syncwarp();
         }
         if (++rslot == L::kRopeSlots) { rslot = 0; rphase ^= 1; }
         if (i == 0 && p.q_tma) {
@@ -404,8 +403,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     // after a timeout, copies in flight land before the CTA ends (`never` is not set: these waits run on)
     if (!alive) {
       const uint32_t never = smem_u32(&mi.never);
-      for (int i = 0; i < L::kSlots; ++i) mbar_wait(full + 8 * i, i < slot ? phase : phase ^ 1, never);
-      for (int i = 0; i < L::kRopeSlots; ++i) mbar_wait(rope_full + 8 * i, i < rslot ? rphase : rphase ^ 1, never);
+      for (int i = 0; i < L::kRopeSlots; ++i) mbar_wait(full + 8 * i, i < rslot ? rphase : rphase ^ 1, never);
     }
   } else if (warp == 5) {
     // ---- products ----
@@ -415,14 +413,13 @@ __global__ void __launch_bounds__(kThreads, 1)
       while (more && it.len == 0) more = it.next();
       return more;
     };
-    const uint32_t full = smem_u32(&mi.full[0]), empty = smem_u32(&mi.empty[0]);
-    const uint32_t rope_full = smem_u32(&mi.rope_full[0]), rope_empty = smem_u32(&mi.rope_empty[0]);
+    const uint32_t full = smem_u32(&mi.full[0]), empty = smem_u32(&mi.empty[0]), rope_empty = smem_u32(&mi.rope_empty[0]);
     const uint32_t s_full = smem_u32(&mi.s_full[0]), s_free = smem_u32(&mi.s_free[0]);
     bool q_more = advance(qi), v_more = advance(vi);
     int q_tile = 0, v_tile = 0;                 // within the items
     uint32_t q_item = 0;                        // items begun, for the queries' barrier
     uint32_t qt = 0, vt = 0;                    // tiles issued
-    int qslot = 0, qphase = 0, rslot = 0, rphase = 0, vslot = 0;
+    int qslot = 0, rslot = 0, rphase = 0, vslot = 0;
     const uint32_t p_full = smem_u32(&mi.p_full);
     // O of the oldest tile
     auto values = [&]() {
@@ -454,36 +451,29 @@ __global__ void __launch_bounds__(kThreads, 1)
         v_more = advance(vi);
       }
     };
-    // Parts of S of a tile as they arrive (the rotated part last); O of the tile before it as soon as its weights are
-    // there, and before a third tile's scores. One loop, so that this role's code stays small.
-    int part = 0;
-    while (q_more || v_more) {
-      const uint32_t buf = qt & 1;
-      if (q_more && part == 0 && qt - vt < 2) {
-        if (qt >= 2) mbar_wait(s_free + 8 * buf, ((qt >> 1) + 1) & 1, stop);
+    // S of a tile when it has arrived; O of the tile before it once its weights are there: while the next tile is still
+    // on its way, or at the latest after its scores.
+    auto wait_for = [&](uint32_t bar, uint32_t parity) {
+      while (vt != qt && mbar_wait_either(p_full, vt & 1, bar, parity, stop)) values();
+      mbar_wait(bar, parity, stop);
+    };
+    while (q_more) {
+      const uint32_t buf = qt & 1, d = tmem + buf * N;
+      if (qt >= 2) mbar_wait(s_free + 8 * buf, ((qt >> 1) + 1) & 1, stop);
+      if (q_tile == 0) {
+        // the queries of a new request come after the last scores with the ones before
+        wait_for(smem_u32(&mi.q_full), q_item & 1);
+        ++q_item;
       }
-      // what the next part of S waits for: its slot, or the queries of a new request
-      const bool new_item = part == 0 && q_tile == 0;
-      const uint32_t bar = new_item ? smem_u32(&mi.q_full) : part < 4 ? full + 8 * qslot : rope_full + 8 * rslot;
-      const uint32_t parity = new_item ? q_item & 1 : part < 4 ? qphase : rphase;
-      if (vt != qt) {
-        bool ready = true;
-        if (!q_more || qt - vt == 2) mbar_wait(p_full, vt & 1, stop);
-        else ready = mbar_wait_either(p_full, vt & 1, bar, parity, stop);
-        if (ready) {
-          values();
-          continue;
-        }
-      }
-      if (new_item) mbar_wait(bar, parity, stop);
-      const uint32_t d = tmem + buf * N;
-      if (part < 4) {
-        mbar_wait(full + 8 * qslot, qphase, stop);
-        tmem_fence_after();
-        if (elect_one()) {
+      wait_for(full + 8 * rslot, rphase);
+      tmem_fence_after();
+      if (elect_one()) {
+        int at = qslot;
+#pragma unroll
+        for (int part = 0; part < 4; ++part) {
 #pragma unroll
           for (int c = 0; c < L::kPieces; ++c) {
-            const uint64_t ka = umma_desc(base + L::kSlotAt + qslot * L::kSlot + c * L::kPiece, 16, 1024);
+            const uint64_t ka = umma_desc(base + L::kSlotAt + at * L::kSlot + c * L::kPiece, 16, 1024);
             const uint64_t qa = umma_desc(base + L::kQAt + (part * L::kPieces + c) * (N * 128), 16, 1024);
 #pragma unroll
             for (int k = 0; k < 4; ++k)  // 32 bytes of K each
@@ -491,35 +481,35 @@ __global__ void __launch_bounds__(kThreads, 1)
               for (int x = 0; x < kParts; ++x)
                 umma_ss<kFp8>(d, ka + 2 * k, qa + 2 * k + x * (5 * N * 8), kIdescS, part > 0 || c > 0 || k > 0 || x > 0);
           }
+          if (++at == L::kSlots) at = 0;
         }
-        __syncwarp();
-        if (++qslot == L::kSlots) { qslot = 0; qphase ^= 1; }
-        ++part;
-      } else {
-        mbar_wait(rope_full + 8 * rslot, rphase, stop);
-        tmem_fence_after();
-        if (elect_one()) {
-          const uint64_t ka = umma_desc(base + L::kRopeAt + rslot * L::kPiece, 16, 1024);
-          const uint64_t qa = umma_desc(base + L::kQAt + 4 * L::kPieces * (N * 128), 16, 1024);
+        const uint64_t ka = umma_desc(base + L::kRopeAt + rslot * L::kPiece, 16, 1024);
+        const uint64_t qa = umma_desc(base + L::kQAt + 4 * L::kPieces * (N * 128), 16, 1024);
 #pragma unroll
-          for (int k = 0; k < (kFp8 ? 2 : 4); ++k)
+        for (int k = 0; k < (kFp8 ? 2 : 4); ++k)
 #pragma unroll
-            for (int x = 0; x < kParts; ++x)
-              umma_ss<kFp8>(d, ka + 2 * k, qa + 2 * k + x * (5 * N * 8), kIdescS, true);
-          umma_commit(rope_empty + 8 * rslot);
-          umma_commit(s_full + 8 * buf);
-          if (p.q_tma && q_tile + 1 == qi.n) umma_commit(smem_u32(&mi.q_empty));
-        }
-        __syncwarp();
-        if (++rslot == L::kRopeSlots) { rslot = 0; rphase ^= 1; }
-        part = 0;
-        ++qt;
-        if (q_tile == 0) ++q_item;
-        if (++q_tile == qi.n) {
-          q_tile = 0;
-          q_more = advance(qi);
-        }
+          for (int x = 0; x < kParts; ++x)
+            umma_ss<kFp8>(d, ka + 2 * k, qa + 2 * k + x * (5 * N * 8), kIdescS, true);
+        umma_commit(rope_empty + 8 * rslot);
+        umma_commit(s_full + 8 * buf);
+        if (p.q_tma && q_tile + 1 == qi.n) umma_commit(smem_u32(&mi.q_empty));
       }
+      __syncwarp();
+      qslot = qslot + 4 < L::kSlots ? qslot + 4 : qslot + 4 - L::kSlots;
+      if (++rslot == L::kRopeSlots) { rslot = 0; rphase ^= 1; }
+      ++qt;
+      if (++q_tile == qi.n) {
+        q_tile = 0;
+        q_more = advance(qi);
+      }
+      if (qt - vt == 2) {
+        mbar_wait(p_full, vt & 1, stop);
+        values();
+      }
+    }
+    while (v_more) {
+      mbar_wait(p_full, vt & 1, stop);
+      values();
     }
     // everything issued ends before the tensor memory is given back
     if (elect_one()) umma_commit(smem_u32(&mi.end));
@@ -542,7 +532,8 @@ __global__ void __launch_bounds__(kThreads, 1)
     const int c = lane & 3, tok = warp * 16 + (lane >> 2);
     JoinNote note{-1, 0, 0, 0};
     uint32_t t = 0;                 // tiles of the share
-    uint32_t slot0 = 0, phase0 = 0; // slot of the tile's first part, its phase
+    uint32_t slot0 = 0;             // slot of the tile's first part
+    uint32_t tile_slot = 0, tile_phase = 0;
     const int step0 = g0 / p.H;  // the group's first new token
     if (tid < N) mi.step[tid] = static_cast<uint8_t>((g0 + tid) / p.H - step0);
     // where row h of the group is in a request's output
@@ -640,8 +631,9 @@ __global__ void __launch_bounds__(kThreads, 1)
       for (int i = 0; i < n; ++i, ++t) {
         const uint32_t buf = t & 1;
         const int j0 = (it.tile + i) * kDecodeTile;
-        // the loading warp's note of the tile is ordered by its first slot's barrier
-        mbar_wait(smem_u32(&mi.full[0]) + 8 * slot0, phase0, stop);
+        // the loading warp's note of the tile is ordered by the tile's barrier
+        mbar_wait(smem_u32(&mi.full[0]) + 8 * tile_slot, tile_phase, stop);
+        if (++tile_slot == L::kRopeSlots) { tile_slot = 0; tile_phase ^= 1; }
         mbar_wait(smem_u32(&mi.s_full[0]) + 8 * buf, t >> 1 & 1, stop);
         __syncwarp();
         tmem_fence_after();
@@ -777,10 +769,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         __syncwarp();
         if (lane == 0) mbar_arrive(smem_u32(&mi.p_full));
         slot0 += 4;
-        if (slot0 >= L::kSlots) {
-          slot0 -= L::kSlots;
-          phase0 ^= 1;
-        }
+        if (slot0 >= L::kSlots) slot0 -= L::kSlots;
       }
 
       // sums of every row over the lanes, then over the warps in their order
