@@ -194,6 +194,21 @@ int pmg_latent_prefill(const void* q, int64_t q_token_stride, int64_t q_head_str
  * sizes), or a negative number where there is no device. */
 int64_t pmg_attention_workspace(void);
 
+/*
+ * pmg_call_packed — one of the calls above with its arguments in an array of
+ * 8-byte words, in the order of its parameter list: pointers and whole numbers
+ * as int64_t, floats as double, the stream among them. For callers whose
+ * foreign-function layer takes longer to pass thirty arguments than the call
+ * itself takes. An unknown call returns PMG_ERR_ARG, NULL words PMG_ERR_NULL.
+ */
+typedef enum pmg_packed {
+  PMG_CALL_PLAN_STEP = 0,
+  PMG_CALL_APPEND = 1,
+  PMG_CALL_LATENT_DECODE = 2,
+  PMG_CALL_LATENT_PREFILL = 3
+} pmg_packed;
+int pmg_call_packed(int call, const void* words);
+
 #ifdef __cplusplus
 }
 #endif

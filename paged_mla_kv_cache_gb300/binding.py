@@ -19,6 +19,7 @@ from __future__ import annotations
 
 import ctypes
 import os
+import struct
 import threading
 from typing import Optional, Tuple
 
@@ -76,6 +77,8 @@ def library_path() -> str:
 def load_library() -> ctypes.CDLL:
     """Load libpmg.so once. Raises if it has not been built."""
     global _lib
+    if _lib is not None:
+        return _lib
     with _lock:
         if _lib is not None:
             return _lib
@@ -114,6 +117,8 @@ def load_library() -> ctypes.CDLL:
         L.pmg_latent_prefill.argtypes = [vp, i64, i64, vp, i64, i64, vp, i64, vp, i64, i64, vp, vp, i32, i64, i64, i32,
                                          i32, i32, i32, i32, f32, vp, i64, i64, vp, vp, i64, i64, vp, vp, i64, vp, vp,
                                          u32]
+        L.pmg_call_packed.restype = ctypes.c_int
+        L.pmg_call_packed.argtypes = [i32, ctypes.c_char_p]
         L.pmg_attention_workspace.restype = i64
         L.pmg_attention_workspace.argtypes = []
         L.pmg_status_string.restype = ctypes.c_char_p
@@ -291,30 +296,72 @@ def debug_plan(cu_seq_lens: torch.Tensor, seq_starts: Optional[torch.Tensor], to
 # --- the operators around the gather (include/pmg_mla.h) -------------------------
 
 
-def _vector(t: Optional[torch.Tensor], dtype: torch.dtype, n: Optional[int], what: str, optional: bool = False):
-    """Pointer of a contiguous 1-D tensor of n elements (n None: any)."""
-    if t is None:
-        if optional:
-            return None
-        raise ValueError(f"{what} is required")
-    if t.dtype != dtype or t.dim() != 1 or (n is not None and t.shape[0] != n) or not t.is_contiguous():
-        raise ValueError(f"{what} must be {dtype} [{'n' if n is None else n}] and contiguous, got "
-                         f"{t.dtype} {list(t.shape)}")
-    return t.data_ptr()
+# Their arguments travel as one array of words (pmg_call_packed): passing thirty
+# of them one by one costs ctypes more than a short call takes on the GPU. For
+# the same reason the checks below first test everything in one expression and
+# look for what is wrong only then.
+PLAN_ARGS = struct.Struct("<19q")
+APPEND_ARGS = struct.Struct("<5qd25q")
+DECODE_WORDS = [(n, "d" if n == "sm_scale" else "q") for n in (
+    "q q_req_stride q_token_stride q_head_stride cache cache_block_stride cache_token_stride num_blocks block_table "
+    "block_table_stride seq_lens num_reqs q_len heads latent_dim rope_dim block_size q_dtype cache_dtype scale sm_scale "
+    "out out_req_stride out_token_stride out_head_stride lse workspace workspace_bytes error_flag stream options").split()]
+DECODE_ARGS = struct.Struct("<" + "".join(f for _, f in DECODE_WORDS))
+PREFILL_ARGS = struct.Struct("<21qd13q")
+_I32, _I64, _F32 = torch.int32, torch.int64, torch.float32
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
 
 
-def _scalar(t: Optional[torch.Tensor], dtype: torch.dtype, what: str):
+def _stream_word(t: torch.Tensor, stream) -> int:
+    """The stream of a call on t's device: the given one, or torch's current one."""
+    if stream is None and _raw_stream is not None:
+        device = t.get_device()
+        if device >= 0:
+            return _raw_stream(device)
+    return _stream_handle(stream) or 0
+
+
+def _is_vector(t: torch.Tensor, dtype: torch.dtype, n: int) -> bool:
+    return t.dtype is dtype and t.numel() == n and t.is_contiguous()
+
+
+def _vector(t: Optional[torch.Tensor], dtype: torch.dtype, n: int, what: str, optional: bool = False) -> None:
     if t is None:
-        return None
-    if t.dtype != dtype or t.numel() != 1:
+        if not optional:
+            raise ValueError(f"{what} is required")
+    elif not _is_vector(t, dtype, n):
+        raise ValueError(f"{what} must be {n} contiguous {dtype}, got {t.dtype} {list(t.shape)}")
+
+
+def _scalar(t: Optional[torch.Tensor], dtype: torch.dtype, what: str) -> int:
+    if t is None:
+        return 0
+    if t.dtype is not dtype or t.numel() != 1:
         raise ValueError(f"{what} must be one {dtype} element")
     return t.data_ptr()
 
 
-def _unit_last(t: torch.Tensor, dims: int, what: str) -> torch.Tensor:
-    if t.dim() != dims or (t.shape[-1] > 1 and t.stride(-1) != 1):
+def _word(t: Optional[torch.Tensor]) -> int:
+    return 0 if t is None else t.data_ptr()
+
+
+def _unit_last(what: str, dims: int, t: torch.Tensor):
+    """Shape and strides of a tensor whose last dimension is contiguous."""
+    shape, strides = t.shape, t.stride()
+    if len(shape) != dims or (strides[-1] != 1 and shape[-1] > 1):
         raise ValueError(f"{what} must have {dims} dimensions, the last of stride 1")
-    return t
+    return shape, strides
+
+
+def _table(block_table: torch.Tensor, reqs: int) -> int:
+    if block_table.dtype is _I32 and block_table.is_contiguous():
+        shape = block_table.shape
+        if len(shape) == 2 and shape[0] == reqs:
+            return shape[1]
+    width = _table_width(block_table)
+    if block_table.shape[0] != reqs:
+        raise ValueError(f"block_table has {block_table.shape[0]} rows for {reqs} requests")
+    return width
 
 
 def plan_step(ctx_lens: torch.Tensor, new_lens: torch.Tensor, block_table: torch.Tensor, free_blocks: torch.Tensor,
@@ -336,27 +383,30 @@ def plan_step(ctx_lens: torch.Tensor, new_lens: torch.Tensor, block_table: torch
     seq_lens      int32 [num_reqs]: total lengths.
     blocks_taken  int32 [1] or None.
     """
-    r = ctx_lens.shape[0]
-    i32 = torch.int32
-    given = [t for t in (slots, positions, token_to_seq) if t is not None]
-    tokens = given[0].shape[0] if given else 0
-    st = load_library().pmg_plan_step(
-        _vector(ctx_lens, i32, r, "ctx_lens"), _vector(new_lens, i32, r, "new_lens"), r,
-        _ptr(block_table), _reqs_table(block_table, r), _vector(free_blocks, i32, None, "free_blocks"),
-        free_blocks.shape[0], int(num_blocks), int(block_size), _vector(slots, torch.int64, tokens, "slots", True),
-        _vector(positions, i32, tokens, "positions", True), _vector(token_to_seq, i32, tokens, "token_to_seq", True),
-        tokens, _vector(cu_new, i32, r + 1, "cu_new"), _vector(seq_lens, i32, r, "seq_lens"),
-        _vector(cu_seq, i32, r + 1, "cu_seq", True), _scalar(blocks_taken, i32, "blocks_taken"),
-        _scalar(error_flag, i32, "error_flag"), _stream_handle(stream))
+    r = ctx_lens.numel()
+    first = slots if slots is not None else positions if positions is not None else token_to_seq
+    tokens = 0 if first is None else first.numel()
+    free = free_blocks.numel()
+    if not (_is_vector(ctx_lens, _I32, r) and _is_vector(new_lens, _I32, r) and _is_vector(free_blocks, _I32, free)
+            and _is_vector(cu_new, _I32, r + 1) and _is_vector(seq_lens, _I32, r)
+            and (slots is None or _is_vector(slots, _I64, tokens))
+            and (positions is None or _is_vector(positions, _I32, tokens))
+            and (token_to_seq is None or _is_vector(token_to_seq, _I32, tokens))
+            and (cu_seq is None or _is_vector(cu_seq, _I32, r + 1))):
+        for what, t, dtype, n, optional in (
+                ("ctx_lens", ctx_lens, _I32, r, False), ("new_lens", new_lens, _I32, r, False),
+                ("free_blocks", free_blocks, _I32, free, False), ("cu_new", cu_new, _I32, r + 1, False),
+                ("seq_lens", seq_lens, _I32, r, False), ("slots", slots, _I64, tokens, True),
+                ("positions", positions, _I32, tokens, True), ("token_to_seq", token_to_seq, _I32, tokens, True),
+                ("cu_seq", cu_seq, _I32, r + 1, True)):
+            _vector(t, dtype, n, what, optional)
+    st = load_library().pmg_call_packed(0, PLAN_ARGS.pack(
+        ctx_lens.data_ptr(), new_lens.data_ptr(), r, block_table.data_ptr(), _table(block_table, r),
+        free_blocks.data_ptr(), free, num_blocks, block_size, _word(slots), _word(positions), _word(token_to_seq), tokens,
+        cu_new.data_ptr(), seq_lens.data_ptr(), _word(cu_seq), _scalar(blocks_taken, _I32, "blocks_taken"),
+        _scalar(error_flag, _I32, "error_flag"), _stream_word(ctx_lens, stream)))
     if st != PMG_OK:
         raise PmgError(st, "pmg_plan_step")
-
-
-def _reqs_table(block_table: torch.Tensor, reqs: int) -> int:
-    width = _table_width(block_table)
-    if block_table.shape[0] != reqs:
-        raise ValueError(f"block_table has {block_table.shape[0]} rows for {reqs} requests")
-    return width
 
 
 def append(c_kv: torch.Tensor, k_pe: torch.Tensor, cache: torch.Tensor, slots: torch.Tensor, positions: torch.Tensor,
@@ -375,37 +425,39 @@ def append(c_kv: torch.Tensor, k_pe: torch.Tensor, cache: torch.Tensor, slots: t
     None (no norm). q_out like q_pe (it may be q_pe). interleaved: pairs are
     neighbours instead of halves apart.
     """
-    _unit_last(c_kv, 2, "c_kv")
-    _unit_last(k_pe, 2, "k_pe")
-    _unit_last(cache, 3, "cache")
-    t, dv = c_kv.shape
-    dr = k_pe.shape[1]
-    if k_pe.shape[0] != t or cache.shape[2] != dv + dr:
+    (t, dv), cs = _unit_last("c_kv", 2, c_kv)
+    (tk, dr), ks = _unit_last("k_pe", 2, k_pe)
+    (blocks, block_size, entry), bs = _unit_last("cache", 3, cache)
+    dtype = c_kv.dtype
+    src, dst = TORCH_DTYPE_CODES.get(dtype), TORCH_DTYPE_CODES.get(cache.dtype)
+    if tk != t or entry != dv + dr:
         raise ValueError(f"c_kv {list(c_kv.shape)}, k_pe {list(k_pe.shape)} and cache {list(cache.shape)} do not fit")
-    if c_kv.dtype not in TORCH_DTYPE_CODES or k_pe.dtype != c_kv.dtype or cache.dtype not in TORCH_DTYPE_CODES:
-        raise ValueError(f"unsupported dtypes {c_kv.dtype}, {k_pe.dtype} -> {cache.dtype}")
-    if cos_sin.dtype != torch.float32 or cos_sin.dim() != 2 or cos_sin.shape[1] != dr or not cos_sin.is_contiguous():
+    if src is None or dst is None or k_pe.dtype is not dtype:
+        raise ValueError(f"unsupported dtypes {dtype}, {k_pe.dtype} -> {cache.dtype}")
+    rot = cos_sin.shape
+    if cos_sin.dtype is not _F32 or len(rot) != 2 or rot[1] != dr or not cos_sin.is_contiguous():
         raise ValueError(f"cos_sin must be float32 [num_positions, {dr}] and contiguous")
-    heads, qs, os_ = 0, (0, 0), (0, 0)
+    if not (_is_vector(slots, _I64, t) and _is_vector(positions, _I32, t)
+            and (norm_weight is None or _is_vector(norm_weight, _F32, dv))):
+        _vector(slots, _I64, t, "slots")
+        _vector(positions, _I32, t, "positions")
+        _vector(norm_weight, _F32, dv, "norm_weight", True)
     if (q_pe is None) != (q_out is None):
         raise ValueError("q_pe and q_out go together")
+    q = o = heads = 0
+    qs = os_ = (0, 0)
     if q_pe is not None:
-        _unit_last(q_pe, 3, "q_pe")
-        _unit_last(q_out, 3, "q_out")
-        heads = q_pe.shape[1]
-        if q_pe.shape != (t, heads, dr) or q_out.shape != q_pe.shape or q_pe.dtype != c_kv.dtype or (
-                q_out.dtype != c_kv.dtype):
-            raise ValueError(f"q_pe {list(q_pe.shape)} and q_out {list(q_out.shape)} must be [{t}, heads, {dr}] "
-                             f"of {c_kv.dtype}")
-        qs, os_ = q_pe.stride(), q_out.stride()
-    st = load_library().pmg_append(
-        c_kv.data_ptr(), c_kv.stride(0), k_pe.data_ptr(), k_pe.stride(0),
-        _vector(norm_weight, torch.float32, dv, "norm_weight", True), float(eps), cos_sin.data_ptr(), cos_sin.shape[0],
-        _vector(slots, torch.int64, t, "slots"), _vector(positions, torch.int32, t, "positions"), t, dv, dr,
-        TORCH_DTYPE_CODES[c_kv.dtype], cache.data_ptr(), cache.stride(0), cache.stride(1), cache.shape[0],
-        cache.shape[1], TORCH_DTYPE_CODES[cache.dtype], _scalar(scale, torch.float32, "scale"), _ptr(q_pe), qs[0],
-        qs[1], _ptr(q_out), os_[0], os_[1], heads, _scalar(error_flag, torch.int32, "error_flag"),
-        _stream_handle(stream), OPT_ROPE_PAIRS if interleaved else 0)
+        shape, qs = _unit_last("q_pe", 3, q_pe)
+        oshape, os_ = _unit_last("q_out", 3, q_out)
+        heads = shape[1]
+        if oshape != shape or shape[0] != t or shape[2] != dr or q_pe.dtype is not dtype or q_out.dtype is not dtype:
+            raise ValueError(f"q_pe {list(shape)} and q_out {list(oshape)} must be [{t}, heads, {dr}] of {dtype}")
+        q, o = q_pe.data_ptr(), q_out.data_ptr()
+    st = load_library().pmg_call_packed(1, APPEND_ARGS.pack(
+        c_kv.data_ptr(), cs[0], k_pe.data_ptr(), ks[0], _word(norm_weight), eps, cos_sin.data_ptr(), rot[0],
+        slots.data_ptr(), positions.data_ptr(), t, dv, dr, src, cache.data_ptr(), bs[0], bs[1], blocks, block_size, dst,
+        _scalar(scale, _F32, "scale"), q, qs[0], qs[1], o, os_[0], os_[1], heads,
+        _scalar(error_flag, _I32, "error_flag"), _stream_word(c_kv, stream), OPT_ROPE_PAIRS if interleaved else 0))
     if st != PMG_OK:
         raise PmgError(st, "pmg_append")
 
@@ -442,25 +494,25 @@ def latent_decode(q: torch.Tensor, cache: torch.Tensor, block_table: torch.Tenso
               sets what is latent and what is rope
     lse       fp32 [num_reqs, q_len, heads], contiguous, or None
     """
-    _unit_last(q, 4, "q")
-    _unit_last(cache, 3, "cache")
-    _unit_last(out, 4, "out")
-    r, q_len, heads, entry = q.shape
-    dv = out.shape[3]
-    if out.shape[:3] != q.shape[:3] or cache.shape[2] != entry or not 1 <= dv <= entry:
-        raise ValueError(f"q {list(q.shape)}, cache {list(cache.shape)} and out {list(out.shape)} do not fit")
-    if q.dtype not in TORCH_DTYPE_CODES or out.dtype != q.dtype or cache.dtype not in TORCH_DTYPE_CODES:
+    shape, qs = _unit_last("q", 4, q)
+    (blocks, block_size, cached), bs = _unit_last("cache", 3, cache)
+    oshape, os_ = _unit_last("out", 4, out)
+    r, q_len, heads, entry = shape
+    dv = oshape[3]
+    if oshape[:3] != shape[:3] or cached != entry or not 1 <= dv <= entry:
+        raise ValueError(f"q {list(shape)}, cache {list(cache.shape)} and out {list(oshape)} do not fit")
+    qd, cd = TORCH_DTYPE_CODES.get(q.dtype), TORCH_DTYPE_CODES.get(cache.dtype)
+    if qd is None or cd is None or out.dtype is not q.dtype:
         raise ValueError(f"unsupported dtypes {q.dtype}, {cache.dtype} -> {out.dtype}")
-    if lse is not None and (lse.dtype != torch.float32 or lse.shape != q.shape[:3] or not lse.is_contiguous()):
-        raise ValueError(f"lse must be float32 {list(q.shape[:3])} and contiguous")
-    qs, os_ = q.stride(), out.stride()
-    st = load_library().pmg_latent_decode(
-        q.data_ptr(), qs[0], qs[1], qs[2], cache.data_ptr(), cache.stride(0), cache.stride(1), cache.shape[0],
-        block_table.data_ptr(), _reqs_table(block_table, r), _vector(seq_lens, torch.int32, r, "seq_lens"), r, q_len,
-        heads, dv, entry - dv, cache.shape[1], TORCH_DTYPE_CODES[q.dtype], TORCH_DTYPE_CODES[cache.dtype],
-        _scalar(scale, torch.float32, "scale"), float(sm_scale), out.data_ptr(), os_[0], os_[1], os_[2], _ptr(lse),
-        workspace.data_ptr(), workspace.numel() * workspace.element_size(),
-        _scalar(error_flag, torch.int32, "error_flag"), _stream_handle(stream), int(options))
+    if not (_is_vector(seq_lens, _I32, r) and (lse is None or _is_vector(lse, _F32, r * q_len * heads))):
+        _vector(seq_lens, _I32, r, "seq_lens")
+        _vector(lse, _F32, r * q_len * heads, "lse", True)
+    st = load_library().pmg_call_packed(2, DECODE_ARGS.pack(
+        q.data_ptr(), qs[0], qs[1], qs[2], cache.data_ptr(), bs[0], bs[1], blocks, block_table.data_ptr(),
+        _table(block_table, r), seq_lens.data_ptr(), r, q_len, heads, dv, entry - dv, block_size, qd, cd,
+        _scalar(scale, _F32, "scale"), sm_scale, out.data_ptr(), os_[0], os_[1], os_[2], _word(lse),
+        workspace.data_ptr(), workspace.nbytes, _scalar(error_flag, _I32, "error_flag"), _stream_word(q, stream),
+        options))
     if st != PMG_OK:
         raise PmgError(st, "pmg_latent_decode")
 
@@ -483,39 +535,38 @@ def latent_prefill(q: torch.Tensor, k_nope: torch.Tensor, k_pe: torch.Tensor, v:
     prev_out, prev_lse  the result over other keys, joined with this one's
             (they may be out and lse).
     """
-    _unit_last(q, 3, "q")
-    _unit_last(k_nope, 3, "k_nope")
-    _unit_last(k_pe, 2, "k_pe")
-    _unit_last(v, 3, "v")
-    _unit_last(out, 3, "out")
-    tq, heads, dk = q.shape
-    tk, _, dn = k_nope.shape
-    dr, dv = k_pe.shape[1], v.shape[2]
-    if k_nope.shape[1] != heads or v.shape[:2] != (tk, heads) or k_pe.shape[0] != tk or dn + dr != dk or (
-            out.shape != (tq, heads, dv)):
+    (tq, heads, dk), qs = _unit_last("q", 3, q)
+    (tk, kh, dn), ks = _unit_last("k_nope", 3, k_nope)
+    (tp, dr), ps = _unit_last("k_pe", 2, k_pe)
+    (tv, vh, dv), vs = _unit_last("v", 3, v)
+    oshape, os_ = _unit_last("out", 3, out)
+    if kh != heads or vh != heads or tv != tk or tp != tk or dn + dr != dk or oshape != (tq, heads, dv):
         raise ValueError(f"q {list(q.shape)}, k_nope {list(k_nope.shape)}, k_pe {list(k_pe.shape)}, v "
-                         f"{list(v.shape)} and out {list(out.shape)} do not fit")
-    if q.dtype not in TORCH_DTYPE_CODES or any(t.dtype != q.dtype for t in (k_nope, k_pe, v, out)):
+                         f"{list(v.shape)} and out {list(oshape)} do not fit")
+    dtype = q.dtype
+    code = TORCH_DTYPE_CODES.get(dtype)
+    if code is None or not (k_nope.dtype is dtype and k_pe.dtype is dtype and v.dtype is dtype and out.dtype is dtype):
         raise ValueError("q, k_nope, k_pe, v and out must have one supported dtype")
     if (prev_out is None) != (prev_lse is None):
         raise ValueError("prev_out and prev_lse go together")
-    ps = (0, 0)
+    prev, rs = 0, (0, 0)
     if prev_out is not None:
-        _unit_last(prev_out, 3, "prev_out")
-        if prev_out.shape != out.shape or prev_out.dtype != out.dtype:
+        pshape, rs = _unit_last("prev_out", 3, prev_out)
+        if pshape != oshape or prev_out.dtype is not dtype:
             raise ValueError("prev_out must be like out")
-        ps = prev_out.stride()
-    for name, t in (("lse", lse), ("prev_lse", prev_lse)):
-        if t is not None and (t.dtype != torch.float32 or t.shape != (tq, heads) or not t.is_contiguous()):
-            raise ValueError(f"{name} must be float32 [{tq}, {heads}] and contiguous")
-    reqs = cu_q.shape[0] - 1
-    qs, ks, vs, os_ = q.stride(), k_nope.stride(), v.stride(), out.stride()
-    st = load_library().pmg_latent_prefill(
-        q.data_ptr(), qs[0], qs[1], k_nope.data_ptr(), ks[0], ks[1], k_pe.data_ptr(), k_pe.stride(0), v.data_ptr(),
-        vs[0], vs[1], _vector(cu_q, torch.int32, reqs + 1, "cu_q"), _vector(cu_k, torch.int32, reqs + 1, "cu_k"), reqs,
-        tq, tk, heads, dn, dr, dv, TORCH_DTYPE_CODES[q.dtype], float(sm_scale), out.data_ptr(), os_[0], os_[1],
-        _ptr(lse), _ptr(prev_out), ps[0], ps[1], _ptr(prev_lse), workspace.data_ptr(),
-        workspace.numel() * workspace.element_size(), _scalar(error_flag, torch.int32, "error_flag"),
-        _stream_handle(stream), (OPT_CAUSAL if causal else 0) | int(options))
+        prev = prev_out.data_ptr()
+    reqs = cu_q.numel() - 1
+    if not (_is_vector(cu_q, _I32, reqs + 1) and _is_vector(cu_k, _I32, reqs + 1)
+            and (lse is None or _is_vector(lse, _F32, tq * heads))
+            and (prev_lse is None or _is_vector(prev_lse, _F32, tq * heads))):
+        _vector(cu_q, _I32, reqs + 1, "cu_q")
+        _vector(cu_k, _I32, reqs + 1, "cu_k")
+        _vector(lse, _F32, tq * heads, "lse", True)
+        _vector(prev_lse, _F32, tq * heads, "prev_lse", True)
+    st = load_library().pmg_call_packed(3, PREFILL_ARGS.pack(
+        q.data_ptr(), qs[0], qs[1], k_nope.data_ptr(), ks[0], ks[1], k_pe.data_ptr(), ps[0], v.data_ptr(), vs[0], vs[1],
+        cu_q.data_ptr(), cu_k.data_ptr(), reqs, tq, tk, heads, dn, dr, dv, code, sm_scale, out.data_ptr(), os_[0], os_[1],
+        _word(lse), prev, rs[0], rs[1], _word(prev_lse), workspace.data_ptr(), workspace.nbytes,
+        _scalar(error_flag, _I32, "error_flag"), _stream_word(q, stream), (OPT_CAUSAL if causal else 0) | options))
     if st != PMG_OK:
         raise PmgError(st, "pmg_latent_prefill")

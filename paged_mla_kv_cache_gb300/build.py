@@ -12,7 +12,7 @@ import shutil
 import subprocess
 
 UNITS = ["mla_plan.cu", "mla_append.cu", "mla_decode.cu", "mla_decode_tc.cu", "mla_prefill.cu",
-         "mla_prefill_tc.cu"]
+         "mla_prefill_tc.cu", "mla_packed.cu"]
 PKG_DIR = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(PKG_DIR)
 CSRC = os.path.join(PKG_DIR, "csrc")

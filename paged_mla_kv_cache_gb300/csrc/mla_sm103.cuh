@@ -59,7 +59,7 @@ __device__ __forceinline__ void mbar_wait(uint32_t bar, uint32_t parity, uint32_
       "r"(parity), "r"(stop)
       : "memory");
 }
-// Waits for either of two; whether it was the first (the second goes before it where both are there).
+// Waits for either of two; whether it was the first (which goes before the second where both are there).
 __device__ __forceinline__ bool mbar_wait_either(uint32_t bar_a, uint32_t parity_a, uint32_t bar_b, uint32_t parity_b,
                                                  uint32_t stop) {
   uint32_t first;
@@ -68,19 +68,19 @@ __device__ __forceinline__ bool mbar_wait_either(uint32_t bar_a, uint32_t parity
       ".reg .pred p;\n\t"
       ".reg .b32 s;\n\t"
       ".reg .b64 t0, t1;\n\t"
-      "mov.b32 %0, 0;\n\t"
-      "mbarrier.test_wait.parity.shared::cta.b64 p, [%3], %4;\n\t"
-      "@p bra DONE%=;\n\t"
       "mov.b32 %0, 1;\n\t"
       "mbarrier.test_wait.parity.shared::cta.b64 p, [%1], %2;\n\t"
+      "@p bra DONE%=;\n\t"
+      "mov.b32 %0, 0;\n\t"
+      "mbarrier.test_wait.parity.shared::cta.b64 p, [%3], %4;\n\t"
       "@p bra DONE%=;\n\t"
       "mov.u64 t0, %%globaltimer;\n\t"
       "AGAIN%=:\n\t"
-      "mov.b32 %0, 0;\n\t"
-      "mbarrier.test_wait.parity.shared::cta.b64 p, [%3], %4;\n\t"
-      "@p bra DONE%=;\n\t"
       "mov.b32 %0, 1;\n\t"
       "mbarrier.test_wait.parity.shared::cta.b64 p, [%1], %2;\n\t"
+      "@p bra DONE%=;\n\t"
+      "mov.b32 %0, 0;\n\t"
+      "mbarrier.test_wait.parity.shared::cta.b64 p, [%3], %4;\n\t"
       "@p bra DONE%=;\n\t"
       "ld.volatile.shared.b32 s, [%5];\n\t"
       "setp.ne.b32 p, s, 0;\n\t"

@@ -14,7 +14,8 @@ ROOT = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
 def test_library_exports_the_operators(cuda_lib):
     text = re.sub(r"/\*.*?\*/", "", open(os.path.join(ROOT, "include", "pmg_mla.h")).read(), flags=re.S)
     names = sorted(set(re.findall(r"^\s*(?:int|int64_t)\s+(pmg_\w+)\s*\(", text, flags=re.M)))
-    assert names == ["pmg_append", "pmg_attention_workspace", "pmg_latent_decode", "pmg_latent_prefill", "pmg_plan_step"]
+    assert names == ["pmg_append", "pmg_attention_workspace", "pmg_call_packed", "pmg_latent_decode", "pmg_latent_prefill",
+                     "pmg_plan_step"]
     out = subprocess.run(["nm", "-D", "--defined-only", build.LIB_PATH], capture_output=True, text=True, check=True)
     for name in names:
         assert re.search(rf"\bT {name}$", out.stdout, flags=re.M)
@@ -119,3 +120,30 @@ def test_binding_refusals(cuda_lib):
     with pytest.raises(ValueError):
         binding.plan_step(z(2, dt=i), z(3, dt=i), z(2, 4, dt=i), z(4, dt=i), 16, None, None, None, z(3, dt=i),
                           z(2, dt=i), None, None, 4)
+
+
+def test_packed_calls_pass_every_argument(cuda_lib):
+    """Each argument in turn, out of range, gives its own refusal through the packed call: none is lost or shifted."""
+    decode = dict(binding.DECODE_WORDS)  # name -> format, in order
+    good = dict(q=4096, q_req_stride=576, q_token_stride=576, q_head_stride=576, cache=4096, cache_block_stride=64 * 576,
+                cache_token_stride=576, num_blocks=4, block_table=4096, block_table_stride=4, seq_lens=4096, num_reqs=2,
+                q_len=1, heads=1, latent_dim=512, rope_dim=64, block_size=64, q_dtype=0, cache_dtype=0, scale=0,
+                sm_scale=0.1, out=4096, out_req_stride=512, out_token_stride=512, out_head_stride=512, lse=4096,
+                workspace=4096, workspace_bytes=0, error_flag=0, stream=0, options=0)
+    assert list(decode) == list(good)
+
+    def run(**over):
+        return cuda_lib.pmg_call_packed(2, binding.DECODE_ARGS.pack(*{**good, **over}.values()))
+    for name, value, status in [("q", 0, 1), ("q", 4097, 4), ("cache", 0, 1), ("cache", 4097, 4), ("block_table", 4098, 4),
+                                ("seq_lens", 0, 1), ("num_reqs", -1, 2), ("q_len", -1, 2), ("heads", -1, 2),
+                                ("latent_dim", 0, 2), ("rope_dim", -1, 2), ("rope_dim", 1000, 5), ("block_size", 0, 2),
+                                ("q_dtype", 9, 3), ("cache_dtype", 9, 3), ("scale", 2, 4), ("sm_scale", -1.0, 2),
+                                ("out", 0, 1), ("lse", 2, 4), ("workspace", 0, 1), ("workspace", 8, 4),
+                                ("error_flag", 2, 4), ("options", 8, 2), ("num_blocks", -1, 2), ("block_table_stride", -1, 2),
+                                *[(n, -1, 2) for n in good if n.endswith("_stride") and n != "block_table_stride"]]:
+        assert run(**{name: value}) == status, name
+    assert cuda_lib.pmg_call_packed(2, None) == 1 and cuda_lib.pmg_call_packed(9, b"12345678") == 2
+    assert len(binding.PLAN_ARGS.pack(*[0] * 19)) == 19 * 8
+    assert cuda_lib.pmg_call_packed(0, binding.PLAN_ARGS.pack(*[0] * 8, 0, *[0] * 10)) == 2  # block_size 0
+    assert cuda_lib.pmg_call_packed(1, binding.APPEND_ARGS.pack(*[0] * 5, 0.0, *[0] * 25)) == 2
+    assert cuda_lib.pmg_call_packed(3, binding.PREFILL_ARGS.pack(*[0] * 21, 0.0, *[0] * 13)) == 2
