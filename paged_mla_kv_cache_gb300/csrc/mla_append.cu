@@ -85,17 +85,32 @@ __device__ __forceinline__ void store_n(T* dst, const float* x) {
   *reinterpret_cast<Pack<T, N>*>(dst) = p;
 }
 
-// The four pairs of unit u of a row: a and b of each.
+// The four pairs of unit u of a row as they are in memory, and a and b of each.
 template <class T>
-__device__ __forceinline__ void load_pairs(const T* row, int u, int half, bool pairs, float* a, float* b) {
+struct RawPairs {
+  Pack<T, 4> lo, hi;  // neighbours: pairs 0, 1 and 2, 3; halves: a and b
+};
+template <class T>
+__device__ __forceinline__ RawPairs<T> load_pairs(const T* row, int u, int half, bool pairs) {
+  RawPairs<T> r;
   if (pairs) {
-    float x[8];
-    load_n<T, 8>(row + 8 * u, x);
+    const Pack<T, 8> p = *reinterpret_cast<const Pack<T, 8>*>(row + 8 * u);
 #pragma unroll
-    for (int i = 0; i < 4; ++i) { a[i] = x[2 * i]; b[i] = x[2 * i + 1]; }
+    for (int i = 0; i < 4; ++i) { r.lo.v[i] = p.v[i]; r.hi.v[i] = p.v[4 + i]; }
   } else {
-    load_n<T, 4>(row + 4 * u, a);
-    load_n<T, 4>(row + half + 4 * u, b);
+    r.lo = *reinterpret_cast<const Pack<T, 4>*>(row + 4 * u);
+    r.hi = *reinterpret_cast<const Pack<T, 4>*>(row + half + 4 * u);
+  }
+  return r;
+}
+template <class T>
+__device__ __forceinline__ void split_pairs(const RawPairs<T>& r, bool pairs, float* a, float* b) {
+  if (pairs) {
+    a[0] = to_f(r.lo.v[0]); b[0] = to_f(r.lo.v[1]); a[1] = to_f(r.lo.v[2]); b[1] = to_f(r.lo.v[3]);
+    a[2] = to_f(r.hi.v[0]); b[2] = to_f(r.hi.v[1]); a[3] = to_f(r.hi.v[2]); b[3] = to_f(r.hi.v[3]);
+  } else {
+#pragma unroll
+    for (int i = 0; i < 4; ++i) { a[i] = to_f(r.lo.v[i]); b[i] = to_f(r.hi.v[i]); }
   }
 }
 
@@ -156,15 +171,15 @@ __global__ void __launch_bounds__(kWarps * 32) append_kernel(const __grid_consta
     const float scale = sizeof(TC) == 1 && p.scale != nullptr ? *p.scale : 1.0f;
     const float inv_n = 1.0f / static_cast<float>(p.dv);
     if constexpr (kVec) {
-      float x[kMaxLatentUnits][8];
+      Pack<TS, 8> raw[kMaxLatentUnits];
       float a[4], b[4], co[4], si[4];
       const bool turns = lane * 8 < p.dr;
       // every load of the token first
 #pragma unroll
       for (int i = 0; i < kMaxLatentUnits; ++i)
-        if ((lane + 32 * i) * 8 < p.dv) load_n<TS, 8>(c + (lane + 32 * i) * 8, x[i]);
+        if ((lane + 32 * i) * 8 < p.dv) raw[i] = *reinterpret_cast<const Pack<TS, 8>*>(c + (lane + 32 * i) * 8);
       if (turns) {
-        load_pairs(kp, lane, half, pairs, a, b);
+        split_pairs(load_pairs(kp, lane, half, pairs), pairs, a, b);
         load_n<float, 4>(cs + 4 * lane, co);
         load_n<float, 4>(cs + half + 4 * lane, si);
       }
@@ -175,7 +190,10 @@ __global__ void __launch_bounds__(kWarps * 32) append_kernel(const __grid_consta
         for (int i = 0; i < kMaxLatentUnits; ++i)
           if ((lane + 32 * i) * 8 < p.dv) {
 #pragma unroll
-            for (int k = 0; k < 8; ++k) sum += x[i][k] * x[i][k];
+            for (int k = 0; k < 8; ++k) {
+              const float v = to_f(raw[i].v[k]);
+              sum += v * v;
+            }
           }
         inv = rsqrtf(warp_sum(sum) * inv_n + p.eps);
       }
@@ -183,18 +201,21 @@ __global__ void __launch_bounds__(kWarps * 32) append_kernel(const __grid_consta
       for (int i = 0; i < kMaxLatentUnits; ++i) {
         const int at = (lane + 32 * i) * 8;
         if (at >= p.dv) continue;
+        float x[8];
+#pragma unroll
+        for (int k = 0; k < 8; ++k) x[k] = to_f(raw[i].v[k]);
         if (p.weight != nullptr) {
           float w[8];
           load_n<float, 4>(p.weight + at, w);
           load_n<float, 4>(p.weight + at + 4, w + 4);
 #pragma unroll
-          for (int k = 0; k < 8; ++k) x[i][k] = x[i][k] * inv * w[k];
+          for (int k = 0; k < 8; ++k) x[k] = x[k] * inv * w[k];
         }
         if constexpr (sizeof(TC) == 1) {
 #pragma unroll
-          for (int k = 0; k < 8; ++k) x[i][k] = x[i][k] / scale;
+          for (int k = 0; k < 8; ++k) x[k] = x[k] / scale;
         }
-        store_n<TC, 8>(row + at, x[i]);
+        store_n<TC, 8>(row + at, x);
       }
       if (turns) {
 #pragma unroll
@@ -231,7 +252,6 @@ __global__ void __launch_bounds__(kWarps * 32) append_kernel(const __grid_consta
   }
 
   // heads of a token's queries
-  if (!turned) return;  // reported by the entry's warp
   const int h0 = (part - 1) * p.heads_per_task;
   const int h1 = min(h0 + p.heads_per_task, p.H);
   const TS* q = reinterpret_cast<const TS*>(p.q) + t * p.qt_stride;
@@ -239,22 +259,27 @@ __global__ void __launch_bounds__(kWarps * 32) append_kernel(const __grid_consta
   if constexpr (kVec) {
     const int lanes = p.dr >> 3;      // lanes of a row: a divisor of 32
     const int u = lane & (lanes - 1), step = 32 / lanes;
+    const int h = h0 + lane / lanes;
+    // the queries do not wait for the position
+    RawPairs<TS> raw[kIters];
+#pragma unroll
+    for (int i = 0; i < kIters; ++i)
+      if (h + i * step < h1) raw[i] = load_pairs(q + (h + i * step) * p.qh_stride, u, half, pairs);
+    if (!turned) return;  // reported by the entry's warp
     float co[4], si[4];
     load_n<float, 4>(cs + 4 * u, co);
     load_n<float, 4>(cs + half + 4 * u, si);
-    float a[kIters][4], b[kIters][4];
-    const int h = h0 + lane / lanes;
-#pragma unroll
-    for (int i = 0; i < kIters; ++i)
-      if (h + i * step < h1) load_pairs(q + (h + i * step) * p.qh_stride, u, half, pairs, a[i], b[i]);
 #pragma unroll
     for (int i = 0; i < kIters; ++i)
       if (h + i * step < h1) {
+        float a[4], b[4];
+        split_pairs(raw[i], pairs, a, b);
 #pragma unroll
-        for (int k = 0; k < 4; ++k) rotate(a[i][k], b[i][k], co[k], si[k]);
-        store_pairs(o + (h + i * step) * p.oh_stride, u, half, pairs, a[i], b[i]);
+        for (int k = 0; k < 4; ++k) rotate(a[k], b[k], co[k], si[k]);
+        store_pairs(o + (h + i * step) * p.oh_stride, u, half, pairs, a, b);
       }
   } else {
+    if (!turned) return;
     for (int h = h0; h < h1; ++h)
       for (int i = lane; i < half; i += 32) {
         const int ia = pairs ? 2 * i : i, ib = pairs ? 2 * i + 1 : i + half;
