@@ -20,7 +20,7 @@
 namespace pmg_mla {
 namespace {
 
-constexpr int kWarps = 4;
+constexpr int kWarps = 4;          // tasks of a CTA
 constexpr int kIters = 4;          // row groups of queries a warp has in flight
 constexpr int kMaxLatentUnits = 4; // units of 8 latent values a lane holds: latent_dim up to 1024
 
@@ -139,27 +139,35 @@ __device__ __forceinline__ float warp_sum(float x) {
   return x;
 }
 
-template <class TS, class TC, bool kVec>
-__global__ void __launch_bounds__(kWarps * 32) append_kernel(const __grid_constant__ AppendParams p) {
+// What a launch does: entries and queries, or one of them. The queries' warps
+// need a third of the entries' registers, and their speed is the number of warps
+// that fit: large calls launch them by themselves.
+enum Work : int { kBoth = 0, kEntries = 1, kQueries = 2 };
+
+template <class TS, class TC, bool kVec, int kWork>
+__global__ void __launch_bounds__(kWarps * 32, kWork == kQueries ? 12 : 8)
+    append_kernel(const __grid_constant__ AppendParams p) {
   pdl_entry();
   const int lane = threadIdx.x & 31;
-  const int64_t task = static_cast<int64_t>(blockIdx.x) * kWarps + (threadIdx.x >> 5);
-  const int64_t t = task / p.tasks_per_token;
+  // tasks token by token: warps that run together read and write neighbouring rows
+  const uint32_t task = blockIdx.x * kWarps + (threadIdx.x >> 5);
+  const uint32_t tasks = kWork == kEntries ? 1 : kWork == kQueries ? p.tasks_per_token - 1 : p.tasks_per_token;
+  const int64_t t = kWork == kEntries ? task : task / tasks;
+  const int part = kWork == kEntries ? 0 : static_cast<int>(task % tasks) + (kWork == kQueries ? 1 : 0);
   if (t >= p.T) return;
-  const int part = static_cast<int>(task - t * p.tasks_per_token);
   const int half = p.dr >> 1;
   const bool pairs = p.pairs != 0;
   const int32_t pos = p.positions[t];
   const bool turned = pos >= 0 && pos < p.num_positions;
   const float* cs = p.cos_sin + static_cast<int64_t>(turned ? pos : 0) * p.dr;
 
-  if (part == 0) {
+  if (kWork == kEntries || (kWork == kBoth && part == 0)) {
     const int64_t slot = p.slots[t];
     if (slot < 0) {
       if (lane == 0 && pos >= p.num_positions) set_flag(p.err, PMG_FLAG_POSITION);
       return;
     }
-    const int64_t block = slot / p.B;
+    const int64_t block = slot <= UINT32_MAX ? static_cast<uint32_t>(slot) / static_cast<uint32_t>(p.B) : slot / p.B;
     if (!turned || block >= p.num_blocks) {
       if (lane == 0)
         set_flag(p.err, (turned ? 0 : PMG_FLAG_POSITION) | (block < p.num_blocks ? 0 : PMG_FLAG_PHYS_BLOCK));
@@ -293,19 +301,26 @@ __global__ void __launch_bounds__(kWarps * 32) append_kernel(const __grid_consta
 
 using Kernel = void (*)(const AppendParams);
 
-template <class TS, class TC>
+template <class TS, class TC, int kWork>
 Kernel pick(bool vec) {
-  return vec ? append_kernel<TS, TC, true> : append_kernel<TS, TC, false>;
+  return vec ? append_kernel<TS, TC, true, kWork> : append_kernel<TS, TC, false, kWork>;
+}
+
+template <class TS, int kWork>
+Kernel pick(int cache_dtype, bool vec) {
+  switch (cache_dtype) {
+    case PMG_BF16: return pick<TS, bf16, kWork>(vec);
+    case PMG_FP16: return pick<TS, f16, kWork>(vec);
+    case PMG_FP32: return pick<TS, float, kWork>(vec);
+    default: return pick<TS, e4m3, kWork>(vec);
+  }
 }
 
 template <class TS>
-Kernel pick(int cache_dtype, bool vec) {
-  switch (cache_dtype) {
-    case PMG_BF16: return pick<TS, bf16>(vec);
-    case PMG_FP16: return pick<TS, f16>(vec);
-    case PMG_FP32: return pick<TS, float>(vec);
-    default: return pick<TS, e4m3>(vec);
-  }
+Kernel pick(int cache_dtype, bool vec, Work work) {
+  // the queries do not depend on the cache's type
+  return work == kBoth ? pick<TS, kBoth>(cache_dtype, vec)
+                       : work == kEntries ? pick<TS, kEntries>(cache_dtype, vec) : pick<TS, bf16, kQueries>(vec);
 }
 
 }  // namespace
@@ -389,9 +404,18 @@ extern "C" int pmg_append(const void* c_kv, int64_t c_kv_stride, const void* k_p
                                    rows16(q_out, es, q_out_token_stride, q_out_head_stride)));
   p.heads_per_task = vec ? kIters * (32 / lanes) : 8;
   p.tasks_per_token = 1 + (heads + p.heads_per_task - 1) / p.heads_per_task;
-  const int64_t ctas = (num_tokens * p.tasks_per_token + kWarps - 1) / kWarps;
-  if (ctas > INT32_MAX) return PMG_ERR_UNSUPPORTED;
-  const Kernel k = src_dtype == PMG_BF16 ? pick<bf16>(cache_dtype, vec)
-                   : src_dtype == PMG_FP16 ? pick<f16>(cache_dtype, vec) : pick<float>(cache_dtype, vec);
-  return launch(k, dim3(static_cast<unsigned>(ctas)), kWarps * 32, 0, stream, p);
+  auto kernel = [&](Work work) {
+    return src_dtype == PMG_BF16 ? pick<bf16>(cache_dtype, vec, work)
+           : src_dtype == PMG_FP16 ? pick<f16>(cache_dtype, vec, work) : pick<float>(cache_dtype, vec, work);
+  };
+  // a warp a task
+  const int64_t tasks = p.tasks_per_token;
+  if (num_tokens * tasks > INT32_MAX) return PMG_ERR_UNSUPPORTED;
+  auto grid = [&](int64_t per_token) { return dim3(static_cast<unsigned>((num_tokens * per_token + kWarps - 1) / kWarps)); };
+  // a second launch costs about 2 us: more than it gives below some 16 MB of queries
+  if (tasks == 1 || num_tokens * heads * rope_dim * es < (int64_t{16} << 20))
+    return launch(kernel(tasks == 1 ? kEntries : kBoth), grid(tasks), kWarps * 32, 0, stream, p);
+  const int st = launch(kernel(kEntries), grid(1), kWarps * 32, 0, stream, p);
+  if (st != PMG_OK) return st;
+  return launch(kernel(kQueries), grid(tasks - 1), kWarps * 32, 0, stream, p);
 }
