@@ -51,19 +51,47 @@ struct Share {
   int64_t offset;      // pieces of it before `begin`
 };
 
+// x * a / b for 0 <= a <= b, in 32 bits where they do
+__device__ __forceinline__ int64_t scaled(int64_t x, int a, int b) {
+  if (x * a <= UINT32_MAX) return static_cast<uint32_t>(x * a) / static_cast<uint32_t>(b);
+  return x * a / b;
+}
+
+__device__ __forceinline__ Share cut_share(int64_t total, int unit, int units) {
+  Share s;
+  s.total = total;
+  s.units = static_cast<int32_t>(min(static_cast<int64_t>(units), total));
+  s.begin = unit < s.units ? scaled(total, unit, s.units) : total;
+  s.end = unit < s.units ? scaled(total, unit + 1, s.units) : total;
+  return s;
+}
+
 // This unit's share of sum over items of pieces(item), found by the whole
-// block. `scratch`: 33 int64, `found`: 2 int64, both shared.
+// block, or for up to 32 items by every warp for itself. `scratch`: 33 int64,
+// `found`: 2 int64, both shared.
 template <class F>
 __device__ __forceinline__ Share find_share(F pieces, int items, int unit, int units, int64_t* scratch, int64_t* found) {
   const int nt = blockDim.x, tid = threadIdx.x;
-  Share s;
+  if (items <= 32) {
+    const int lane = tid & 31;
+    const int64_t mine = lane < items ? pieces(lane) : 0;
+    int64_t inc = mine;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const int64_t y = __shfl_up_sync(0xffffffffu, inc, o);
+      if (lane >= o) inc += y;
+    }
+    Share s = cut_share(__shfl_sync(0xffffffffu, inc, 31), unit, units);
+    const bool here = inc - mine <= s.begin && s.begin < inc;
+    const int at = __ffs(__ballot_sync(0xffffffffu, here)) - 1;
+    s.item = at < 0 ? items : at;
+    s.offset = at < 0 ? 0 : s.begin - __shfl_sync(0xffffffffu, inc - mine, at);
+    return s;
+  }
   int64_t mine = 0, total = 0;
   for (int i = tid; i < items; i += nt) mine += pieces(i);
   int64_t before = block_scan<int64_t>(mine, scratch, total);
-  s.total = total;
-  s.units = static_cast<int32_t>(min(static_cast<int64_t>(units), total));
-  s.begin = unit < s.units ? total * unit / s.units : total;
-  s.end = unit < s.units ? total * (unit + 1) / s.units : total;
+  Share s = cut_share(total, unit, units);
   if (tid == 0) {
     found[0] = items;
     found[1] = 0;
@@ -97,7 +125,9 @@ __device__ __forceinline__ Share find_share(F pieces, int items, int unit, int u
 // The unit whose share holds flat piece x.
 __device__ __forceinline__ int unit_of(int64_t x, int64_t total, int units) {
   int64_t u = x * units / total;
+#pragma unroll 1
   while (u + 1 < units && total * (u + 1) / units <= x) ++u;
+#pragma unroll 1
   while (u > 0 && total * u / units > x) --u;
   return static_cast<int>(u);
 }

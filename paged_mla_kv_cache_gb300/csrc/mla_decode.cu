@@ -108,7 +108,7 @@ __global__ void __launch_bounds__(kGenThreads) decode_general_kernel(const __gri
 }
 
 template <class TQ>
-__global__ void __launch_bounds__(kJoinThreads) decode_join_kernel(const __grid_constant__ DecodeParams p) {
+__global__ void __launch_bounds__(kJoinThreads, kJoinCtasPerSm) decode_join_kernel(const __grid_constant__ DecodeParams p) {
   pdl_entry();
   const int rows = p.q_len * p.H;
   auto row_of = [&](int cta, int row) { return cta % p.groups * p.rows_per_group + row; };

@@ -238,6 +238,9 @@ __global__ void __launch_bounds__(kThreads, 1)
                           it.x.q0 + it.tile * kRows + h * kHalf);
         }
         __syncwarp();
+        // keys that few row tiles share come from HBM (512 rows over 60000 keys: 256 -> 244 us); where many do, they
+        // are in L2 and the hints only cost (causal 8192: 525 -> 532 us)
+        const bool stream = tiles_of(it.x) <= 4;
         for (int b = it.b0; b < it.b0 + it.n; ++b, ++step) {
           const int row = it.x.k0 + b * kBlock;
           // the pieces of a group share a barrier but come as soon as their own slots are free
@@ -258,6 +261,16 @@ __global__ void __launch_bounds__(kThreads, 1)
           __syncwarp();
           piece(&map_v, v_full, 3, 0, it.head, row);
           piece(&map_v, v_full, 4, 64, it.head, row);
+          if (stream && b + 2 < it.b0 + it.n && elect_one()) {
+            // the block after the next on its way into L2: shared memory has room for little more than one
+            const int ahead = row + 2 * kBlock;
+            tma_prefetch_3d(&map_k, 0, it.head, ahead);
+            tma_prefetch_3d(&map_k, 64, it.head, ahead);
+            tma_prefetch_3d(&map_v, 0, it.head, ahead);
+            tma_prefetch_3d(&map_v, 64, it.head, ahead);
+            tma_prefetch_3d(&map_pe, 0, 0, ahead);
+          }
+          __syncwarp();
         }
       }
       // after a timeout, copies in flight land before the CTA ends (`never` is not set: these waits run on)
@@ -576,7 +589,7 @@ __global__ void __launch_bounds__(kThreads, 1)
 }
 
 template <class T>
-__global__ void __launch_bounds__(kJoinThreads) prefill_join_kernel(const __grid_constant__ PrefillParams p) {
+__global__ void __launch_bounds__(kJoinThreads, kJoinCtasPerSm) prefill_join_kernel(const __grid_constant__ PrefillParams p) {
   pdl_entry();
   join_rows(
       p.ws, p.units, 1, kRows, kVal, kSlotFloats,
