@@ -174,16 +174,19 @@ __device__ __forceinline__ void load_queries(const DecodeParams& p, int b, int g
       for (int k = 0; k < 3; ++k)
         x[i][k] = r < n_rows && lane + 32 * k < kUnits ? src[lane + 32 * k] : make_uint4(0, 0, 0, 0);
     }
+    // (two rows a turn: their chains of instructions overlap)
 #pragma unroll 1
-    for (int i = 0; i < kBatch; ++i) {
-      const int r = r0 + 4 * i;
-      uint4 y[3] = {x[0][0], x[0][1], x[0][2]};
+    for (int i0 = 0; i0 < kBatch; i0 += 2) {
 #pragma unroll
-      for (int j = 1; j < kBatch; ++j)
-        if (i == j) {
-          y[0] = x[j][0];
-          y[1] = x[j][1];
-          y[2] = x[j][2];
+    for (int half = 0; half < 2; ++half) {
+      const int r = r0 + 4 * (i0 + half);
+      uint4 y[3] = {x[half][0], x[half][1], x[half][2]};
+#pragma unroll
+      for (int j = 2; j < kBatch; j += 2)
+        if (i0 == j) {
+          y[0] = x[j + half][0];
+          y[1] = x[j + half][1];
+          y[2] = x[j + half][2];
         }
       if constexpr (kParts == 1) {
         if (lane == 0) mi.factor[r] = factor;
@@ -226,6 +229,7 @@ __device__ __forceinline__ void load_queries(const DecodeParams& p, int b, int g
           }
         }
       }
+    }
     }
   }
 }

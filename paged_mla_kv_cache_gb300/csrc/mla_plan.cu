@@ -24,7 +24,8 @@ namespace {
 constexpr int kThreads = 512;
 constexpr int kGroup = 4096;               // requests of one group
 constexpr int kPer = kGroup / kThreads;    // requests a thread scans
-constexpr int kTokensPerCta = 2048;
+constexpr int kBatch = 4;                  // tokens of a thread whose page ids are looked up together
+constexpr int kTokensPerCta = kBatch * kThreads;
 
 struct PlanParams {
   const int32_t* ctx;
@@ -46,6 +47,8 @@ struct PlanParams {
   int32_t* taken;
   int32_t* err;
   int32_t slices;  // CTAs of a group
+  uint32_t magic;  // division by B
+  int32_t shift;
 };
 
 struct Lens {
@@ -65,26 +68,72 @@ __device__ __forceinline__ Lens lens_of(const PlanParams& p, int64_t r) {
   return l;
 }
 
-__device__ __forceinline__ uint32_t pages_of(uint32_t len, uint32_t B) { return len / B + (len % B != 0 ? 1u : 0u); }
+// n / B by one multiply-high, an add and a shift (the invariant-divisor method
+// of Granlund and Montgomery, 1994); the host computes magic and shift. Every
+// CTA divides twice a request: as plain divisions that took half the kernel.
+__device__ __forceinline__ uint32_t page_of(const PlanParams& p, uint32_t n) {
+  return static_cast<uint32_t>((static_cast<uint64_t>(__umulhi(p.magic, n)) + n) >> p.shift);
+}
+__device__ __forceinline__ uint32_t pages_of(const PlanParams& p, uint32_t len) {
+  return len == 0 ? 0 : page_of(p, len - 1) + 1;
+}
 
 __device__ __forceinline__ int32_t cut(int64_t x) { return static_cast<int32_t>(x < INT32_MAX ? x : INT32_MAX); }
 
-// last i in [0, n) with a[i] <= key, where a[0] <= key
+// Exclusive prefix sums of three values over the threads of the block, and the totals.
+struct Sums {
+  int64_t fresh, seq, page;
+};
+__device__ __forceinline__ Sums scan_sums(const Sums& x, Sums* scratch, Sums& all) {
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  Sums inc = x;
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const int64_t a = __shfl_up_sync(0xffffffffu, inc.fresh, o), b = __shfl_up_sync(0xffffffffu, inc.seq, o),
+                  c = __shfl_up_sync(0xffffffffu, inc.page, o);
+    if (lane >= o) {
+      inc.fresh += a;
+      inc.seq += b;
+      inc.page += c;
+    }
+  }
+  __syncthreads();  // scratch is free again
+  if (lane == 31) scratch[warp] = inc;
+  __syncthreads();
+  Sums before{0, 0, 0};
+  all = Sums{0, 0, 0};
+#pragma unroll
+  for (int w = 0; w < kThreads / 32; ++w) {
+    const Sums y = scratch[w];
+    if (w == warp) before = all;
+    all.fresh += y.fresh;
+    all.seq += y.seq;
+    all.page += y.page;
+  }
+  return {before.fresh + inc.fresh - x.fresh, before.seq + inc.seq - x.seq, before.page + inc.page - x.page};
+}
+
+// A thread scans kPer neighbours: with one place left out after each kPer, the
+// threads of a warp write different banks.
+__device__ __forceinline__ int place(int k) { return k + k / kPer; }
+constexpr int kPlaces = kGroup + kGroup / kPer + 1;
+
+// last i in [0, n) with a[place(i)] <= key, where the first one is
 __device__ __forceinline__ int find(const int64_t* a, int n, int64_t key) {
   int lo = 0, hi = n;
   while (hi - lo > 1) {
     const int mid = (lo + hi) >> 1;
-    if (a[mid] <= key) lo = mid; else hi = mid;
+    if (a[place(mid)] <= key) lo = mid; else hi = mid;
   }
   return lo;
 }
 
 __global__ void __launch_bounds__(kThreads) plan_step_kernel(const __grid_constant__ PlanParams p) {
   extern __shared__ __align__(16) uint8_t smem[];
-  int64_t* cu = reinterpret_cast<int64_t*>(smem);   // [n + 1] first new token of each request
-  int64_t* pg = cu + (kGroup + 1);                  // [n + 1] first fresh page of each request
-  int32_t* ctx = reinterpret_cast<int32_t*>(pg + (kGroup + 1));  // [n]
-  __shared__ int64_t scratch[33];
+  int64_t* cu = reinterpret_cast<int64_t*>(smem);   // first new token of each request, by place()
+  int64_t* pg = cu + kPlaces;                  // first fresh page of each request
+  int32_t* ctx = reinterpret_cast<int32_t*>(pg + kPlaces);  // cached tokens
+  __shared__ Sums scratch[kThreads / 32];
   pdl_entry();
 
   const int group = blockIdx.x / p.slices, slice = blockIdx.x % p.slices;
@@ -96,57 +145,64 @@ __global__ void __launch_bounds__(kThreads) plan_step_kernel(const __grid_consta
   // the groups before this one
   int64_t base_new = 0, base_seq = 0, base_page = 0;
   if (r0 > 0) {
-    int64_t a = 0, b = 0, c = 0;
+    Sums x{0, 0, 0}, all;
     for (int64_t r = threadIdx.x; r < r0; r += kThreads) {
       const Lens l = lens_of(p, r);
-      a += l.fresh;
-      b += static_cast<int64_t>(l.ctx) + l.fresh;
-      c += pages_of(l.ctx + l.fresh, B) - pages_of(l.ctx, B);
+      x.fresh += l.fresh;
+      x.seq += static_cast<int64_t>(l.ctx) + l.fresh;
+      x.page += pages_of(p, l.ctx + l.fresh) - pages_of(p, l.ctx);
     }
-    block_scan<int64_t>(a, scratch, base_new);
-    block_scan<int64_t>(b, scratch, base_seq);
-    block_scan<int64_t>(c, scratch, base_page);
+    scan_sums(x, scratch, all);
+    base_new = all.fresh;
+    base_seq = all.seq;
+    base_page = all.page;
   }
 
-  // this group: each thread owns kPer consecutive requests
-  int64_t an = 0, as = 0, ap = 0;
-  Lens own[kPer];
+  // this group's lengths into shared memory (the new ones in the page sums' place for now); then each thread owns kPer
+  // consecutive requests
+  int32_t* fresh = reinterpret_cast<int32_t*>(pg);
+  for (int k = threadIdx.x; k < n; k += kThreads) {
+    const Lens l = lens_of(p, r0 + k);
+    bad |= l.bad;
+    ctx[place(k)] = l.ctx;
+    fresh[place(k)] = l.fresh;
+  }
+  __syncthreads();
+  Sums mine{0, 0, 0};
+  int32_t own_ctx[kPer], own_new[kPer];
 #pragma unroll
   for (int i = 0; i < kPer; ++i) {
     const int k = static_cast<int>(threadIdx.x) * kPer + i;
-    own[i] = k < n ? lens_of(p, r0 + k) : Lens{0, 0, 0};
-    bad |= own[i].bad;
-    an += own[i].fresh;
-    as += static_cast<int64_t>(own[i].ctx) + own[i].fresh;
-    ap += pages_of(own[i].ctx + own[i].fresh, B) - pages_of(own[i].ctx, B);
+    own_ctx[i] = k < n ? ctx[place(k)] : 0;
+    own_new[i] = k < n ? fresh[place(k)] : 0;
+    mine.fresh += own_new[i];
+    mine.seq += static_cast<int64_t>(own_ctx[i]) + own_new[i];
+    mine.page += pages_of(p, own_ctx[i] + own_new[i]) - pages_of(p, own_ctx[i]);
   }
-  int64_t tn, ts, tp;
-  int64_t cn = base_new + block_scan<int64_t>(an, scratch, tn);
-  int64_t cs = base_seq + block_scan<int64_t>(as, scratch, ts);
-  int64_t cp = base_page + block_scan<int64_t>(ap, scratch, tp);
+  Sums all;
+  const Sums before = scan_sums(mine, scratch, all);  // (its barriers come before the page sums are written)
+  const int64_t tn = all.fresh, ts = all.seq, tp = all.page;
+  int64_t cn = base_new + before.fresh, cs = base_seq + before.seq, cp = base_page + before.page;
   const bool writer = slice == 0;
 #pragma unroll
   for (int i = 0; i < kPer; ++i) {
     const int k = static_cast<int>(threadIdx.x) * kPer + i;
     if (k < n) {
-      cu[k] = cn;
-      pg[k] = cp;
-      ctx[k] = own[i].ctx;
+      cu[place(k)] = cn;
+      pg[place(k)] = cp;
       if (writer) {
         p.cu_new[r0 + k] = cut(cn);
         if (p.cu_seq != nullptr) p.cu_seq[r0 + k] = cut(cs);
-        p.seq_lens[r0 + k] = own[i].ctx + own[i].fresh;
+        p.seq_lens[r0 + k] = own_ctx[i] + own_new[i];
       }
     }
-    cn += own[i].fresh;
-    cs += static_cast<int64_t>(own[i].ctx) + own[i].fresh;
-    cp += pages_of(own[i].ctx + own[i].fresh, B) - pages_of(own[i].ctx, B);
+    cn += own_new[i];
+    cs += static_cast<int64_t>(own_ctx[i]) + own_new[i];
+    cp += pages_of(p, own_ctx[i] + own_new[i]) - pages_of(p, own_ctx[i]);
   }
   const int64_t end_new = base_new + tn, end_page = base_page + tp;
   const bool last = r0 + n == p.R;
   if (threadIdx.x == 0) {
-    cu[n] = end_new;
-    pg[n] = end_page;
     if (writer && last) {
       p.cu_new[p.R] = cut(end_new);
       if (p.cu_seq != nullptr) p.cu_seq[p.R] = cut(base_seq + ts);
@@ -161,7 +217,7 @@ __global__ void __launch_bounds__(kThreads) plan_step_kernel(const __grid_consta
     const int64_t lo = base_page + tp * slice / p.slices, hi = base_page + tp * (slice + 1) / p.slices;
     for (int64_t i = lo + threadIdx.x; i < hi; i += kThreads) {
       const int k = find(pg, n, i);
-      const int64_t column = pages_of(ctx[k], B) + (i - pg[k]);
+      const int64_t column = pages_of(p, ctx[place(k)]) + (i - pg[place(k)]);
       int32_t id = -1;
       if (i >= p.num_free) {
         bad |= PMG_FLAG_NO_BLOCKS;
@@ -182,40 +238,65 @@ __global__ void __launch_bounds__(kThreads) plan_step_kernel(const __grid_consta
     const int64_t begin = min(base_new, p.max_tokens), end = last ? p.max_tokens : min(end_new, p.max_tokens);
     const int64_t span = end - begin;
     const int64_t lo = begin + span * slice / p.slices, hi = begin + span * (slice + 1) / p.slices;
-    for (int64_t t = lo + threadIdx.x; t < hi; t += kThreads) {
-      int64_t slot = -1;
-      int32_t pos = -1, seq = -1;
-      if (t < end_new) {
-        const int k = find(cu, n, t);
-        seq = static_cast<int32_t>(r0 + k);
-        const uint32_t at = static_cast<uint32_t>(ctx[k]) + static_cast<uint32_t>(t - cu[k]);
-        pos = static_cast<int32_t>(at);
-        if (p.slots != nullptr) {
-          const uint32_t page = at / B, first = pages_of(ctx[k], B);
-          int64_t id = -1;
-          if (page < p.bt_stride) {
-            if (page >= first) {
-              const int64_t i = pg[k] + (page - first);
-              if (i < p.num_free) id = p.free_ids[i];
-            } else {
-              id = p.bt[static_cast<int64_t>(seq) * p.bt_stride + page];
-            }
-            if (id >= 0 && id < p.num_blocks) slot = id * p.B + at % B;
-            else if (page < first) bad |= PMG_FLAG_PHYS_BLOCK;
-          } else {
-            bad |= PMG_FLAG_LOGICAL_BLOCK;
+    // a warp takes 32 kBatch neighbouring tokens: one search for the first, then the requests that begin among the next 32
+    const int lane = threadIdx.x & 31;
+    for (int64_t w0 = lo + (threadIdx.x >> 5) * (32 * kBatch); w0 < hi; w0 += kBatch * kThreads) {
+      int64_t id[kBatch];
+      int32_t pos[kBatch], seq[kBatch];
+      uint32_t in_page[kBatch];
+      int k0 = w0 < end_new ? find(cu, n, w0) : 0;
+      // every look-up before the first store
+#pragma unroll
+      for (int j = 0; j < kBatch; ++j) {
+        const int64_t tw = w0 + 32 * j, t = tw + lane;
+        id[j] = -1;
+        pos[j] = seq[j] = -1;
+        in_page[j] = 0;
+        // token `lane` is in request k0 + c: c beginnings of the next 32 requests are not after it
+        const int64_t begin_k = k0 + 1 + lane < n ? cu[place(k0 + 1 + lane)] - tw : 32;
+        const int rel = static_cast<int>(min(begin_k, int64_t{32}));
+        int c = 0;
+#pragma unroll
+        for (int o = 16; o > 0; o >>= 1)
+          if (__shfl_sync(0xffffffffu, rel, c + o - 1) <= lane) c += o;
+        if (__shfl_sync(0xffffffffu, rel, 31) <= lane) c = 32;  // (the search ends at 31)
+        const int k = c < 32 || t >= end_new ? k0 + c : find(cu, n, t);
+        k0 = __shfl_sync(0xffffffffu, k, 31);
+        if (t >= hi || t >= end_new) continue;
+        seq[j] = static_cast<int32_t>(r0 + k);
+        const uint32_t at = static_cast<uint32_t>(ctx[place(k)]) + static_cast<uint32_t>(t - cu[place(k)]);
+        pos[j] = static_cast<int32_t>(at);
+        if (p.slots == nullptr) continue;
+        const uint32_t page = page_of(p, at), first = pages_of(p, ctx[place(k)]);
+        in_page[j] = at - page * B;
+        if (page >= p.bt_stride) {
+          bad |= PMG_FLAG_LOGICAL_BLOCK;
+        } else if (page >= first) {
+          const int64_t i = pg[place(k)] + (page - first);
+          if (i < p.num_free) id[j] = p.free_ids[i];
+          if (id[j] >= p.num_blocks) id[j] = -1;  // reported where the table is written
+        } else {
+          id[j] = p.bt[static_cast<int64_t>(seq[j]) * p.bt_stride + page];
+          if (id[j] < 0 || id[j] >= p.num_blocks) {
+            bad |= PMG_FLAG_PHYS_BLOCK;
+            id[j] = -1;
           }
         }
       }
-      if (p.slots != nullptr) p.slots[t] = slot;
-      if (p.positions != nullptr) p.positions[t] = pos;
-      if (p.t2s != nullptr) p.t2s[t] = seq;
+#pragma unroll
+      for (int j = 0; j < kBatch; ++j) {
+        const int64_t t = w0 + 32 * j + lane;
+        if (t >= hi) continue;
+        if (p.slots != nullptr) p.slots[t] = id[j] < 0 ? -1 : id[j] * p.B + in_page[j];
+        if (p.positions != nullptr) p.positions[t] = pos[j];
+        if (p.t2s != nullptr) p.t2s[t] = seq[j];
+      }
     }
   }
   set_flag(p.err, bad);
 }
 
-constexpr int kSmem = (kGroup + 1) * 16 + kGroup * 4;
+constexpr int kSmem = kPlaces * 20;
 
 }  // namespace
 }  // namespace pmg_mla
@@ -241,7 +322,11 @@ extern "C" int pmg_plan_step(const int32_t* ctx_lens, const int32_t* new_lens, i
     return PMG_ERR_ALIGN;
   PlanParams p{ctx_lens, new_lens, num_reqs, block_table, block_table_stride, free_blocks, num_free, num_blocks,
                block_size, slots, positions, token_to_seq, max_tokens, cu_new, seq_lens, cu_seq, blocks_taken,
-               error_flag, 1};
+               error_flag, 1, 0, 0};
+  uint32_t l = 0;
+  while ((1ull << l) < static_cast<uint64_t>(block_size)) ++l;
+  p.magic = static_cast<uint32_t>((((1ull << l) - static_cast<uint64_t>(block_size)) << 32) / static_cast<uint64_t>(block_size) + 1);
+  p.shift = static_cast<int32_t>(l);
   int sms = 0;
   int st = sm_count(&sms);
   if (st == PMG_OK) st = allow_smem(reinterpret_cast<const void*>(plan_step_kernel), kSmem);
