@@ -1,0 +1,166 @@
+"""Where the operators could go wrong besides their sizes: far offsets, many requests, graphs, streams, scales."""
+import math
+
+import numpy as np
+import pytest
+import torch
+
+from paged_mla_kv_cache_gb300 import binding
+
+import mla_reference as ref
+from test_mla_ops_gpu import BF16, DEV, FP8, GENERAL, decode_case, gen, i32, normal, prefill_case, run_decode, run_prefill
+
+pytestmark = pytest.mark.gpu
+
+
+@pytest.fixture(scope="module", autouse=True)
+def _lib(cuda_lib):
+    if not torch.cuda.is_available():
+        pytest.fail("a GPU test ran without a CUDA device")
+    return cuda_lib
+
+
+@pytest.fixture(scope="module")
+def ws():
+    return binding.new_attention_workspace(DEV)
+
+
+@pytest.mark.parametrize("options", [0, GENERAL])
+def test_decode_pages_past_32_bit_offsets(ws, options):
+    """Pages whose byte and element offsets pass 2^32."""
+    blocks, block = 120000, 64  # 4.6e9 elements
+    cache = torch.empty(blocks, block, 600, dtype=BF16, device=DEV)[:, :, :576]
+    pages = [0, blocks - 1, 60001, blocks - 7]
+    for p in pages:
+        cache[p] = normal(gen(p + 1), block, 576, dtype=BF16)
+    table, lens = i32([pages]), i32([230])
+    q = normal(gen(9), 1, 1, 16, 576, dtype=BF16)
+    out, lse = torch.empty(1, 1, 16, 512, dtype=BF16, device=DEV), torch.empty(1, 1, 16, device=DEV)
+    binding.latent_decode(q, cache, table, lens, out, lse, sm_scale=0.07, workspace=ws, options=options)
+    small = torch.stack([cache[p] for p in pages])
+    want, wl, pv, worst, _ = ref.decode(q, small, i32([[0, 1, 2, 3]]), lens, 512, 0.07)
+    ref.check_attention(out, lse, want, wl, pv, worst, 576, ref.U[BF16])
+
+
+def test_append_slots_past_32_bit_offsets():
+    blocks, block = 120000, 64
+    cache = torch.empty(blocks, block, 576, dtype=BF16, device=DEV)
+    c, kp = normal(gen(1), 3, 512, dtype=BF16), normal(gen(2), 3, 64, dtype=BF16)
+    slots = torch.tensor([blocks * block - 1, 5, 70000 * block + 3], device=DEV)
+    cs = torch.cat([torch.ones(4, 32, device=DEV), torch.zeros(4, 32, device=DEV)], 1).contiguous()
+    binding.append(c, kp, cache, slots, i32([0, 1, 2]), cs)
+    got = cache.view(-1, 576)[slots]
+    assert torch.equal(got, torch.cat([c, kp], 1))
+
+
+@pytest.mark.parametrize("options", [0, GENERAL])
+def test_prefill_rows_past_32_bit_offsets(ws, options):
+    tk, heads = 72000, 128  # 2.36e9 elements
+    kv = torch.empty(tk, heads, 256, dtype=BF16, device=DEV)
+    kv[-200:] = normal(gen(3), 200, heads, 256, dtype=BF16)
+    pe = torch.empty(tk, 64, dtype=BF16, device=DEV)
+    pe[-200:] = normal(gen(4), 200, 64, dtype=BF16)
+    q = normal(gen(5), 70, heads, 192, dtype=BF16)
+    out, lse = torch.empty(70, heads, 128, dtype=BF16, device=DEV), torch.empty(70, heads, device=DEV)
+    cu_q, cu_k = i32([0, 0, 70]), i32([0, tk - 200, tk])
+    binding.latent_prefill(q, kv[:, :, :128], pe, kv[:, :, 128:], cu_q, cu_k, out, lse, sm_scale=0.07, causal=True,
+                           workspace=ws, options=options)
+    want, wl, pv, worst = ref.prefill(q, kv[-200:, :, :128], pe[-200:], kv[-200:, :, 128:], [0, 70], [0, 200], 0.07, True)
+    ref.check_attention(out, lse, want, wl, pv, worst, 192, ref.U[BF16])
+
+
+@pytest.mark.parametrize("reqs", [32, 33, 500])
+@pytest.mark.parametrize("options", [0, GENERAL])
+def test_many_requests(ws, reqs, options):
+    rng = np.random.default_rng(reqs)
+    lens = rng.integers(0, 90, reqs)
+    lens[::7] = 0
+    run_decode(decode_case(lens.tolist(), 8, 1, BF16, BF16, 16), ws, options=options)
+    q_lens = np.minimum(rng.integers(0, 40, reqs), lens)
+    for causal in (False, True):
+        run_prefill(prefill_case(q_lens.tolist(), lens.tolist(), 2, BF16, prev=True), ws, causal, options)
+
+
+@pytest.mark.parametrize("options", [0, GENERAL])
+def test_scale_of_zero(ws, options):
+    """Every seen key weighs the same."""
+    run_decode(decode_case([100, 7], 16, 2, BF16, BF16, 16), ws, options=options, sm=0.0)
+    run_decode(decode_case([100, 7], 16, 2, BF16, FP8, 16), ws, options=options, sm=0.0)
+    run_prefill(prefill_case([30, 5], [130, 5], 2, BF16), ws, True, options, sm=0.0)
+
+
+def test_rows_that_see_nothing(ws):
+    """More new tokens than entries: the first rows see none; a prefill of more queries than keys likewise."""
+    for options in (0, GENERAL):
+        for cdt in (BF16, FP8):
+            out, lse = run_decode(decode_case([2, 5, 0], 16, 4, BF16, cdt, 16), ws, options=options)
+            assert (out[0, :2] == 0).all() and (lse[0, :2] == -math.inf).all() and (lse[0, 2:] > -math.inf).all()
+        out, lse = run_prefill(prefill_case([300, 200], [50, 0], 2, BF16), ws, True, options)
+        assert (out[:250] == 0).all() and (lse[:250] == -math.inf).all() and (lse[250:300] > -math.inf).all()
+
+
+def test_entries_that_share_pages(ws):
+    """Requests with a common prefix name the same pages."""
+    q, cache, table, lens, sc = decode_case([300, 300, 300], 16, 1, BF16, BF16, 64, nan_tail=False)
+    table[1, :3], table[2, :4] = table[0, :3], table[0, :4]
+    run_decode((q, cache, table, lens, sc), ws)
+
+
+def test_a_step_in_a_graph_follows_its_inputs(ws):
+    """plan, append and decode captured once; replays follow the lengths, queries and entries of the moment."""
+    reqs, heads, block = 3, 16, 16
+    ctx, new = i32([20, 0, 100]), i32([1, 1, 1])
+    table = torch.full((reqs, 16), -1, dtype=torch.int32, device=DEV)
+    for r in range(reqs):
+        table[r, :8] = torch.arange(8, dtype=torch.int32) + 8 * r
+    free = torch.arange(24, 40, dtype=torch.int32, device=DEV)
+    cache = normal(gen(1), 40, block, 576, dtype=BF16)
+    slots = torch.empty(4, dtype=torch.int64, device=DEV)
+    positions, t2s, cu, cu_seq = i32([0] * 4), i32([0] * 4), i32([0] * 4), i32([0] * 4)
+    lens, taken = i32([0] * 3), i32([0])
+    down, q = normal(gen(2), 4, 576, dtype=BF16), normal(gen(3), 4, heads, 576, dtype=BF16)
+    cs = torch.cat([torch.ones(200, 32, device=DEV), torch.zeros(200, 32, device=DEV)], 1).contiguous()
+    out = torch.empty(reqs, 1, heads, 512, dtype=BF16, device=DEV)
+
+    def step():
+        binding.plan_step(ctx, new, table, free, block, slots, positions, t2s, cu, lens, cu_seq, taken, 40)
+        binding.append(down[:, :512], down[:, 512:], cache, slots, positions, cs, q_pe=q[:, :, 512:], q_out=q[:, :, 512:])
+        binding.latent_decode(q[:3].view(3, 1, heads, 576), cache, table, lens, out, sm_scale=0.07, workspace=ws)
+
+    step()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        step()
+    for lengths in ([20, 0, 100], [31, 15, 127], [32, 16, 5]):
+        ctx.copy_(i32(lengths))
+        down.copy_(normal(gen(sum(lengths)), 4, 576, dtype=BF16))
+        graph.replay()
+        torch.cuda.synchronize()
+        assert lens.tolist() == [n + 1 for n in lengths]
+        assert slots.tolist()[:3] == [int(table[r, n // block]) * block + n % block for r, n in enumerate(lengths)]
+        assert slots[3] == -1 and positions[3] == -1
+        for r, n in enumerate(lengths):
+            assert torch.equal(cache[int(table[r, n // block]), n % block], down[r])
+        want, _, pv, worst, _ = ref.decode(q[:3].view(3, 1, heads, 576), cache, table, lens, 512, 0.07)
+        err = (out.double() - want).abs()
+        assert (err <= ref.U[BF16] * want.abs() + (ref.U[BF16] + 1e-3) * pv).all()
+
+
+def test_prefill_on_another_stream_and_in_a_graph(ws):
+    c = prefill_case([300, 77], [900, 500], 4, BF16)
+    want, _ = run_prefill(c, ws, True)
+    out, side, ws2 = torch.zeros_like(want), torch.cuda.Stream(), torch.empty_like(ws).fill_(255)
+    torch.cuda.synchronize()
+    args = (c["q"], c["k"], c["pe"], c["v"], c["cu_q"], c["cu_k"], out)
+    kw = dict(sm_scale=1 / math.sqrt(192), causal=True, workspace=ws2)
+    binding.latent_prefill(*args, **kw, stream=side)
+    torch.cuda.synchronize()
+    assert torch.equal(out, want)
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        binding.latent_prefill(*args, **kw)
+    for _ in range(3):
+        out.zero_()
+        graph.replay()
+        torch.cuda.synchronize()
+        assert torch.equal(out, want)
