@@ -136,9 +136,8 @@ int pmg_append(const void* c_kv, int64_t c_kv_stride, const void* k_pe, int64_t 
  *  lse        fp32 [num_reqs, q_len, heads], contiguous, or NULL
  *  workspace  pmg_attention_workspace() bytes, 16-byte aligned; its content
  *             does not matter. Calls that may overlap need one each.
- * Slots of the cache at or past seq_lens[r] may hold anything, NaN too. An
- * entry that a row does not see only for its place among the new tokens has to
- * be finite.
+ * Slots of the cache at or past seq_lens[r] may hold anything, NaN too, and a
+ * row is not touched by infinities or NaN in entries that it does not see.
  *
  * The tensor-core kernel runs for latent_dim 512, rope_dim 64, q_dtype bf16 or
  * fp16, a block_size that is a multiple of 8, 16-byte aligned cache rows of
@@ -166,6 +165,8 @@ int pmg_latent_decode(const void* q, int64_t q_req_stride, int64_t q_token_strid
  *   lse' = log(exp(lse) + exp(prev_lse)),
  *   out' = exp(lse - lse') out + exp(prev_lse - lse') prev_out.
  * A row that sees nothing gives out = 0, lse = -inf (or the previous state).
+ * A row is not touched by infinities or NaN in keys and values that it does not
+ * see, nor by a previous result whose prev_lse is -inf.
  *
  *  q       [total_q, heads, nope_dim + rope_dim], k_nope [total_k, heads,
  *          nope_dim], k_pe [total_k, rope_dim], v [total_k, heads, v_dim], out

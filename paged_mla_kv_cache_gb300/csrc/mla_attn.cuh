@@ -199,7 +199,7 @@ __device__ __forceinline__ void join_rows(const Workspace& ws, int notes, int st
         if (d + 2 < dv) x.z = o[2];
         if (d + 3 < dv) x.w = o[3];
       }
-      if (m == -INFINITY) continue;  // the row saw nothing there, and may have no values
+      if (part_l == 0.0f) continue;  // the row saw nothing there (a NaN among its scores makes a sum of NaN, which counts)
       const float w = exp2f(m - top);
       l += w * part_l;
       a.x += w * x.x;

@@ -75,11 +75,11 @@ __global__ void __launch_bounds__(kGenThreads) decode_general_kernel(const __gri
     float* slot = p.ws.slots + (static_cast<int64_t>(blockIdx.x) * 2 + (tile == 0 ? 1 : 0)) * p.slot_floats;
     __syncthreads();
     if (lane == 0) {  // what every row is multiplied by, and its log sum
-      s.scale[row] = whole ? (l > 0.0f ? 1.0f / l : 0.0f) : 1.0f;
+      s.scale[row] = whole ? (l != 0.0f ? 1.0f / l : 0.0f) : 1.0f;
       if (row < n_rows) {
         const int rr = g0 + row;
         if (whole && p.lse != nullptr)
-          p.lse[static_cast<int64_t>(b) * rows + rr] = l > 0.0f ? (m + log2f(l)) * kLn2 : -INFINITY;
+          p.lse[static_cast<int64_t>(b) * rows + rr] = l != 0.0f ? (m + log2f(l)) * kLn2 : -INFINITY;
         if (!whole) {
           float* ml = slot + p.rows_per_group * p.dv + 2 * row;
           ml[0] = m;
@@ -117,9 +117,9 @@ __global__ void __launch_bounds__(kJoinThreads, kJoinCtasPerSm) decode_join_kern
       [&](const JoinNote&, int cta, int row) { return row_of(cta, row) < rows; },
       [&](const JoinNote& note, int cta, int row, int d, const float4& a, float top, float l) {
         const int rr = row_of(cta, row);
-        const float inv = l > 0.0f ? 1.0f / l : 0.0f;
+        const float inv = l != 0.0f ? 1.0f / l : 0.0f;
         if (d == 0 && p.lse != nullptr)
-          p.lse[static_cast<int64_t>(note.item) * rows + rr] = l > 0.0f ? (top + log2f(l)) * kLn2 : -INFINITY;
+          p.lse[static_cast<int64_t>(note.item) * rows + rr] = l != 0.0f ? (top + log2f(l)) * kLn2 : -INFINITY;
         TQ* out = static_cast<TQ*>(p.out) + note.item * p.or_stride + (rr / p.H) * p.ot_stride + (rr % p.H) * p.oh_stride + d;
         const float y[4] = {a.x * inv, a.y * inv, a.z * inv, a.w * inv};
 #pragma unroll

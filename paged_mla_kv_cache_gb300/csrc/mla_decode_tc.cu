@@ -210,7 +210,10 @@ __device__ __forceinline__ void load_queries(const DecodeParams& p, int b, int g
         int e = 135 - static_cast<int>(top >> 23) - ((top & 0x7fffff) >= 0x600000 ? 1 : 0);
         e = top == 0 ? 0 : max(-126, min(126, e));
         const float scale = __uint_as_float(static_cast<uint32_t>(127 + e) << 23);
-        if (lane == 0) mi.factor[r] = factor * __uint_as_float(static_cast<uint32_t>(127 - e) << 23);
+        // (an infinite or NaN query makes NaN of its row, which e4m3 values that saturate would not)
+        if (lane == 0)
+          mi.factor[r] = top < 0x7f800000u ? factor * __uint_as_float(static_cast<uint32_t>(127 - e) << 23)
+                                           : __uint_as_float(0x7fffffffu);
 #pragma unroll
         for (int k = 0; k < 3; ++k) {
           const int u = lane + 32 * k;  // 8 values: 8 bytes of each part
@@ -654,6 +657,26 @@ __global__ void __launch_bounds__(kThreads, 1)
         const bool all = __all_sync(0xffffffffu, in0 && in1);
         // some row does not see the whole tile for its place among the new tokens
         const bool edge = p.q_len > 1 && j0 + kDecodeTile > it.full_len - p.q_len + 1;
+        if (edge) {
+          // An entry that only later tokens see may hold infinities or NaN, and a weight of 0 would not keep them out of
+          // the product. Such an entry makes scores that are not finite; its values are then set to 0, and the rows that
+          // do see it have the NaN of their score.
+          bool odd = false;
+#pragma unroll
+          for (int k = 0; k < 4 * kG; ++k) odd |= (raw_s[k] & 0x7f800000u) == 0x7f800000u;
+          if (__any_sync(0xffffffffu, odd)) {
+            using TC = std::conditional_t<kFp8, e4m3, TQ>;
+            for (uint32_t m = 0; m < 4; ++m) {
+              const uint32_t sl = slot0 + m < L::kSlots ? slot0 + m : slot0 + m - L::kSlots;
+#pragma unroll
+              for (int q = 0; q < L::kPieces; ++q) {
+                // this warp's 16 entries
+                uint4* at = reinterpret_cast<uint4*>(smem + L::kSlotAt + sl * L::kSlot + q * L::kPiece + warp * 2048);
+                for (int y = lane; y < 128; y += 32) at[y] = only_finite<TC>(at[y]);
+              }
+            }
+          }
+        }
         if (!all || edge) {
           const int first = it.full_len - p.q_len + 1 + step0 - j0 - tok;  // of row 0's token: entries tok + k < first are seen
 #pragma unroll
@@ -793,11 +816,11 @@ __global__ void __launch_bounds__(kThreads, 1)
       if (tid < N) {
         const float sum = (mi.warp_sums[tid] + mi.warp_sums[N + tid]) + (mi.warp_sums[2 * N + tid] + mi.warp_sums[3 * N + tid]);
         const float r = mi.factor[tid];
-        mi.inv[tid] = sum > 0.0f ? kv_scale / sum : 0.0f;
+        mi.inv[tid] = sum != 0.0f ? kv_scale / sum : 0.0f;
         if (tid < n_rows) {
           if (!whole) *reinterpret_cast<float2*>(slot + p.rows_per_group * kLatent + 2 * tid) = make_float2(r, sum);
           else if (p.lse != nullptr)
-            p.lse[static_cast<int64_t>(it.b) * rows + g0 + tid] = sum > 0.0f ? (r + log2f(sum)) * kLn2 : -INFINITY;
+            p.lse[static_cast<int64_t>(it.b) * rows + g0 + tid] = sum != 0.0f ? (r + log2f(sum)) * kLn2 : -INFINITY;
         }
       }
       if (!whole && it.tile == 0 && tid == 0) {

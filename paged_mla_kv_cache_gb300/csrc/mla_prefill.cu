@@ -63,8 +63,8 @@ __global__ void __launch_bounds__(kGenThreads) prefill_general_kernel(const __gr
     general_rows(s, E, p.dv, 0, j1, p.sm_scale * kLog2e, load, seen, value, acc, m, l);
     __syncthreads();
     if (lane == 0) {
-      float lse = l > 0.0f ? (m + log2f(l)) * kLn2 : -INFINITY;
-      float now = l > 0.0f ? 1.0f / l : 0.0f, before = 0.0f;
+      float lse = l != 0.0f ? (m + log2f(l)) * kLn2 : -INFINITY;
+      float now = l != 0.0f ? 1.0f / l : 0.0f, before = 0.0f;
       if (row < rows) {
         const int64_t at_lse = static_cast<int64_t>(x.q0 + i0 + row) * p.H + h;
         if (p.prev_lse != nullptr) {

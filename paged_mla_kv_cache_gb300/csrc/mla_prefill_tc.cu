@@ -55,6 +55,7 @@ struct Misc {
   int64_t scratch[33], found[2];
   uint32_t tmem;
   int32_t stop, never;
+  int32_t spoiled;  // values were set to 0 that rows see: the epilogue adds them
 };
 static_assert(sizeof(Misc) <= kMisc, "Misc fits");
 
@@ -87,13 +88,14 @@ struct Items {
   int nb, b0, n;
   int act[2];   // blocks that each half takes part in (of the item's nb)
   int keys;     // keys of the item
+  int common;   // keys that all its rows see
   int skip;     // pieces of the item before this share
   int64_t first;  // its first piece
   bool begun;
 
   __device__ Items(const PrefillParams& p_, const Share& s) : p(&p_), at(s.begin), end(s.end) {
     r = s.item;
-    head = tile = nb = b0 = n = keys = 0;
+    head = tile = nb = b0 = n = keys = common = 0;
     skip = 0;
     begun = false;
     if (at < end) {
@@ -133,6 +135,7 @@ struct Items {
     } while (n == 0);
     // the first half's last row may see fewer keys; the second half may not exist
     const int rows = x.lq - tile * kRows;
+    common = p->causal ? max(0, min(x.lk, x.lk - x.lq + 1 + tile * kRows)) : x.lk;
     int k0 = keys;
     if (p->causal && rows > kHalf)
       k0 = max(0, min(x.lk, x.lk - x.lq + tile * kRows + kHalf));
@@ -142,6 +145,9 @@ struct Items {
   }
   // the piece of the item's last block
   __device__ int64_t last_piece() const { return first + kItemCost + nb - 1; }
+  // A block that reaches past the keys that every row sees: some row has weights of 0 there, which do not keep
+  // infinities and NaN out of a product. Its values are made finite first.
+  __device__ bool mixed(int b) const { return (b + 1) * kBlock > common; }
   // blocks of this share that half h takes part in: [b0, last(h))
   __device__ int last(int h) const { return min(b0 + n, act[h]); }
 };
@@ -167,7 +173,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     mbar_init(smem_u32(&mi.q_full), 1);
     mbar_init(smem_u32(&mi.q_empty), 1);
     mbar_init(smem_u32(&mi.dirty), 1);
-    mbar_init(smem_u32(&mi.clean), 1);
+    mbar_init(smem_u32(&mi.clean), 2);
     mbar_init(smem_u32(&mi.end), 1);
     for (int h = 0; h < 2; ++h) {
       mbar_init(smem_u32(&mi.s_full[h]), 1);
@@ -175,7 +181,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       mbar_init(smem_u32(&mi.p_full[2 * h + 1]), 4);
       mbar_init(smem_u32(&mi.o_done[h]), 1);
     }
-    mi.stop = mi.never = 0;
+    mi.stop = mi.never = mi.spoiled = 0;
     mbar_fence_init();
     tma_prefetch(&map_q);
     tma_prefetch(&map_k);
@@ -338,7 +344,6 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (uniform(it.keys) == 0) continue;
         mbar_wait(smem_u32(&mi.q_full), items++ & 1, stop);
         const int end = uniform(it.b0 + it.n), begin = uniform(it.b0);
-        const bool partial_end = uniform(end == it.nb && it.x.lk - (end - 1) * kBlock < kBlock);  // warp 10's rule
         const int last0 = uniform(it.last(0)), last1 = uniform(it.last(1));
         wait_block(k_full, step);
         tmem_fence_after();
@@ -352,7 +357,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         for (int b = begin; b < end; ++b, ++step) {
           const bool more = b + 1 < end;
           wait_block(v_full, step);
-          if (!more && partial_end) {
+          if (uniform(it.mixed(b))) {  // (the rule of warps 10 and 11)
             if (elect_one()) mbar_arrive(smem_u32(&mi.dirty));
             __syncwarp();
             mbar_wait(smem_u32(&mi.clean), cleans++ & 1, stop);
@@ -387,26 +392,35 @@ __global__ void __launch_bounds__(kThreads, 1)
       if (elect_one()) umma_commit(smem_u32(&mi.end));
       __syncwarp();
       mbar_wait(smem_u32(&mi.end), 0, smem_u32(&mi.never));
-    } else if (warp == 10) {
-      // ---- value rows past a request's end ----
+    } else {
+      // ---- values that must not meet a weight of 0: warp 10 takes the first piece of a block, warp 11 the second ----
       Items it(p, share);
-      int64_t step = 0;
-      uint32_t cleans = 0;
+      uint32_t step = 0, cleans = 0;
       while (it.next()) {
         if (it.keys == 0) continue;
-        step += it.n;
-        const int end = it.b0 + it.n;
-        const int first = it.x.lk - (end - 1) * kBlock;  // rows of the last block that belong to the request
-        if (end != it.nb || first >= kBlock) continue;
-        mbar_wait(smem_u32(&mi.dirty), cleans++ & 1, stop);  // the block is there
-        for (int c = 3; c < 5; ++c) {
-          const int slot = static_cast<int>((5 * (step - 1) + c) % kSlots);
-          uint4* at = reinterpret_cast<uint4*>(smem + kSlotAt + slot * kPiece + first * 128);
-          for (int i = lane; i < (kBlock - first) * 8; i += 32) at[i] = make_uint4(0, 0, 0, 0);
+        for (int b = it.b0; b < it.b0 + it.n; ++b, ++step) {
+          if (!it.mixed(b)) continue;
+          mbar_wait(smem_u32(&mi.dirty), cleans++ & 1, stop);  // the block is there
+          const int slot = static_cast<int>((5 * step + warp - 7) & (kSlots - 1));
+          uint4* at = reinterpret_cast<uint4*>(smem + kSlotAt + slot * kPiece);
+          const int first = min(kBlock, it.x.lk - b * kBlock);  // rows that belong to the request: the others are 0
+          for (int i = first * 8 + lane; i < kBlock * 8; i += 32) at[i] = make_uint4(0, 0, 0, 0);
+          if (p.causal) {
+            uint32_t odd = 0;
+#pragma unroll 8
+            for (int i = lane; i < first * 8; i += 32) {
+              const uint4 v = at[i];
+              odd |= nonfinite<T>(v.x) | nonfinite<T>(v.y) | nonfinite<T>(v.z) | nonfinite<T>(v.w);
+            }
+            if (__any_sync(0xffffffffu, odd != 0)) {
+              for (int i = lane; i < first * 8; i += 32) at[i] = only_finite<T>(at[i]);
+              if (lane == 0) *reinterpret_cast<volatile int32_t*>(&mi.spoiled) = 1;
+            }
+          }
+          fence_async_smem();
+          __syncwarp();
+          if (lane == 0) mbar_arrive(smem_u32(&mi.clean));
         }
-        fence_async_smem();
-        __syncwarp();
-        if (lane == 0) mbar_arrive(smem_u32(&mi.clean));
       }
     }
   } else {
@@ -509,6 +523,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         tmem_fence_after();
       }
       const bool mine = i < it.x.lq;
+      const bool spoiled = some && *reinterpret_cast<volatile int32_t*>(&mi.spoiled) != 0;
       if (!whole && it.b0 == 0 && tid == 0) {
         note.item = it.r;
         note.head = it.head;
@@ -517,9 +532,9 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
       float* slot = p.ws.slots + (static_cast<int64_t>(unit) * 2 + (it.b0 == 0 ? 1 : 0)) * kSlotFloats;
       const int64_t t = it.x.q0 + i;
-      float now = l > 0.0f ? 1.0f / l : 0.0f, before = 0.0f;
+      float now = l != 0.0f ? 1.0f / l : 0.0f, before = 0.0f;
       if (whole && mine) {
-        float lse = l > 0.0f ? (ref + log2f(l)) * kLn2 : -INFINITY;
+        float lse = l != 0.0f ? (ref + log2f(l)) * kLn2 : -INFINITY;
         if (p.prev_lse != nullptr) {
           const Joined g = join_state(lse, p.prev_lse[t * p.H + it.head]);
           now *= g.now;
@@ -546,6 +561,26 @@ __global__ void __launch_bounds__(kThreads, 1)
           for (int k = 0; k < 16; ++k) o[k] = 0;
         }
         if (!mine) continue;
+        if (spoiled) {
+          // infinities and NaN that were kept out of the products, for the rows that see them
+          const int hi = min(limit, last * kBlock);
+#pragma unroll 1
+          for (int j = max(it.b0, it.common / kBlock) * kBlock; j < hi; ++j) {
+            const uint4* v = reinterpret_cast<const uint4*>(static_cast<const T*>(p.v) + static_cast<int64_t>(it.x.k0 + j) * p.vt_stride +
+                                                            it.head * p.vh_stride + c);
+#pragma unroll
+            for (int q = 0; q < 2; ++q) {
+              const uint32_t w[4] = {v[q].x, v[q].y, v[q].z, v[q].w};
+#pragma unroll
+              for (int k = 0; k < 4; ++k) {
+                const uint32_t odd = nonfinite<T>(w[k]);
+                const float2 two = unpack2<T>(w[k]);
+                if (odd & 0xffff) o[8 * q + 2 * k] = __float_as_uint(__uint_as_float(o[8 * q + 2 * k]) + two.x);
+                if (odd >> 16) o[8 * q + 2 * k + 1] = __float_as_uint(__uint_as_float(o[8 * q + 2 * k + 1]) + two.y);
+              }
+            }
+          }
+        }
         if (whole) {
           float y[16];
 #pragma unroll
@@ -596,8 +631,8 @@ __global__ void __launch_bounds__(kJoinThreads, kJoinCtasPerSm) prefill_join_ker
       [&](const JoinNote& note, int, int row) { return note.tile * kRows + row < prefill_req(p, note.item).lq; },
       [&](const JoinNote& note, int, int row, int d, const float4& a, float top, float l) {
         const int64_t t = static_cast<int64_t>(prefill_req(p, note.item).q0) + note.tile * kRows + row;
-        float lse = l > 0.0f ? (top + log2f(l)) * kLn2 : -INFINITY;
-        float now = l > 0.0f ? 1.0f / l : 0.0f, before = 0.0f;
+        float lse = l != 0.0f ? (top + log2f(l)) * kLn2 : -INFINITY;
+        float now = l != 0.0f ? 1.0f / l : 0.0f, before = 0.0f;
         if (p.prev_lse != nullptr) {
           const Joined g = join_state(lse, p.prev_lse[t * p.H + note.head]);
           now *= g.now;

@@ -5,6 +5,8 @@
 
 #include <cuda.h>
 
+#include <type_traits>
+
 #include "mla_common.cuh"
 
 namespace pmg_mla {
@@ -384,6 +386,24 @@ __device__ __forceinline__ uint32_t e4m3_part(uint32_t& x) {
   asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(back) : "h"(two));
   asm("sub.rn.f16x2 %0, %0, %1;" : "+r"(x) : "r"(back));
   return two;
+}
+
+template <class T>
+__device__ __forceinline__ float2 unpack2(uint32_t x) {
+  if constexpr (std::is_same<T, bf16>::value) return make_float2(__uint_as_float(x << 16), __uint_as_float(x & 0xffff0000u));
+  else return make_float2(__half2float(__ushort_as_half(static_cast<unsigned short>(x))),
+                          __half2float(__ushort_as_half(static_cast<unsigned short>(x >> 16))));
+}
+
+// Which of two 16-bit or four e4m3 values are infinite or NaN (all bits of those), and the values with 0 in their place.
+template <class T>
+__device__ __forceinline__ uint32_t nonfinite(uint32_t x) {
+  if constexpr (sizeof(T) == 1) return __vcmpeq4(x & 0x7f7f7f7fu, 0x7f7f7f7fu);
+  else return __vcmpgeu2(x & 0x7fff7fffu, std::is_same<T, bf16>::value ? 0x7f807f80u : 0x7c007c00u);
+}
+template <class T>
+__device__ __forceinline__ uint4 only_finite(uint4 x) {
+  return make_uint4(x.x & ~nonfinite<T>(x.x), x.y & ~nonfinite<T>(x.y), x.z & ~nonfinite<T>(x.z), x.w & ~nonfinite<T>(x.w));
 }
 
 // ---- host: tensor maps ------------------------------------------------------------

@@ -8,7 +8,7 @@ import torch
 from paged_mla_kv_cache_gb300 import binding
 
 import mla_reference as ref
-from test_mla_ops_gpu import BF16, DEV, FP8, GENERAL, decode_case, gen, i32, normal, prefill_case, run_decode, run_prefill
+from test_mla_ops_gpu import BF16, DEV, FP8, GENERAL, check_decode, decode_case, gen, i32, normal, prefill_case, run_decode, run_prefill
 
 pytestmark = pytest.mark.gpu
 
@@ -164,3 +164,73 @@ def test_prefill_on_another_stream_and_in_a_graph(ws):
         graph.replay()
         torch.cuda.synchronize()
         assert torch.equal(out, want)
+
+
+@pytest.mark.parametrize("options", [0, GENERAL])
+@pytest.mark.parametrize("cdt", [BF16, FP8])
+@pytest.mark.parametrize("n,block", [(300, 64), (300, 16), (20000, 64)])
+def test_decode_odd_values_in_unseen_entries(ws, options, cdt, n, block):
+    """A row of an earlier token does not meet the infinities and NaN of a later token's entry; a row that sees them has NaN."""
+    q, cache, table, lens, sc = decode_case([n, 90], 16, 4, BF16, cdt, block)
+    clean, lse0 = run_decode((q, cache, table, lens, sc), ws, options=options)
+    places = [(n - 1, 5), (n - 2, 570), (n - 1, 400)]
+    odd = cache.clone()
+    for i, (j, d) in enumerate(places):
+        odd[int(table[0, j // block]), j % block, d] = math.nan if cdt is FP8 or i < 2 else math.inf
+    out, lse = torch.empty_like(clean), torch.empty(2, 4, 16, device=DEV)
+    binding.latent_decode(q, odd, table, lens, out, lse, sm_scale=1 / math.sqrt(192), scale=sc, workspace=ws, options=options)
+    assert out[0, 2:].isnan().all() and lse[0, 2:].isnan().all() and lse[0, :2].isfinite().all()
+    out[0, 2:], lse[0, 2:] = clean[0, 2:], lse0[0, 2:]
+    check_decode((q, cache, table, lens, sc), out, lse, options=options)
+
+
+@pytest.mark.parametrize("options", [0, GENERAL])
+@pytest.mark.parametrize("dtype", [BF16, torch.float16])
+@pytest.mark.parametrize("q_len,k_len", [(300, 300), (300, 700), (130, 9000), (40, 20)])
+def test_prefill_odd_values_in_unseen_keys(ws, options, dtype, q_len, k_len):
+    """Only rows that see a key have its infinities and NaN, and those only in their columns."""
+    c = prefill_case([q_len, 50], [k_len, 50], 3, dtype)
+    clean, lse0 = run_prefill(c, ws, True, options)
+    v = c["v"].clone()
+    places = [(k_len - 1, 0, 5, math.nan), (k_len - 17, 1, 127, math.inf), (k_len - 18, 1, 64, -math.inf),
+              (max(k_len - 130, 0), 2, 0, math.nan)]
+    want = clean.clone()
+    rows = torch.arange(q_len, device=DEV)
+    for j, h, d, x in places:
+        v[j, h, d] = x
+        sees = rows + k_len - q_len >= j
+        want[:q_len, h, d] = torch.where(sees, torch.tensor(x, dtype=dtype, device=DEV), want[:q_len, h, d])
+    out, lse = torch.empty_like(clean), torch.empty_like(lse0)
+    binding.latent_prefill(c["q"], c["k"], c["pe"], v, c["cu_q"], c["cu_k"], out, lse, sm_scale=1 / math.sqrt(192),
+                           causal=True, workspace=ws, options=options)
+    assert torch.equal(lse, lse0)
+    assert torch.equal(out.isnan(), want.isnan()) and torch.equal(out.nan_to_num(7.0), want.nan_to_num(7.0))
+
+
+@pytest.mark.parametrize("options", [0, GENERAL])
+@pytest.mark.parametrize("x", [math.nan, math.inf])
+@pytest.mark.parametrize("n", [100, 20000])
+def test_odd_queries_make_their_row_nan(ws, options, x, n):
+    """Result and log sum, whether one share holds the row or several; other rows do not change."""
+    for src, cdt in ((BF16, BF16), (BF16, FP8), (torch.float16, FP8)):
+        q, cache, table, lens, sc = decode_case([n], 16, 1, src, cdt, 64)
+        clean, lse0 = run_decode((q, cache, table, lens, sc), ws, options=options)
+        out, lse = torch.empty_like(clean), torch.empty_like(lse0)
+        odd = q.clone()
+        odd[0, 0, 3, 7] = x
+        binding.latent_decode(odd, cache, table, lens, out, lse, sm_scale=1 / math.sqrt(192), scale=sc, workspace=ws,
+                              options=options)
+        assert out[0, 0, 3].isnan().all() and lse[0, 0, 3].isnan()
+        out[0, 0, 3], lse[0, 0, 3] = clean[0, 0, 3], lse0[0, 0, 3]
+        check_decode((q, cache, table, lens, sc), out, lse, options=options)
+    c = prefill_case([130], [n + 130], 2, BF16)
+    clean, lse0 = run_prefill(c, ws, True, options)
+    want, wl, pv, worst = ref.prefill(c["q"], c["k"], c["pe"], c["v"], c["cu_q"], c["cu_k"], 1 / math.sqrt(192), True)
+    odd = c["q"].clone()
+    odd[77, 1, 7] = x
+    out, lse = torch.empty_like(clean), torch.empty_like(lse0)
+    binding.latent_prefill(odd, c["k"], c["pe"], c["v"], c["cu_q"], c["cu_k"], out, lse, sm_scale=1 / math.sqrt(192),
+                           causal=True, workspace=ws, options=options)
+    assert out[77, 1].isnan().all() and lse[77, 1].isnan()
+    out[77, 1], lse[77, 1] = clean[77, 1], lse0[77, 1]
+    ref.check_attention(out, lse, want, wl, pv, worst, 192, ref.U[BF16])

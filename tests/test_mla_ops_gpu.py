@@ -222,6 +222,12 @@ def run_decode(case, ws, dv=512, options=0, sm=None, weights_u=None, flag=0):
                           options=options)
     torch.cuda.synchronize()
     assert int(err) == flag
+    check_decode(case, out, lse, dv, options, sm, weights_u)
+    return out, lse
+
+
+def check_decode(case, out, lse, dv=512, options=0, sm=1.0 / math.sqrt(192), weights_u=None):
+    q, cache, table, lens, sc = case
     f = 1.0 if sc is None else float(sc)
     want, wl, pv, worst, flat = ref.decode(q, cache, table, lens, dv, sm, f)
     u, extra, below = ref.U[q.dtype] if weights_u is None else weights_u, 0.0, 0.0
@@ -232,7 +238,6 @@ def run_decode(case, ws, dv=512, options=0, sm=None, weights_u=None, flag=0):
         size = cache.double().nan_to_num(0).abs().sum(2).max() * f
         extra = sm * 2.0 ** -16.8 * q.double().abs().amax(3) * size
     ref.check_attention(out, lse, want, wl, pv, worst, q.shape[3], u, extra, below)
-    return out, lse
 
 
 GENERAL = binding.OPT_FORCE_GENERAL
