@@ -8,7 +8,11 @@
 // saturating).
 //
 // Bound by memory: an entry in and out, 2 * rope_dim elements a head, one row
-// of cosines and sines a token. One warp takes either a token's entry (the
+// of cosines and sines a token. Measured: 8192 tokens of 128 heads into an e4m3
+// cache 70 us (285 MB, 61% of copy bandwidth; a plain copy of the same strided
+// 128-byte rows takes 46 us: the rest is the chain of slot, position, angles
+// and values that each short warp goes through); 64 tokens 7.4 us, the host's
+// call and one launch. One warp takes either a token's entry (the
 // latent row stays in registers between the sum and the store, so it is read
 // once) or a few heads of a token's queries, for which a lane keeps one set of
 // four cosines and sines in registers and issues all its loads before the
@@ -412,7 +416,8 @@ extern "C" int pmg_append(const void* c_kv, int64_t c_kv_stride, const void* k_p
   const int64_t tasks = p.tasks_per_token;
   if (num_tokens * tasks > INT32_MAX) return PMG_ERR_UNSUPPORTED;
   auto grid = [&](int64_t per_token) { return dim3(static_cast<unsigned>((num_tokens * per_token + kWarps - 1) / kWarps)); };
-  // a second launch costs about 2 us: more than it gives below some 16 MB of queries
+  // Two launches let entries and queries have the registers that each needs: 8192 tokens of 128 heads (134 MB of queries)
+  // 70 us instead of 78. The second launch costs about 2 us, more than it gives below some 16 MB of queries.
   if (tasks == 1 || num_tokens * heads * rope_dim * es < (int64_t{16} << 20))
     return launch(kernel(tasks == 1 ? kEntries : kBoth), grid(tasks), kWarps * 32, 0, stream, p);
   const int st = launch(kernel(kEntries), grid(1), kWarps * 32, 0, stream, p);
