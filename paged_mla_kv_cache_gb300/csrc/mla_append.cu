@@ -19,6 +19,8 @@
 // first store. Units are four pairs: 16 bytes of 16-bit values where pairs are
 // neighbours, two times 8 bytes where halves are rotated. Rows that are not
 // 16-byte aligned or not whole units take the same warps element by element.
+#include <algorithm>
+
 #include "mla_common.cuh"
 
 namespace pmg_mla {
@@ -143,15 +145,19 @@ __device__ __forceinline__ float warp_sum(float x) {
   return x;
 }
 
-// What a launch does: entries and queries, or one of them. The queries' warps
-// need a third of the entries' registers, and their speed is the number of warps
-// that fit: large calls launch them by themselves.
+// What a launch does: entries and queries, or one of them. Large calls launch
+// the queries by themselves (below, or here where rows are not whole units).
 enum Work : int { kBoth = 0, kEntries = 1, kQueries = 2 };
 
 template <class TS, class TC, bool kVec, int kWork>
-__global__ void __launch_bounds__(kWarps * 32, kWork == kQueries ? 12 : 8)
-    append_kernel(const __grid_constant__ AppendParams p) {
-  pdl_entry();
+__global__ void __launch_bounds__(kWarps * 32, 8) append_kernel(const __grid_constant__ AppendParams p) {
+  if constexpr (kWork == kEntries) {
+    // the queries' launch that may follow reads what earlier kernels wrote without a wait of its own
+    pdl_wait();
+    pdl_launch();
+  } else {
+    pdl_entry();
+  }
   const int lane = threadIdx.x & 31;
   // tasks token by token: warps that run together read and write neighbouring rows
   const uint32_t task = blockIdx.x * kWarps + (threadIdx.x >> 5);
@@ -303,6 +309,119 @@ __global__ void __launch_bounds__(kWarps * 32, kWork == kQueries ? 12 : 8)
   }
 }
 
+// The queries of a large call. A warp's rows pass through shared memory with
+// asynchronous copies, kStages tasks of kIters row groups in flight: a lane
+// waits for its own copies only, and what is in flight costs no registers. (As
+// one task a warp, twelve CTAs an SM, the chain of position, angles and values
+// left 52% of the memory's rate.) Positions are looked up 32 tasks ahead.
+constexpr int kStages = 3;
+constexpr int kQueryCtas = 6;  // an SM
+
+template <int kBytes>
+__device__ __forceinline__ void copy_async(void* dst, const void* src) {
+  const uint32_t at = static_cast<uint32_t>(__cvta_generic_to_shared(dst));
+  if constexpr (kBytes == 16) asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(at), "l"(src) : "memory");
+  else asm volatile("cp.async.ca.shared.global [%0], [%1], 8;" ::"r"(at), "l"(src) : "memory");
+}
+
+template <class TS>
+struct QueryStage {
+  RawPairs<TS> raw[kIters][32];
+  float4 co[32], si[32];
+};
+template <class TS>
+constexpr int query_smem() { return kWarps * kStages * static_cast<int>(sizeof(QueryStage<TS>)); }
+
+template <class TS>
+__global__ void __launch_bounds__(kWarps * 32, sizeof(TS) == 2 ? kQueryCtas : kQueryCtas / 2)
+    append_queries_kernel(const __grid_constant__ AppendParams p) {
+  pdl_launch();
+  extern __shared__ __align__(16) uint8_t smem[];
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  QueryStage<TS>* stages = reinterpret_cast<QueryStage<TS>*>(smem) + warp * kStages;
+  const uint32_t per_token = p.tasks_per_token - 1, tasks = static_cast<uint32_t>(p.T) * per_token;
+  const uint32_t warps = gridDim.x * kWarps, first = blockIdx.x * kWarps + warp;
+  const uint32_t n = first < tasks ? (tasks - first + warps - 1) / warps : 0;  // this warp's: first + i * warps
+  const int half = p.dr >> 1, lanes = p.dr >> 3;
+  const bool pairs = p.pairs != 0;
+  const int u = lane & (lanes - 1), step = 32 / lanes;
+  auto positions = [&](uint32_t i) {  // of tasks i + lane
+    return i + lane < n ? p.positions[(first + (i + lane) * warps) / per_token] : -1;
+  };
+  int32_t now = positions(0), then = positions(32);
+  uint32_t seen = 0;  // bit: the tasks in flight, newest first, whose queries are turned
+  auto begin = [&](uint32_t i, QueryStage<TS>& s) {
+    if (i > 0 && i % 32 == 0) {
+      now = then;
+      then = positions(i + 32);
+    }
+    const int32_t pos = __shfl_sync(0xffffffffu, now, i % 32);
+    const bool turned = i < n && pos >= 0 && pos < p.num_positions;
+    seen = seen << 1 | turned;
+    if (turned) {
+      const uint32_t task = first + i * warps, t = task / per_token;
+      const int h0 = static_cast<int>(task - t * per_token) * p.heads_per_task + lane / lanes;
+      const int h1 = min(h0 - lane / lanes + p.heads_per_task, p.H);
+      const float* cs = p.cos_sin + static_cast<int64_t>(pos) * p.dr + 4 * u;
+      copy_async<16>(&s.co[lane], cs);
+      copy_async<16>(&s.si[lane], cs + half);
+      const TS* q = reinterpret_cast<const TS*>(p.q) + t * p.qt_stride;
+#pragma unroll
+      for (int k = 0; k < kIters; ++k)
+        if (h0 + k * step < h1) {
+          const TS* row = q + (h0 + k * step) * p.qh_stride;
+          RawPairs<TS>* dst = &s.raw[k][lane];
+          if (pairs && sizeof(TS) == 2) {
+            copy_async<16>(dst, row + 8 * u);
+          } else {
+            copy_async<4 * sizeof(TS)>(&dst->lo, pairs ? row + 8 * u : row + 4 * u);
+            copy_async<4 * sizeof(TS)>(&dst->hi, pairs ? row + 8 * u + 4 : row + half + 4 * u);
+          }
+        }
+    }
+    asm volatile("cp.async.commit_group;" ::: "memory");
+  };
+  uint32_t ahead = 0, at = 0;
+  for (; ahead < kStages - 1; ++ahead) begin(ahead, stages[ahead]);
+  for (uint32_t i = 0; i < n; ++i) {
+    // the stage of the task before is free: its lanes have their values in registers
+    begin(i + kStages - 1, stages[at == 0 ? kStages - 1 : at - 1]);
+    asm volatile("cp.async.wait_group %0;" ::"n"(kStages - 1) : "memory");
+    if (seen >> (kStages - 1) & 1) {
+      const QueryStage<TS>& s = stages[at];
+      const uint32_t task = first + i * warps, t = task / per_token;
+      const int h0 = static_cast<int>(task - t * per_token) * p.heads_per_task + lane / lanes;
+      const int h1 = min(h0 - lane / lanes + p.heads_per_task, p.H);
+      TS* o = reinterpret_cast<TS*>(p.qo) + t * p.ot_stride;
+      const float4 c4 = s.co[lane], s4 = s.si[lane];
+      const float co[4] = {c4.x, c4.y, c4.z, c4.w}, si[4] = {s4.x, s4.y, s4.z, s4.w};
+#pragma unroll
+      for (int k = 0; k < kIters; ++k)
+        if (h0 + k * step < h1) {
+          float a[4], b[4];
+          split_pairs(s.raw[k][lane], pairs, a, b);
+#pragma unroll
+          for (int j = 0; j < 4; ++j) rotate(a[j], b[j], co[j], si[j]);
+          store_pairs(o + (h0 + k * step) * p.oh_stride, u, half, pairs, a, b);
+        }
+    }
+    at = at + 1 == kStages ? 0 : at + 1;
+  }
+  asm volatile("cp.async.wait_all;" ::: "memory");
+  pdl_wait();  // this kernel ends after the one before it
+}
+
+template <class TS>
+int launch_queries(const AppendParams& p, int sms, void* stream) {
+  auto k = append_queries_kernel<TS>;
+  const int st = allow_smem(reinterpret_cast<const void*>(k), query_smem<TS>());
+  if (st != PMG_OK) return st;
+  const int64_t tasks = p.T * (p.tasks_per_token - 1);
+  const int64_t ctas = std::min<int64_t>(static_cast<int64_t>(sms) * (sizeof(TS) == 2 ? kQueryCtas : kQueryCtas / 2),
+                                         (tasks + kWarps - 1) / kWarps);
+  return launch(k, dim3(static_cast<unsigned>(ctas)), kWarps * 32, query_smem<TS>(), stream, p);
+}
+
 using Kernel = void (*)(const AppendParams);
 
 template <class TS, class TC, int kWork>
@@ -324,7 +443,7 @@ template <class TS>
 Kernel pick(int cache_dtype, bool vec, Work work) {
   // the queries do not depend on the cache's type
   return work == kBoth ? pick<TS, kBoth>(cache_dtype, vec)
-                       : work == kEntries ? pick<TS, kEntries>(cache_dtype, vec) : pick<TS, bf16, kQueries>(vec);
+                       : work == kEntries ? pick<TS, kEntries>(cache_dtype, vec) : append_kernel<TS, bf16, false, kQueries>;
 }
 
 }  // namespace
@@ -422,5 +541,11 @@ extern "C" int pmg_append(const void* c_kv, int64_t c_kv_stride, const void* k_p
     return launch(kernel(tasks == 1 ? kEntries : kBoth), grid(tasks), kWarps * 32, 0, stream, p);
   const int st = launch(kernel(kEntries), grid(1), kWarps * 32, 0, stream, p);
   if (st != PMG_OK) return st;
-  return launch(kernel(kQueries), grid(tasks - 1), kWarps * 32, 0, stream, p);
+  if (!vec) return launch(kernel(kQueries), grid(tasks - 1), kWarps * 32, 0, stream, p);
+  int sms = 0;
+  const int found = sm_count(&sms);
+  if (found != PMG_OK) return found;
+  return src_dtype == PMG_BF16   ? launch_queries<bf16>(p, sms, stream)
+         : src_dtype == PMG_FP16 ? launch_queries<f16>(p, sms, stream)
+                                 : launch_queries<float>(p, sms, stream);
 }

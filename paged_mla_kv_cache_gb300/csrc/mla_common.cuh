@@ -51,9 +51,11 @@ __device__ __forceinline__ void set_flag(int32_t* err, int bits) {
 // Every kernel here is launched with programmatic dependent launch: the next
 // kernel may begin its launch now, and nothing is read or written before the
 // previous one has finished.
+__device__ __forceinline__ void pdl_launch() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
+__device__ __forceinline__ void pdl_wait() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
 __device__ __forceinline__ void pdl_entry() {
-  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
-  asm volatile("griddepcontrol.wait;" ::: "memory");
+  pdl_launch();
+  pdl_wait();
 }
 
 // ---- block-wide sums ------------------------------------------------------

@@ -8,7 +8,7 @@ import torch
 from paged_mla_kv_cache_gb300 import binding
 
 import mla_reference as ref
-from test_mla_ops_gpu import BF16, DEV, FP8, GENERAL, check_decode, decode_case, gen, i32, normal, prefill_case, run_decode, run_prefill
+from test_mla_ops_gpu import BF16, DEV, FP8, GENERAL, check_decode, decode_case, gen, i32, normal, prefill_case, run_append, run_decode, run_prefill
 
 pytestmark = pytest.mark.gpu
 
@@ -234,3 +234,37 @@ def test_odd_queries_make_their_row_nan(ws, options, x, n):
     assert out[77, 1].isnan().all() and lse[77, 1].isnan()
     out[77, 1], lse[77, 1] = clean[77, 1], lse0[77, 1]
     ref.check_attention(out, lse, want, wl, pv, worst, 192, ref.U[BF16])
+
+
+@pytest.mark.parametrize("t,dr,heads,src,unaligned,inplace", [
+    (2100, 64, 65, BF16, 0, False), (8192, 64, 16, BF16, 0, True), (2100, 64, 33, torch.float32, 0, False),
+    (700, 256, 49, torch.float16, 0, False), (9001, 8, 130, torch.float16, 0, True), (66000, 128, 1, BF16, 0, False),
+    (2100, 64, 65, BF16, 3, False)])
+@pytest.mark.parametrize("pairs", [True, False])
+def test_append_large(t, dr, heads, src, unaligned, inplace, pairs):
+    """Calls whose queries are launched by themselves."""
+    assert t * heads * dr * (4 if src is torch.float32 else 2) >= 2 ** 24
+    run_append(t, 64, dr, heads, src, FP8 if heads % 2 else src, 64, 64 + dr, pairs, unaligned=unaligned, inplace=inplace)
+
+
+def test_append_large_skips_tokens_and_repeats():
+    t, heads, dr = 9000, 16, 64
+    g = gen(4)
+    c, kp, q = normal(g, t, 64, dtype=BF16), normal(g, t, dr, dtype=BF16), normal(g, t, heads, dr, dtype=BF16)
+    cs = torch.rand(500, dr, generator=g, device=DEV)
+    positions = torch.as_tensor(np.random.default_rng(1).integers(0, 500, t).astype(np.int32), device=DEV)
+    positions[::7], positions[5], positions[8990:] = -1, 500, -1
+    slots = torch.where((positions >= 0) & (positions < 500), torch.arange(t, device=DEV), -1)
+    cache = torch.zeros(150, 64, 128, dtype=BF16, device=DEV)
+    want = None
+    for _ in range(3):
+        out, err = torch.full_like(q, 7.0), i32([0])
+        binding.append(c, kp, cache, slots, positions, cs, q_pe=q, q_out=out, error_flag=err)
+        got = out.clone()  # follows in the stream
+        assert int(err) == binding.FLAG_POSITION
+        skipped = slots < 0
+        assert (got[skipped] == 7).all()
+        turned, mag = ref.rotate(q[~skipped].double(), cs.double()[positions[~skipped].long()], False)
+        assert ((got[~skipped].double() - turned).abs() <= ref.U[BF16] * turned.abs() + mag * 2.0 ** -21).all()
+        want = got if want is None else want
+        assert torch.equal(got, want) and torch.equal(cache.view(-1, 128)[slots[~skipped], :64], c[~skipped])
