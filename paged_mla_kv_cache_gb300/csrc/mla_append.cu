@@ -9,10 +9,10 @@
 //
 // Bound by memory: an entry in and out, 2 * rope_dim elements a head, one row
 // of cosines and sines a token. Measured: 8192 tokens of 128 heads into an e4m3
-// cache 70 us (285 MB, 61% of copy bandwidth; a plain copy of the same strided
-// 128-byte rows takes 46 us: the rest is the chain of slot, position, angles
-// and values that each short warp goes through); 64 tokens 7.4 us, the host's
-// call and one launch. One warp takes either a token's entry (the
+// cache 60 us (285 MB, 71% of copy bandwidth; a plain copy of the same strided
+// 128-byte rows takes 46 us: the rest is mostly the entries, whose warps go
+// through a chain of slot, values, sum and store, beside the queries); 64 tokens
+// 7.4 us, the host's call and one launch. One warp takes either a token's entry (the
 // latent row stays in registers between the sum and the store, so it is read
 // once) or a few heads of a token's queries, for which a lane keeps one set of
 // four cosines and sines in registers and issues all its loads before the
@@ -313,7 +313,9 @@ __global__ void __launch_bounds__(kWarps * 32, 8) append_kernel(const __grid_con
 // asynchronous copies, kStages tasks of kIters row groups in flight: a lane
 // waits for its own copies only, and what is in flight costs no registers. (As
 // one task a warp, twelve CTAs an SM, the chain of position, angles and values
-// left 52% of the memory's rate.) Positions are looked up 32 tasks ahead.
+// left 52% of the memory's rate: 70 us instead of 60 for 8192 tokens of 128
+// heads.) Positions are looked up 32 tasks ahead. Two stages in seven or eight CTAs
+// an SM measured 63 us, three in five 65, four in four 60.
 constexpr int kStages = 3;
 constexpr int kQueryCtas = 6;  // an SM
 
@@ -535,8 +537,8 @@ extern "C" int pmg_append(const void* c_kv, int64_t c_kv_stride, const void* k_p
   const int64_t tasks = p.tasks_per_token;
   if (num_tokens * tasks > INT32_MAX) return PMG_ERR_UNSUPPORTED;
   auto grid = [&](int64_t per_token) { return dim3(static_cast<unsigned>((num_tokens * per_token + kWarps - 1) / kWarps)); };
-  // Two launches let entries and queries have the registers that each needs: 8192 tokens of 128 heads (134 MB of queries)
-  // 70 us instead of 78. The second launch costs about 2 us, more than it gives below some 16 MB of queries.
+  // Queries by themselves: 128 heads, back to back on the device, 34 us instead of 40 at 64 MB of queries, 10.3 instead of
+  // 10.9 at 16 MB, 6.7 instead of 6.3 at 8 MB; and a second launch takes the host about 2 us.
   if (tasks == 1 || num_tokens * heads * rope_dim * es < (int64_t{16} << 20))
     return launch(kernel(tasks == 1 ? kEntries : kBoth), grid(tasks), kWarps * 32, 0, stream, p);
   const int st = launch(kernel(kEntries), grid(1), kWarps * 32, 0, stream, p);
