@@ -184,6 +184,19 @@ __device__ __forceinline__ void join_rows(const Workspace& ws, int notes, int st
   auto slot_of = [&](int cta, int i) {  // part 0 is the noting share's own end, the others begin their shares
     return ws.slots + ((cta + static_cast<int64_t>(i) * stride) * 2 + (i == 0 ? 1 : 0)) * slot_floats;
   };
+  auto values = [&](int cta, int row, int d, int i) {
+    const float* o = slot_of(cta, i) + static_cast<int64_t>(row) * dv + d;
+    float4 x = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+    if (vec) {
+      if (d < dv) x = *reinterpret_cast<const float4*>(o);
+    } else {
+      if (d < dv) x.x = o[0];
+      if (d + 1 < dv) x.y = o[1];
+      if (d + 2 < dv) x.z = o[2];
+      if (d + 3 < dv) x.w = o[3];
+    }
+    return x;
+  };
   // adds parts i0, i0 + step, ... of a row's columns d to d + 3 under the reference `top`
   auto add = [&](int cta, int row, int d, int i0, int parts, int step, float top, float4& a, float& l) {
     const int64_t ml = static_cast<int64_t>(rows) * dv + 2 * row;
@@ -191,16 +204,7 @@ __device__ __forceinline__ void join_rows(const Workspace& ws, int notes, int st
     for (int i = i0; i < parts; i += step) {
       const float* slot = slot_of(cta, i);
       const float m = slot[ml], part_l = slot[ml + 1];
-      const float* o = slot + static_cast<int64_t>(row) * dv + d;
-      float4 x = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-      if (vec) {
-        if (d < dv) x = *reinterpret_cast<const float4*>(o);
-      } else {
-        if (d < dv) x.x = o[0];
-        if (d + 1 < dv) x.y = o[1];
-        if (d + 2 < dv) x.z = o[2];
-        if (d + 3 < dv) x.w = o[3];
-      }
+      const float4 x = values(cta, row, d, i);
       if (part_l == 0.0f) continue;  // the row saw nothing there (a NaN among its scores makes a sum of NaN, which counts)
       const float w = exp2f(m - top);
       l += w * part_l;
@@ -222,10 +226,41 @@ __device__ __forceinline__ void join_rows(const Workspace& ws, int notes, int st
     const int cta = few[x / (rows * quarters)], row = x / quarters % rows, d = x % quarters * 128 + lane * 4;
     const JoinNote note = ws.notes[cta];
     if (!valid(note, cta, row)) continue;
-    const float top = top_of(cta, row, note.parts);
+    // four parts at a time, all of their loads before any is used; every lane has the references and sums
     float4 a = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-    float l = 0.0f;
-    add(cta, row, d, 0, note.parts, 1, top, a, l);
+    float l = 0.0f, top = -INFINITY;
+    for (int i0 = 0; i0 < note.parts; i0 += 4) {
+      float4 o[4];
+      float m[4], part_l[4];
+#pragma unroll
+      for (int k = 0; k < 4; ++k) {
+        const bool in = i0 + k < note.parts;
+        const float* ml = slot_of(cta, in ? i0 + k : 0) + static_cast<int64_t>(rows) * dv + 2 * row;
+        m[k] = in ? ml[0] : -INFINITY;
+        part_l[k] = in ? ml[1] : 0.0f;
+        o[k] = in ? values(cta, row, d, i0 + k) : make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+      }
+      const float next = fmaxf(fmaxf(fmaxf(m[0], m[1]), fmaxf(m[2], m[3])), top);
+      if (i0 > 0 && l != 0.0f) {
+        const float keep = exp2f(top - next);
+        l *= keep;
+        a.x *= keep;
+        a.y *= keep;
+        a.z *= keep;
+        a.w *= keep;
+      }
+      top = next;
+#pragma unroll
+      for (int k = 0; k < 4; ++k) {
+        if (part_l[k] == 0.0f) continue;
+        const float w = exp2f(m[k] - top);
+        l += w * part_l[k];
+        a.x += w * o[k].x;
+        a.y += w * o[k].y;
+        a.z += w * o[k].z;
+        a.w += w * o[k].w;
+      }
+    }
     __syncwarp();
     if (d < dv) emit(note, cta, row, d, a, top, l);
   }
