@@ -137,9 +137,10 @@ __device__ __forceinline__ int unit_of(int64_t x, int64_t total, int units) {
 // Sums of the rows that shares cut. Work is one warp for each row and 128
 // columns where a request lies in a few shares, and a whole CTA (its warps take
 // the shares in turn) where it lies in many: a request cut into a hundred
-// parts and a hundred requests cut in two both fill the SMs in one wave. 5 to 8
-// us a call, launch and read-back of the parts; CTAs of 512 threads, or six or
-// eight an SM, measured no faster.
+// parts and a hundred requests cut in two both fill the SMs in one wave. 5 to 12
+// us a call: launch, read-back of the parts (up to 40 MB, mostly from L2), and
+// the arithmetic of addresses. CTAs of 512 threads, or six or eight an SM, a
+// whole row a warp, or references reduced over the lanes, measured slower.
 //   part i of a note by CTA c is in the slots of CTA c + i * stride;
 //   valid(note, c, row): whether the row exists;
 //   emit(note, c, row, d, sums, top, l): columns d to d + 3 of the unnormalised
