@@ -35,16 +35,19 @@
 // the lanes at all.
 //
 // An e4m3 cache is not widened. The 8-bit tensor core multiplies it as it is
-// with queries and weights split in e4m3 parts of 4 significant bits each
-// (x = x0 + x1 + ...): two parts hold a bf16 query's 8 bits, three an fp16
-// query's 11, and two a weight to 2^-8 of its value, as bf16 would. With two
-// parts that is as many instructions as the 16-bit products at half the bytes.
-// Queries are first scaled by a power of two for each row that puts its
-// largest value in [224, 448); what is lost is below a step of 2^-9, 2^-16.8 of
-// the largest. Weights are kept below 2^8.5: a request's first tile sets its
-// largest weights to 2^4, which leaves room for the maximum to grow as more
-// entries come, later corrections to 2^6; the step is 2^-13 to 2^-17 of the
-// largest weight.
+// with queries and weights split in parts (x = x0 + x1 + ...).
+// Queries: e4m3 parts of 4 significant bits, two for a bf16 query's 8 bits,
+// three for an fp16 query's 11, after a scaling by a power of two for each row
+// that puts its largest value in [224, 448); what is lost is below a step of
+// 2^-9, 2^-16.8 of the largest.
+// Weights: rounded to fp16, then three e5m2 parts of 3 significant bits, which
+// holds them to 2^-9 of their value, as bf16 would, down to half a step of
+// 2^-17. They are kept below 2^15.5 (fp16 ends at 2^16): a request's first
+// tile sets its largest weights to 2^11, which leaves room for the maximum to
+// grow as more entries come, later corrections to 2^13. So one strong key
+// among n weak ones costs them at most n 2^-28 of its weight. (Two e4m3 parts,
+// one product less, end at 2^-10 with the largest at 2^4: of a tail of 16384
+// keys that together weigh as much as a strong first one a quarter was lost.)
 #include <algorithm>
 #include <type_traits>
 
@@ -69,7 +72,8 @@ struct Lay {
   static constexpr int kSlot = kPiece * kPieces;
   static constexpr int kQPieces = kFp8 ? 5 : 9;
   static constexpr int kQ = kQPieces * N * 128 * kParts;
-  static constexpr int kP = kPiece * (kFp8 ? 2 : 1);
+  static constexpr int kWeights = kFp8 ? 3 : 1;          // parts of a weight
+  static constexpr int kP = kPiece * kWeights;
   static constexpr int kMisc = 2048;
   static constexpr int kRoom = kSmemMax - 1024 - kMisc - kQ - kP;
   // a rope slot for each tile in flight
@@ -295,8 +299,8 @@ __global__ void __launch_bounds__(kThreads, 1)
   const uint32_t tmem = mi.tmem;
   const uint32_t stop = smem_u32(&mi.stop);
   constexpr int kFmt = kFp8 ? 0 : (sizeof(TQ) == 2 && std::is_same<TQ, bf16>::value ? 1 : 0);
-  constexpr uint32_t kIdescS = umma_idesc(kFmt, 0, 0, 64, N);
-  constexpr uint32_t kIdescO = umma_idesc(kFmt, 1, 1, 128, N);
+  constexpr uint32_t kIdescS = umma_idesc(kFmt, kFmt, 0, 0, 64, N);
+  constexpr uint32_t kIdescO = umma_idesc(kFmt, kFp8 ? 1 : kFmt, 1, 1, 128, N);  // e5m2 weights of e4m3 values
 
   if (warp == 4) {
     // ---- loads ----
@@ -450,8 +454,9 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
           for (int k = 0; k < (kFp8 ? 2 : 4); ++k) {
             const uint32_t step = k * (kFp8 ? 32 : 16) * 8;  // rows of 128 bytes, in units of 16
-            umma_ss<kFp8>(d, va + step, pa + step, kIdescO, !first || k > 0);
-            if constexpr (kFp8) umma_ss<kFp8>(d, va + step, pa + step + L::kPiece / 16, kIdescO, true);
+#pragma unroll
+            for (int x = 0; x < L::kWeights; ++x)
+              umma_ss<kFp8>(d, va + step, pa + step + x * (L::kPiece / 16), kIdescO, !first || k > 0 || x > 0);
           }
           umma_commit(empty + 8 * at);
           if (++at == L::kSlots) at = 0;
@@ -538,8 +543,8 @@ __global__ void __launch_bounds__(kThreads, 1)
     const int n_rows = min(p.rows_per_group, rows - g0);
     const float kv_scale = kFp8 && p.scale != nullptr ? *p.scale : 1.0f;
     const float factor = p.sm_scale * kLog2e * kv_scale;
-    constexpr float kCap = kFp8 ? 8.5f : 8.0f;       // weights stay below 2^kCap
-    constexpr float kFirst = kFp8 ? 4.0f : 0.0f, kLater = kFp8 ? 6.0f : 0.0f;  // where a new reference puts the largest
+    constexpr float kCap = kFp8 ? 15.5f : 8.0f;      // weights stay below 2^kCap
+    constexpr float kFirst = kFp8 ? 11.0f : 0.0f, kLater = kFp8 ? 13.0f : 0.0f;  // where a new reference puts the largest
     const uint32_t lanes = static_cast<uint32_t>(warp * 32) << 16;
     // Scores (M = 64: 16 rows in each quarter of the lanes) are read so that this thread has entries tok and tok + 8
     // of the tile, and of every 8 columns 2 c and 2 c + 1.
@@ -787,8 +792,10 @@ __global__ void __launch_bounds__(kThreads, 1)
             } else {
               uint8_t* at = row + (((g >> 1) ^ (tok & 7)) << 4) + (g & 1) * 8 + 2 * c;
               uint32_t two = pack2<f16>(a, b);
-#pragma unroll
-              for (int q = 0; q < 2; ++q) *reinterpret_cast<uint16_t*>(at + q * L::kPiece) = static_cast<uint16_t>(e4m3_part(two));
+              const uint32_t part0 = e5m2_cut(two), part1 = e5m2_cut(two);
+              reinterpret_cast<uint16_t*>(at)[0] = static_cast<uint16_t>(part0);
+              reinterpret_cast<uint16_t*>(at + L::kPiece)[0] = static_cast<uint16_t>(part1);
+              reinterpret_cast<uint16_t*>(at + 2 * L::kPiece)[0] = static_cast<uint16_t>(e5m2_last(two));
             }
           }
         }

@@ -210,8 +210,8 @@ __global__ void __launch_bounds__(kThreads, 1)
   const uint32_t tmem = static_cast<uint32_t>(uniform(static_cast<int>(mi.tmem)));  // S of the halves at columns 0 and 128, O at 256 and 384
   const uint32_t stop = smem_u32(&mi.stop);
   constexpr int kFmt = std::is_same<T, bf16>::value ? 1 : 0;
-  constexpr uint32_t kIdescS = umma_idesc(kFmt, 0, 0, 128, kBlock);
-  constexpr uint32_t kIdescO = umma_idesc(kFmt, 0, 1, 128, kVal);
+  constexpr uint32_t kIdescS = umma_idesc(kFmt, kFmt, 0, 0, 128, kBlock);
+  constexpr uint32_t kIdescO = umma_idesc(kFmt, kFmt, 0, 1, 128, kVal);
 
   if (warp >= 8) {
     regs_down<kRegsDown>();
@@ -332,7 +332,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           }
         } else {
           const uint64_t v1 = umma_desc(base + kSlotAt + w * 8192, kPiece, 1024);
-          constexpr uint32_t kIdescHalf = umma_idesc(kFmt, 0, 1, 128, 64);
+          constexpr uint32_t kIdescHalf = umma_idesc(kFmt, kFmt, 0, 1, 128, 64);
           if (elect_one()) {
 #pragma unroll
             for (int k = 0; k < 4; ++k) {

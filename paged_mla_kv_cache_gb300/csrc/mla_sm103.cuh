@@ -204,9 +204,9 @@ __device__ __forceinline__ uint64_t umma_desc(uint32_t addr, uint32_t lbo, uint3
 }
 
 // Instruction descriptor: fp32 accumulation, operand formats (16-bit: 0 fp16,
-// 1 bf16; 8-bit: 0 e4m3), majors (0 K, 1 MN), N and M.
-__host__ __device__ constexpr uint32_t umma_idesc(int fmt, int a_mn, int b_mn, int m, int n) {
-  return (1u << 4) | (static_cast<uint32_t>(fmt) << 7) | (static_cast<uint32_t>(fmt) << 10) |
+// 1 bf16, the same for both; 8-bit: 0 e4m3, 1 e5m2), majors (0 K, 1 MN), N and M.
+__host__ __device__ constexpr uint32_t umma_idesc(int fmt_a, int fmt_b, int a_mn, int b_mn, int m, int n) {
+  return (1u << 4) | (static_cast<uint32_t>(fmt_a) << 7) | (static_cast<uint32_t>(fmt_b) << 10) |
          (static_cast<uint32_t>(a_mn) << 15) | (static_cast<uint32_t>(b_mn) << 16) |
          (static_cast<uint32_t>(n >> 3) << 17) | (static_cast<uint32_t>(m >> 4) << 24);
 }
@@ -385,6 +385,20 @@ __device__ __forceinline__ uint32_t e4m3_part(uint32_t& x) {
   asm("cvt.rn.satfinite.e4m3x2.f16x2 %0, %1;" : "=h"(two) : "r"(x));
   asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(back) : "h"(two));
   asm("sub.rn.f16x2 %0, %0, %1;" : "+r"(x) : "r"(back));
+  return two;
+}
+
+// Parts of two values held as f16x2, packed low first, in e5m2: the upper byte
+// of an fp16 value is an e5m2 value, cut. What is left, exactly, stays in x;
+// the last part is rounded.
+__device__ __forceinline__ uint32_t e5m2_cut(uint32_t& x) {
+  const uint32_t top = x & 0xff00ff00u;
+  asm("sub.rn.f16x2 %0, %0, %1;" : "+r"(x) : "r"(top));
+  return __byte_perm(top, 0, 0x4431);
+}
+__device__ __forceinline__ uint32_t e5m2_last(uint32_t x) {
+  uint16_t two;
+  asm("cvt.rn.satfinite.e5m2x2.f16x2 %0, %1;" : "=h"(two) : "r"(x));
   return two;
 }
 
