@@ -28,8 +28,9 @@
 // when its product is done, so loads run up to two tiles ahead of the softmax.
 //
 // The reference of a row follows its maximum only when a score passes it by
-// 2^kCap: weights then stay far inside the range of their type, sums are
-// 32-bit, and the accumulators are rescaled (read, multiplied, written back)
+// 2^kCap: weights then stay inside the range of their type (fp16 ones are kept
+// from 2^8 to 2^15 where the largest are, so that those beside a strong key do
+// not fall below 2^-24), sums are 32-bit, and the accumulators are rescaled (read, multiplied, written back)
 // only in the first tiles of a request. All threads learn whether a tile needs
 // that from one barrier with a vote, so the usual tile has no maximum over
 // the lanes at all.
@@ -543,8 +544,10 @@ __global__ void __launch_bounds__(kThreads, 1)
     const int n_rows = min(p.rows_per_group, rows - g0);
     const float kv_scale = kFp8 && p.scale != nullptr ? *p.scale : 1.0f;
     const float factor = p.sm_scale * kLog2e * kv_scale;
-    constexpr float kCap = kFp8 ? 15.5f : 8.0f;      // weights stay below 2^kCap
-    constexpr float kFirst = kFp8 ? 11.0f : 0.0f, kLater = kFp8 ? 13.0f : 0.0f;  // where a new reference puts the largest
+    constexpr bool kF16 = std::is_same<TQ, f16>::value;
+    constexpr float kCap = kFp8 ? 15.5f : kF16 ? 15.0f : 8.0f;       // weights stay below 2^kCap
+    constexpr float kFirst = kFp8 ? 11.0f : kF16 ? 8.0f : 0.0f;      // where a first reference puts the largest
+    constexpr float kLater = kFp8 ? 13.0f : kF16 ? 8.0f : 0.0f;      // where a later one does
     const uint32_t lanes = static_cast<uint32_t>(warp * 32) << 16;
     // Scores (M = 64: 16 rows in each quarter of the lanes) are read so that this thread has entries tok and tok + 8
     // of the tile, and of every 8 columns 2 c and 2 c + 1.

@@ -24,7 +24,12 @@
 // anything, and infinities and NaN of keys that some row does not see.
 //
 // A row's reference follows its maximum only when a score passes it by 2^8, so
-// the accumulator is rescaled in the first blocks at most. Work is cut into
+// the accumulator is rescaled in the first blocks at most. Weights are rounded
+// to the type of the values for the second product (2^-8 or 2^-11 of each; the
+// sum of weights is of the unrounded ones): wider ones would need the values
+// widened too, for products of half the rate. fp16 weights are kept from 2^8 to 2^15
+// where the largest ones are, so that one strong key does not push the weights
+// of the others below fp16's smallest, 2^-24. Work is cut into
 // equal shares of blocks over the whole call (see mla_attn.cuh): causal
 // triangles, short and long requests cost every SM the same, and a chunk of
 // few rows over a long context uses them all.
@@ -445,7 +450,8 @@ __global__ void __launch_bounds__(kThreads, 1)
     const uint32_t lanes = static_cast<uint32_t>((warp & 3) * 32) << 16;
     const uint32_t s_at = tmem + h * kBlock + lanes, o_at = tmem + 256 + h * kVal + lanes;
     const float sc = p.sm_scale * kLog2e;
-    constexpr float kSlack = 8.0f;
+    constexpr float kFirst = std::is_same<T, f16>::value ? 8.0f : 0.0f;  // where a new reference puts the largest weight
+    constexpr float kCap = std::is_same<T, f16>::value ? 15.0f : 8.0f;   // weights stay below 2^kCap
     JoinNote note{-1, 0, 0, 0};
     Items it(p, share);
     uint32_t count = 0;  // blocks taken part in
@@ -480,11 +486,12 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
         for (int k = 12; k < 128; k += 2) m4[(k >> 1) & 3] = max3(m4[(k >> 1) & 3], s[k], s[k + 1]);
         const float top = fmaxf(max3(m4[0], m4[1], m4[2]), m4[3]) * sc;
-        if (__any_sync(0xffffffffu, top > ref + kSlack)) {
+        if (__any_sync(0xffffffffu, top > ref + kCap)) {
           float a = 1.0f;
-          if (top > ref) {
-            a = ref == -INFINITY ? 0.0f : ex2(ref - top);
-            ref = top;
+          const float next = top - kFirst;
+          if (next > ref) {
+            a = ref == -INFINITY ? 0.0f : ex2(ref - next);
+            ref = next;
           }
           l *= a;
           if (b > it.b0) {

@@ -5,7 +5,8 @@ their parts hold them, the strong key is the request's first entry and its value
 mean. So the result is the tail's share alone, and a bound that is relative to it has no room for weights that vanish.
 
 Weights of an e4m3 cache are held as fp16 in three e5m2 parts: to 2^-11 and 2^-9 of their value, or, where that is more, to
-half a step of 2^-28 of the largest weight, which is at most 2^-8.7 of a tail's usual weight here: together below 2^-8."""
+half a step of 2^-28 of the largest weight, which is at most 2^-8.7 of a tail's usual weight here: together below 2^-8.
+Weights of 16-bit products have their type's rounding: 2^-8, or 2^-11 with the subnormal ones' half step far below it."""
 import math
 
 import pytest
@@ -14,7 +15,7 @@ import torch
 from paged_mla_kv_cache_gb300 import binding
 
 import mla_reference as ref
-from test_mla_ops_gpu import BF16, DEV, F16, FP8, gen, i32, normal
+from test_mla_ops_gpu import BF16, DEV, F16, FP8, GENERAL, gen, i32, normal
 
 pytestmark = pytest.mark.gpu
 SM = 1 / math.sqrt(192)
@@ -98,3 +99,34 @@ def test_decode_fp8_even_tail(ws, src, octaves):
     """Every key of the tail has the same weight, so its rounding does not average out."""
     run_tail(ws, tail_case([8000, 64, 65], 32, 1, src, FP8, octaves, 0.0), 2.0 ** -8)
     run_tail(ws, tail_case([3000] * 100, 128, 1, src, FP8, octaves, 0.0), 2.0 ** -8)
+
+
+@pytest.mark.parametrize("options", [0, GENERAL])
+@pytest.mark.parametrize("src", [BF16, F16])
+def test_decode_tail(ws, src, options):
+    """16-bit caches; for fp16, weights that are subnormal where the largest is 1."""
+    for octaves in (6.3, 14.6, 20.5):
+        u = ref.U[src] if options == 0 else 0.0
+        run_tail(ws, tail_case([8000, 64, 65], 32, 1, src, src, octaves, 0.0), u, options)
+        run_tail(ws, tail_case([1000] * 100, 128, 1, src, src, octaves, 0.0), u, options)
+
+
+@pytest.mark.parametrize("dtype", [BF16, F16])
+@pytest.mark.parametrize("causal", [False, True])
+@pytest.mark.parametrize("octaves", [6.3, 14.6, 20.5])
+def test_prefill_tail(ws, dtype, causal, octaves):
+    g = gen(7)
+    heads, lq, lk = 128, 300, 2000  # more row tiles than SMs: most shares hold whole ones
+    kv = torch.cat([torch.zeros(lk, heads, 128, device=DEV), 1.0 + 0.5 * normal(g, lk, heads, 128)], 2)
+    kv[0] = 0.0
+    pe = torch.zeros(lk, 64, device=DEV)
+    pe[0, 0] = 16.0
+    q = torch.zeros(lq, heads, 192, device=DEV)
+    q[:, :, 128] = octaves * math.log(2) / SM / 16.0
+    kv, pe, q = kv.to(dtype), pe.to(dtype), q.to(dtype)
+    cu_q, cu_k = i32([0, lq]), i32([0, lk])
+    out, lse = torch.empty(lq, heads, 128, dtype=dtype, device=DEV), torch.empty(lq, heads, device=DEV)
+    binding.latent_prefill(q, kv[:, :, :128], pe, kv[:, :, 128:], cu_q, cu_k, out, lse, sm_scale=SM, causal=causal,
+                           workspace=ws)
+    want, wl, pv, worst = ref.prefill(q, kv[:, :, :128], pe, kv[:, :, 128:], [0, lq], [0, lk], SM, causal)
+    ref.check_attention(out, lse, want, wl, pv, worst, 192, ref.U[dtype])
