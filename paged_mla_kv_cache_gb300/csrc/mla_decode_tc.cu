@@ -337,14 +337,12 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
         const uint32_t boxes = __ballot_sync(0xffffffffu, in), goods = __ballot_sync(0xffffffffu, in && good);
         const int n_boxes = __popc(boxes);
-        if (lane == 0) {
-          uint64_t m = 0;
-          for (int s = 0; s < segs; ++s)
-            if (goods >> s & 1) m |= (box_rows == 64 ? ~0ull : ((1ull << box_rows) - 1) << (s * box_rows));
-          const int left = it.len - j0;
-          if (left < 64) m &= (1ull << left) - 1;
-          mi.mask[t & 7] = m;
-        }
+        // which entries of the tile exist
+        uint64_t mask = 0;
+        for (int s = 0; s < segs; ++s)
+          if (goods >> s & 1) mask |= (box_rows == 64 ? ~0ull : ((1ull << box_rows) - 1) << (s * box_rows));
+        const int left = it.len - j0;
+        if (left < 64) mask &= (1ull << left) - 1;
         const uint32_t bytes = static_cast<uint32_t>(n_boxes * box_rows * 128);
         const int id0 = __shfl_sync(0xffffffffu, id, 0), row0 = __shfl_sync(0xffffffffu, row, 0);
         if (box_rows == kDecodeTile && group == 0 && i + 1 < it.n) {
@@ -365,7 +363,10 @@ __global__ void __launch_bounds__(kThreads, 1)
         // the rotated part's slot, free since the tile's scores two tiles ago, brings the tile's barrier
         const uint32_t bar = full + 8 * rslot;
         mbar_wait(rope_empty + 8 * rslot, rphase ^ 1, stop);
-        if (elect_one()) mbar_expect(bar, bytes * (4 * L::kPieces + 1));
+        if (elect_one()) {
+          mi.mask[t & 7] = mask;  // by the lane that arrives: the barrier orders it for its readers
+          mbar_expect(bar, bytes * (4 * L::kPieces + 1));
+        }
         __syncwarp();
         const bool one_box = n_boxes == 1 && box_rows == kDecodeTile;
         if (one_box) {
