@@ -289,6 +289,15 @@ __global__ void __launch_bounds__(kThreads, 1)
     if (p.q_tma) tma_prefetch(&q_map);
   }
   if (warp == 5) tmem_alloc(smem_u32(&mi.tmem), kColumns);
+  if (p.q_tma) {
+    // rows of queries that no copy fills: 0, before the CTA's barrier below, after which they are multiplied
+    const int fill = N - p.rows_per_group;
+    for (int i = tid; i < 9 * fill * 8; i += kThreads) {
+      const int c = i / (fill * 8), y = i % (fill * 8);
+      *reinterpret_cast<uint4*>(smem + L::kQAt + c * (N * 128) + p.rows_per_group * 128 + y * 16) = make_uint4(0, 0, 0, 0);
+    }
+    fence_async_smem();
+  }
   pdl_entry();
 
   const int unit = blockIdx.x / p.groups, group = blockIdx.x % p.groups;
@@ -567,15 +576,6 @@ __global__ void __launch_bounds__(kThreads, 1)
     };
     // For each request: its queries, then the epilogue of the request before (whose last product runs meanwhile), then
     // its tiles.
-    if (p.q_tma) {
-      // rows that no copy fills: 0
-      for (int i = tid; i < 9 * (N - p.rows_per_group) * 8; i += kSoft) {
-        const int c = i / ((N - p.rows_per_group) * 8), y = i % ((N - p.rows_per_group) * 8);
-        *reinterpret_cast<uint4*>(smem + L::kQAt + c * (N * 128) + p.rows_per_group * 128 + y * 16) = make_uint4(0, 0, 0, 0);
-      }
-      fence_async_smem();
-      named_sync<kSoft>(1);
-    }
     bool more = it.next();
     int prev_b = -1, prev_n = 0;
     bool prev_whole = false;
