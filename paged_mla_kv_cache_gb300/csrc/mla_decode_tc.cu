@@ -117,7 +117,10 @@ struct MiscOf {
 // one, which writes its rows. (Four: without them the CTAs that got many short
 // requests ended last.)
 constexpr int kItemCost = 4;
-__device__ __forceinline__ int tiles_of(int len) { return (len + kDecodeTile - 1) / kDecodeTile; }
+// (lengths go up to INT32_MAX: no sum passes it before it is divided)
+__device__ __forceinline__ int tiles_of(int len) {
+  return static_cast<int>((static_cast<uint32_t>(len) + kDecodeTile - 1) / kDecodeTile);
+}
 __device__ __forceinline__ int pieces_of(int len) { return len > 0 ? kItemCost + tiles_of(len) : 1; }
 
 // Walks the requests of a share. The next request's length is loaded one step
@@ -326,18 +329,18 @@ __global__ void __launch_bounds__(kThreads, 1)
       if (lane == 0) bad |= decode_len(p, it.b).bad;
       if (it.len == 0) continue;
       const int32_t* table = p.bt + static_cast<int64_t>(it.b) * p.bt_stride;
-      // lane s < segs looks up the page of box s, one tile ahead of its use
-      auto page_of = [&](int j) {
-        return lane < segs && j < it.len ? table[static_cast<uint32_t>(j) / static_cast<uint32_t>(p.B)] : -1;
-      };
-      int j = it.tile * kDecodeTile + lane * box_rows;
+      // lane s < segs looks up the page of box s, one tile ahead of its use (places have no sign: boxes past the end of a
+      // request may lie past INT32_MAX)
+      const uint32_t len = static_cast<uint32_t>(it.len);
+      auto page_of = [&](uint32_t j) { return lane < segs && j < len ? table[j / static_cast<uint32_t>(p.B)] : -1; };
+      uint32_t j = static_cast<uint32_t>(it.tile * kDecodeTile) + lane * box_rows;
       int next_id = page_of(j);
 #pragma unroll 1
       for (int i = 0; i < it.n; ++i, ++t, j += kDecodeTile) {
         const int j0 = (it.tile + i) * kDecodeTile;
-        const bool in = lane < segs && j < it.len;
+        const bool in = lane < segs && j < len;
         int id = next_id;
-        const int row = static_cast<int>(static_cast<uint32_t>(j) % static_cast<uint32_t>(p.B));
+        const int row = static_cast<int>(j % static_cast<uint32_t>(p.B));
         next_id = i + 1 < it.n ? page_of(j + kDecodeTile) : -1;
         const bool good = id >= 0 && id < p.num_blocks;
         if (in && !good) {
@@ -673,9 +676,10 @@ __global__ void __launch_bounds__(kThreads, 1)
         float* s = reinterpret_cast<float*>(raw_s);
         const bool all = __all_sync(0xffffffffu, in0 && in1);
         // some row does not see the whole tile for its place among the new tokens
-        const bool edge = p.q_len > 1 && j0 + kDecodeTile > it.full_len - p.q_len + 1;
+        const int common = it.full_len - j0 - p.q_len + 1;  // entries from the tile's first on that all rows see
+        const bool edge = p.q_len > 1 && common < kDecodeTile;
         if (!all || edge) {
-          const int first = it.full_len - p.q_len + 1 + step0 - j0 - tok;  // of row 0's token: entries tok + k < first are seen
+          const int first = common + step0 - tok;  // of row 0's token: entries tok + k < first are seen
 #pragma unroll
           for (int g = 0; g < kG; ++g)
 #pragma unroll

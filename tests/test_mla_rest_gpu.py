@@ -7,7 +7,7 @@ import torch
 
 from paged_mla_kv_cache_gb300 import binding
 
-from test_mla_ops_gpu import BF16, DEV, F16, decode_case, gen, i32, normal, run_decode
+from test_mla_ops_gpu import BF16, DEV, F16, FP8, check_decode, decode_case, gen, i32, normal, run_decode
 
 pytestmark = pytest.mark.gpu
 SM = 1 / math.sqrt(192)
@@ -39,3 +39,21 @@ def test_decode_bits_do_not_depend_on_the_call_before(ws, src, heads, q_len):
         binding.latent_decode(other, cache, pages, n, left, sm_scale=SM, workspace=ws)
         binding.latent_decode(q, cache, table, lens, out, got, sm_scale=SM, workspace=ws)
         assert torch.equal(out, want) and torch.equal(got, lse)
+
+
+@pytest.mark.parametrize("cdt", [BF16, FP8])
+@pytest.mark.parametrize("q_len,short", [(1, 0), (3, 1), (2, 63), (2, 64)])
+def test_decode_of_the_longest_request(ws, cdt, q_len, short):
+    """INT32_MAX entries and a few fewer, of which the table holds the last page: the others' are left out."""
+    block, heads = 4096, 16
+    longest = 2 ** 31 - 1 - short
+    q, cache, _, _, sc = decode_case([block, 70], heads, q_len, BF16, cdt, block, nan_tail=False)
+    table = torch.full((2, 2 ** 31 // block), -1, dtype=torch.int32, device=DEV)
+    table[0, -1], table[1, 0] = 1, 0
+    out, lse = torch.empty(2, q_len, heads, 512, dtype=BF16, device=DEV), torch.empty(2, q_len, heads, device=DEV)
+    err = i32([0])
+    binding.latent_decode(q, cache, table, i32([longest, 70]), out, lse, sm_scale=SM, scale=sc, workspace=ws, error_flag=err)
+    torch.cuda.synchronize()
+    assert int(err) == binding.FLAG_PHYS_BLOCK
+    few = i32([[1], [0]])
+    check_decode((q, cache, few, i32([longest % block, 70]), sc), out, lse)
