@@ -23,7 +23,7 @@ __global__ void __launch_bounds__(kGenThreads) prefill_general_kernel(const __gr
   const int E = p.dn + p.dr;
   const GenSmem s = general_smem_at(smem, E);
   auto pieces = [&](int r) -> int64_t {
-    return static_cast<int64_t>((prefill_req(p, r).lq + kGenRows - 1) / kGenRows) * p.H;
+    return (static_cast<int64_t>(prefill_req(p, r).lq) + kGenRows - 1) / kGenRows * p.H;
   };
   const Share share = find_share(pieces, p.R, blockIdx.x, p.units, scratch, found);
   const int tid = threadIdx.x, lane = tid & 31, row = tid >> 5;

@@ -77,8 +77,12 @@ __device__ __forceinline__ int keys_of(const PrefillReq& x, int t, int causal) {
   return static_cast<int>(max(static_cast<int64_t>(0), min(static_cast<int64_t>(x.lk), x.lk - x.lq + end)));
 }
 constexpr int kItemCost = 1;  // what an item's beginning and end cost, in blocks
-__device__ __forceinline__ int blocks_of(int keys) { return keys > 0 ? (keys + kBlock - 1) / kBlock : 1; }
-__device__ __forceinline__ int tiles_of(const PrefillReq& x) { return (x.lq + kRows - 1) / kRows; }
+// (rows and keys go up to INT32_MAX: no sum passes it before it is divided)
+__device__ __forceinline__ int parts_of(int n, uint32_t size) {
+  return static_cast<int>((static_cast<uint32_t>(n) + size - 1) / size);
+}
+__device__ __forceinline__ int blocks_of(int keys) { return keys > 0 ? parts_of(keys, kBlock) : 1; }
+__device__ __forceinline__ int tiles_of(const PrefillReq& x) { return parts_of(x.lq, kRows); }
 
 // pieces of one head of a request
 __device__ __forceinline__ int64_t head_pieces(const PrefillReq& x, int causal) {
@@ -148,7 +152,7 @@ struct Items {
     int k0 = keys;
     if (p->causal && rows > kHalf)
       k0 = max(0, min(x.lk, x.lk - x.lq + tile * kRows + kHalf));
-    act[0] = k0 > 0 ? (k0 + kBlock - 1) / kBlock : 0;
+    act[0] = k0 > 0 ? parts_of(k0, kBlock) : 0;
     act[1] = rows > kHalf && keys > 0 ? nb : 0;
     return true;
   }
@@ -475,7 +479,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         tmem_pin<128>(raw_s);
         float* s = reinterpret_cast<float*>(raw_s);
         const int j0 = b * kBlock;
-        if (j0 + kBlock > low) {
+        if (low - j0 < kBlock) {
 #pragma unroll
           for (int k = 0; k < 128; ++k)
             if (j0 + k >= limit) s[k] = -INFINITY;
@@ -545,7 +549,8 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
       if (some && *reinterpret_cast<volatile int32_t*>(&mi.spoiled) != 0) {
         // infinities and NaN that were kept out of the products, for the rows that see them
-        const int lo = max(it.b0, it.clean_from()) * kBlock, hi = min(limit, last * kBlock);
+        const int lo = max(it.b0, it.clean_from()) * kBlock;
+        const int hi = static_cast<int>(min(static_cast<int64_t>(limit), static_cast<int64_t>(last) * kBlock));
         const T* v0 = static_cast<const T*>(p.v) + static_cast<int64_t>(it.x.k0) * p.vt_stride + it.head * p.vh_stride;
 #pragma unroll 1
         for (int c = 0; c < kVal; c += 16) {

@@ -57,3 +57,30 @@ def test_decode_of_the_longest_request(ws, cdt, q_len, short):
     assert int(err) == binding.FLAG_PHYS_BLOCK
     few = i32([[1], [0]])
     check_decode((q, cache, few, i32([longest % block, 70]), sc), out, lse)
+
+
+@pytest.mark.parametrize("causal", [False, True])
+@pytest.mark.parametrize("few", [0, 127, 128])
+def test_prefill_over_the_most_keys(ws, causal, few):
+    """INT32_MAX keys and a few fewer: rows that overlap, all 0 but the end of the last one, which weighs as much as all
+    others together."""
+    tk, tq = 2 ** 31 - 1 - few, 3
+    flat = torch.zeros(8 * (tk - 1) + 128, dtype=BF16, device=DEV)
+    flat[-8] = 1.0
+    rows = flat.as_strided((tk, 1, 128), (8, 128, 1))
+    q = torch.zeros(tq, 1, 192, dtype=BF16, device=DEV)
+    q[:, :, 120] = math.log(tk) / SM
+    out, lse = torch.empty(tq, 1, 128, dtype=BF16, device=DEV), torch.empty(tq, 1, device=DEV)
+    binding.latent_prefill(q, rows, flat.as_strided((tk, 64), (8, 1)), rows, i32([0, tq]), i32([0, tk]), out, lse,
+                           sm_scale=SM, causal=causal, workspace=ws)
+    # the last key's weight in 64 bits; other rows of keys and values meet that element nowhere
+    strong = math.exp(float(q[0, 0, 120].double()) * SM)
+    for i in range(tq):
+        sees = tk - (tq - 1 - i if causal else 0)
+        others, w = (tk - 1, strong) if sees == tk else (sees, 0.0)
+        # sums of 1 are exact up to 2^24 in a share and joined in 32 bits; the score is one product, its weight's error 2^-19
+        assert abs(float(lse[i, 0]) - math.log(others + w)) < 2.0 ** -18 * 22
+        got = out[i, 0].double()
+        assert abs(float(got[120]) - w / (others + w)) <= 2.0 ** -8 + 2.0 ** -16
+        got[120] = 0.0
+        assert (got == 0).all()
