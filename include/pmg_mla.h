@@ -63,7 +63,9 @@ extern "C" {
  *  seq_lens            int32 [num_reqs]: ctx + new.
  *  blocks_taken        int32 [1]: ids taken from free_blocks.
  * num_reqs <= PMG_MAX_REQS, max_tokens <= INT32_MAX. slots, positions,
- * token_to_seq, cu_seq and blocks_taken may be NULL (not wanted).
+ * token_to_seq, cu_seq and blocks_taken may be NULL (not wanted). Results must
+ * not overlap ctx_lens, new_lens or free_blocks, which are read throughout the
+ * call (PMG_ERR_ARG): lengths are not updated in place.
  */
 int pmg_plan_step(const int32_t* ctx_lens, const int32_t* new_lens, int32_t num_reqs, int32_t* block_table,
                   int64_t block_table_stride, const int32_t* free_blocks, int64_t num_free, int64_t num_blocks,

@@ -380,7 +380,8 @@ def plan_step(ctx_lens: torch.Tensor, new_lens: torch.Tensor, block_table: torch
     positions, token_to_seq  int32 [max_tokens] or None (-1 past the last token).
     cu_new, cu_seq  int32 [num_reqs + 1]: prefix sums of new and total lengths
                   (cu_seq is the gather's cu_seq_lens; it may be None).
-    seq_lens      int32 [num_reqs]: total lengths.
+    seq_lens      int32 [num_reqs]: total lengths, in memory of their own: no
+                  result may overlap ctx_lens, new_lens or free_blocks.
     blocks_taken  int32 [1] or None.
     """
     r = ctx_lens.numel()

@@ -300,6 +300,16 @@ __global__ void __launch_bounds__(kThreads) plan_step_kernel(const __grid_consta
 
 constexpr int kSmem = kPlaces * 20;
 
+struct Bytes {
+  const void* at;
+  int64_t n;
+};
+bool overlap(const Bytes& a, const Bytes& b) {
+  const uintptr_t x = reinterpret_cast<uintptr_t>(a.at), y = reinterpret_cast<uintptr_t>(b.at);
+  return a.at != nullptr && b.at != nullptr && a.n > 0 && b.n > 0 && x < y + static_cast<uintptr_t>(b.n) &&
+         y < x + static_cast<uintptr_t>(a.n);
+}
+
 }  // namespace
 }  // namespace pmg_mla
 
@@ -322,6 +332,14 @@ extern "C" int pmg_plan_step(const int32_t* ctx_lens, const int32_t* new_lens, i
       !aligned(slots, 8) || !aligned(positions, 4) || !aligned(token_to_seq, 4) || !aligned(cu_new, 4) ||
       !aligned(seq_lens, 4) || !aligned(cu_seq, 4) || !aligned(blocks_taken, 4) || !aligned(error_flag, 4))
     return PMG_ERR_ALIGN;
+  // CTAs that have not begun yet read the lengths and the free ids while others write their results
+  const int64_t r = num_reqs;
+  for (const Bytes& in : {Bytes{ctx_lens, 4 * r}, Bytes{new_lens, 4 * r}, Bytes{free_blocks, 4 * num_free}})
+    for (const Bytes& out : {Bytes{block_table, 4 * r * block_table_stride}, Bytes{slots, 8 * max_tokens},
+                             Bytes{positions, 4 * max_tokens}, Bytes{token_to_seq, 4 * max_tokens},
+                             Bytes{cu_new, 4 * (r + 1)}, Bytes{seq_lens, 4 * r}, Bytes{cu_seq, 4 * (r + 1)},
+                             Bytes{blocks_taken, 4}, Bytes{error_flag, 4}})
+      if (overlap(in, out)) return PMG_ERR_ARG;
   PlanParams p{ctx_lens, new_lens, num_reqs, block_table, block_table_stride, free_blocks, num_free, num_blocks,
                block_size, slots, positions, token_to_seq, max_tokens, cu_new, seq_lens, cu_seq, blocks_taken,
                error_flag, 1, 0, 0};

@@ -84,3 +84,23 @@ def test_prefill_over_the_most_keys(ws, causal, few):
         assert abs(float(got[120]) - w / (others + w)) <= 2.0 ** -8 + 2.0 ** -16
         got[120] = 0.0
         assert (got == 0).all()
+
+
+def test_plan_takes_neighbours_in_one_buffer():
+    """Inputs and results side by side in one tensor do not overlap."""
+    r, n = 3, 9
+    buffer = torch.full((53,), 7, dtype=torch.int32, device=DEV)
+    cut = iter(buffer.split([r, r, 4, 4 * r, r, r + 1, r + 1, 1, 1, n, n]))
+    ctx, new, free, table, lens, cu, cu_seq, taken, err, positions, t2s = (next(cut) for _ in range(11))
+    ctx.copy_(i32([3, 0, 4]))
+    new.copy_(i32([2, 4, 1]))
+    free.copy_(i32([9, 8, 7, 6]))
+    table.copy_(i32([0, -1, -1, -1, -1, -1, -1, -1, 1, -1, -1, -1]))
+    err.zero_()
+    slots = torch.empty(n, dtype=torch.int64, device=DEV)
+    binding.plan_step(ctx, new, table.view(r, 4), free, 4, slots, positions, t2s, cu, lens, cu_seq, taken, 10, err)
+    assert table.tolist() == [0, 9, -1, -1, 8, -1, -1, -1, 1, 7, -1, -1] and int(taken) == 3 and int(err) == 0
+    assert slots.tolist() == [3, 36, 32, 33, 34, 35, 28, -1, -1] and positions.tolist() == [3, 4, 0, 1, 2, 3, 4, -1, -1]
+    assert t2s.tolist() == [0, 0, 1, 1, 1, 1, 2, -1, -1]
+    assert lens.tolist() == [5, 4, 5] and cu.tolist() == [0, 2, 6, 7] and cu_seq.tolist() == [0, 5, 9, 14]
+    assert ctx.tolist() == [3, 0, 4] and new.tolist() == [2, 4, 1] and free.tolist() == [9, 8, 7, 6]
