@@ -309,16 +309,39 @@ DECODE_WORDS = [(n, "d" if n == "sm_scale" else "q") for n in (
 DECODE_ARGS = struct.Struct("<" + "".join(f for _, f in DECODE_WORDS))
 PREFILL_ARGS = struct.Struct("<21qd13q")
 _I32, _I64, _F32 = torch.int32, torch.int64, torch.float32
-_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or (
+    lambda device: torch.cuda.current_stream(device).cuda_stream)
 
 
-def _stream_word(t: torch.Tensor, stream) -> int:
-    """The stream of a call on t's device: the given one, or torch's current one."""
-    if stream is None and _raw_stream is not None:
-        device = t.get_device()
-        if device >= 0:
-            return _raw_stream(device)
-    return _stream_handle(stream) or 0
+_one_device = False  # known that this process sees one device: what is on a device is on that one
+
+
+def _same_device(**tensors: Optional[torch.Tensor]) -> int:
+    """The device of a call's tensors: one for all of them, or pinned host memory, which every device reaches."""
+    global _one_device
+    device = None
+    for what, t in tensors.items():
+        if t is None:
+            continue
+        if not t.is_cuda:
+            if not t.is_pinned():
+                raise ValueError(f"{what} must be on a CUDA device, got {t.device}")
+        elif device is None:
+            device = t.get_device()
+        elif t.get_device() != device:
+            raise ValueError(f"{what} is on {t.device}, other tensors are on cuda:{device}")
+    if device is None:
+        raise ValueError("no tensor is on a CUDA device")
+    _one_device = torch.cuda.device_count() == 1
+    return device
+
+
+def _call(which: int, words: bytes, device: int) -> int:
+    """pmg_call_packed with `device` current: the library launches there."""
+    if torch.cuda.current_device() == device:
+        return load_library().pmg_call_packed(which, words)
+    with torch.cuda.device(device):
+        return load_library().pmg_call_packed(which, words)
 
 
 def _is_vector(t: torch.Tensor, dtype: torch.dtype, n: int) -> bool:
@@ -339,10 +362,6 @@ def _scalar(t: Optional[torch.Tensor], dtype: torch.dtype, what: str) -> int:
     if t.dtype is not dtype or t.numel() != 1:
         raise ValueError(f"{what} must be one {dtype} element")
     return t.data_ptr()
-
-
-def _word(t: Optional[torch.Tensor]) -> int:
-    return 0 if t is None else t.data_ptr()
 
 
 def _unit_last(what: str, dims: int, t: torch.Tensor):
@@ -401,11 +420,24 @@ def plan_step(ctx_lens: torch.Tensor, new_lens: torch.Tensor, block_table: torch
                 ("positions", positions, _I32, tokens, True), ("token_to_seq", token_to_seq, _I32, tokens, True),
                 ("cu_seq", cu_seq, _I32, r + 1, True)):
             _vector(t, dtype, n, what, optional)
-    st = load_library().pmg_call_packed(0, PLAN_ARGS.pack(
-        ctx_lens.data_ptr(), new_lens.data_ptr(), r, block_table.data_ptr(), _table(block_table, r),
-        free_blocks.data_ptr(), free, num_blocks, block_size, _word(slots), _word(positions), _word(token_to_seq), tokens,
-        cu_new.data_ptr(), seq_lens.data_ptr(), _word(cu_seq), _scalar(blocks_taken, _I32, "blocks_taken"),
-        _scalar(error_flag, _I32, "error_flag"), _stream_word(ctx_lens, stream)))
+    width, taken = _table(block_table, r), _scalar(blocks_taken, _I32, "blocks_taken")
+    flag = _scalar(error_flag, _I32, "error_flag")
+    device = 0
+    if not (_one_device and ctx_lens.is_cuda and new_lens.is_cuda and block_table.is_cuda and free_blocks.is_cuda
+            and cu_new.is_cuda and seq_lens.is_cuda and (slots is None or slots.is_cuda)
+            and (positions is None or positions.is_cuda) and (token_to_seq is None or token_to_seq.is_cuda)
+            and (cu_seq is None or cu_seq.is_cuda) and (blocks_taken is None or blocks_taken.is_cuda)
+            and (error_flag is None or error_flag.is_cuda)):
+        device = _same_device(ctx_lens=ctx_lens, new_lens=new_lens, block_table=block_table, free_blocks=free_blocks,
+                              slots=slots, positions=positions, token_to_seq=token_to_seq, cu_new=cu_new,
+                              seq_lens=seq_lens, cu_seq=cu_seq, blocks_taken=blocks_taken, error_flag=error_flag)
+    words = PLAN_ARGS.pack(
+        ctx_lens.data_ptr(), new_lens.data_ptr(), r, block_table.data_ptr(), width,
+        free_blocks.data_ptr(), free, num_blocks, block_size, 0 if slots is None else slots.data_ptr(),
+        0 if positions is None else positions.data_ptr(), 0 if token_to_seq is None else token_to_seq.data_ptr(), tokens,
+        cu_new.data_ptr(), seq_lens.data_ptr(), 0 if cu_seq is None else cu_seq.data_ptr(), taken, flag,
+        _raw_stream(device) if stream is None else _stream_handle(stream) or 0)
+    st = load_library().pmg_call_packed(0, words) if _one_device else _call(0, words, device)
     if st != PMG_OK:
         raise PmgError(st, "pmg_plan_step")
 
@@ -426,9 +458,12 @@ def append(c_kv: torch.Tensor, k_pe: torch.Tensor, cache: torch.Tensor, slots: t
     None (no norm). q_out like q_pe (it may be q_pe). interleaved: pairs are
     neighbours instead of halves apart.
     """
-    (t, dv), cs = _unit_last("c_kv", 2, c_kv)
-    (tk, dr), ks = _unit_last("k_pe", 2, k_pe)
-    (blocks, block_size, entry), bs = _unit_last("cache", 3, cache)
+    shape, cs, kshape, ks, bshape, bs = c_kv.shape, c_kv.stride(), k_pe.shape, k_pe.stride(), cache.shape, cache.stride()
+    if not (len(cs) == 2 and len(ks) == 2 and len(bs) == 3 and cs[1] == 1 and ks[1] == 1 and bs[2] == 1):
+        _unit_last("c_kv", 2, c_kv)
+        _unit_last("k_pe", 2, k_pe)
+        _unit_last("cache", 3, cache)
+    (t, dv), (tk, dr), (blocks, block_size, entry) = shape, kshape, bshape
     dtype = c_kv.dtype
     src, dst = TORCH_DTYPE_CODES.get(dtype), TORCH_DTYPE_CODES.get(cache.dtype)
     if tk != t or entry != dv + dr:
@@ -438,7 +473,8 @@ def append(c_kv: torch.Tensor, k_pe: torch.Tensor, cache: torch.Tensor, slots: t
     rot = cos_sin.shape
     if cos_sin.dtype is not _F32 or len(rot) != 2 or rot[1] != dr or not cos_sin.is_contiguous():
         raise ValueError(f"cos_sin must be float32 [num_positions, {dr}] and contiguous")
-    if not (_is_vector(slots, _I64, t) and _is_vector(positions, _I32, t)
+    if not (slots.dtype is _I64 and slots.numel() == t and slots.is_contiguous()
+            and positions.dtype is _I32 and positions.numel() == t and positions.is_contiguous()
             and (norm_weight is None or _is_vector(norm_weight, _F32, dv))):
         _vector(slots, _I64, t, "slots")
         _vector(positions, _I32, t, "positions")
@@ -448,17 +484,28 @@ def append(c_kv: torch.Tensor, k_pe: torch.Tensor, cache: torch.Tensor, slots: t
     q = o = heads = 0
     qs = os_ = (0, 0)
     if q_pe is not None:
-        shape, qs = _unit_last("q_pe", 3, q_pe)
-        oshape, os_ = _unit_last("q_out", 3, q_out)
+        shape, qs, oshape, os_ = q_pe.shape, q_pe.stride(), q_out.shape, q_out.stride()
+        if not (len(qs) == 3 and len(os_) == 3 and qs[2] == 1 and os_[2] == 1):
+            _unit_last("q_pe", 3, q_pe)
+            _unit_last("q_out", 3, q_out)
         heads = shape[1]
         if oshape != shape or shape[0] != t or shape[2] != dr or q_pe.dtype is not dtype or q_out.dtype is not dtype:
             raise ValueError(f"q_pe {list(shape)} and q_out {list(oshape)} must be [{t}, heads, {dr}] of {dtype}")
         q, o = q_pe.data_ptr(), q_out.data_ptr()
-    st = load_library().pmg_call_packed(1, APPEND_ARGS.pack(
-        c_kv.data_ptr(), cs[0], k_pe.data_ptr(), ks[0], _word(norm_weight), eps, cos_sin.data_ptr(), rot[0],
+    factor, flag = _scalar(scale, _F32, "scale"), _scalar(error_flag, _I32, "error_flag")
+    device = 0
+    if not (_one_device and c_kv.is_cuda and k_pe.is_cuda and cache.is_cuda and slots.is_cuda and positions.is_cuda
+            and cos_sin.is_cuda and (norm_weight is None or norm_weight.is_cuda) and (scale is None or scale.is_cuda)
+            and (q_pe is None or q_pe.is_cuda and q_out.is_cuda) and (error_flag is None or error_flag.is_cuda)):
+        device = _same_device(c_kv=c_kv, k_pe=k_pe, cache=cache, slots=slots, positions=positions, cos_sin=cos_sin,
+                              norm_weight=norm_weight, scale=scale, q_pe=q_pe, q_out=q_out, error_flag=error_flag)
+    words = APPEND_ARGS.pack(
+        c_kv.data_ptr(), cs[0], k_pe.data_ptr(), ks[0], 0 if norm_weight is None else norm_weight.data_ptr(), eps,
+        cos_sin.data_ptr(), rot[0],
         slots.data_ptr(), positions.data_ptr(), t, dv, dr, src, cache.data_ptr(), bs[0], bs[1], blocks, block_size, dst,
-        _scalar(scale, _F32, "scale"), q, qs[0], qs[1], o, os_[0], os_[1], heads,
-        _scalar(error_flag, _I32, "error_flag"), _stream_word(c_kv, stream), OPT_ROPE_PAIRS if interleaved else 0))
+        factor, q, qs[0], qs[1], o, os_[0], os_[1], heads, flag,
+        _raw_stream(device) if stream is None else _stream_handle(stream) or 0, OPT_ROPE_PAIRS if interleaved else 0)
+    st = load_library().pmg_call_packed(1, words) if _one_device else _call(1, words, device)
     if st != PMG_OK:
         raise PmgError(st, "pmg_append")
 
@@ -508,12 +555,22 @@ def latent_decode(q: torch.Tensor, cache: torch.Tensor, block_table: torch.Tenso
     if not (_is_vector(seq_lens, _I32, r) and (lse is None or _is_vector(lse, _F32, r * q_len * heads))):
         _vector(seq_lens, _I32, r, "seq_lens")
         _vector(lse, _F32, r * q_len * heads, "lse", True)
-    st = load_library().pmg_call_packed(2, DECODE_ARGS.pack(
-        q.data_ptr(), qs[0], qs[1], qs[2], cache.data_ptr(), bs[0], bs[1], blocks, block_table.data_ptr(),
-        _table(block_table, r), seq_lens.data_ptr(), r, q_len, heads, dv, entry - dv, block_size, qd, cd,
-        _scalar(scale, _F32, "scale"), sm_scale, out.data_ptr(), os_[0], os_[1], os_[2], _word(lse),
-        workspace.data_ptr(), workspace.nbytes, _scalar(error_flag, _I32, "error_flag"), _stream_word(q, stream),
-        options))
+    width, factor = _table(block_table, r), _scalar(scale, _F32, "scale")
+    flag = _scalar(error_flag, _I32, "error_flag")
+    if not workspace.is_contiguous():
+        raise ValueError("workspace must be contiguous")
+    device = 0
+    if not (_one_device and q.is_cuda and cache.is_cuda and block_table.is_cuda and seq_lens.is_cuda and out.is_cuda
+            and workspace.is_cuda and (lse is None or lse.is_cuda) and (scale is None or scale.is_cuda)
+            and (error_flag is None or error_flag.is_cuda)):
+        device = _same_device(q=q, cache=cache, block_table=block_table, seq_lens=seq_lens, out=out, workspace=workspace,
+                              lse=lse, scale=scale, error_flag=error_flag)
+    words = DECODE_ARGS.pack(
+        q.data_ptr(), qs[0], qs[1], qs[2], cache.data_ptr(), bs[0], bs[1], blocks, block_table.data_ptr(), width,
+        seq_lens.data_ptr(), r, q_len, heads, dv, entry - dv, block_size, qd, cd, factor, sm_scale, out.data_ptr(),
+        os_[0], os_[1], os_[2], 0 if lse is None else lse.data_ptr(), workspace.data_ptr(), workspace.nbytes, flag,
+        _raw_stream(device) if stream is None else _stream_handle(stream) or 0, options)
+    st = load_library().pmg_call_packed(2, words) if _one_device else _call(2, words, device)
     if st != PMG_OK:
         raise PmgError(st, "pmg_latent_decode")
 
@@ -564,10 +621,21 @@ def latent_prefill(q: torch.Tensor, k_nope: torch.Tensor, k_pe: torch.Tensor, v:
         _vector(cu_k, _I32, reqs + 1, "cu_k")
         _vector(lse, _F32, tq * heads, "lse", True)
         _vector(prev_lse, _F32, tq * heads, "prev_lse", True)
-    st = load_library().pmg_call_packed(3, PREFILL_ARGS.pack(
+    flag = _scalar(error_flag, _I32, "error_flag")
+    if not workspace.is_contiguous():
+        raise ValueError("workspace must be contiguous")
+    device = 0
+    if not (_one_device and q.is_cuda and k_nope.is_cuda and k_pe.is_cuda and v.is_cuda and cu_q.is_cuda and cu_k.is_cuda
+            and out.is_cuda and workspace.is_cuda and (lse is None or lse.is_cuda)
+            and (prev_out is None or prev_out.is_cuda and prev_lse.is_cuda) and (error_flag is None or error_flag.is_cuda)):
+        device = _same_device(q=q, k_nope=k_nope, k_pe=k_pe, v=v, cu_q=cu_q, cu_k=cu_k, out=out, workspace=workspace,
+                              lse=lse, prev_out=prev_out, prev_lse=prev_lse, error_flag=error_flag)
+    words = PREFILL_ARGS.pack(
         q.data_ptr(), qs[0], qs[1], k_nope.data_ptr(), ks[0], ks[1], k_pe.data_ptr(), ps[0], v.data_ptr(), vs[0], vs[1],
         cu_q.data_ptr(), cu_k.data_ptr(), reqs, tq, tk, heads, dn, dr, dv, code, sm_scale, out.data_ptr(), os_[0], os_[1],
-        _word(lse), prev, rs[0], rs[1], _word(prev_lse), workspace.data_ptr(), workspace.nbytes,
-        _scalar(error_flag, _I32, "error_flag"), _stream_word(q, stream), (OPT_CAUSAL if causal else 0) | options))
+        0 if lse is None else lse.data_ptr(), prev, rs[0], rs[1], 0 if prev_lse is None else prev_lse.data_ptr(),
+        workspace.data_ptr(), workspace.nbytes, flag,
+        _raw_stream(device) if stream is None else _stream_handle(stream) or 0, (OPT_CAUSAL if causal else 0) | options)
+    st = load_library().pmg_call_packed(3, words) if _one_device else _call(3, words, device)
     if st != PMG_OK:
         raise PmgError(st, "pmg_latent_prefill")
