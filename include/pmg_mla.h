@@ -16,7 +16,9 @@
  * `stream`, host-detected errors returned as a pmg_status with nothing
  * launched, data errors OR-ed into *error_flag with the affected rows skipped.
  * No call allocates memory or synchronises. Every index read from the device
- * is checked before it is used.
+ * is checked before it is used. Waits on the device are bounded: where one of
+ * the attention calls' runs out (two seconds; PMG_FLAG_TIMEOUT), the rows that
+ * it was for become NaN, result and log sum, whether or not a flag was given.
  */
 #ifndef PMG_MLA_H_
 #define PMG_MLA_H_

@@ -593,6 +593,16 @@ __global__ void __launch_bounds__(kThreads, 1)
       if (prev_b >= 0) {
         if (prev_n > 0) mbar_wait(smem_u32(&mi.pv_done), (t - 1) & 1, stop);
         tmem_fence_after();
+        if (stopped(stop)) {  // a wait ran out: the rows become NaN by their factors or sums (every warp sees to it for itself)
+          const float nan = __uint_as_float(0x7fffffffu);
+#pragma unroll 1
+          for (int i = lane; i < n_rows; i += 32) {
+            mi.inv[i] = nan;
+            if (!prev_whole) prev_slot[p.rows_per_group * kLatent + 2 * i + 1] = nan;
+            else if (p.lse != nullptr) p.lse[static_cast<int64_t>(prev_b) * rows + g0 + i] = nan;
+          }
+          __syncwarp();
+        }
         TQ* out = static_cast<TQ*>(p.out) + prev_b * p.or_stride;
         const int d = warp * 32 + lane;  // and 128 further for each m
 #pragma unroll 1

@@ -547,6 +547,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         __syncwarp();
         tmem_fence_after();
       }
+      if (stopped(stop)) l = __uint_as_float(0x7fffffffu);  // a NaN for the row's result and log sum, split or whole
       if (some && *reinterpret_cast<volatile int32_t*>(&mi.spoiled) != 0) {
         // infinities and NaN that were kept out of the products, for the rows that see them
         const int lo = max(it.b0, it.clean_from()) * kBlock;

@@ -32,7 +32,8 @@ __device__ __forceinline__ void mbar_expect(uint32_t bar, uint32_t bytes) {
 // Every wait is bounded: after two seconds it gives up and sets `stop`, a word
 // of shared memory that makes all later waits of the CTA return at once. Roles
 // then run their (finite) loops to the end over whatever is there, the loading
-// role issues nothing more, and the CTA reports PMG_FLAG_TIMEOUT. One block of
+// role issues nothing more, the CTA's rows become NaN and it reports
+// PMG_FLAG_TIMEOUT. One block of
 // instructions with no result: nothing of the waiting role's own control flow
 // depends on it.
 __device__ __forceinline__ void mbar_wait(uint32_t bar, uint32_t parity, uint32_t stop) {
