@@ -67,7 +67,9 @@ extern "C" {
  * num_reqs <= PMG_MAX_REQS, max_tokens <= INT32_MAX. slots, positions,
  * token_to_seq, cu_seq and blocks_taken may be NULL (not wanted). Results must
  * not overlap ctx_lens, new_lens or free_blocks, which are read throughout the
- * call (PMG_ERR_ARG): lengths are not updated in place.
+ * call (PMG_ERR_ARG): lengths are not updated in place. Ids are taken from the
+ * list's beginning each time: before the next call, a replayed graph's too, the
+ * caller moves the list on by *blocks_taken.
  */
 int pmg_plan_step(const int32_t* ctx_lens, const int32_t* new_lens, int32_t num_reqs, int32_t* block_table,
                   int64_t block_table_stride, const int32_t* free_blocks, int64_t num_free, int64_t num_blocks,
@@ -144,8 +146,13 @@ int pmg_append(const void* c_kv, int64_t c_kv_stride, const void* k_pe, int64_t 
  * row is not touched by infinities or NaN in entries that it does not see.
  *
  * The tensor-core kernel runs for latent_dim 512, rope_dim 64, q_dtype bf16 or
- * fp16, a block_size that is a multiple of 8, 16-byte aligned cache rows of
- * stride below 2^40; the general kernel for everything else.
+ * fp16, a block_size that is a multiple of 8, 16-byte aligned rows of cache and
+ * q, strides below 2^38 elements; the general kernel, many times slower on long
+ * requests, for everything else. Scores, sums and accumulators are 32-bit in
+ * both. For the second product the tensor-core kernel rounds weights to the
+ * type of a 16-bit cache (2^-8 of each, fp16 2^-11); over an e4m3 cache to 2^-9
+ * of each, or to 2^-28 of the row's largest where that is more. Over an e4m3
+ * cache it takes query values to within 2^-17 of the row's largest.
  */
 int pmg_latent_decode(const void* q, int64_t q_req_stride, int64_t q_token_stride, int64_t q_head_stride,
                       const void* cache, int64_t cache_block_stride, int64_t cache_token_stride, int64_t num_blocks,
@@ -183,8 +190,10 @@ int pmg_latent_decode(const void* q, int64_t q_req_stride, int64_t q_token_strid
  *  workspace as in pmg_latent_decode.
  *
  * The tensor-core kernel runs for nope_dim 128, rope_dim 64, v_dim 128, bf16
- * or fp16 with 16-byte aligned rows; the general kernel for everything else
- * (nope_dim + rope_dim and v_dim up to PMG_MAX_ENTRY).
+ * or fp16 with 16-byte aligned rows, no stride of 0 and sm_scale > 0; the
+ * general kernel for everything else (nope_dim + rope_dim and v_dim up to
+ * PMG_MAX_ENTRY). Scores, sums and accumulators are 32-bit in both; the
+ * tensor-core kernel rounds weights to the type of v for the second product.
  */
 int pmg_latent_prefill(const void* q, int64_t q_token_stride, int64_t q_head_stride, const void* k_nope,
                        int64_t k_token_stride, int64_t k_head_stride, const void* k_pe, int64_t k_pe_stride,

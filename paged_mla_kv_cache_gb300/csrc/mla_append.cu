@@ -9,9 +9,10 @@
 //
 // Bound by memory: an entry in and out, 2 * rope_dim elements a head, one row
 // of cosines and sines a token. Measured: 8192 tokens of 128 heads into an e4m3
-// cache 60 us (285 MB, 71% of copy bandwidth; a plain copy of the same strided
+// cache 59 us (285 MB, 72% of copy bandwidth; a plain copy of the same strided
 // 128-byte rows takes 46 us: the rest is mostly the entries, whose warps go
-// through a chain of slot, values, sum and store, beside the queries); 64 tokens
+// through a chain of slot, values, sum and store: alone the two launches take
+// 12.5 and 43.5 us, so they hardly overlap); 64 tokens
 // 7.4 us, the host's call and one launch. One warp takes either a token's entry (the
 // latent row stays in registers between the sum and the store, so it is read
 // once) or a few heads of a token's queries, for which a lane keeps one set of

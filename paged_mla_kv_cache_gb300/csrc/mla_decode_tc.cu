@@ -13,11 +13,14 @@
 // bytes for 64 * 1088 multiply-adds); with 128 rows two CTAs read the same
 // entries side by side, the second from L2, and the tensor core's products come
 // to about the same time as the stream. Measured: 64 ragged requests of 1 to
-// 32768 entries, 128 heads, 83 us (1.83 TB/s, 390 TFLOP/s): queries of 64 rows
-// leave room for two tiles in flight, and a tile's way from its arrival over
-// its scores and weights to its freed slots takes about 2 us, which two tiles
-// do not hide. One request of 60000 entries, 16 heads, 32 us (floor 10): the
-// first loads, seven tiles a CTA and the join.
+// 32768 entries, 128 heads, 83 us (1.83 TB/s, 390 TFLOP/s; memory at 29%, the
+// tensor pipe at 32% of the kernel's 70 us): neither bounds it. A tile's way
+// from its scores over its weights to its freed slots is one chain of about
+// 2 us, with one buffer of weights and one group of softmax warps. 8 skewed
+// requests over an e4m3 cache, 64 heads of 2 tokens, 55 us (memory at 7%, the
+// tensor pipe at 23% of 47 us), with three tiles in flight where the 16-bit
+// layout has two. One request of 60000 entries, 16 heads, 31 us (floor 10):
+// the first loads, seven tiles a CTA and the join.
 //
 // Roles: warp 4 loads (a copy a tile where a page holds whole tiles, else one
 // for each page: pages of any multiple of 8 tokens), warp 5 issues products,
@@ -30,7 +33,9 @@
 // The reference of a row follows its maximum only when a score passes it by
 // 2^kCap: weights then stay inside the range of their type (fp16 ones are kept
 // from 2^8 to 2^15 where the largest are, so that those beside a strong key do
-// not fall below 2^-24), sums are 32-bit, and the accumulators are rescaled (read, multiplied, written back)
+// not fall below 2^-24). They are rounded to the type of the entries for the
+// second product (2^-8 or 2^-11 of each; wider ones would need the entries
+// widened too), their sum is of the unrounded ones. Sums are 32-bit, and the accumulators are rescaled (read, multiplied, written back)
 // only in the first tiles of a request. All threads learn whether a tile needs
 // that from one barrier with a vote, so the usual tile has no maximum over
 // the lanes at all.
