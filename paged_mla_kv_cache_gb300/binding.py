@@ -1,5 +1,5 @@
-"""Thin ctypes binding of ``libpmg.so`` (declared in ``include/pmg.h`` and
-``include/pmg_mla.h``).
+"""Thin ctypes binding of ``libpmg.so`` (declared in ``include/pmg.h``,
+``include/pmg_mla.h`` and ``include/pmg_long.h``).
 
 Argument marshalling only: shapes, strides, dtypes and raw pointers are taken
 from torch tensors and passed to the C ABI; every step of the gather runs in
@@ -13,7 +13,9 @@ the FP8 scale, an error flag and the stream made explicit.
 
 plan_step, append, latent_decode and latent_prefill are the operators around
 the gather: a step's pages and slots, the cache write, and the attention over
-the cache (absorbed) or over gathered and expanded entries.
+the cache (absorbed) or over gathered and expanded entries. block_bounds,
+block_scores and select_blocks choose the pages of a long request that a token
+attends to, and latent_decode_shared attends behind prefixes that requests share.
 """
 from __future__ import annotations
 
@@ -51,7 +53,7 @@ OPT_IMPLIED_END = 4
 OPT_EARLY_METADATA = 8
 OPT_ROPE_PAIRS = 1         # append
 OPT_CAUSAL = 1             # latent_prefill
-OPT_FORCE_GENERAL = 2      # latent_decode, latent_prefill
+OPT_FORCE_GENERAL = 2      # latent_decode, latent_prefill, block_scores, latent_decode_shared
 MAX_ENTRY = 1024           # largest latent_dim + rope_dim of the attention calls
 
 PATH_NAMES = {0: "none", 1: "bulk", 2: "vector", 3: "scalar", 4: "realign"}
@@ -117,6 +119,19 @@ def load_library() -> ctypes.CDLL:
         L.pmg_latent_prefill.argtypes = [vp, i64, i64, vp, i64, i64, vp, i64, vp, i64, i64, vp, vp, i32, i64, i64, i32,
                                          i32, i32, i32, i32, f32, vp, i64, i64, vp, vp, i64, i64, vp, vp, i64, vp, vp,
                                          u32]
+        L.pmg_block_bounds.restype = ctypes.c_int
+        L.pmg_block_bounds.argtypes = [vp, i64, i64, i64, i32, i32, i32, vp, i64, i64, i32, vp, i64, vp, vp, i32, vp, vp]
+        L.pmg_block_scores.restype = ctypes.c_int
+        L.pmg_block_scores.argtypes = [vp, i64, i64, i64, vp, i64, i64, i64, vp, i64, vp, i32, i32, i32, i32, i32, i32,
+                                       vp, f32, vp, vp, i64, vp, vp, u32]
+        L.pmg_select_blocks.restype = ctypes.c_int
+        L.pmg_select_blocks.argtypes = [vp, i64, vp, i64, vp, i32, i32, i32, vp, i64, vp, vp, i64, i32, i32, vp, vp]
+        L.pmg_latent_decode_shared.restype = ctypes.c_int
+        L.pmg_latent_decode_shared.argtypes = [vp, i64, i64, i64, vp, i64, i64, i64, vp, i64, vp, vp, i32, vp, i64, vp,
+                                               i32, i32, i32, i32, i32, i32, i32, i32, vp, f32, vp, i64, i64, i64, vp,
+                                               vp, i64, vp, vp, u32]
+        L.pmg_shared_workspace.restype = i64
+        L.pmg_shared_workspace.argtypes = [i64, i32]
         L.pmg_call_packed.restype = ctypes.c_int
         L.pmg_call_packed.argtypes = [i32, ctypes.c_char_p]
         L.pmg_attention_workspace.restype = i64
@@ -308,6 +323,10 @@ DECODE_WORDS = [(n, "d" if n == "sm_scale" else "q") for n in (
     "out out_req_stride out_token_stride out_head_stride lse workspace workspace_bytes error_flag stream options").split()]
 DECODE_ARGS = struct.Struct("<" + "".join(f for _, f in DECODE_WORDS))
 PREFILL_ARGS = struct.Struct("<21qd13q")
+BOUNDS_ARGS = struct.Struct("<18q")
+SCORES_ARGS = struct.Struct("<18qd6q")
+SELECT_ARGS = struct.Struct("<17q")
+SHARED_ARGS = struct.Struct("<25qd10q")
 _I32, _I64, _F32 = torch.int32, torch.int64, torch.float32
 _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or (
     lambda device: torch.cuda.current_stream(device).cuda_stream)
@@ -639,3 +658,222 @@ def latent_prefill(q: torch.Tensor, k_nope: torch.Tensor, k_pe: torch.Tensor, v:
     st = load_library().pmg_call_packed(3, words) if _one_device else _call(3, words, device)
     if st != PMG_OK:
         raise PmgError(st, "pmg_latent_prefill")
+
+
+# --- long contexts (include/pmg_long.h) ------------------------------------------
+
+
+def block_bounds(cache: torch.Tensor, bounds: torch.Tensor, block_table: torch.Tensor, seq_lens: torch.Tensor,
+                 ctx_lens: Optional[torch.Tensor] = None, error_flag: Optional[torch.Tensor] = None,
+                 stream=None) -> None:
+    """Largest and smallest value of each column of the pages that entries
+    joined (pmg_block_bounds).
+
+    cache     [num_blocks, block_size, entry] (bf16, fp16, fp32 or e4m3)
+    bounds    [num_blocks, 2, entry]: largest, then smallest; of cache's dtype, or
+              for an e4m3 cache of the queries' (its values without the scale)
+    ctx_lens  int32 [num_reqs]: places that bounds knows of already, or None
+    seq_lens  int32 [num_reqs]: places up to which it shall know. plan_step has
+              both: one call a step, after append.
+    """
+    (blocks, block_size, entry), cs = _unit_last("cache", 3, cache)
+    bshape, bs = _unit_last("bounds", 3, bounds)
+    if bshape != (blocks, 2, entry):
+        raise ValueError(f"bounds {list(bshape)} must be [{blocks}, 2, {entry}]")
+    cd, bd = TORCH_DTYPE_CODES.get(cache.dtype), TORCH_DTYPE_CODES.get(bounds.dtype)
+    if cd is None or bd is None:
+        raise ValueError(f"unsupported dtypes {cache.dtype} -> {bounds.dtype}")
+    r = seq_lens.numel()
+    if not (_is_vector(seq_lens, _I32, r) and (ctx_lens is None or _is_vector(ctx_lens, _I32, r))):
+        _vector(seq_lens, _I32, r, "seq_lens")
+        _vector(ctx_lens, _I32, r, "ctx_lens", True)
+    width, flag = _table(block_table, r), _scalar(error_flag, _I32, "error_flag")
+    device = 0
+    if not (_one_device and cache.is_cuda and bounds.is_cuda and block_table.is_cuda and seq_lens.is_cuda
+            and (ctx_lens is None or ctx_lens.is_cuda) and (error_flag is None or error_flag.is_cuda)):
+        device = _same_device(cache=cache, bounds=bounds, block_table=block_table, seq_lens=seq_lens, ctx_lens=ctx_lens,
+                              error_flag=error_flag)
+    words = BOUNDS_ARGS.pack(
+        cache.data_ptr(), cs[0], cs[1], blocks, block_size, entry, cd, bounds.data_ptr(), bs[0], bs[1], bd,
+        block_table.data_ptr(), width, 0 if ctx_lens is None else ctx_lens.data_ptr(), seq_lens.data_ptr(), r, flag,
+        _raw_stream(device) if stream is None else _stream_handle(stream) or 0)
+    st = load_library().pmg_call_packed(4, words) if _one_device else _call(4, words, device)
+    if st != PMG_OK:
+        raise PmgError(st, "pmg_block_bounds")
+
+
+def _token_rows(what: str, scores: torch.Tensor) -> int:
+    """The stride of [num_reqs, q_len, width] scores as num_reqs * q_len rows."""
+    (r, n, width), s = _unit_last(what, 3, scores)
+    if r > 1 and n > 1 and s[0] != n * s[1]:
+        raise ValueError(f"{what}' rows must lie at one stride")
+    step = s[1] if n > 1 else s[0] if r > 1 else width
+    return max(step, width) if r * n <= 1 else step
+
+
+def block_scores(q: torch.Tensor, bounds: torch.Tensor, block_table: torch.Tensor, seq_lens: torch.Tensor,
+                 scores: torch.Tensor, *, block_size: int, sm_scale: float, scale: Optional[torch.Tensor] = None,
+                 lse: Optional[torch.Tensor] = None, error_flag: Optional[torch.Tensor] = None, stream=None,
+                 options: int = 0) -> None:
+    """The most that entries of each page can score for each new token, over the
+    heads (pmg_block_scores).
+
+    q         [num_reqs, q_len, heads, entry] (bf16, fp16 or fp32), as for
+              latent_decode
+    bounds    [num_blocks, 2, entry] of q's dtype, as block_bounds keeps them
+    seq_lens  int32 [num_reqs], lengths with the new tokens
+    scores    fp32 [num_reqs, q_len, width of block_table]; -inf for pages of
+              which a token sees nothing
+    scale     fp32 device scalar of an e4m3 cache, or None
+    lse       fp32 [num_reqs, q_len, heads], contiguous, or None: subtracted from
+              a head's scores; the log sums of an earlier step make them bounds of
+              the logarithms of weights, comparable over the heads
+    """
+    shape, qs = _unit_last("q", 4, q)
+    bshape, bs = _unit_last("bounds", 3, bounds)
+    r, q_len, heads, entry = shape
+    blocks = bshape[0]
+    if bshape[1] != 2 or bshape[2] != entry:
+        raise ValueError(f"q {list(shape)} and bounds {list(bshape)} do not fit")
+    code = TORCH_DTYPE_CODES.get(q.dtype)
+    if code is None or bounds.dtype is not q.dtype or scores.dtype is not _F32:
+        raise ValueError(f"unsupported dtypes {q.dtype}, {bounds.dtype} -> {scores.dtype}")
+    if not (_is_vector(seq_lens, _I32, r) and (lse is None or _is_vector(lse, _F32, r * q_len * heads))):
+        _vector(seq_lens, _I32, r, "seq_lens")
+        _vector(lse, _F32, r * q_len * heads, "lse", True)
+    width, factor = _table(block_table, r), _scalar(scale, _F32, "scale")
+    if scores.shape != (r, q_len, width):
+        raise ValueError(f"scores {list(scores.shape)} must be [{r}, {q_len}, {width}]")
+    step, flag = _token_rows("scores", scores), _scalar(error_flag, _I32, "error_flag")
+    device = 0
+    if not (_one_device and q.is_cuda and bounds.is_cuda and block_table.is_cuda and seq_lens.is_cuda and scores.is_cuda
+            and (scale is None or scale.is_cuda) and (lse is None or lse.is_cuda)
+            and (error_flag is None or error_flag.is_cuda)):
+        device = _same_device(q=q, bounds=bounds, block_table=block_table, seq_lens=seq_lens, scores=scores, scale=scale,
+                              lse=lse, error_flag=error_flag)
+    words = SCORES_ARGS.pack(
+        q.data_ptr(), qs[0], qs[1], qs[2], bounds.data_ptr(), bs[0], bs[1], blocks, block_table.data_ptr(), width,
+        seq_lens.data_ptr(), r, q_len, heads, entry, block_size, code, factor, sm_scale,
+        0 if lse is None else lse.data_ptr(), scores.data_ptr(), step, flag,
+        _raw_stream(device) if stream is None else _stream_handle(stream) or 0, options)
+    st = load_library().pmg_call_packed(5, words) if _one_device else _call(5, words, device)
+    if st != PMG_OK:
+        raise PmgError(st, "pmg_block_scores")
+
+
+def select_blocks(scores: torch.Tensor, block_table: torch.Tensor, seq_lens: torch.Tensor, selected: torch.Tensor,
+                  selected_lens: torch.Tensor, *, block_size: int, first: int = 1, last: int = 1,
+                  columns: Optional[torch.Tensor] = None, error_flag: Optional[torch.Tensor] = None,
+                  stream=None) -> None:
+    """The pages that each new token attends to (pmg_select_blocks): its first
+    and last ones and those with the largest scores, selected.shape[1] in all.
+
+    scores         fp32 [num_reqs, q_len, width of block_table]
+    selected       int32 [num_reqs * q_len, keep]: their ids in the order of
+                   their columns, -1 behind the last
+    selected_lens  int32 [num_reqs * q_len]: entries on them that the token sees
+    columns        like selected, or None: their columns
+    latent_decode(q.view(-1, 1, heads, entry), cache, selected, selected_lens,
+    ...) attends to them.
+    """
+    (r, q_len, width), _ = _unit_last("scores", 3, scores)
+    (tokens, keep), ss = _unit_last("selected", 2, selected)
+    if scores.dtype is not _F32 or selected.dtype is not _I32:
+        raise ValueError(f"scores must be float32 and selected int32, got {scores.dtype} and {selected.dtype}")
+    if tokens != r * q_len or _table(block_table, r) != width:
+        raise ValueError(f"scores {list(scores.shape)}, block_table {list(block_table.shape)} and selected "
+                         f"{list(selected.shape)} do not fit")
+    if not (_is_vector(seq_lens, _I32, r) and _is_vector(selected_lens, _I32, tokens)):
+        _vector(seq_lens, _I32, r, "seq_lens")
+        _vector(selected_lens, _I32, tokens, "selected_lens")
+    if columns is not None and (columns.dtype is not _I32 or columns.shape != selected.shape
+                                or columns.stride() != selected.stride()):
+        raise ValueError("columns must be like selected")
+    step, flag = _token_rows("scores", scores), _scalar(error_flag, _I32, "error_flag")
+    device = 0
+    if not (_one_device and scores.is_cuda and block_table.is_cuda and seq_lens.is_cuda and selected.is_cuda
+            and selected_lens.is_cuda and (columns is None or columns.is_cuda)
+            and (error_flag is None or error_flag.is_cuda)):
+        device = _same_device(scores=scores, block_table=block_table, seq_lens=seq_lens, selected=selected,
+                              selected_lens=selected_lens, columns=columns, error_flag=error_flag)
+    words = SELECT_ARGS.pack(
+        scores.data_ptr(), step, block_table.data_ptr(), width, seq_lens.data_ptr(), r, q_len, block_size,
+        selected.data_ptr(), ss[0] if tokens > 1 else keep, 0 if columns is None else columns.data_ptr(),
+        selected_lens.data_ptr(), keep, first, last, flag,
+        _raw_stream(device) if stream is None else _stream_handle(stream) or 0)
+    st = load_library().pmg_call_packed(6, words) if _one_device else _call(6, words, device)
+    if st != PMG_OK:
+        raise PmgError(st, "pmg_select_blocks")
+
+
+def shared_workspace_bytes(num_reqs: int, q_len: int, heads: int, latent: int) -> int:
+    """Bytes of the workspace of latent_decode_shared for so many rows on the
+    current device; enough for any fewer, and for the other attention calls."""
+    n = load_library().pmg_shared_workspace(num_reqs * q_len * heads, latent)
+    if n < 0:
+        raise PmgError(2, "pmg_shared_workspace")
+    return int(n)
+
+
+def new_shared_workspace(device, num_reqs: int, q_len: int, heads: int, latent: int) -> torch.Tensor:
+    """A workspace for latent_decode_shared of at most so many rows. One per
+    stream: calls that may overlap must not share one."""
+    with torch.cuda.device(device):
+        return torch.empty(shared_workspace_bytes(num_reqs, q_len, heads, latent), dtype=torch.uint8, device=device)
+
+
+def latent_decode_shared(q: torch.Tensor, cache: torch.Tensor, prefix_table: torch.Tensor, prefix_lens: torch.Tensor,
+                         cu_groups: torch.Tensor, block_table: torch.Tensor, seq_lens: torch.Tensor, out: torch.Tensor,
+                         lse: Optional[torch.Tensor] = None, *, sm_scale: float,
+                         scale: Optional[torch.Tensor] = None, workspace: torch.Tensor,
+                         error_flag: Optional[torch.Tensor] = None, stream=None, options: int = 0) -> None:
+    """Absorbed latent attention of requests behind prefixes that they share
+    (pmg_latent_decode_shared).
+
+    prefix_table  int32 [num_groups, width], prefix_lens int32 [num_groups]: pages
+                  and lengths of the prefixes
+    cu_groups     int32 [num_groups + 1]: requests [cu_groups[g], cu_groups[g + 1])
+                  see prefix g; requests of no group see none
+    block_table   int32 [num_reqs, width'], seq_lens int32 [num_reqs]: the entries
+                  of each request's own, behind its prefix, as in latent_decode
+    workspace     new_shared_workspace(device, num_reqs, q_len, heads, latent)
+    The rest as in latent_decode.
+    """
+    shape, qs = _unit_last("q", 4, q)
+    (blocks, block_size, cached), bs = _unit_last("cache", 3, cache)
+    oshape, os_ = _unit_last("out", 4, out)
+    r, q_len, heads, entry = shape
+    dv = oshape[3]
+    if oshape[:3] != shape[:3] or cached != entry or not 1 <= dv <= entry:
+        raise ValueError(f"q {list(shape)}, cache {list(cache.shape)} and out {list(oshape)} do not fit")
+    qd, cd = TORCH_DTYPE_CODES.get(q.dtype), TORCH_DTYPE_CODES.get(cache.dtype)
+    if qd is None or cd is None or out.dtype is not q.dtype:
+        raise ValueError(f"unsupported dtypes {q.dtype}, {cache.dtype} -> {out.dtype}")
+    g = prefix_lens.numel()
+    if not (_is_vector(seq_lens, _I32, r) and _is_vector(prefix_lens, _I32, g) and _is_vector(cu_groups, _I32, g + 1)
+            and (lse is None or _is_vector(lse, _F32, r * q_len * heads))):
+        _vector(seq_lens, _I32, r, "seq_lens")
+        _vector(prefix_lens, _I32, g, "prefix_lens")
+        _vector(cu_groups, _I32, g + 1, "cu_groups")
+        _vector(lse, _F32, r * q_len * heads, "lse", True)
+    prefix_width, width, factor = _table(prefix_table, g), _table(block_table, r), _scalar(scale, _F32, "scale")
+    flag = _scalar(error_flag, _I32, "error_flag")
+    if not workspace.is_contiguous():
+        raise ValueError("workspace must be contiguous")
+    device = 0
+    if not (_one_device and q.is_cuda and cache.is_cuda and prefix_table.is_cuda and prefix_lens.is_cuda
+            and cu_groups.is_cuda and block_table.is_cuda and seq_lens.is_cuda and out.is_cuda and workspace.is_cuda
+            and (lse is None or lse.is_cuda) and (scale is None or scale.is_cuda)
+            and (error_flag is None or error_flag.is_cuda)):
+        device = _same_device(q=q, cache=cache, prefix_table=prefix_table, prefix_lens=prefix_lens, cu_groups=cu_groups,
+                              block_table=block_table, seq_lens=seq_lens, out=out, workspace=workspace, lse=lse,
+                              scale=scale, error_flag=error_flag)
+    words = SHARED_ARGS.pack(
+        q.data_ptr(), qs[0], qs[1], qs[2], cache.data_ptr(), bs[0], bs[1], blocks, prefix_table.data_ptr(), prefix_width,
+        prefix_lens.data_ptr(), cu_groups.data_ptr(), g, block_table.data_ptr(), width, seq_lens.data_ptr(), r, q_len,
+        heads, dv, entry - dv, block_size, qd, cd, factor, sm_scale, out.data_ptr(), os_[0], os_[1], os_[2],
+        0 if lse is None else lse.data_ptr(), workspace.data_ptr(), workspace.nbytes, flag,
+        _raw_stream(device) if stream is None else _stream_handle(stream) or 0, options)
+    st = load_library().pmg_call_packed(7, words) if _one_device else _call(7, words, device)
+    if st != PMG_OK:
+        raise PmgError(st, "pmg_latent_decode_shared")

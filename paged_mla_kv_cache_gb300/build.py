@@ -12,14 +12,15 @@ import shutil
 import subprocess
 
 UNITS = ["mla_plan.cu", "mla_append.cu", "mla_decode.cu", "mla_decode_tc.cu", "mla_prefill.cu",
-         "mla_prefill_tc.cu", "mla_packed.cu"]
+         "mla_prefill_tc.cu", "mla_bounds.cu", "mla_scores.cu", "mla_scores_tc.cu", "mla_select.cu", "mla_shared.cu",
+         "mla_shared_tc.cu", "mla_packed.cu"]
 PKG_DIR = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(PKG_DIR)
 CSRC = os.path.join(PKG_DIR, "csrc")
 SRC = os.path.join(CSRC, "pmg_gather.cu")
 SOURCES = [SRC] + [os.path.join(CSRC, f) for f in UNITS]
 HEADER = os.path.join(ROOT, "include", "pmg.h")
-HEADERS = [HEADER, os.path.join(ROOT, "include", "pmg_mla.h")]
+HEADERS = [HEADER, os.path.join(ROOT, "include", "pmg_mla.h"), os.path.join(ROOT, "include", "pmg_long.h")]
 LIB_DIR = os.path.join(PKG_DIR, "lib")
 LIB_PATH = os.path.join(LIB_DIR, "libpmg.so")
 

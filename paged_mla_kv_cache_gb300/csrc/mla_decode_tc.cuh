@@ -1,4 +1,5 @@
-// The tensor-core decode kernel (mla_decode_tc.cu).
+// The tensor-core decode kernel (mla_decode_tc_kernel.cuh) over requests
+// (mla_decode_tc.cu) and over shared prefixes (mla_shared_tc.cu).
 #pragma once
 
 #include "mla_decode.cuh"
@@ -10,5 +11,6 @@ bool decode_tc_takes(const DecodeParams& p, int q_dtype, int cache_dtype);
 
 // Chooses groups and units, and launches it. The join follows as for the general kernel.
 int decode_tc(DecodeParams& p, int q_dtype, int cache_dtype, int sms, void* stream);
+int prefix_tc(DecodeParams& p, int q_dtype, int cache_dtype, int sms, void* stream);
 
 }  // namespace pmg_mla

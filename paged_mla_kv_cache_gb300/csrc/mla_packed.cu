@@ -4,6 +4,7 @@
 #include <type_traits>
 #include <utility>
 
+#include "pmg_long.h"
 #include "pmg_mla.h"
 
 namespace {
@@ -41,6 +42,10 @@ extern "C" int pmg_call_packed(int which, const void* words) {
     case PMG_CALL_APPEND: return call(pmg_append, words);
     case PMG_CALL_LATENT_DECODE: return call(pmg_latent_decode, words);
     case PMG_CALL_LATENT_PREFILL: return call(pmg_latent_prefill, words);
+    case PMG_CALL_BLOCK_BOUNDS: return call(pmg_block_bounds, words);
+    case PMG_CALL_BLOCK_SCORES: return call(pmg_block_scores, words);
+    case PMG_CALL_SELECT_BLOCKS: return call(pmg_select_blocks, words);
+    case PMG_CALL_LATENT_DECODE_SHARED: return call(pmg_latent_decode_shared, words);
     default: return PMG_ERR_ARG;
   }
 }

@@ -1,0 +1,57 @@
+// Parameters of the page scores' kernels.
+#pragma once
+
+#include "mla_attn.cuh"
+#include "mla_long.cuh"
+#include "pmg_long.h"
+
+namespace pmg_mla {
+
+struct ScoreParams {
+  const uint8_t* q;
+  int64_t qr_stride, qt_stride, qh_stride;
+  const uint8_t* bounds;
+  int64_t bb_stride, br_stride;
+  int64_t num_blocks;
+  const int32_t* bt;
+  int64_t bt_stride;
+  const int32_t* seq;
+  int32_t R, q_len, H, E, B;
+  const float* scale;
+  float sm_scale;
+  const float* lse;
+  float* scores;
+  int64_t s_stride;
+  int32_t units;
+  int32_t* err;
+};
+
+// Columns of a request of which some token sees an entry, and pieces of work of
+// kScoreTile columns; one more writes the columns behind them.
+constexpr int kScoreTile = 64;
+__device__ __forceinline__ int64_t score_pages(const ScoreParams& p, const SparseLen& l) {
+  const uint32_t n = static_cast<uint32_t>(sparse_seen(l, p.q_len - 1, p.q_len)), b = static_cast<uint32_t>(p.B);
+  return (n + b - 1) / b;
+}
+__device__ __forceinline__ int64_t score_pieces(const ScoreParams& p, int r) {
+  return (score_pages(p, sparse_len(p.seq, r, p.bt_stride, p.B)) + kScoreTile - 1) / kScoreTile + 1;
+}
+
+__device__ __forceinline__ float score_shift(const ScoreParams& p, int64_t row) {
+  const float x = p.lse != nullptr ? p.lse[row] : 0.0f;
+  return isfinite(x) ? x : 0.0f;
+}
+
+// Columns [from, width) of a request that no token sees anything of.
+__device__ __forceinline__ void score_rest(const ScoreParams& p, int r, int64_t from, int tid, int threads) {
+  for (int i = 0; i < p.q_len; ++i) {
+    float* row = p.scores + (static_cast<int64_t>(r) * p.q_len + i) * p.s_stride;
+    for (int64_t c = from + tid; c < p.bt_stride; c += threads) row[c] = -INFINITY;
+  }
+}
+
+// The tensor-core kernel: entries of 576 16-bit values, rows of 16 bytes.
+bool scores_tc_takes(const ScoreParams& p, int dtype);
+int scores_tc(const ScoreParams& p, int dtype, void* stream);
+
+}  // namespace pmg_mla

@@ -1,0 +1,176 @@
+// The pages that each new token attends to (pmg_select_blocks).
+//
+// Mathematics: the k-th largest of a row's competing scores is found digit by
+// digit: scores are mapped to whole numbers of the same order (all bits of a
+// negative one flipped, the sign bit of the others; NaN above all, -0 as 0),
+// eight bits are counted in shared memory, and the digit that holds the k-th is
+// kept. Pages above that value stay, and of those equal to it the first ones. A
+// thread owns a run of neighbouring columns, so that one prefix sum over the
+// threads gives every kept page its place, in order.
+//
+// Bound by latency: a row is a few thousand scores, read once. A CTA takes a
+// row and holds it in shared memory (what does not fit there is read again in
+// each pass, from L2).
+#include <algorithm>
+
+#include "mla_long.cuh"
+#include "pmg_long.h"
+
+namespace pmg_mla {
+namespace {
+
+constexpr int kThreads = 256;
+constexpr int kHeld = 8192;  // scores in shared memory
+
+struct SelectParams {
+  const float* scores;
+  int64_t s_stride;
+  const int32_t* bt;
+  int64_t bt_stride;
+  const int32_t* seq;
+  int32_t q_len, B;
+  int32_t* selected;
+  int64_t sel_stride;
+  int32_t* columns;
+  int32_t* lens;
+  int64_t keep;
+  int32_t first, last;
+  int32_t* err;
+};
+
+// Whole numbers in the order of the scores.
+__device__ __forceinline__ uint32_t score_key(float x) {
+  if (isnan(x)) return 0xffffffffu;
+  const uint32_t u = __float_as_uint(x + 0.0f);
+  return u & 0x80000000u ? ~u : u | 0x80000000u;
+}
+
+__global__ void __launch_bounds__(kThreads) select_kernel(const __grid_constant__ SelectParams p) {
+  __shared__ uint32_t held[kHeld];
+  __shared__ uint32_t counts[256];
+  __shared__ int64_t scratch[33];
+  __shared__ uint32_t digit, left;
+  pdl_entry();
+  const int tid = threadIdx.x;
+  const int64_t token = blockIdx.x;
+  const int r = static_cast<int>(token / p.q_len), i = static_cast<int>(token - static_cast<int64_t>(r) * p.q_len);
+  const SparseLen len = sparse_len(p.seq, r, p.bt_stride, p.B);
+  const int64_t seen = sparse_seen(len, i, p.q_len);
+  const uint32_t B = static_cast<uint32_t>(p.B);
+  const uint32_t pages = (static_cast<uint32_t>(seen) + B - 1) / B;
+  const int32_t* table = p.bt + static_cast<int64_t>(r) * p.bt_stride;
+  int32_t* selected = p.selected + token * p.sel_stride;
+  int32_t* columns = p.columns != nullptr ? p.columns + token * p.sel_stride : nullptr;
+  if (tid == 0 && i == 0) set_flag(p.err, len.bad);
+  if (pages <= p.keep) {
+    for (int64_t c = tid; c < p.keep; c += kThreads) {
+      selected[c] = c < pages ? table[c] : -1;
+      if (columns != nullptr) columns[c] = c < pages ? static_cast<int32_t>(c) : -1;
+    }
+    if (tid == 0) p.lens[token] = static_cast<int32_t>(seen);
+    return;
+  }
+  // pages [lo, hi) compete for `need` places
+  const uint32_t lo = static_cast<uint32_t>(p.first), hi = pages - static_cast<uint32_t>(p.last);
+  const uint32_t need = static_cast<uint32_t>(p.keep) - p.first - p.last;
+  const float* scores = p.scores + token * p.s_stride;
+  for (uint32_t c = lo + tid; c < min(hi, static_cast<uint32_t>(kHeld)); c += kThreads) held[c] = score_key(scores[c]);
+  auto key = [&](uint32_t c) { return c < kHeld ? held[c] : score_key(scores[c]); };
+  uint32_t prefix = 0, rest = need;  // digits so far of the need-th largest; how many of its like are wanted
+  if (need > 0) {
+#pragma unroll 1
+    for (int shift = 24; shift >= 0; shift -= 8) {
+      counts[tid] = 0;
+      __syncthreads();
+      const uint32_t above = shift == 24 ? 0 : 0xffffffffu << (shift + 8);
+      for (uint32_t c = lo + tid; c < hi; c += kThreads) {
+        const uint32_t k = key(c);
+        if ((k & above) == prefix) atomicAdd(&counts[k >> shift & 255], 1u);
+      }
+      __syncthreads();
+      // the largest digit at or above which there are `rest`: a thread holds digit 255 - tid
+      int64_t total;
+      const uint32_t mine = counts[255 - tid];
+      const uint32_t before = static_cast<uint32_t>(block_scan<int64_t>(mine, scratch, total));
+      if (before < rest && rest <= before + mine) {
+        digit = 255 - tid;
+        left = rest - before;
+      }
+      __syncthreads();
+      prefix |= digit << shift;
+      rest = left;
+    }
+  }
+  __syncthreads();
+  // a run of columns a thread: those that stay for sure, and those equal to the border of which `rest` stay
+  const uint32_t run = (pages + kThreads - 1) / kThreads, c0 = min(pages, tid * run), c1 = min(pages, c0 + run);
+  uint32_t sure = 0, equal = 0;
+  auto competes = [&](uint32_t c) { return c >= lo && c < hi; };
+  for (uint32_t c = c0; c < c1; ++c) {
+    if (!competes(c)) ++sure;
+    else if (need > 0) {
+      const uint32_t k = key(c);
+      sure += k > prefix;
+      equal += k == prefix;
+    }
+  }
+  int64_t total;
+  const int64_t before = block_scan<int64_t>(static_cast<int64_t>(equal) << 32 | sure, scratch, total);
+  uint32_t equals = static_cast<uint32_t>(before >> 32);
+  int64_t at = static_cast<int64_t>(before & 0xffffffff) + min(equals, rest);
+  for (uint32_t c = c0; c < c1; ++c) {
+    bool stays = !competes(c);
+    if (!stays && need > 0) {
+      const uint32_t k = key(c);
+      stays = k > prefix || (k == prefix && equals++ < rest);
+    }
+    if (stays) {
+      selected[at] = table[c];
+      if (columns != nullptr) columns[at] = static_cast<int32_t>(c);
+      ++at;
+    }
+  }
+  if (tid == 0) p.lens[token] = static_cast<int32_t>(seen - static_cast<int64_t>(pages - static_cast<uint32_t>(p.keep)) * B);
+}
+
+}  // namespace
+}  // namespace pmg_mla
+
+extern "C" int pmg_select_blocks(const float* scores, int64_t score_stride, const int32_t* block_table,
+                                 int64_t block_table_stride, const int32_t* seq_lens, int32_t num_reqs, int32_t q_len,
+                                 int32_t block_size, int32_t* selected, int64_t selected_stride, int32_t* columns,
+                                 int32_t* selected_lens, int64_t keep, int32_t first, int32_t last, int32_t* error_flag,
+                                 void* stream) {
+  using namespace pmg_mla;
+  if (num_reqs < 0 || q_len < 0 || block_size < 1 || block_table_stride < 0 || first < 0 || last < 1 ||
+      static_cast<int64_t>(first) + last > keep || selected_stride < keep || score_stride < block_table_stride ||
+      !stride_ok(score_stride) || !stride_ok(selected_stride))
+    return PMG_ERR_ARG;
+  if (block_table_stride > INT32_MAX || num_reqs > PMG_MAX_REQS || static_cast<int64_t>(num_reqs) * q_len > INT32_MAX ||
+      keep > INT32_MAX)
+    return PMG_ERR_UNSUPPORTED;
+  if (num_reqs == 0 || q_len == 0) return PMG_OK;
+  if (seq_lens == nullptr || selected == nullptr || selected_lens == nullptr ||
+      ((scores == nullptr || block_table == nullptr) && block_table_stride > 0))
+    return PMG_ERR_NULL;
+  if (!aligned(scores, 4) || !aligned(block_table, 4) || !aligned(seq_lens, 4) || !aligned(selected, 4) ||
+      !aligned(columns, 4) || !aligned(selected_lens, 4) || !aligned(error_flag, 4))
+    return PMG_ERR_ALIGN;
+  SelectParams p{};
+  p.scores = scores;
+  p.s_stride = score_stride;
+  p.bt = block_table;
+  p.bt_stride = block_table_stride;
+  p.seq = seq_lens;
+  p.q_len = q_len;
+  p.B = block_size;
+  p.selected = selected;
+  p.sel_stride = selected_stride;
+  p.columns = columns;
+  p.lens = selected_lens;
+  p.keep = keep;
+  p.first = first;
+  p.last = last;
+  p.err = error_flag;
+  return launch(select_kernel, dim3(static_cast<unsigned>(num_reqs) * q_len), kThreads, 0, stream, p);
+}

@@ -1,0 +1,20 @@
+// Absorbed latent attention on the tensor core: groups of requests over their
+// prefixes (the kernel of mla_decode_tc_kernel.cuh, as a prefix pass).
+#include "mla_decode_tc.cuh"
+#include "mla_decode_tc_kernel.cuh"
+
+namespace pmg_mla {
+
+int prefix_tc(DecodeParams& p, int q_dtype, int cache_dtype, int sms, void* stream) {
+  const int64_t rows = static_cast<int64_t>(p.reqs) * p.q_len * p.H;
+  // whole tokens in a row tile, where that leaves at most an eighth of it empty: its queries are then one box of the copy
+  // engine (an e4m3 cache's are converted by the softmax warps anyhow)
+  const int whole = p.H <= 64 ? 64 / p.H * p.H : 64;
+  const int tile = cache_dtype != PMG_FP8_E4M3 && whole >= 56 ? whole : 64;
+  p.rows_per_group = static_cast<int32_t>(std::min<int64_t>(rows, tile));
+  p.groups = 1;
+  p.units = sms;
+  return launch_tc<true>(p, q_dtype, cache_dtype, stream);
+}
+
+}  // namespace pmg_mla
