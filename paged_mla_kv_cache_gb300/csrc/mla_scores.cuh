@@ -27,14 +27,16 @@ struct ScoreParams {
 };
 
 // Columns of a request of which some token sees an entry, and pieces of work of
-// kScoreTile columns; one more writes the columns behind them.
+// kScoreTile columns. Whoever has the last piece writes the columns behind them;
+// a request without any has a piece for that.
 constexpr int kScoreTile = 64;
 __device__ __forceinline__ int64_t score_pages(const ScoreParams& p, const SparseLen& l) {
   const uint32_t n = static_cast<uint32_t>(sparse_seen(l, p.q_len - 1, p.q_len)), b = static_cast<uint32_t>(p.B);
   return (n + b - 1) / b;
 }
+__device__ __forceinline__ int64_t score_tiles(int64_t pages) { return (pages + kScoreTile - 1) / kScoreTile; }
 __device__ __forceinline__ int64_t score_pieces(const ScoreParams& p, int r) {
-  return (score_pages(p, sparse_len(p.seq, r, p.bt_stride, p.B)) + kScoreTile - 1) / kScoreTile + 1;
+  return max(score_tiles(score_pages(p, sparse_len(p.seq, r, p.bt_stride, p.B))), static_cast<int64_t>(1));
 }
 
 __device__ __forceinline__ float score_shift(const ScoreParams& p, int64_t row) {

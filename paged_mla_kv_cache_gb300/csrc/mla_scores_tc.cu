@@ -16,8 +16,8 @@
 // asked for as soon as the last product with the one in its place is done, five
 // steps (pieces) before it is multiplied.
 //
-// Roles: warps 0-3 load, split and take the largest over the heads; warp 4
-// issues products. The flat list of tiles of all requests is cut into equal
+// Roles: warps 0-7 load and split, warps 8-11 take the largest over the heads,
+// warp 12 issues products. The flat list of tiles of all requests is cut into equal
 // shares, a CTA each.
 #include <algorithm>
 
@@ -27,16 +27,24 @@
 namespace pmg_mla {
 namespace {
 
-constexpr int kThreads = 160;
-constexpr int kLoaders = 128;
+constexpr int kLoaders = 256, kReaders = 128;
+constexpr int kThreads = kLoaders + kReaders + 32;
+constexpr int kLoadWarps = kLoaders / 32, kIssuer = kThreads / 32 - 1;
 constexpr int kEntry = 576;
 constexpr int kPieces = kEntry / 64;        // of 128 bytes
 constexpr int kPiece = kScoreTile * 128;    // 64 pages of one piece
-constexpr int kStages = 4;                  // of queries
-constexpr int kLead = kPieces - kStages;    // steps between a piece's copy and its product
+constexpr int kTurn = 3;                    // steps between a load of queries and their split: pieces come in turns of so many
+static_assert(kPieces % kTurn == 0, "whole turns");
+constexpr int kHalfway = 5;
 
 template <int N>
 struct Lay {
+  static constexpr int kStages = N == 128 ? 2 : 4;  // of queries: 64 KB
+  static constexpr int kLead = kPieces - kStages;   // steps between a piece's copy and its product
+  // Accumulators of a row and page: hi and lo, and of each the first kHalfway pieces and the others, as far as tensor
+  // memory reaches twice. The tensor core cuts a sum at every addition, and all of these have one sign: one sum of 72
+  // additions was off by 1.2e-6 of the score, four of 16 or 20 by 3e-7.
+  static constexpr int kSums = N == 128 ? 2 : 4;
   static constexpr int kStage = 2 * N * 128;
   static constexpr int kStageAt = 2 * kPieces * kPiece;
   static constexpr int kBytes = kStageAt + kStages * kStage + 1024;
@@ -44,8 +52,9 @@ struct Lay {
 };
 
 struct Misc {
-  uint64_t full[kStages], empty[kStages], s_full[2], s_free[2], end;
+  uint64_t page_full[kPieces], full[4], empty[4], s_full[2], s_free[2], end;
   int64_t scratch[33], found[2];
+  float shift[kReaders / 32][128];  // of a chunk's rows, each reading warp's own
   uint32_t tmem;
   int32_t stop, never;
 };
@@ -70,10 +79,10 @@ struct Tiles {
       ++r;
       len = sparse_len(p->seq, r, p->bt_stride, p->B);
       pages = score_pages(*p, len);
-      const int64_t pieces = (pages + kScoreTile - 1) / kScoreTile + 1;
-      const int64_t n = min(pieces - skip, end - at);
+      const int64_t tiles = score_tiles(pages);
+      const int64_t n = min(max(tiles, static_cast<int64_t>(1)) - skip, end - at);
       tile = skip;
-      last = min(skip + n, pieces - 1);
+      last = min(skip + n, tiles);
       at += n;
       skip = 0;
     } while (tile >= last);
@@ -88,15 +97,17 @@ __device__ __forceinline__ void copy16(uint32_t dst, const void* src, bool there
 template <class T, int N>
 __global__ void __launch_bounds__(kThreads, 1) scores_tc_kernel(const __grid_constant__ ScoreParams p) {
   using L = Lay<N>;
+  constexpr int kStages = L::kStages, kLead = L::kLead, kSums = L::kSums;
   extern __shared__ uint8_t raw[];
   __shared__ Misc mi;
   uint8_t* smem = raw + ((1024 - (smem_u32(raw) & 1023)) & 1023);
   const uint32_t base = smem_u32(smem);
   const int tid = threadIdx.x, warp = __shfl_sync(0xffffffffu, tid >> 5, 0), lane = tid & 31;
-  constexpr int kColumns = 2 * N < 32 ? 32 : 2 * N;
+  constexpr int kColumns = 2 * kSums * N;
   if (tid == 0) {
+    for (int i = 0; i < kPieces; ++i) mbar_init(smem_u32(&mi.page_full[i]), kLoaders);
     for (int i = 0; i < kStages; ++i) {
-      mbar_init(smem_u32(&mi.full[i]), 4);
+      mbar_init(smem_u32(&mi.full[i]), kLoadWarps);
       mbar_init(smem_u32(&mi.empty[i]), 1);
     }
     for (int i = 0; i < 2; ++i) {
@@ -107,7 +118,7 @@ __global__ void __launch_bounds__(kThreads, 1) scores_tc_kernel(const __grid_con
     mi.stop = mi.never = 0;
     mbar_fence_init();
   }
-  if (warp == 4) tmem_alloc(smem_u32(&mi.tmem), kColumns);
+  if (warp == kIssuer) tmem_alloc(smem_u32(&mi.tmem), kColumns);
   pdl_entry();
   const Share share = find_share([&](int r) { return score_pieces(p, r); }, p.R, blockIdx.x, p.units, mi.scratch, mi.found);
   tmem_fence_before();
@@ -118,21 +129,24 @@ __global__ void __launch_bounds__(kThreads, 1) scores_tc_kernel(const __grid_con
   const uint32_t s_full = smem_u32(&mi.s_full[0]), s_free = smem_u32(&mi.s_free[0]);
   const int rows = p.q_len * p.H, chunks = (rows + N - 1) / N;
 
-  if (warp == 4) {
+  if (warp == kIssuer) {
     // ---- products ----
     constexpr int kFmt = std::is_same<T, bf16>::value ? 1 : 0;
     constexpr uint32_t kIdesc = umma_idesc(kFmt, kFmt, 0, 0, kScoreTile, N);
     Tiles it(p, share);
-    uint32_t step = 0, chunk = 0;
-    while (it.next()) {
+    uint32_t step = 0, chunk = 0, tile = 0;
+    for (; it.next(); ++tile) {
 #pragma unroll 1
       for (int c = 0; c < chunks; ++c, ++chunk) {
-        const uint32_t buf = chunk & 1, d = tmem + buf * N;
+        const uint32_t buf = chunk & 1, d = tmem + buf * (kSums * N);
         if (chunk >= 2) mbar_wait(s_free + 8 * buf, ((chunk >> 1) + 1) & 1, stop);
 #pragma unroll 1
         for (int k = 0; k < kPieces; ++k, ++step) {
           const uint32_t stage = step % kStages;
+          if (c == 0) mbar_wait(smem_u32(&mi.page_full[k]), tile & 1, stop);
           mbar_wait(full + 8 * stage, step / kStages & 1, stop);
+          fence_async_smem();  // (the barriers order the loading warps' writes before it)
+          __syncwarp();
           tmem_fence_after();
           if (elect_one()) {
 #pragma unroll
@@ -140,7 +154,9 @@ __global__ void __launch_bounds__(kThreads, 1) scores_tc_kernel(const __grid_con
               const uint64_t a = umma_desc(base + (2 * k + half) * kPiece, 16, 1024);
               const uint64_t b = umma_desc(base + L::kStageAt + stage * L::kStage + half * (N * 128), 16, 1024);
 #pragma unroll
-              for (int x = 0; x < 4; ++x) umma_ss<false>(d, a + 2 * x, b + 2 * x, kIdesc, k > 0 || half > 0 || x > 0);
+              for (int x = 0; x < 4; ++x)
+                umma_ss<false>(d + (half + (kSums == 2 || k < kHalfway ? 0 : 2)) * N, a + 2 * x, b + 2 * x, kIdesc,
+                               (k > 0 && (kSums == 2 || k != kHalfway)) || x > 0);
             }
             umma_commit(empty + 8 * stage);
             if (k + 1 == kPieces) umma_commit(s_full + 8 * buf);
@@ -152,21 +168,20 @@ __global__ void __launch_bounds__(kThreads, 1) scores_tc_kernel(const __grid_con
     if (elect_one()) umma_commit(smem_u32(&mi.end));
     __syncwarp();
     mbar_wait(smem_u32(&mi.end), 0, smem_u32(&mi.never));
-  } else {
-    // ---- loads, and the largest over the heads ----
-    const float factor = p.sm_scale * (p.scale != nullptr ? *p.scale : 1.0f);
-    const int unit = tid & 7, row0 = tid >> 3;  // a 16-byte unit of every 16th row of a piece
-    int bad = 0;
+  } else if (warp < kLoadWarps) {
+    // ---- loads ----
+    const int unit = tid & 7, row0 = tid >> 3;  // a 16-byte unit of every kApart-th row of a piece
     // bounds: of the tile `ahead`, whose pages this thread knows
+    constexpr int kApart = kLoaders / 8, kPageRows = kScoreTile / kApart;
     Tiles ahead(p, share);
-    const T* page[4];
-    bool there[4];
+    const T* page[kPageRows];
+    bool there[kPageRows];
     auto look = [&]() {
       const bool more = ahead.next();
       const int32_t* table = p.bt + static_cast<int64_t>(more ? ahead.r : 0) * p.bt_stride;
 #pragma unroll
-      for (int k = 0; k < 4; ++k) {
-        const int64_t c = ahead.tile * kScoreTile + row0 + 16 * k;
+      for (int k = 0; k < kPageRows; ++k) {
+        const int64_t c = ahead.tile * kScoreTile + row0 + kApart * k;
         const int32_t id = more && c < ahead.pages ? table[c] : -1;
         there[k] = id >= 0 && id < p.num_blocks;
         page[k] = reinterpret_cast<const T*>(p.bounds) + (there[k] ? id : 0) * p.bb_stride + unit * 8;
@@ -175,151 +190,185 @@ __global__ void __launch_bounds__(kThreads, 1) scores_tc_kernel(const __grid_con
     };
     auto copy = [&](int piece) {
 #pragma unroll
-      for (int k = 0; k < 4; ++k) {
-        const int row = row0 + 16 * k;
+      for (int k = 0; k < kPageRows; ++k) {
+        const int row = row0 + kApart * k;
         const uint32_t dst = base + 2 * piece * kPiece + row * 128 + ((unit ^ (row & 7)) << 4);
         copy16(dst, page[k] + piece * 64, there[k]);
         copy16(dst + kPiece, page[k] + p.br_stride + piece * 64, there[k]);
       }
+      // arrives when this thread's copies have
+      asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" ::"r"(smem_u32(&mi.page_full[piece])) : "memory");
     };
-    auto commit = [] { asm volatile("cp.async.commit_group;" ::: "memory"); };
     bool ahead_more = look();
-    for (int k = 0; k < kLead; ++k) {
+    for (int k = 0; k < kLead; ++k)
       if (ahead_more) copy(k);
-      commit();
+    // queries: units of 16 bytes of this thread's rows of a chunk, kTurn steps ahead
+    constexpr int kRows = N < kApart ? 1 : N / kApart;
+    const bool splits = N >= kApart || row0 < N;
+    uint4 x[kTurn][kRows];
+    const T* rows_at[kRows];  // of the chunk whose queries are loaded, or NULL
+    auto begin = [&](int r, int c) {
+#pragma unroll
+      for (int i = 0; i < kRows; ++i) {
+        const int rr = c * N + row0 + kApart * i;
+        rows_at[i] = splits && rr < rows ? reinterpret_cast<const T*>(p.q) + r * p.qr_stride + (rr / p.H) * p.qt_stride +
+                                     (rr % p.H) * p.qh_stride + unit * 8
+                               : nullptr;
+      }
+    };
+    auto load = [&](uint4 (&y)[kRows], int k) {
+#pragma unroll
+      for (int i = 0; i < kRows; ++i)
+        y[i] = rows_at[i] != nullptr ? *reinterpret_cast<const uint4*>(rows_at[i] + k * 64) : make_uint4(0, 0, 0, 0);
+    };
+    Tiles next(p, share);  // the tile after the one that is filled
+    bool more = next.next();
+    int r = next.r;  // request of the tile that is filled
+    bool next_more = more && next.next();
+    uint32_t step = 0;
+    if (more) {
+      begin(r, 0);
+#pragma unroll
+      for (int k = 0; k < kTurn; ++k) load(x[k], k);
     }
-    // queries: units of 16 bytes of this thread's rows of a chunk
-    constexpr int kRows = N / 16;
-    uint4 x[kRows];
-    auto load = [&](int r, int c, int k) {
-#pragma unroll
-      for (int y = 0; y < kRows; ++y) {
-        const int rr = c * N + row0 + 16 * y;
-        x[y] = make_uint4(0, 0, 0, 0);
-        if (rr < rows)
-          x[y] = *reinterpret_cast<const uint4*>(reinterpret_cast<const T*>(p.q) + r * p.qr_stride + (rr / p.H) * p.qt_stride +
-                                                 (rr % p.H) * p.qh_stride + k * 64 + unit * 8);
-      }
-    };
-    // the largest bound so far of this lane's page for the token of the current row
-    float best = -INFINITY;
-    int token = 0, head = 0;
-    Tiles now(p, share), then(p, share);  // the tile that is filled, and the one whose products are read
-    bool more = now.next();
-    then.next();
-    int then_c = 0;
-    uint32_t step = 0, chunk = 0, read = 0;
-    auto reduce = [&]() {
-      const uint32_t buf = read & 1;
-      mbar_wait(s_full + 8 * buf, read >> 1 & 1, stop);
-      __syncwarp();
-      tmem_fence_after();
-      const bool lost = stopped(stop);
-      const int64_t c = then.tile * kScoreTile + warp * 16 + lane;  // the page of this lane (of the first 16)
-      const bool in = lane < 16 && c < then.pages;
-      const int32_t id = in ? p.bt[static_cast<int64_t>(then.r) * p.bt_stride + c] : -1;
-      const bool good = id >= 0 && id < p.num_blocks;
-      if (in && !good) bad |= PMG_FLAG_PHYS_BLOCK;
-      const int64_t first = static_cast<int64_t>(then.r) * rows;
-#pragma unroll 1
-      for (int h = 0; h < N; h += 16) {
-        uint32_t s[16];
-        tmem_ld16(tmem + buf * N + h + (static_cast<uint32_t>(warp * 32) << 16), s);
-        tmem_wait_ld();
-        tmem_pin<16>(s);
-#pragma unroll
-        for (int k = 0; k < 16; ++k) {
-          const int rr = then_c * N + h + k;
-          if (rr < rows) {
-            best = max_nan(best, __uint_as_float(s[k]) * factor - score_shift(p, first + rr));
-            if (++head == p.H) {
-              const bool seen = c * p.B < sparse_seen(then.len, token, p.q_len);
-              if (in)
-                p.scores[(static_cast<int64_t>(then.r) * p.q_len + token) * p.s_stride + c] =
-                    lost ? __uint_as_float(0x7fffffffu) : good && seen ? best : -INFINITY;
-              best = -INFINITY;
-              head = 0;
-              ++token;
-            }
-          }
-        }
-      }
-      tmem_fence_before();
-      __syncwarp();
-      if (lane == 0) mbar_arrive(s_free + 8 * buf);
-      ++read;
-      if (++then_c == chunks) {
-        then_c = 0;
-        token = 0;
-        then.next();
-      }
-    };
-    if (more) load(now.r, 0, 0);
     int drop = kLead;  // the next piece of `ahead` to be copied
     while (more) {
 #pragma unroll 1
-      for (int c = 0; c < chunks; ++c, ++chunk) {
+      for (int c = 0; c < chunks; ++c) {
 #pragma unroll 1
-        for (int k = 0; k < kPieces; ++k, ++step) {
-          const uint32_t stage = step % kStages;
-          if (step >= kStages) mbar_wait(empty + 8 * stage, (step / kStages + 1) & 1, stop);
-          // the piece that was multiplied kStages steps ago makes room in a tile's last chunk (the first tile's rest
-          // has room from the start)
-          const bool last_chunk = k >= kStages ? c + 1 == chunks : c == 0;
-          if (last_chunk) {
-            if (drop == kPieces) {
-              drop = 0;
-              ahead_more = look();
-            }
-            if (ahead_more) copy(drop);
-            ++drop;
-          }
-          commit();
-          // queries by sign
-          uint8_t* at = smem + L::kStageAt + stage * L::kStage;
+        for (int k0 = 0; k0 < kPieces; k0 += kTurn) {
 #pragma unroll
-          for (int y = 0; y < kRows; ++y) {
-            const int row = row0 + 16 * y;
-            uint4 up, down;
-            const uint32_t w[4] = {x[y].x, x[y].y, x[y].z, x[y].w};
-            uint32_t u[4], d[4];
-#pragma unroll
-            for (int j = 0; j < 4; ++j) {
-              const uint32_t below = (w[j] >> 15 & 0x00010001u) * 0xffffu;
-              u[j] = w[j] & ~below;
-              d[j] = w[j] & below;
+          for (int turn = 0; turn < kTurn; ++turn, ++step) {
+            const int k = k0 + turn;
+            const uint32_t stage = step % kStages;
+            if (step >= kStages) mbar_wait(empty + 8 * stage, (step / kStages + 1) & 1, stop);
+            // the piece that was multiplied kStages steps ago makes room in a tile's last chunk (the first tile's rest
+            // has room from the start)
+            if (k >= kStages ? c + 1 == chunks : c == 0) {
+              if (drop == kPieces) {
+                drop = 0;
+                ahead_more = look();
+              }
+              if (ahead_more) copy(drop);
+              ++drop;
             }
-            up = make_uint4(u[0], u[1], u[2], u[3]);
-            down = make_uint4(d[0], d[1], d[2], d[3]);
-            const int place = row * 128 + ((unit ^ (row & 7)) << 4);
-            *reinterpret_cast<uint4*>(at + place) = up;
-            *reinterpret_cast<uint4*>(at + N * 128 + place) = down;
+            // queries by sign
+            uint8_t* at = smem + L::kStageAt + stage * L::kStage;
+#pragma unroll
+            for (int y = 0; y < kRows; ++y) {
+              const int row = row0 + kApart * y;
+              const uint32_t w[4] = {x[turn][y].x, x[turn][y].y, x[turn][y].z, x[turn][y].w};
+              uint32_t u[4], d[4];
+#pragma unroll
+              for (int j = 0; j < 4; ++j) {
+                const uint32_t below = (w[j] >> 15 & 0x00010001u) * 0xffffu;
+                u[j] = w[j] & ~below;
+                d[j] = w[j] & below;
+              }
+              const int place = row * 128 + ((unit ^ (row & 7)) << 4);
+              if (splits) {
+                *reinterpret_cast<uint4*>(at + place) = make_uint4(u[0], u[1], u[2], u[3]);
+                *reinterpret_cast<uint4*>(at + N * 128 + place) = make_uint4(d[0], d[1], d[2], d[3]);
+              }
+            }
+            // the queries of the step kTurn further on their way
+            if (k + kTurn < kPieces) {
+              load(x[turn], k + kTurn);
+            } else if (c + 1 < chunks || next_more) {
+              if (k + kTurn == kPieces) begin(c + 1 < chunks ? r : next.r, c + 1 < chunks ? c + 1 : 0);
+              load(x[turn], k + kTurn - kPieces);
+            }
+            __syncwarp();
+            if (lane == 0) mbar_arrive(full + 8 * stage);
           }
-          // the next step's queries on their way
-          if (k + 1 < kPieces) load(now.r, c, k + 1);
-          else if (c + 1 < chunks) load(now.r, c + 1, 0);
-          asm volatile("cp.async.wait_group %0;" ::"n"(kLead) : "memory");
-          fence_async_smem();
-          __syncwarp();
-          if (lane == 0) mbar_arrive(full + 8 * stage);
         }
-        if (chunk > 0) reduce();
       }
-      more = now.next();
-      if (more) load(now.r, 0, 0);
+      more = next_more;
+      r = next.r;
+      if (more) next_more = next.next();
     }
-    if (chunk > 0) reduce();
     asm volatile("cp.async.wait_all;" ::: "memory");
+  } else {
+    // ---- the largest over the heads ----
+    const float factor = p.sm_scale * (p.scale != nullptr ? *p.scale : 1.0f);
+    const int part = warp - kLoadWarps;  // of the lanes
+    int bad = 0;
+    uint32_t chunk = 0;
+    for (Tiles it(p, share); it.next();) {
+      const int64_t c = it.tile * kScoreTile + part * 16 + lane;  // the page of this lane (of the first 16)
+      const bool in = lane < 16 && c < it.pages;
+      const int32_t id = in ? p.bt[static_cast<int64_t>(it.r) * p.bt_stride + c] : -1;
+      const bool good = id >= 0 && id < p.num_blocks;
+      if (in && !good) bad |= PMG_FLAG_PHYS_BLOCK;
+      const int64_t first = static_cast<int64_t>(it.r) * rows, place = c * p.B;
+      float* out = p.scores + static_cast<int64_t>(it.r) * p.q_len * p.s_stride + c;
+      float best = -INFINITY;  // of the heads so far of the token at hand
+      int token = 0, head = 0;
+      auto done = [&]() {
+        const bool seen = place < sparse_seen(it.len, token, p.q_len);
+        const bool lost = stopped(stop);  // (by all lanes)
+        if (in) *out = lost ? __uint_as_float(0x7fffffffu) : good && seen ? best : -INFINITY;
+        out += p.s_stride;
+        best = -INFINITY;
+        head = 0;
+        ++token;
+      };
+#pragma unroll 1
+      for (int row = 0; row < rows; row += N, ++chunk) {
+        const uint32_t buf = chunk & 1;
+        for (int k = lane; k < N; k += 32) mi.shift[part][k] = row + k < rows ? score_shift(p, first + row + k) : 0.0f;
+        mbar_wait(s_full + 8 * buf, chunk >> 1 & 1, stop);
+        __syncwarp();
+        tmem_fence_after();
+#pragma unroll 1
+        for (int h = 0; h < N; h += 16) {
+          uint32_t s[kSums][16];
+#pragma unroll
+          for (int k = 0; k < kSums; ++k)
+            tmem_ld16(tmem + (buf * kSums + k) * N + h + (static_cast<uint32_t>(part * 32) << 16), s[k]);
+          const int left = rows - row - h;
+          tmem_wait_ld();
+#pragma unroll
+          for (int k = 0; k < kSums; ++k) tmem_pin<16>(s[k]);
+          float x[16];
+#pragma unroll
+          for (int k = 0; k < 16; ++k) {
+            float sum = __uint_as_float(s[0][k]) + __uint_as_float(s[1][k]);
+            if constexpr (kSums == 4) sum += __uint_as_float(s[2][k]) + __uint_as_float(s[3][k]);
+            x[k] = sum * factor - mi.shift[part][h + k];
+          }
+          if (left >= 16 && head + 16 <= p.H) {  // one token's
+#pragma unroll
+            for (int o = 8; o > 0; o >>= 1)
+#pragma unroll
+              for (int k = 0; k < o; ++k) x[k] = max_nan(x[k], x[k + o]);
+            best = max_nan(best, x[0]);
+            head += 16;
+            if (head == p.H) done();
+          } else {
+#pragma unroll
+            for (int k = 0; k < 16; ++k)
+              if (k < left) {
+                best = max_nan(best, x[k]);
+                if (++head == p.H) done();
+              }
+          }
+        }
+        tmem_fence_before();
+        __syncwarp();  // (the shifts are read too)
+        if (lane == 0) mbar_arrive(s_free + 8 * buf);
+      }
+    }
     // columns that no token sees anything of, and what is wrong with a length: with a request's last piece
     int64_t at = share.begin, skip = share.offset;
     for (int r = share.item; at < share.end; ++r, skip = 0) {
       const SparseLen len = sparse_len(p.seq, r, p.bt_stride, p.B);
-      const int64_t pages = score_pages(p, len), pieces = (pages + kScoreTile - 1) / kScoreTile + 1;
+      const int64_t pages = score_pages(p, len), pieces = max(score_tiles(pages), static_cast<int64_t>(1));
       const int64_t n = min(pieces - skip, share.end - at);
       at += n;
       if (skip + n == pieces) {
         bad |= len.bad;
-        score_rest(p, r, pages, tid, kLoaders);
+        score_rest(p, r, pages, tid - kLoaders, kReaders);
       }
     }
     if (stopped(stop)) bad |= PMG_FLAG_TIMEOUT;
@@ -328,7 +377,7 @@ __global__ void __launch_bounds__(kThreads, 1) scores_tc_kernel(const __grid_con
   tmem_fence_before();
   __syncthreads();
   tmem_fence_after();
-  if (warp == 4) tmem_free(tmem, kColumns);
+  if (warp == kIssuer) tmem_free(tmem, kColumns);
 }
 
 template <class T, int N>
@@ -341,7 +390,8 @@ int run(const ScoreParams& p, void* stream) {
 template <class T>
 int run(const ScoreParams& p, void* stream) {
   const int rows = p.q_len * p.H;
-  return rows <= 16 ? run<T, 16>(p, stream) : rows <= 32 ? run<T, 32>(p, stream) : run<T, 64>(p, stream);
+  return rows <= 16 ? run<T, 16>(p, stream) : rows <= 32 ? run<T, 32>(p, stream)
+         : rows <= 64 ? run<T, 64>(p, stream) : run<T, 128>(p, stream);
 }
 
 }  // namespace
