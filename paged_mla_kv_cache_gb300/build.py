@@ -13,7 +13,7 @@ import subprocess
 
 UNITS = ["mla_plan.cu", "mla_append.cu", "mla_decode.cu", "mla_decode_tc.cu", "mla_prefill.cu",
          "mla_prefill_tc.cu", "mla_bounds.cu", "mla_scores.cu", "mla_scores_tc.cu", "mla_select.cu", "mla_shared.cu",
-         "mla_shared_tc.cu", "mla_packed.cu"]
+         "mla_shared_tc.cu", "mla_shared_pair.cu", "mla_packed.cu"]
 PKG_DIR = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(PKG_DIR)
 CSRC = os.path.join(PKG_DIR, "csrc")

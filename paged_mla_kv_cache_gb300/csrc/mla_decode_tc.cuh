@@ -13,4 +13,8 @@ bool decode_tc_takes(const DecodeParams& p, int q_dtype, int cache_dtype);
 int decode_tc(DecodeParams& p, int q_dtype, int cache_dtype, int sms, void* stream);
 int prefix_tc(DecodeParams& p, int q_dtype, int cache_dtype, int sms, void* stream);
 
+// A prefix pass on pairs of SMs (mla_shared_pair.cu), where prefix_tc would do as well.
+bool prefix_pair_takes(const DecodeParams& p, int q_dtype, int cache_dtype);
+int prefix_pair(DecodeParams& p, int q_dtype, int sms, void* stream);
+
 }  // namespace pmg_mla

@@ -6,6 +6,7 @@
 namespace pmg_mla {
 
 int prefix_tc(DecodeParams& p, int q_dtype, int cache_dtype, int sms, void* stream) {
+  if (prefix_pair_takes(p, q_dtype, cache_dtype)) return prefix_pair(p, q_dtype, sms, stream);
   const int64_t rows = static_cast<int64_t>(p.reqs) * p.q_len * p.H;
   // whole tokens in a row tile, where that leaves at most an eighth of it empty: its queries are then one box of the copy
   // engine (an e4m3 cache's are converted by the softmax warps anyhow)
