@@ -20,8 +20,9 @@
 // a row of tensor memory: lanes 0-63 have the entries or values of the first
 // CTA's half, lanes 64-127 those of the second's, so two threads share a row.
 //
-// Roles in each CTA: warp 4 loads, warp 5 of the pair's first CTA issues all
-// products, warps 5 and 6 of the second tell it what has arrived there, warps 0-3
+// Roles in each CTA: warps 4 and 7 load, entries for S and for O (as one warp, the
+// entries for S waited until the place for O before them was free), warp 5 of the
+// pair's first CTA issues all products, warps 5 and 6 of the second tell it what has arrived there, warps 0-3
 // do the softmax and the epilogue of their CTA's rows. All waits are bounded; a CTA
 // whose wait ran out stops its pair, and the rows of all work that either did not
 // finish before become NaN.
@@ -35,7 +36,7 @@
 namespace pmg_mla {
 namespace {
 
-constexpr int kThreads = 224;
+constexpr int kThreads = 256;
 constexpr int kSoft = 128;
 constexpr int kLatent = 512, kRope = 64, kEntry = kLatent + kRope;
 constexpr int kRows = 64;                  // of a CTA
@@ -185,8 +186,9 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
   PrefixItems<kItemCost> it(p, share);
   auto wait = [&](uint32_t bar, uint32_t parity) { pair_wait(bar, parity, stop, peer); };
 
-  if (warp == 4) {
+  if (warp == 4 || warp == 7) {
     // ---- loads ----
+    const bool for_s = warp == 4;
     uint32_t t = 0, items = 0;
     int bad = 0;
     bool alive = true;
@@ -215,85 +217,85 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
         }
         const uint32_t goods = __ballot_sync(0xffffffffu, in && good);
         const int n_boxes = __popc(__ballot_sync(0xffffffffu, in)), n_mine = max(0, min(half, n_boxes - mine));
-        uint64_t mask = 0;  // entries that exist
-        for (int s = 0; s < segs; ++s)
-          if (goods >> s & 1) mask |= ((1ull << box_rows) - 1) << (s * box_rows);
-        const int left = it.len - (it.tile + i) * kDecodeTile;
-        if (left < 64) mask &= (1ull << left) - 1;
         if (stopped(stop)) {
           alive = false;
           break;
         }
-        if (i == 0) {  // the row tile's queries, once the products with the ones before are done
-          if (items > 0) wait(smem_u32(&mi.q_empty), (items - 1) & 1);
-          ++items;
-          if (elect_one()) {
-            const int64_t r0 = it.row0 + static_cast<int64_t>(rank) * rpc;
-            const int token = static_cast<int>(r0 / p.H);
-            const uint32_t bar = smem_u32(&mi.q_full);
-            mbar_expect(bar, static_cast<uint32_t>(rpc) * kEntry * 2);
-#pragma unroll 1
-            for (int c = 0; c < 9; ++c)
-              tma_load_4d(base + kQAt + c * kQPiece, &q_map, bar, 64 * c, static_cast<int>(r0 % p.H), token % p.q_tma, token / p.q_tma);
-          }
-          __syncwarp();
-        }
         const uint32_t k_at = base + kStageAt + stage * kStage, v_at = k_at + kK;
-        wait(k_empty + 8 * stage, parity);
-        if (elect_one()) {
-          // The mask has barriers of its own, four of them: those of the entries may be a phase ahead of the softmax warps,
-          // which then wait in vain. A tile's entries are loaded when the scores two tiles before are done, and those when
-          // the softmax warps had read the scores, and the mask, of another two before.
-          mi.mask[t & 3] = mask;  // by the lane that arrives
-          mbar_arrive(smem_u32(&mi.m_full[t & 3]));
-          mbar_expect(k_full + 8 * stage, static_cast<uint32_t>(n_mine * box_rows) * (kEntry * 2));
-        }
-        __syncwarp();
+        if (for_s) {
+          uint64_t mask = 0;  // entries that exist
+          for (int s = 0; s < segs; ++s)
+            if (goods >> s & 1) mask |= ((1ull << box_rows) - 1) << (s * box_rows);
+          const int left = it.len - (it.tile + i) * kDecodeTile;
+          if (left < 64) mask &= (1ull << left) - 1;
+          if (i == 0) {  // the row tile's queries, once the products with the ones before are done
+            if (items > 0) wait(smem_u32(&mi.q_empty), (items - 1) & 1);
+            ++items;
+            if (elect_one()) {
+              const int64_t r0 = it.row0 + static_cast<int64_t>(rank) * rpc;
+              const int token = static_cast<int>(r0 / p.H);
+              const uint32_t bar = smem_u32(&mi.q_full);
+              mbar_expect(bar, static_cast<uint32_t>(rpc) * kEntry * 2);
 #pragma unroll 1
-        for (int s = 0; s < n_mine; ++s) {
-          const int sid = __shfl_sync(0xffffffffu, id, mine + s), srow = __shfl_sync(0xffffffffu, row, mine + s);
-          if (elect_one()) {
-            const uint32_t dst = k_at + s * box_rows * 128, bar = k_full + 8 * stage;
-            if (box_rows == kKeys) {
-              tma_load_4d(dst, &map, bar, 0, srow, 0, sid);
-              tma_load_4d(dst + 4 * kKPiece, &map, bar, 0, srow, 4, sid);
-            } else {
-#pragma unroll 1
-              for (int c = 0; c < 8; ++c) tma_load_4d(dst + c * kKPiece, &map, bar, 0, srow, c, sid);
+              for (int c = 0; c < 9; ++c)
+                tma_load_4d(base + kQAt + c * kQPiece, &q_map, bar, 64 * c, static_cast<int>(r0 % p.H), token % p.q_tma, token / p.q_tma);
             }
-            tma_load_3d(dst + 8 * kKPiece, &rope_map, bar, kLatent, srow, sid);
+            __syncwarp();
+          }
+          wait(k_empty + 8 * stage, parity);
+          if (elect_one()) {
+            // The mask has barriers of its own, four of them: those of the entries may be a phase ahead of the softmax warps,
+            // which then wait in vain. A tile's entries are loaded when the scores two tiles before are done, and those when
+            // the softmax warps had read the scores, and the mask, of another two before.
+            mi.mask[t & 3] = mask;  // by the lane that arrives
+            mbar_arrive(smem_u32(&mi.m_full[t & 3]));
+            mbar_expect(k_full + 8 * stage, static_cast<uint32_t>(n_mine * box_rows) * (kEntry * 2));
           }
           __syncwarp();
-        }
-        wait(v_empty + 8 * stage, parity);
-        if (elect_one()) mbar_expect(v_full + 8 * stage, static_cast<uint32_t>(n_boxes * box_rows) * kLatent);
-        __syncwarp();
 #pragma unroll 1
-        for (int s = 0; s < n_boxes; ++s) {
-          const int sid = __shfl_sync(0xffffffffu, id, s), srow = __shfl_sync(0xffffffffu, row, s);
-          if (elect_one()) {
-            const uint32_t dst = v_at + (s / half) * (4 * kKPiece) + (s % half) * box_rows * 128, bar = v_full + 8 * stage;
-            const int c0 = static_cast<int>(rank) * 4;
-            if (box_rows == kKeys) {
-              tma_load_4d(dst, &map, bar, 0, srow, c0, sid);
-            } else {
+          for (int s = 0; s < n_mine; ++s) {
+            const int sid = __shfl_sync(0xffffffffu, id, mine + s), srow = __shfl_sync(0xffffffffu, row, mine + s);
+            if (elect_one()) {
+              const uint32_t dst = k_at + s * box_rows * 128, bar = k_full + 8 * stage;
+              if (box_rows == kKeys) {
+                tma_load_4d(dst, &map, bar, 0, srow, 0, sid);
+                tma_load_4d(dst + 4 * kKPiece, &map, bar, 0, srow, 4, sid);
+              } else {
 #pragma unroll 1
-              for (int c = 0; c < 4; ++c) tma_load_4d(dst + c * kKPiece, &map, bar, 0, srow, c0 + c, sid);
+                for (int c = 0; c < 8; ++c) tma_load_4d(dst + c * kKPiece, &map, bar, 0, srow, c, sid);
+              }
+              tma_load_3d(dst + 8 * kKPiece, &rope_map, bar, kLatent, srow, sid);
             }
+            __syncwarp();
           }
+        } else {
+          wait(v_empty + 8 * stage, parity);
+          if (elect_one()) mbar_expect(v_full + 8 * stage, static_cast<uint32_t>(n_boxes * box_rows) * kLatent);
           __syncwarp();
+#pragma unroll 1
+          for (int s = 0; s < n_boxes; ++s) {
+            const int sid = __shfl_sync(0xffffffffu, id, s), srow = __shfl_sync(0xffffffffu, row, s);
+            if (elect_one()) {
+              const uint32_t dst = v_at + (s / half) * (4 * kKPiece) + (s % half) * box_rows * 128, bar = v_full + 8 * stage;
+              const int c0 = static_cast<int>(rank) * 4;
+              if (box_rows == kKeys) {
+                tma_load_4d(dst, &map, bar, 0, srow, c0, sid);
+              } else {
+#pragma unroll 1
+                for (int c = 0; c < 4; ++c) tma_load_4d(dst + c * kKPiece, &map, bar, 0, srow, c0 + c, sid);
+              }
+            }
+            __syncwarp();
+          }
         }
       }
     }
-    if (rank == 0) set_flag(p.err, bad);
+    if (rank == 0 && for_s) set_flag(p.err, bad);
     // after a timeout, copies in flight land before the CTA ends (`never` is not set: these waits run on)
     if (!alive) {
       const uint32_t never = smem_u32(&mi.never);
       if (items > 0) mbar_wait(smem_u32(&mi.q_full), (items - 1) & 1, never);
-      for (uint32_t s = t < 2 ? 0 : t - 2; s < t; ++s) {
-        mbar_wait(k_full + 8 * (s & 1), s >> 1 & 1, never);
-        mbar_wait(v_full + 8 * (s & 1), s >> 1 & 1, never);
-      }
+      for (uint32_t s = t < 2 ? 0 : t - 2; s < t; ++s) mbar_wait((for_s ? k_full : v_full) + 8 * (s & 1), s >> 1 & 1, never);
     }
   } else if (warp >= 5) {
     if (rank == 1) {
