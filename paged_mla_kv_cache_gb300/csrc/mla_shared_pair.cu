@@ -324,9 +324,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
       bool first = false;  // the tile before is a row tile's first
       auto values = [&](uint32_t u) {  // O of tile u
         const uint32_t stage = u & 1, parity = u >> 1 & 1;
-        wait(smem_u32(&mi.p_full[0]) + 8 * stage, parity);
-        wait(v_full + 8 * stage, parity);
-        wait(v_peer + 8 * stage, parity);
+        wait((lane == 0 ? smem_u32(&mi.p_full[0]) : lane == 1 ? v_full : v_peer) + 8 * stage, parity);
+        __syncwarp();
         tmem_fence_after();
         if (elect_one()) {
           const uint64_t pa = umma_desc(base + kPAt + stage * kP, 16, 1024);
@@ -350,9 +349,9 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
         for (int i = 0; i < it.n; ++i, ++t) {
           const uint32_t stage = t & 1, parity = t >> 1 & 1;
           if (i == 0) wait(smem_u32(&mi.q_full), q);
-          wait(k_full + 8 * stage, parity);
-          wait(k_peer + 8 * stage, parity);
-          if (t >= 2) wait(s_free + 8 * stage, parity ^ 1);
+          // (the lanes wait for one barrier each: one after the other, each took 80 clocks also where it was there)
+          wait((lane == 0 ? k_full : lane == 1 ? k_peer : s_free) + 8 * stage, lane < 2 ? parity : parity ^ 1);
+          __syncwarp();
           tmem_fence_after();
           if (elect_one()) {
             const uint32_t d = tmem + kSAt + stage * kKeys;
