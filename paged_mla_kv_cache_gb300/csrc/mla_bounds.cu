@@ -5,12 +5,13 @@
 // minimum are exact in any order and any wider type: 16-bit values are compared
 // two at a time as they are, e4m3 ones as the fp16 values that they stand for.
 //
-// Bound by memory: the new entries once, two rows a touched page. The touched
-// pages of all requests are a flat list, cut into equal shares, a CTA each. In a
-// CTA a thread keeps one 16-byte column unit of every kGroups-th entry, up to
-// kAhead of them on their way at once, and the groups' extremes meet in shared
-// memory. Rows that are not whole aligned units take the same CTAs element by
-// element.
+// Bound by memory: the new entries once, two rows a touched page. A thread takes
+// one 16-byte column unit of a touched page through all of its entries, kAhead of
+// them on their way at once, so neighbours read neighbouring units and nothing
+// has to meet; the units of all requests' pages are a flat list, cut into equal
+// shares, a CTA each. (A CTA a page, with groups of threads over its entries that
+// meet in shared memory, took 44 us at best for 300000 e4m3 entries.) Rows that
+// are not whole aligned units take the same threads element by element.
 #include <algorithm>
 
 #include "mla_attn.cuh"
@@ -20,9 +21,9 @@
 namespace pmg_mla {
 namespace {
 
-constexpr int kThreads = 288;  // four groups of the 72 units of 576 16-bit values, eight of 36 e4m3 units
-constexpr int kAhead = 8;      // entries of a thread on their way
-constexpr int kCtasPerSm = 4;
+constexpr int kThreads = 192;
+constexpr int kAhead = 16;  // entries of a thread on their way
+constexpr int kCtasPerSm = 2;
 
 struct BoundsParams {
   const uint8_t* cache;
@@ -78,17 +79,19 @@ struct Extremes {
       lo[i] = inf;
     }
   }
+  __device__ __forceinline__ static void largest(uint32_t& x, uint32_t a) {
+    if constexpr (!kPacked) x = __float_as_uint(max_nan(__uint_as_float(x), __uint_as_float(a)));
+    else if constexpr (std::is_same<TC, bf16>::value) asm("max.NaN.bf16x2 %0, %0, %1;" : "+r"(x) : "r"(a));
+    else asm("max.NaN.f16x2 %0, %0, %1;" : "+r"(x) : "r"(a));
+  }
+  __device__ __forceinline__ static void smallest(uint32_t& x, uint32_t a) {
+    if constexpr (!kPacked) x = __float_as_uint(min_nan(__uint_as_float(x), __uint_as_float(a)));
+    else if constexpr (std::is_same<TC, bf16>::value) asm("min.NaN.bf16x2 %0, %0, %1;" : "+r"(x) : "r"(a));
+    else asm("min.NaN.f16x2 %0, %0, %1;" : "+r"(x) : "r"(a));
+  }
   __device__ __forceinline__ void fold(int i, uint32_t a, uint32_t b) {
-    if constexpr (!kPacked) {
-      hi[i] = __float_as_uint(max_nan(__uint_as_float(hi[i]), __uint_as_float(a)));
-      lo[i] = __float_as_uint(min_nan(__uint_as_float(lo[i]), __uint_as_float(b)));
-    } else if constexpr (std::is_same<TC, bf16>::value) {
-      asm("max.NaN.bf16x2 %0, %0, %1;" : "+r"(hi[i]) : "r"(a));
-      asm("min.NaN.bf16x2 %0, %0, %1;" : "+r"(lo[i]) : "r"(b));
-    } else {
-      asm("max.NaN.f16x2 %0, %0, %1;" : "+r"(hi[i]) : "r"(a));
-      asm("min.NaN.f16x2 %0, %0, %1;" : "+r"(lo[i]) : "r"(b));
-    }
+    largest(hi[i], a);
+    smallest(lo[i], b);
   }
   __device__ __forceinline__ void fold(const Raw& x) {
     if constexpr (!kVec) {
@@ -120,99 +123,77 @@ struct Extremes {
 };
 
 template <class TC, class TB, bool kVec>
-__global__ void __launch_bounds__(kThreads) bounds_kernel(const __grid_constant__ BoundsParams p) {
+__global__ void __launch_bounds__(kThreads, kCtasPerSm) bounds_kernel(const __grid_constant__ BoundsParams p) {
   using X = Extremes<TC, kVec>;
   __shared__ int64_t scratch[33], found[2];
-  __shared__ uint32_t meet[kThreads][2 * X::kWords + 1];  // (one word more: neighbours lie in different banks)
   pdl_entry();
-  const Share share = find_share([&](int r) { return joined_pages(p, joined(p, r)); }, p.R, blockIdx.x, p.units, scratch, found);
-  const int tid = threadIdx.x;
-  // kVec: `units` columns in `groups` groups of threads; else columns in turns
-  const int columns = kVec ? p.E / X::kValues : p.E;
-  const int groups = max(1, kThreads / columns);
-  const int group = tid / columns, at = kVec || groups > 1 ? tid % columns : tid;
-  const bool works = group < groups;
-  const uint32_t B = static_cast<uint32_t>(p.B);
+  const uint32_t columns = static_cast<uint32_t>(p.E) / X::kValues, B = static_cast<uint32_t>(p.B);
+  const Share share = find_share([&](int r) { return joined_pages(p, joined(p, r)) * columns; }, p.R, blockIdx.x, p.units,
+                                 scratch, found);
   int bad = 0;
-  int64_t item_at = share.begin, skip = share.offset;
-  for (int r = share.item; item_at < share.end; ++r, skip = 0) {
-    const Joined j = joined(p, r);
-    const int64_t n = min(joined_pages(p, j) - skip, share.end - item_at);
+  // The thread's request: units [base, base + n) of the flat list.
+  int r = share.item;
+  int64_t base = share.begin - share.offset, n = 0;
+  Joined j{};
+  auto enter = [&]() {
+    j = joined(p, r);
+    n = joined_pages(p, j) * columns;
     bad |= j.bad;
-    item_at += n;
-    const int32_t* table = p.bt + static_cast<int64_t>(r) * p.bt_stride;
-    const uint32_t first = static_cast<uint32_t>(j.from) / B + static_cast<uint32_t>(skip);
-    int32_t next = n > 0 ? table[first] : -1;
-    for (uint32_t page = first; page < first + static_cast<uint32_t>(n); ++page) {
-      const int32_t id = next;
-      if (page + 1 < first + static_cast<uint32_t>(n)) next = table[page + 1];
-      if (id < 0 || id >= p.num_blocks) {
-        bad |= PMG_FLAG_PHYS_BLOCK;
-        continue;
-      }
-      const int64_t place = static_cast<int64_t>(page) * B;  // the page's first
-      const int r0 = static_cast<int>(max(static_cast<int64_t>(j.from) - place, static_cast<int64_t>(0)));
-      const int r1 = static_cast<int>(min(static_cast<int64_t>(j.to) - place, static_cast<int64_t>(B)));
-      const TC* rows = reinterpret_cast<const TC*>(p.cache) + id * p.blk_stride;
-      TB* hi = reinterpret_cast<TB*>(p.bounds) + id * p.bb_stride;
-      TB* lo = hi + p.br_stride;
-      const int together = min(groups, r1 - r0);  // groups that have an entry
-      for (int column = at; column < columns; column += kVec ? columns : kThreads) {
-        X x;
-        x.clear();
-        const TC* src = rows + column * X::kValues;
-        TB* h = hi + column * X::kValues;
-        TB* l = lo + column * X::kValues;
-        // (what is known of the page, on its way with the entries)
-        Values<TB, X::kValues> old_hi, old_lo;
-        if (group == 0 && r0 > 0) {
-          old_hi.load(h);
-          old_lo.load(l);
-        }
-        if (works) {
-#pragma unroll 1
-          for (int row = r0 + group; row < r1; row += kAhead * groups) {
-            typename X::Raw raw[kAhead];
-#pragma unroll
-            for (int k = 0; k < kAhead; ++k) {  // (past the last entry: the same once more)
-              const int rr = row + k * groups < r1 ? row + k * groups : row;
-              raw[k] = *reinterpret_cast<const typename X::Raw*>(src + rr * p.tok_stride);
-            }
-#pragma unroll
-            for (int k = 0; k < kAhead; ++k) x.fold(raw[k]);
-          }
-        }
-        if (together > 1) {  // the same in all threads
-          __syncthreads();
-#pragma unroll
-          for (int k = 0; k < X::kWords; ++k) {
-            meet[tid][k] = x.hi[k];
-            meet[tid][X::kWords + k] = x.lo[k];
-          }
-          __syncthreads();
-          if (group == 0)
-            for (int g = 1; g < together; ++g)
-#pragma unroll
-              for (int k = 0; k < X::kWords; ++k) x.fold(k, meet[tid + g * columns][k], meet[tid + g * columns][X::kWords + k]);
-        }
-        if (group == 0) {
-          Values<TB, X::kValues> a, b;
-#pragma unroll
-          for (int k = 0; k < X::kValues; ++k) {
-            float top = X::value(x.hi, k), low = X::value(x.lo, k);
-            if (r0 > 0) {
-              top = max_nan(top, to_f(old_hi.v[k]));
-              low = min_nan(low, to_f(old_lo.v[k]));
-            }
-            a.v[k] = from_f<TB>(top);  // a value of the entries or of the bounds: nothing is rounded
-            b.v[k] = from_f<TB>(low);
-          }
-          a.store(h);
-          b.store(l);
-        }
-      }
+  };
+  const int64_t first = share.begin + threadIdx.x;
+  if (first < share.end) enter();
+  for (int64_t at = first; at < share.end; at += kThreads) {
+    while (at >= base + n) {
+      base += n;
+      ++r;
+      enter();
     }
+    const uint32_t y = static_cast<uint32_t>(at - base), in = y / columns, column = y - in * columns;  // (2^31 pages of 256 units are not there)
+    const uint32_t page = static_cast<uint32_t>(j.from) / B + in;
+    const int32_t id = p.bt[static_cast<int64_t>(r) * p.bt_stride + page];
+    if (id < 0 || id >= p.num_blocks) {
+      bad |= PMG_FLAG_PHYS_BLOCK;
+      continue;
+    }
+    const int64_t place = static_cast<int64_t>(page) * B;  // the page's first
+    const int r0 = static_cast<int>(max(static_cast<int64_t>(j.from) - place, static_cast<int64_t>(0)));
+    const int r1 = static_cast<int>(min(static_cast<int64_t>(j.to) - place, static_cast<int64_t>(B)));
+    const TC* src = reinterpret_cast<const TC*>(p.cache) + id * p.blk_stride + r0 * p.tok_stride + column * X::kValues;
+    TB* hi = reinterpret_cast<TB*>(p.bounds) + id * p.bb_stride + column * X::kValues;
+    TB* lo = hi + p.br_stride;
+    X x;
+    x.clear();
+    Values<TB, X::kValues> known_hi, known_lo;
+    if (r0 > 0) {
+      known_hi.load(hi);
+      known_lo.load(lo);
+    }
+#pragma unroll 1
+    for (int row = r0; row < r1; row += kAhead) {
+      typename X::Raw raw[kAhead];
+#pragma unroll
+      for (int k = 0; k < kAhead; ++k)  // (past the last entry: the first of these once more)
+        raw[k] = *reinterpret_cast<const typename X::Raw*>(src + (row + k < r1 ? k : 0) * p.tok_stride);
+      src += kAhead * p.tok_stride;
+#pragma unroll
+      for (int k = 0; k < kAhead; ++k) x.fold(raw[k]);
+    }
+    Values<TB, X::kValues> a, b;
+#pragma unroll
+    for (int k = 0; k < X::kValues; ++k) {
+      float top = X::value(x.hi, k), low = X::value(x.lo, k);
+      if (r0 > 0) {
+        top = max_nan(top, to_f(known_hi.v[k]));
+        low = min_nan(low, to_f(known_lo.v[k]));
+      }
+      a.v[k] = from_f<TB>(top);  // a value of the entries or of the bounds: nothing is rounded
+      b.v[k] = from_f<TB>(low);
+    }
+    a.store(hi);
+    b.store(lo);
   }
+  // what is wrong with lengths of requests without pages here
+  for (int i = blockIdx.x * kThreads + threadIdx.x; i < p.R; i += gridDim.x * kThreads) bad |= joined(p, i).bad;
   set_flag(p.err, bad);
 }
 
