@@ -26,7 +26,7 @@ constexpr float kLn2 = 0.6931471805599453f;
 struct JoinNote {
   int32_t item;         // request that begins in this share and goes on in the next, or -1
   int32_t parts;        // shares that hold it
-  int32_t head, tile;   // prefill: which of the request's row tiles
+  int32_t head, tile;   // prefill: which of the request's row tiles; passes over shared prefixes: first row, rows
 };
 constexpr int kNotesPerSm = 4;
 constexpr int64_t kSlotFloats = 256 * 130;  // the largest slot: 256 rows of 128 values, or 64 of 512, and two sums each

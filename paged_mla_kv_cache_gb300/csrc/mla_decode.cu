@@ -22,7 +22,7 @@ template <class TQ, class TC, bool kPrefix>
 __global__ void __launch_bounds__(kGenThreads) decode_general_kernel(const __grid_constant__ DecodeParams p) {
   extern __shared__ __align__(16) uint8_t smem[];
   __shared__ int64_t scratch[33], found[2];
-  pdl_entry();
+  pass_entry<kPrefix>(p);
   const int E = p.dv + p.dr;
   const GenSmem s = general_smem_at(smem, E);
   const int unit = kPrefix ? blockIdx.x : blockIdx.x / p.groups, group = kPrefix ? 0 : blockIdx.x % p.groups;
@@ -39,7 +39,7 @@ __global__ void __launch_bounds__(kGenThreads) decode_general_kernel(const __gri
   const int rows = p.q_len * p.H;
   const int g0 = group * p.rows_per_group;
   const float scale = sizeof(TC) == 1 && p.scale != nullptr ? *p.scale : 1.0f;
-  const Covered covered = kPrefix ? Covered{0, 0} : covered_requests(p);
+  const bool keeps = kPrefix || p.state != nullptr;  // rows are left for the join over shared prefixes
   JoinNote note{-1, 0, 0, 0};
   int bad = 0;
   int64_t at = share.begin;
@@ -93,36 +93,27 @@ __global__ void __launch_bounds__(kGenThreads) decode_general_kernel(const __gri
     general_rows(s, E, p.dv, tile * kDecodeTile, min((tile + n) * kDecodeTile, static_cast<int64_t>(len.use)),
                  p.sm_scale * kLog2e, load, seen, value, acc, m, l);
     const bool whole = tile == 0 && n == tiles;
-    if (!whole && tile == 0) {
-      note.item = b;
-      note.parts = unit_of(at + tiles - 1, share.total, share.units) - unit + 1;
-      if constexpr (kPrefix) note.tile = it.row_tile;
-    }
-    // where the rows go that are not finished here: a slot of the workspace, or the prefix's state
+    const int parts = whole || tile > 0 ? 0 : unit_of(at + tiles - 1, share.total, share.units) - unit + 1;
+    if (parts > 0) note = {b, parts, keeps ? static_cast<int32_t>(row0) : 0, keeps ? n_rows : 0};
+    // where the rows go that are not finished here: a slot of the workspace, or the state of a pass
     float* slot = p.ws.slots + (static_cast<int64_t>(blockIdx.x) * 2 + (tile == 0 ? 1 : 0)) * p.slot_floats;
     float* slot_ml = slot + p.rows_per_group * p.dv;
-    if (kPrefix && whole) {
+    const bool finished = whole && !keeps;
+    if (whole && keeps) {
       slot = p.state + row0 * p.dv;
       slot_ml = p.state_ml + 2 * row0;
     }
-    const bool joins = !kPrefix && whole && b >= covered.from && b < covered.to;
     __syncthreads();
     if (lane == 0) {  // what every row is multiplied by, and its log sum
-      s.scale[row] = whole ? (l != 0.0f ? 1.0f / l : 0.0f) : 1.0f;
-      s.p[row] = 0.0f;  // and what its state is (the weights are done with)
+      s.scale[row] = finished ? (l != 0.0f ? 1.0f / l : 0.0f) : 1.0f;
       if (row < n_rows) {
-        float lse = l != 0.0f ? (m + log2f(l)) * kLn2 : -INFINITY;
-        if (joins) {
-          const Joint x = joint_of(m, l, p.state_ml + 2 * (row0 + row));
-          s.scale[row] = x.mine;
-          s.p[row] = x.other;
-          lse = x.lse;
-        }
-        if (!kPrefix && whole && p.lse != nullptr) p.lse[row0 + row] = lse;
-        if (kPrefix || !whole) {
+        if (finished && p.lse != nullptr) p.lse[row0 + row] = l != 0.0f ? (m + log2f(l)) * kLn2 : -INFINITY;
+        if (!finished) {
           slot_ml[2 * row] = m;
           slot_ml[2 * row + 1] = l;
         }
+        if (keeps && (whole || tile == 0))
+          p.row_notes[row0 + row] = {static_cast<uint16_t>(whole ? 0 : blockIdx.x), static_cast<uint16_t>(parts), row};
       }
     }
     __syncthreads();
@@ -131,76 +122,39 @@ __global__ void __launch_bounds__(kGenThreads) decode_general_kernel(const __gri
       if (r >= n_rows) continue;
       const int rr = g0 + r;
       TQ* out = reinterpret_cast<TQ*>(p.out) + b * p.or_stride + (rr / p.H) * p.ot_stride + (rr % p.H) * p.oh_stride;
-      const float keep = s.p[r];
 #pragma unroll
       for (int c = 0; c < kGenCols; ++c) {
         const int d = tid + c * kGenThreads;
         if (d >= p.dv) continue;
-        if (kPrefix || !whole) {
-          slot[r * p.dv + d] = acc[r][c];
-        } else {
-          float y = acc[r][c] * s.scale[r];
-          if (keep != 0.0f) y += keep * p.state[(row0 + r) * p.dv + d];
-          out[d] = from_f<TQ>(y);
-        }
+        if (finished) out[d] = from_f<TQ>(acc[r][c] * s.scale[r]);
+        else slot[r * p.dv + d] = acc[r][c];
       }
     }
     at += n;
   }
   if (tid == 0 && p.units > 1) p.ws.notes[blockIdx.x] = note;  // one unit cuts nothing
   set_flag(p.err, bad);
+  pass_exit<kPrefix>(p);
 }
 
 template <class TQ>
 __global__ void __launch_bounds__(kJoinThreads, kJoinCtasPerSm) decode_join_kernel(const __grid_constant__ DecodeParams p) {
   pdl_entry();
   const int rows = p.q_len * p.H;
-  const Covered covered = covered_requests(p);
   auto row_of = [&](int cta, int row) { return cta % p.groups * p.rows_per_group + row; };
   join_rows(
       p.ws, p.units * p.groups, p.groups, p.rows_per_group, p.dv, p.slot_floats,
       [&](const JoinNote&, int cta, int row) { return row_of(cta, row) < rows; },
       [&](const JoinNote& note, int cta, int row, int d, const float4& a, float top, float l) {
         const int rr = row_of(cta, row);
-        const int64_t at = static_cast<int64_t>(note.item) * rows + rr;
-        float inv = l != 0.0f ? 1.0f / l : 0.0f, keep = 0.0f, lse = l != 0.0f ? (top + log2f(l)) * kLn2 : -INFINITY;
-        if (note.item >= covered.from && note.item < covered.to) {
-          const Joint x = joint_of(top, l, p.state_ml + 2 * at);
-          inv = x.mine;
-          keep = x.other;
-          lse = x.lse;
-        }
-        if (d == 0 && p.lse != nullptr) p.lse[at] = lse;
+        const float inv = l != 0.0f ? 1.0f / l : 0.0f;
+        if (d == 0 && p.lse != nullptr)
+          p.lse[static_cast<int64_t>(note.item) * rows + rr] = l != 0.0f ? (top + log2f(l)) * kLn2 : -INFINITY;
         TQ* out = static_cast<TQ*>(p.out) + note.item * p.or_stride + (rr / p.H) * p.ot_stride + (rr % p.H) * p.oh_stride + d;
         const float y[4] = {a.x * inv, a.y * inv, a.z * inv, a.w * inv};
 #pragma unroll
         for (int k = 0; k < 4; ++k)
-          if (d + k < p.dv) out[k] = from_f<TQ>(keep != 0.0f ? y[k] + keep * p.state[at * p.dv + d + k] : y[k]);
-      });
-}
-
-// Row tiles of a prefix that shares cut.
-__global__ void __launch_bounds__(kJoinThreads, kJoinCtasPerSm) prefix_join_kernel(const __grid_constant__ DecodeParams p) {
-  pdl_entry();
-  auto row_at = [&](const JoinNote& note, int row) {
-    return static_cast<int64_t>(group_of(p, note.item).from) * p.q_len * p.H + static_cast<int64_t>(note.tile) * p.rows_per_group + row;
-  };
-  join_rows(
-      p.ws, p.units, 1, p.rows_per_group, p.dv, p.slot_floats,
-      [&](const JoinNote& note, int, int row) {
-        return row_at(note, row) < static_cast<int64_t>(group_of(p, note.item).to) * p.q_len * p.H;
-      },
-      [&](const JoinNote& note, int, int row, int d, const float4& a, float top, float l) {
-        const int64_t at = row_at(note, row);
-        if (d == 0) {
-          p.state_ml[2 * at] = top;
-          p.state_ml[2 * at + 1] = l;
-        }
-        float* out = p.state + at * p.dv + d;
-        const float y[4] = {a.x, a.y, a.z, a.w};
-#pragma unroll
-        for (int k = 0; k < 4; ++k)
-          if (d + k < p.dv) out[k] = y[k];
+          if (d + k < p.dv) out[k] = from_f<TQ>(y[k]);
       });
 }
 
@@ -298,10 +252,7 @@ int run_decode(DecodeParams& p, int q_dtype, int cache_dtype, int sms, void* str
     p.units = std::max(1, sms / p.groups);
     st = run_general<false>(p, q_dtype, cache_dtype, stream);
   }
-  if (st != PMG_OK || p.units == 1) return st;
-  const Kernel join = q_dtype == PMG_BF16 ? decode_join_kernel<bf16>
-                      : q_dtype == PMG_FP16 ? decode_join_kernel<f16> : decode_join_kernel<float>;
-  return launch(join, dim3(static_cast<unsigned>(kJoinCtasPerSm * sms)), kJoinThreads, 0, stream, p);
+  return st;
 }
 
 int run_prefix(DecodeParams& p, int q_dtype, int cache_dtype, int sms, void* stream, uint32_t options) {
@@ -314,8 +265,15 @@ int run_prefix(DecodeParams& p, int q_dtype, int cache_dtype, int sms, void* str
     p.units = sms;
     st = run_general<true>(p, q_dtype, cache_dtype, stream);
   }
-  if (st != PMG_OK) return st;
-  return launch(prefix_join_kernel, dim3(static_cast<unsigned>(kJoinCtasPerSm * sms)), kJoinThreads, 0, stream, p);
+  return st;
+}
+
+int decode_alone(DecodeParams& p, int q_dtype, int cache_dtype, int sms, void* stream, uint32_t options) {
+  const int st = run_decode(p, q_dtype, cache_dtype, sms, stream, options);
+  if (st != PMG_OK || p.units == 1) return st;
+  const Kernel join = q_dtype == PMG_BF16 ? decode_join_kernel<bf16>
+                      : q_dtype == PMG_FP16 ? decode_join_kernel<f16> : decode_join_kernel<float>;
+  return launch(join, dim3(static_cast<unsigned>(kJoinCtasPerSm * sms)), kJoinThreads, 0, stream, p);
 }
 
 }  // namespace pmg_mla
@@ -347,5 +305,5 @@ extern "C" int pmg_latent_decode(const void* q, int64_t q_req_stride, int64_t q_
   if (st != PMG_OK) return st;
   if (workspace_bytes_given < workspace_bytes(sms)) return PMG_ERR_ARG;
   p.ws = workspace_at(workspace, sms);
-  return run_decode(p, q_dtype, cache_dtype, sms, stream, options);
+  return decode_alone(p, q_dtype, cache_dtype, sms, stream, options);
 }

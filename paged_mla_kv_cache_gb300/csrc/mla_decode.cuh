@@ -1,12 +1,14 @@
 // Parameters, length arithmetic and work lists of the decode kernels.
 //
 // A call over shared prefixes (pmg_latent_decode_shared) is two passes of these
-// kernels. The first, a prefix pass, takes groups of requests in place of
-// requests: `cu` says which, bt and seq_lens are the prefixes', R is their
-// number, and all rows of a group see all of its prefix. It leaves every row's
-// unnormalised sums, reference (in base 2) and sum of weights as a state. The
-// second is a decode over the requests' own entries that joins the state as it
-// finishes its rows.
+// kernels, whose rows a join of its own finishes (mla_shared.cu). The first, a
+// prefix pass, takes groups of requests in place of requests: `cu` says which, bt
+// and seq_lens are the prefixes', R is their number, and all rows of a group see
+// all of its prefix. The second is a decode over the requests' own entries. Both
+// leave every row's unnormalised sums, reference (in base 2) and sum of weights:
+// of rows whose keys one share held in `state`, of others in the shares' slots.
+// Neither reads what the other writes, so the second starts where the first
+// leaves SMs free, and ends after it.
 #pragma once
 
 #include "mla_attn.cuh"
@@ -14,6 +16,12 @@
 namespace pmg_mla {
 
 constexpr int kDecodeTile = 64;  // keys of one piece of work
+
+// Where a pass left a row.
+struct RowNote {
+  uint16_t cta, parts;  // in the slots of so many shares from this CTA's on; 0: in the state
+  int32_t row;          // which row of a slot
+};
 
 struct DecodeParams {
   const void* q;
@@ -39,10 +47,29 @@ struct DecodeParams {
   int32_t q_tma;      // heads of a query box (0: queries are loaded and converted by the softmax warps)
   const int32_t* cu;  // a prefix pass: the groups' first requests
   int32_t reqs;       // and how many requests there are
-  float* state;       // [rows][dv] written by a prefix pass, joined by the pass after it, or NULL
+  float* state;       // [rows][dv] of a pass of a call over shared prefixes, or NULL
   float* state_ml;    // [rows][2]: reference and sum
-  int32_t* covered;   // [2]: requests whose rows have a state
+  RowNote* row_notes; // [rows]
+  int32_t* covered;   // [2]: requests whose rows have a prefix, noted by the prefix pass
 };
+
+// The beginning and end of a kernel of a pass: the second pass does not wait for
+// the first, whose launch of it comes when the kernels before are done, but ends
+// after it.
+template <bool kPrefix>
+__device__ __forceinline__ void pass_entry(const DecodeParams& p) {
+  if constexpr (kPrefix) {
+    pdl_wait();
+    pdl_launch();
+  } else {
+    if (p.state != nullptr) pdl_launch();
+    else pdl_entry();
+  }
+}
+template <bool kPrefix>
+__device__ __forceinline__ void pass_exit(const DecodeParams& p) {
+  if (!kPrefix && p.state != nullptr) pdl_wait();
+}
 
 struct DecodeLen {
   int32_t full;  // the request's length
@@ -98,12 +125,6 @@ __device__ __forceinline__ Group group_of(const DecodeParams& p, int g) {
   return x;
 }
 
-struct Covered {
-  int32_t from, to;
-};
-__device__ __forceinline__ Covered covered_requests(const DecodeParams& p) {
-  return p.state != nullptr ? Covered{p.covered[0], p.covered[1]} : Covered{0, 0};
-}
 // By a whole CTA of the prefix pass, which reports what is wrong with the groups too; `to` is shared.
 __device__ __forceinline__ void note_covered(const DecodeParams& p, int tid, int threads, int32_t& to) {
   if (tid == 0) to = 0;
@@ -189,21 +210,6 @@ struct PrefixItems {
   __device__ int64_t last_piece() const { return first + kCost + tiles - 1; }
 };
 
-// A row's share and that of its state in their joint result: `mine` of the sums
-// under reference m whose weights add up to l, `other` of the state's.
-struct Joint {
-  float mine, other, lse;
-};
-__device__ __forceinline__ Joint joint_of(float m, float l, const float* state_ml) {
-  const float m2 = state_ml[0], l2 = state_ml[1];
-  // (a sum of 0 saw nothing: its sums are not used; NaN counts)
-  const float top = l == 0.0f ? m2 : l2 == 0.0f ? m : fmaxf(m, m2);
-  const float w = l == 0.0f ? 0.0f : exp2f(m - top), w2 = l2 == 0.0f ? 0.0f : exp2f(m2 - top);
-  const float sum = w * l + w2 * l2;
-  const float inv = sum != 0.0f ? 1.0f / sum : 0.0f;
-  return {w * inv, w2 * inv, sum != 0.0f ? (top + log2f(sum)) * kLn2 : -INFINITY};
-}
-
 // ---- host: what the entries share --------------------------------------------------
 
 // Checks the arguments of a decode and fills p (workspace and state apart). PMG_OK
@@ -216,10 +222,11 @@ int decode_params(DecodeParams& p, const void* q, int64_t q_req_stride, int64_t 
                   int64_t out_req_stride, int64_t out_token_stride, int64_t out_head_stride, float* lse,
                   void* workspace, int32_t* error_flag, uint32_t options);
 
-// Launches a decode over the requests' entries, and its join.
+// Launch a decode over the requests' entries, or a prefix pass, without a join.
 int run_decode(DecodeParams& p, int q_dtype, int cache_dtype, int sms, void* stream, uint32_t options);
-// Launches a prefix pass, and its join.
 int run_prefix(DecodeParams& p, int q_dtype, int cache_dtype, int sms, void* stream, uint32_t options);
+// A decode over the requests' entries with its join.
+int decode_alone(DecodeParams& p, int q_dtype, int cache_dtype, int sms, void* stream, uint32_t options);
 
 // Tiles of a request; an empty one has a piece too, which writes its rows.
 __device__ __forceinline__ int64_t decode_tiles(const DecodeParams& p, int b) {

@@ -250,9 +250,8 @@ __device__ __forceinline__ void load_queries(RowAt row_at, int n_rows, uint8_t* 
 }
 
 // kPrefix: the items are groups of requests and row tiles of them, their keys a
-// prefix that all rows see, and every result is left as a state (a prefix pass
-// of mla_decode.cuh); else they are requests, each CTA has one of the groups of
-// their rows, and what a prefix pass left is joined.
+// prefix that all rows see (a prefix pass of mla_decode.cuh); else they are
+// requests, and each CTA has one of the groups of their rows.
 template <class TQ, int kParts, int N, bool kPrefix>
 __global__ void __launch_bounds__(kThreads, 1)
     decode_tc_kernel(const __grid_constant__ DecodeParams p, const __grid_constant__ CUtensorMap map,
@@ -302,7 +301,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
     fence_async_smem();
   }
-  pdl_entry();
+  pass_entry<kPrefix>(p);
 
   const int unit = kPrefix ? blockIdx.x : blockIdx.x / p.groups, group = kPrefix ? 0 : blockIdx.x % p.groups;
   const Share share = find_share(
@@ -587,7 +586,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       const int step = step0 + mi.step[h];
       return step * p.ot_stride + (g0 + h - step * p.H) * p.oh_stride;
     };
-    const Covered covered = kPrefix ? Covered{0, 0} : covered_requests(p);
+    const bool keeps = kPrefix || p.state != nullptr;  // rows are left for the join over shared prefixes
     // For each request: its queries, then the epilogue of the request before (whose last product runs meanwhile), then
     // its tiles.
     bool more = it.next();
@@ -596,7 +595,6 @@ __global__ void __launch_bounds__(kThreads, 1)
     float* prev_slot = nullptr;   // where its unfinished rows go
     float* prev_ml = nullptr;
     int prev_rows = 0;
-    const float* prev_state = nullptr;  // what a prefix left of its rows
     for (;;) {
       if (more && it.len > 0 && !p.q_tma) {
         load_queries<TQ, kParts, N>(
@@ -654,26 +652,11 @@ __global__ void __launch_bounds__(kThreads, 1)
                 for (int m = 0; m < 4; ++m) at[k * kLatent + m * 128] = __uint_as_float(o[m][k]) * kv_scale;
               }
           } else {
-            if (prev_state != nullptr) {  // both shares of the result
-#pragma unroll
-              for (int k = 0; k < 16; ++k) {
-                const float keep = h0 + k < prev_rows ? mi.warp_sums[h0 + k] : 0.0f;
-                if (keep != 0.0f) {
-                  const float* at = prev_state + static_cast<int64_t>(h0 + k) * kLatent + d;
-#pragma unroll
-                  for (int m = 0; m < 4; ++m)
-                    o[m][k] = __float_as_uint(__uint_as_float(o[m][k]) * mi.inv[h0 + k] + at[m * 128] * keep);
-                } else {
-#pragma unroll
-                  for (int m = 0; m < 4; ++m) o[m][k] = __float_as_uint(__uint_as_float(o[m][k]) * mi.inv[h0 + k]);
-                }
-              }
-            }
 #pragma unroll
             for (int k = 0; k < 16; k += 2) {
               // even lanes write row k, odd lanes row k + 1, two neighbours' values each
               const int h = h0 + k + (lane & 1);
-              const float ia = prev_state != nullptr ? 1.0f : mi.inv[h0 + k], ib = prev_state != nullptr ? 1.0f : mi.inv[h0 + k + 1];
+              const float ia = mi.inv[h0 + k], ib = mi.inv[h0 + k + 1];
               TQ* at = out + out_at(min(h, prev_rows - 1)) + (d & ~1);
 #pragma unroll
               for (int m = 0; m < 4; ++m) {
@@ -876,46 +859,38 @@ __global__ void __launch_bounds__(kThreads, 1)
         for (int k = 0; k < 2 * kG; ++k) mi.factor[(k >> 1) * 8 + 2 * c + (k & 1)] = ref[k];
       }
       named_sync<kSoft>(1);
-      // where the rows go that are not finished here: a slot of the workspace, or the prefix's state
+      // where the rows go that are not finished here: a slot of the workspace, or the state of a pass
       float* slot = p.ws.slots + (static_cast<int64_t>(blockIdx.x) * 2 + (it.tile == 0 ? 1 : 0)) * p.slot_floats;
       float* ml = slot + p.rows_per_group * kLatent;
       if (kPrefix) n_rows = it.n_rows;
-      if (kPrefix && whole) {
-        slot = p.state + it.row0 * kLatent;
-        ml = p.state_ml + 2 * it.row0;
+      const int64_t first_row = kPrefix ? it.row0 : static_cast<int64_t>(it.b) * rows + g0;
+      const bool finished = whole && !keeps;
+      if (whole && keeps) {
+        slot = p.state + first_row * kLatent;
+        ml = p.state_ml + 2 * first_row;
       }
-      const int64_t first_row = static_cast<int64_t>(it.b) * rows + g0;
-      const bool joins = !kPrefix && whole && it.b >= covered.from && it.b < covered.to;
       if (tid < N) {
         const float sum = (mi.warp_sums[tid] + mi.warp_sums[N + tid]) + (mi.warp_sums[2 * N + tid] + mi.warp_sums[3 * N + tid]);
         const float r = mi.factor[tid];
-        if (kPrefix || !whole) {
-          if (tid < n_rows) *reinterpret_cast<float2*>(ml + 2 * tid) = make_float2(r, sum);
-        } else {
-          float lse = sum != 0.0f ? (r + log2f(sum)) * kLn2 : -INFINITY;
-          mi.inv[tid] = sum != 0.0f ? kv_scale / sum : 0.0f;
-          if (joins && tid < n_rows) {
-            const Joint x = joint_of(r, sum, p.state_ml + 2 * (first_row + tid));
-            mi.inv[tid] = x.mine * kv_scale;
-            mi.warp_sums[tid] = x.other;  // (this thread has read the sums there)
-            lse = x.lse;
-          }
-          if (tid < n_rows && p.lse != nullptr) p.lse[first_row + tid] = lse;
+        mi.inv[tid] = sum != 0.0f ? kv_scale / sum : 0.0f;
+        if (tid < n_rows) {
+          if (!finished) *reinterpret_cast<float2*>(ml + 2 * tid) = make_float2(r, sum);
+          else if (p.lse != nullptr) p.lse[first_row + tid] = sum != 0.0f ? (r + log2f(sum)) * kLn2 : -INFINITY;
         }
       }
-      if (!whole && it.tile == 0 && tid == 0) {
-        note.item = it.b;
-        note.parts = unit_of(it.last_piece(), share.total, share.units) - unit + 1;
-        if constexpr (kPrefix) note.tile = it.row_tile;
+      if (whole || it.tile == 0) {
+        const int parts = whole ? 0 : unit_of(it.last_piece(), share.total, share.units) - unit + 1;
+        if (keeps && tid < n_rows)
+          p.row_notes[first_row + tid] = {static_cast<uint16_t>(whole ? 0 : blockIdx.x), static_cast<uint16_t>(parts), tid};
+        if (!whole && tid == 0) note = {it.b, parts, keeps ? static_cast<int32_t>(first_row) : 0, keeps ? n_rows : 0};
       }
       named_sync<kSoft>(1);  // the rows' factors are there for the epilogue
       prev_b = it.b;
       prev_n = n;
-      prev_whole = !kPrefix && whole;
+      prev_whole = finished;
       prev_slot = slot;
       prev_ml = ml;
       prev_rows = n_rows;
-      prev_state = joins ? p.state + first_row * kLatent : nullptr;
       more = it.next();
     }
     if (tid == 0 && p.units > 1) p.ws.notes[blockIdx.x] = note;
@@ -925,6 +900,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   __syncthreads();
   tmem_fence_after();
   if (warp == 5) tmem_free(tmem, kColumns);
+  pass_exit<kPrefix>(p);
 }
 
 struct Maps {

@@ -7,9 +7,12 @@
 //
 // The prefix is a product of few entries with the rows of many requests, which
 // is bound by the tensor core from a few hundred rows on; the own entries are a
-// decode as before. Two passes: the first leaves (o1, m1, l1) of every row in the
-// workspace, in 32 bits (2 KB a row, written and read once, mostly in L2), the
-// second joins them as it finishes its rows.
+// decode as before. Two passes leave (o, m, l) of every row (mla_decode.cuh), in
+// 32 bits: 2 KB a row and pass, written and read once, mostly in L2. The join adds
+// them up, and the parts of rows whose keys several shares held, in their order.
+// The passes run beside each other where the first leaves SMs free. (Each with a
+// join of its own, the second's rows joined as they were finished: four launches
+// one after the other, 33 us for four requests behind 513 entries.)
 #include <algorithm>
 
 #include "mla_decode.cuh"
@@ -18,17 +21,222 @@
 namespace pmg_mla {
 namespace {
 
-// What lies behind the attention workspace: sums of all rows, references and
-// sums of weights, covered requests.
+// What a pass left.
+struct PassRows {
+  Workspace ws;
+  int64_t slot_floats;
+  int32_t slot_rows, stride, notes;  // rows of a slot, CTAs between the parts of a row, CTAs that may have noted one
+  const float* state;
+  const float* state_ml;
+  const RowNote* rows;
+};
+
+struct JoinParams {
+  PassRows pass[2];        // prefixes, own entries
+  const int32_t* covered;
+  int32_t rows, H, q_len, dv;
+  void* out;
+  int64_t or_stride, ot_stride, oh_stride;
+  float* lse;
+};
+
+// A warp takes a row's next 128 columns; rows that a pass left in more than
+// kJoinFew parts are taken by a whole CTA, from the list of the CTAs that noted
+// one, its warps the parts in turn.
+template <class TQ>
+__global__ void __launch_bounds__(kJoinThreads, kJoinCtasPerSm) shared_join_kernel(const __grid_constant__ JoinParams p) {
+  __shared__ float4 sums[kJoinThreads];
+  __shared__ float sums_l[kJoinWarps];
+  pdl_entry();
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  const int dv = p.dv, quarters = (dv + 127) / 128, per_req = p.q_len * p.H;
+  const bool vec = dv % 4 == 0;
+  const int covered0 = p.covered[0] * per_req, covered1 = p.covered[1] * per_req;
+  // which notes are of rows in many parts, looked up by all threads at once: thread t notes t, t + 256, ...
+  const int n0 = p.pass[0].notes, notes = n0 + p.pass[1].notes;
+  uint32_t mine = 0;
+#pragma unroll
+  for (int k = 0; k < 2 * kJoinNotes / kJoinThreads; ++k) {
+    const int i = tid + k * kJoinThreads;
+    if (i < notes) {
+      const JoinNote& note = p.pass[i < n0 ? 0 : 1].ws.notes[i < n0 ? i : i - n0];
+      if (note.item >= 0 && note.parts > kJoinFew) mine |= 1u << k;
+    }
+  }
+  // parts of a row: of its prefix, then of its own entries
+  struct Row {
+    RowNote note[2];
+    int n[2];
+  };
+  auto row_of = [&](int row) {
+    Row r;
+    const bool has = row >= covered0 && row < covered1;
+    r.note[0] = has ? p.pass[0].rows[row] : RowNote{0, 0, 0};
+    r.note[1] = p.pass[1].rows[row];
+    r.n[0] = has ? max(static_cast<int>(r.note[0].parts), 1) : 0;
+    r.n[1] = max(static_cast<int>(r.note[1].parts), 1);
+    return r;
+  };
+  // reference and sum of part i, and its columns d to d + 3
+  auto place = [&](const Row& r, int row, int i, const float*& ml) {
+    const int k = i < r.n[0] ? 0 : 1;
+    const PassRows& x = p.pass[k];
+    const RowNote& note = r.note[k];
+    i -= k == 0 ? 0 : r.n[0];
+    if (note.parts == 0) {
+      ml = x.state_ml + 2 * static_cast<int64_t>(row);
+      return x.state + static_cast<int64_t>(row) * dv;
+    }
+    // part 0 is the noting share's own end, the others begin their shares
+    const float* slot = x.ws.slots + ((note.cta + static_cast<int64_t>(i) * x.stride) * 2 + (i == 0 ? 1 : 0)) * x.slot_floats;
+    ml = slot + static_cast<int64_t>(x.slot_rows) * dv + 2 * note.row;
+    return slot + static_cast<int64_t>(note.row) * dv;
+  };
+  auto values = [&](const float* o, int d) {
+    float4 y = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+    if (vec) {
+      if (d < dv) y = *reinterpret_cast<const float4*>(o + d);
+    } else {
+      if (d < dv) y.x = o[d];
+      if (d + 1 < dv) y.y = o[d + 1];
+      if (d + 2 < dv) y.z = o[d + 2];
+      if (d + 3 < dv) y.w = o[d + 3];
+    }
+    return y;
+  };
+  auto scale = [](float4& a, float& l, float w) {
+    l *= w;
+    a.x *= w;
+    a.y *= w;
+    a.z *= w;
+    a.w *= w;
+  };
+  auto add = [](float4& a, float& l, float w, const float4& x, float part_l) {
+    l += w * part_l;
+    a.x += w * x.x;
+    a.y += w * x.y;
+    a.z += w * x.z;
+    a.w += w * x.w;
+  };
+  auto emit = [&](int row, int d, const float4& a, float top, float l) {
+    if (d >= dv) return;
+    if (d == 0 && p.lse != nullptr) p.lse[row] = l != 0.0f ? (top + log2f(l)) * kLn2 : -INFINITY;
+    const float inv = l != 0.0f ? 1.0f / l : 0.0f;
+    const int req = row / per_req, rr = row - req * per_req;
+    TQ* out = static_cast<TQ*>(p.out) + req * p.or_stride + (rr / p.H) * p.ot_stride + (rr % p.H) * p.oh_stride + d;
+    const float y[4] = {a.x * inv, a.y * inv, a.z * inv, a.w * inv};
+#pragma unroll
+    for (int k = 0; k < 4; ++k)
+      if (d + k < dv) out[k] = from_f<TQ>(y[k]);
+  };
+  for (int64_t x = static_cast<int64_t>(blockIdx.x) * kJoinWarps + warp; x < static_cast<int64_t>(p.rows) * quarters;
+       x += gridDim.x * kJoinWarps) {
+    const int row = static_cast<int>(x / quarters), d = static_cast<int>(x % quarters) * 128 + lane * 4;
+    const Row r = row_of(row);
+    if (r.n[0] > kJoinFew || r.n[1] > kJoinFew) continue;
+    // four parts at a time, all of their loads before any is used; every lane has the references and sums
+    float4 a = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+    float l = 0.0f, top = -INFINITY;
+    const int parts = r.n[0] + r.n[1];
+    for (int i0 = 0; i0 < parts; i0 += 4) {
+      float4 o[4];
+      float m[4], part_l[4];
+#pragma unroll
+      for (int k = 0; k < 4; ++k) {
+        m[k] = -INFINITY;
+        part_l[k] = 0.0f;
+        o[k] = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+        if (i0 + k < parts) {
+          const float* ml;
+          const float* from = place(r, row, i0 + k, ml);
+          m[k] = ml[0];  // (slots of odd rows and columns: not aligned to two)
+          part_l[k] = ml[1];
+          o[k] = values(from, d);
+        }
+      }
+      // (a part whose sum is 0 saw nothing: its reference may be anything; a NaN among the scores makes a sum of NaN, which counts)
+      float next = top;
+#pragma unroll
+      for (int k = 0; k < 4; ++k)
+        if (part_l[k] != 0.0f) next = fmaxf(next, m[k]);
+      if (l != 0.0f) scale(a, l, exp2f(top - next));
+      top = next;
+#pragma unroll
+      for (int k = 0; k < 4; ++k)
+        if (part_l[k] != 0.0f) add(a, l, exp2f(m[k] - top), o[k], part_l[k]);
+    }
+    emit(row, d, a, top, l);
+  }
+  // rows in many parts, if there are any (all of this is the same for a whole CTA)
+  if (!__syncthreads_or(mine != 0)) return;
+  __shared__ uint8_t many[2 * kJoinNotes];
+#pragma unroll
+  for (int k = 0; k < 2 * kJoinNotes / kJoinThreads; ++k) many[tid + k * kJoinThreads] = mine >> k & 1;
+  __syncthreads();
+  int at = 0;  // tasks before those of the note at hand: CTAs take them in turn
+  for (int i = 0; i < notes; ++i) {
+    if (!many[i]) continue;
+    const int k = i < n0 ? 0 : 1;
+    const JoinNote note = p.pass[k].ws.notes[k == 0 ? i : i - n0];
+    const int tasks = note.tile * quarters, begin = (static_cast<int>(blockIdx.x) - at % static_cast<int>(gridDim.x) + gridDim.x) % gridDim.x;
+    at += tasks;
+    for (int x = begin; x < tasks; x += gridDim.x) {
+      const int row = note.head + x / quarters, d = x % quarters * 128 + lane * 4;
+      const Row r = row_of(row);
+      if (k == 1 && r.n[0] > kJoinFew) continue;  // done with its prefix's
+      const int parts = r.n[0] + r.n[1];
+      float top = -INFINITY;
+      for (int y = lane; y < parts; y += 32) {
+        const float* ml;
+        place(r, row, y, ml);
+        if (ml[1] != 0.0f) top = fmaxf(top, ml[0]);
+      }
+#pragma unroll
+      for (int o = 16; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
+      float4 a = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+      float l = 0.0f;
+#pragma unroll 4
+      for (int y = warp; y < parts; y += kJoinWarps) {
+        const float* ml;
+        const float* from = place(r, row, y, ml);
+        const float m = ml[0], part_l = ml[1];
+        const float4 o = values(from, d);
+        if (part_l != 0.0f) add(a, l, exp2f(m - top), o, part_l);
+      }
+      sums[tid] = a;
+      if (lane == 0) sums_l[warp] = l;
+      __syncthreads();
+      if (warp == 0) {
+#pragma unroll
+        for (int w = 1; w < kJoinWarps; ++w) add(a, l, 1.0f, sums[w * 32 + lane], sums_l[w]);
+        emit(row, d, a, top, l);
+      }
+      __syncthreads();
+    }
+  }
+}
+
+// The workspace: one of the attention calls for each pass, then what both leave of all rows, and the covered requests.
 struct StateBytes {
-  int64_t sums, ml, covered, end;
-  StateBytes(int sms, int64_t rows, int32_t dv) {
-    sums = (workspace_bytes(sms) + 255) / 256 * 256;
-    ml = sums + (rows * dv * 4 + 255) / 256 * 256;
-    covered = ml + (rows * 8 + 255) / 256 * 256;
+  int64_t second, sums[2], ml[2], rows[2], covered, end;
+  StateBytes(int sms, int64_t n, int32_t dv) {
+    auto up = [](int64_t x) { return (x + 255) / 256 * 256; };
+    second = up(workspace_bytes(sms));
+    int64_t at = 2 * second;
+    for (int i = 0; i < 2; ++i) {
+      sums[i] = at;
+      ml[i] = up(sums[i] + n * dv * 4);
+      rows[i] = up(ml[i] + n * 8);
+      at = up(rows[i] + n * static_cast<int64_t>(sizeof(RowNote)));
+    }
+    covered = at;
     end = covered + 256;
   }
 };
+
+PassRows rows_of(const DecodeParams& p) {
+  return {p.ws, p.slot_floats, p.rows_per_group, p.groups, p.units > 1 ? p.units * p.groups : 0, p.state, p.state_ml, p.row_notes};
+}
 
 }  // namespace
 }  // namespace pmg_mla
@@ -70,20 +278,40 @@ extern "C" int pmg_latent_decode_shared(
   const StateBytes at(sms, rows, latent_dim);
   if (workspace_bytes_given < at.end) return PMG_ERR_ARG;
   p.ws = workspace_at(workspace, sms);
-  if (num_groups > 0) {
-    uint8_t* base = static_cast<uint8_t*>(workspace);
-    p.state = reinterpret_cast<float*>(base + at.sums);
-    p.state_ml = reinterpret_cast<float*>(base + at.ml);
-    p.covered = reinterpret_cast<int32_t*>(base + at.covered);
-    DecodeParams prefix = p;
-    prefix.cu = cu_groups;
-    prefix.reqs = num_reqs;
-    prefix.R = num_groups;
-    prefix.bt = prefix_table;
-    prefix.bt_stride = prefix_table_stride;
-    prefix.seq_lens = prefix_lens;
-    st = run_prefix(prefix, q_dtype, cache_dtype, sms, stream, options);
-    if (st != PMG_OK) return st;
-  }
-  return run_decode(p, q_dtype, cache_dtype, sms, stream, options);
+  if (num_groups == 0) return decode_alone(p, q_dtype, cache_dtype, sms, stream, options);
+  uint8_t* base = static_cast<uint8_t*>(workspace);
+  auto keep = [&](DecodeParams& x, int i) {
+    x.ws = workspace_at(base + i * at.second, sms);
+    x.state = reinterpret_cast<float*>(base + at.sums[i]);
+    x.state_ml = reinterpret_cast<float*>(base + at.ml[i]);
+    x.row_notes = reinterpret_cast<RowNote*>(base + at.rows[i]);
+    x.covered = reinterpret_cast<int32_t*>(base + at.covered);
+  };
+  DecodeParams prefix = p;
+  prefix.cu = cu_groups;
+  prefix.reqs = num_reqs;
+  prefix.R = num_groups;
+  prefix.bt = prefix_table;
+  prefix.bt_stride = prefix_table_stride;
+  prefix.seq_lens = prefix_lens;
+  keep(prefix, 0);
+  keep(p, 1);
+  st = run_prefix(prefix, q_dtype, cache_dtype, sms, stream, options);
+  if (st == PMG_OK) st = run_decode(p, q_dtype, cache_dtype, sms, stream, options);
+  if (st != PMG_OK) return st;
+  JoinParams j{};
+  j.pass[0] = rows_of(prefix);
+  j.pass[1] = rows_of(p);
+  j.covered = p.covered;
+  j.rows = static_cast<int32_t>(rows);
+  j.H = heads;
+  j.q_len = q_len;
+  j.dv = latent_dim;
+  j.out = out;
+  j.or_stride = out_req_stride;
+  j.ot_stride = out_token_stride;
+  j.oh_stride = out_head_stride;
+  j.lse = lse;
+  const auto join = q_dtype == PMG_BF16 ? shared_join_kernel<bf16> : q_dtype == PMG_FP16 ? shared_join_kernel<f16> : shared_join_kernel<float>;
+  return launch(join, dim3(static_cast<unsigned>(kJoinCtasPerSm * sms)), kJoinThreads, 0, stream, j);
 }

@@ -169,7 +169,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     *reinterpret_cast<uint4*>(smem + kQAt + c * kQPiece + rpc * 128 + y * 16) = make_uint4(0, 0, 0, 0);
   }
   fence_async_smem();
-  pdl_entry();
+  pass_entry<true>(p);
   const int unit = blockIdx.x >> 1;
   const Share share = find_share([&](int b) { return prefix_pieces<kItemCost>(p, b); }, p.R, unit, p.units, mi.scratch, mi.found);
   if (blockIdx.x == 0) note_covered(p, tid, kThreads, *reinterpret_cast<int32_t*>(mi.scratch));
@@ -545,10 +545,11 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
         }
       }
       tmem_fence_before();
-      if (!whole && it.tile == 0 && tid == 0) {
-        note.item = it.b;
-        note.parts = unit_of(it.last_piece(), share.total, share.units) - unit + 1;
-        note.tile = it.row_tile;
+      if (whole || it.tile == 0) {
+        const int parts = whole ? 0 : unit_of(it.last_piece(), share.total, share.units) - unit + 1;
+        if (half == 0 && row < n_rows)
+          p.row_notes[it.row0 + first_row + row] = {static_cast<uint16_t>(whole ? 0 : unit), static_cast<uint16_t>(parts), first_row + row};
+        if (!whole && tid == 0) note = {it.b, parts, static_cast<int32_t>(it.row0), it.n_rows};
       }
     }
     if (tid == 0 && rank == 0) p.ws.notes[unit] = note;
