@@ -40,9 +40,11 @@ struct JoinParams {
   float* lse;
 };
 
-// A warp takes a row's next 128 columns; rows that a pass left in more than
-// kJoinFew parts are taken by a whole CTA, from the list of the CTAs that noted
-// one, its warps the parts in turn.
+// A warp takes a row's next 128 columns. Rows that a pass left in many parts are
+// taken by a whole CTA, from the list of the CTAs that noted one, its warps the
+// parts in turn: more than kJoinFew for each time that the CTAs would have to
+// take a task (a CTA takes about 3 us a task, a warp 1 us and 0.2 a part; 1024 rows
+// of 10 parts took 20 us as tasks of CTAs).
 template <class TQ>
 __global__ void __launch_bounds__(kJoinThreads, kJoinCtasPerSm) shared_join_kernel(const __grid_constant__ JoinParams p) {
   __shared__ float4 sums[kJoinThreads];
@@ -54,13 +56,15 @@ __global__ void __launch_bounds__(kJoinThreads, kJoinCtasPerSm) shared_join_kern
   const int covered0 = p.covered[0] * per_req, covered1 = p.covered[1] * per_req;
   // which notes are of rows in many parts, looked up by all threads at once: thread t notes t, t + 256, ...
   const int n0 = p.pass[0].notes, notes = n0 + p.pass[1].notes;
+  const int64_t turns = (static_cast<int64_t>(p.rows) * quarters + gridDim.x - 1) / gridDim.x;
+  const int few = static_cast<int>(min(kJoinFew * turns, static_cast<int64_t>(INT32_MAX)));
   uint32_t mine = 0;
 #pragma unroll
   for (int k = 0; k < 2 * kJoinNotes / kJoinThreads; ++k) {
     const int i = tid + k * kJoinThreads;
     if (i < notes) {
       const JoinNote& note = p.pass[i < n0 ? 0 : 1].ws.notes[i < n0 ? i : i - n0];
-      if (note.item >= 0 && note.parts > kJoinFew) mine |= 1u << k;
+      if (note.item >= 0 && note.parts > few) mine |= 1u << k;
     }
   }
   // parts of a row: of its prefix, then of its own entries
@@ -81,7 +85,7 @@ __global__ void __launch_bounds__(kJoinThreads, kJoinCtasPerSm) shared_join_kern
   auto place = [&](const Row& r, int row, int i, const float*& ml) {
     const int k = i < r.n[0] ? 0 : 1;
     const PassRows& x = p.pass[k];
-    const RowNote& note = r.note[k];
+    const RowNote note = k == 0 ? r.note[0] : r.note[1];
     i -= k == 0 ? 0 : r.n[0];
     if (note.parts == 0) {
       ml = x.state_ml + 2 * static_cast<int64_t>(row);
@@ -133,16 +137,17 @@ __global__ void __launch_bounds__(kJoinThreads, kJoinCtasPerSm) shared_join_kern
        x += gridDim.x * kJoinWarps) {
     const int row = static_cast<int>(x / quarters), d = static_cast<int>(x % quarters) * 128 + lane * 4;
     const Row r = row_of(row);
-    if (r.n[0] > kJoinFew || r.n[1] > kJoinFew) continue;
-    // four parts at a time, all of their loads before any is used; every lane has the references and sums
+    if (r.n[0] > few || r.n[1] > few) continue;
+    // so many parts at a time, all of their loads before any is used; every lane has the references and sums
     float4 a = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
     float l = 0.0f, top = -INFINITY;
     const int parts = r.n[0] + r.n[1];
-    for (int i0 = 0; i0 < parts; i0 += 4) {
-      float4 o[4];
-      float m[4], part_l[4];
+    constexpr int kAhead = 4;
+    for (int i0 = 0; i0 < parts; i0 += kAhead) {
+      float4 o[kAhead];
+      float m[kAhead], part_l[kAhead];
 #pragma unroll
-      for (int k = 0; k < 4; ++k) {
+      for (int k = 0; k < kAhead; ++k) {
         m[k] = -INFINITY;
         part_l[k] = 0.0f;
         o[k] = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
@@ -157,33 +162,45 @@ __global__ void __launch_bounds__(kJoinThreads, kJoinCtasPerSm) shared_join_kern
       // (a part whose sum is 0 saw nothing: its reference may be anything; a NaN among the scores makes a sum of NaN, which counts)
       float next = top;
 #pragma unroll
-      for (int k = 0; k < 4; ++k)
+      for (int k = 0; k < kAhead; ++k)
         if (part_l[k] != 0.0f) next = fmaxf(next, m[k]);
       if (l != 0.0f) scale(a, l, exp2f(top - next));
       top = next;
 #pragma unroll
-      for (int k = 0; k < 4; ++k)
+      for (int k = 0; k < kAhead; ++k)
         if (part_l[k] != 0.0f) add(a, l, exp2f(m[k] - top), o[k], part_l[k]);
     }
     emit(row, d, a, top, l);
   }
   // rows in many parts, if there are any (all of this is the same for a whole CTA)
   if (!__syncthreads_or(mine != 0)) return;
-  __shared__ uint8_t many[2 * kJoinNotes];
+  __shared__ uint8_t is_many[2 * kJoinNotes];
+  __shared__ uint16_t many[2 * kJoinNotes];
+  __shared__ int n_many;
 #pragma unroll
-  for (int k = 0; k < 2 * kJoinNotes / kJoinThreads; ++k) many[tid + k * kJoinThreads] = mine >> k & 1;
+  for (int k = 0; k < 2 * kJoinNotes / kJoinThreads; ++k) is_many[tid + k * kJoinThreads] = mine >> k & 1;
+  __syncthreads();
+  if (warp == 0) {  // in the order of the notes
+    int n = 0;
+    for (int i0 = 0; i0 < notes; i0 += 32) {
+      const bool one = is_many[i0 + lane];
+      const uint32_t ones = __ballot_sync(0xffffffffu, one);
+      if (one) many[n + __popc(ones & ((1u << lane) - 1))] = static_cast<uint16_t>(i0 + lane);
+      n += __popc(ones);
+    }
+    if (lane == 0) n_many = n;
+  }
   __syncthreads();
   int at = 0;  // tasks before those of the note at hand: CTAs take them in turn
-  for (int i = 0; i < notes; ++i) {
-    if (!many[i]) continue;
-    const int k = i < n0 ? 0 : 1;
+  for (int y = 0; y < n_many; ++y) {
+    const int i = many[y], k = i < n0 ? 0 : 1;
     const JoinNote note = p.pass[k].ws.notes[k == 0 ? i : i - n0];
     const int tasks = note.tile * quarters, begin = (static_cast<int>(blockIdx.x) - at % static_cast<int>(gridDim.x) + gridDim.x) % gridDim.x;
     at += tasks;
     for (int x = begin; x < tasks; x += gridDim.x) {
       const int row = note.head + x / quarters, d = x % quarters * 128 + lane * 4;
       const Row r = row_of(row);
-      if (k == 1 && r.n[0] > kJoinFew) continue;  // done with its prefix's
+      if (k == 1 && r.n[0] > few) continue;  // done with its prefix's
       const int parts = r.n[0] + r.n[1];
       float top = -INFINITY;
       for (int y = lane; y < parts; y += 32) {

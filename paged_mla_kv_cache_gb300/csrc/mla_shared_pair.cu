@@ -130,6 +130,13 @@ __device__ __forceinline__ void pair_commit(uint32_t bar) {
       : "memory");
 }
 
+// A whole sector: lanes write rows of their own.
+__device__ __forceinline__ void store32(float* to, const uint32_t* x) {
+  asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(to), "r"(x[0]), "r"(x[1]), "r"(x[2]), "r"(x[3]),
+               "r"(x[4]), "r"(x[5]), "r"(x[6]), "r"(x[7])
+               : "memory");
+}
+
 template <class T>
 __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     shared_pair_kernel(const __grid_constant__ DecodeParams p, const __grid_constant__ CUtensorMap map,
@@ -541,7 +548,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
         }
         if (row < n_rows) {
 #pragma unroll
-          for (int k = 0; k < 32; k += 4) *reinterpret_cast<uint4*>(out + c + k) = make_uint4(o[k], o[k + 1], o[k + 2], o[k + 3]);
+          for (int k = 0; k < 32; k += 8) store32(out + c + k, o + k);
         }
       }
       tmem_fence_before();
@@ -615,7 +622,7 @@ int prefix_pair(DecodeParams& p, int q_dtype, int sms, void* stream) {
   p.groups = 1;
   p.units = sms / 2;
   // a pair's slot is two CTAs'
-  p.slot_floats = static_cast<int64_t>(p.rows_per_group) * (kLatent + 2);
+  p.slot_floats = (static_cast<int64_t>(p.rows_per_group) * (kLatent + 2) + 7) / 8 * 8;
   static_assert(2 * kRows * (kLatent + 2) <= 2 * kSlotFloats, "fits");
   const CUtensorMapDataType type = q_dtype == PMG_BF16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT16;
   const int box_rows = gcd(p.B, kKeys);
