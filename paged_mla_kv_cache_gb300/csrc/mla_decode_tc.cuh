@@ -15,6 +15,6 @@ int prefix_tc(DecodeParams& p, int q_dtype, int cache_dtype, int sms, void* stre
 
 // A prefix pass on pairs of SMs (mla_shared_pair.cu), where prefix_tc would do as well.
 bool prefix_pair_takes(const DecodeParams& p, int q_dtype, int cache_dtype);
-int prefix_pair(DecodeParams& p, int q_dtype, int sms, void* stream);
+int prefix_pair(DecodeParams& p, int q_dtype, int cache_dtype, int sms, void* stream);
 
 }  // namespace pmg_mla

@@ -31,6 +31,7 @@
 
 #include "mla_decode.cuh"
 #include "mla_decode_tc.cuh"
+#include "mla_queries.cuh"
 #include "mla_sm103.cuh"
 
 namespace pmg_mla {
@@ -38,21 +39,36 @@ namespace {
 
 constexpr int kThreads = 256;
 constexpr int kSoft = 128;
-constexpr int kLatent = 512, kRope = 64, kEntry = kLatent + kRope;
+constexpr int kLatent = 512;               // and 64 rotated ones: kEntry
 constexpr int kRows = 64;                  // of a CTA
 constexpr int kKeys = kDecodeTile / 2;     // of a tile that a CTA holds whole
-constexpr int kKPiece = kKeys * 128;       // 64 values of them
+constexpr int kKPiece = kKeys * 128;       // 128 bytes of them
 constexpr int kQPiece = kRows * 128;
-constexpr int kQ = 9 * kQPiece, kK = 9 * kKPiece, kV = 2 * 4 * kKPiece, kP = kRows * 128;
-constexpr int kQAt = 0, kPAt = kQ, kStageAt = kQ + 2 * kP, kStage = kK + kV, kMiscAt = kStageAt + 2 * kStage;
-constexpr int kMisc = 2048;
-constexpr int kBytes = kMiscAt + kMisc + 1024;
-static_assert(kBytes <= 232448, "fits");
+constexpr int kMisc = 2560;
+
+// Shared memory, by the parts of a query: 1 for a 16-bit cache, for an e4m3 one 2 (bf16) or 3 (fp16).
+template <int kParts>
+struct Lay {
+  static constexpr bool kFp8 = kParts > 1;
+  static constexpr int kPieces = kFp8 ? 4 : 8;     // of the latent values
+  static constexpr int kWeights = kFp8 ? 3 : 1;    // parts of a weight
+  static constexpr int kQPart = (kPieces + 1) * kQPiece;
+  static constexpr int kK = (kPieces + 1) * kKPiece, kV = kPieces * kKPiece;  // (V: both halves' half of the values)
+  static constexpr int kStage = kK + kV;
+  // Weights of two tiles: 16-bit ones one behind the other, of e5m2 parts 64 bytes of a row each.
+  static constexpr int kPNext = kFp8 ? 64 : kRows * 128, kPPart = kRows * 128;
+  static constexpr int kPAt = kQPart * kParts;
+  static constexpr int kStageAt = kPAt + (kFp8 ? kWeights : 2) * kPPart;
+  static constexpr int kMiscAt = kStageAt + 2 * kStage;
+  static constexpr int kBytes = kMiscAt + kMisc + 512;
+  static_assert(kBytes <= 232448, "fits");
+};
 constexpr int kColumns = 512, kSAt = 256;  // O: 256 columns, then two S of 32
 
 struct Misc {
   uint64_t k_full[2], v_full[2], k_peer[2], v_peer[2], k_empty[2], v_empty[2], s_full[2], s_free[2], m_full[4], p_full[2], q_full, q_empty, end;
   uint64_t mask[4];    // entries of a tile that exist, by tile & 3
+  float factor[kRows]; // e4m3: what a row's raw scores are multiplied by
   union {
     struct {
       int64_t scratch[33], found[2];
@@ -115,12 +131,21 @@ __device__ __forceinline__ void pair_wait(uint32_t bar, uint32_t parity, uint32_
 }
 
 // All products of the kernel are a pair's.
+template <bool kFp8>
 __device__ __forceinline__ void pair_umma(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, bool add) {
-  asm volatile(
-      "{\n\t.reg .pred p;\n\tsetp.ne.u32 p, %4, 0;\n\t"
-      "tcgen05.mma.cta_group::2.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(d),
-      "l"(a), "l"(b), "r"(idesc), "r"(static_cast<uint32_t>(add))
-      : "memory");
+  if constexpr (kFp8) {
+    asm volatile(
+        "{\n\t.reg .pred p;\n\tsetp.ne.u32 p, %4, 0;\n\t"
+        "tcgen05.mma.cta_group::2.kind::f8f6f4 [%0], %1, %2, %3, p;\n\t}" ::"r"(d),
+        "l"(a), "l"(b), "r"(idesc), "r"(static_cast<uint32_t>(add))
+        : "memory");
+  } else {
+    asm volatile(
+        "{\n\t.reg .pred p;\n\tsetp.ne.u32 p, %4, 0;\n\t"
+        "tcgen05.mma.cta_group::2.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(d),
+        "l"(a), "l"(b), "r"(idesc), "r"(static_cast<uint32_t>(add))
+        : "memory");
+  }
 }
 // arrives at the same barrier of both CTAs when every product issued so far by this thread is done
 __device__ __forceinline__ void pair_commit(uint32_t bar) {
@@ -137,13 +162,15 @@ __device__ __forceinline__ void store32(float* to, const uint32_t* x) {
                : "memory");
 }
 
-template <class T>
+template <class T, int kParts>
 __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     shared_pair_kernel(const __grid_constant__ DecodeParams p, const __grid_constant__ CUtensorMap map,
                        const __grid_constant__ CUtensorMap rope_map, const __grid_constant__ CUtensorMap q_map, int box_rows) {
-  extern __shared__ uint8_t raw[];
-  uint8_t* smem = raw + ((1024 - (smem_u32(raw) & 1023)) & 1023);
-  Misc& mi = *reinterpret_cast<Misc*>(smem + kMiscAt);
+  using L = Lay<kParts>;
+  constexpr bool kFp8 = L::kFp8;
+  constexpr int kK = L::kK, kStage = L::kStage, kStageAt = L::kStageAt, kPieces = L::kPieces;
+  extern __shared__ __align__(1024) uint8_t smem[];
+  Misc& mi = *reinterpret_cast<Misc*>(smem + L::kMiscAt);
   const uint32_t base = smem_u32(smem);
   const int tid = threadIdx.x, warp = __shfl_sync(0xffffffffu, tid >> 5, 0), lane = tid & 31;
   const uint32_t rank = cta_rank();
@@ -155,7 +182,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
       mbar_init(smem_u32(&mi.p_full[i]), 8);
     }
     for (int i = 0; i < 4; ++i) mbar_init(smem_u32(&mi.m_full[i]), 1);
-    mbar_init(smem_u32(&mi.q_full), 1);
+    mbar_init(smem_u32(&mi.q_full), kFp8 ? kSoft / 32 : 1);
     mbar_init(smem_u32(&mi.q_empty), 1);
     mbar_init(smem_u32(&mi.end), 1);
     mi.stop = mi.never = 0;
@@ -163,7 +190,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     mbar_fence_init();
     tma_prefetch(&map);
     tma_prefetch(&rope_map);
-    tma_prefetch(&q_map);
+    if (!kFp8) tma_prefetch(&q_map);
+    if (base & 1023) mi.stop = 1;  // (the swizzled tiles' alignment; the attribute sees to it)
   }
   if (warp == 5) {
     asm volatile("tcgen05.alloc.cta_group::2.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(smem_u32(&mi.tmem)), "n"(kColumns) : "memory");
@@ -171,9 +199,9 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
   }
   const int rpc = p.rows_per_group / 2;  // rows of a CTA
   // rows of queries that no copy fills: 0
-  for (int i = tid; i < 9 * (kRows - rpc) * 8; i += kThreads) {
+  for (int i = tid; i < (kFp8 ? 0 : 9 * (kRows - rpc) * 8); i += kThreads) {
     const int c = i / ((kRows - rpc) * 8), y = i % ((kRows - rpc) * 8);
-    *reinterpret_cast<uint4*>(smem + kQAt + c * kQPiece + rpc * 128 + y * 16) = make_uint4(0, 0, 0, 0);
+    *reinterpret_cast<uint4*>(smem + c * kQPiece + rpc * 128 + y * 16) = make_uint4(0, 0, 0, 0);
   }
   fence_async_smem();
   pass_entry<true>(p);
@@ -185,9 +213,9 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
   pair_sync();
   tmem_fence_after();
   const uint32_t tmem = mi.tmem, stop = smem_u32(&mi.stop), peer = at_rank(stop, rank ^ 1);
-  constexpr int kFmt = std::is_same<T, bf16>::value ? 1 : 0;
+  constexpr int kFmt = !kFp8 && std::is_same<T, bf16>::value ? 1 : 0;
   constexpr uint32_t kIdescS = umma_idesc(kFmt, kFmt, 0, 0, 128, kDecodeTile);
-  constexpr uint32_t kIdescO = umma_idesc(kFmt, kFmt, 0, 1, 128, 256);
+  constexpr uint32_t kIdescO = umma_idesc(kFp8 ? 1 : kFmt, kFmt, 0, 1, 128, 256);  // e5m2 weights of e4m3 values
   const uint32_t k_full = smem_u32(&mi.k_full[0]), v_full = smem_u32(&mi.v_full[0]);
   const uint32_t k_empty = smem_u32(&mi.k_empty[0]), v_empty = smem_u32(&mi.v_empty[0]);
   PrefixItems<kItemCost> it(p, share);
@@ -235,7 +263,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
             if (goods >> s & 1) mask |= ((1ull << box_rows) - 1) << (s * box_rows);
           const int left = it.len - (it.tile + i) * kDecodeTile;
           if (left < 64) mask &= (1ull << left) - 1;
-          if (i == 0) {  // the row tile's queries, once the products with the ones before are done
+          if (!kFp8 && i == 0) {  // the row tile's queries, once the products with the ones before are done
             if (items > 0) wait(smem_u32(&mi.q_empty), (items - 1) & 1);
             ++items;
             if (elect_one()) {
@@ -245,7 +273,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
               mbar_expect(bar, static_cast<uint32_t>(rpc) * kEntry * 2);
 #pragma unroll 1
               for (int c = 0; c < 9; ++c)
-                tma_load_4d(base + kQAt + c * kQPiece, &q_map, bar, 64 * c, static_cast<int>(r0 % p.H), token % p.q_tma, token / p.q_tma);
+                tma_load_4d(base + c * kQPiece, &q_map, bar, 64 * c, static_cast<int>(r0 % p.H), token % p.q_tma, token / p.q_tma);
             }
             __syncwarp();
           }
@@ -256,7 +284,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
             // the softmax warps had read the scores, and the mask, of another two before.
             mi.mask[t & 3] = mask;  // by the lane that arrives
             mbar_arrive(smem_u32(&mi.m_full[t & 3]));
-            mbar_expect(k_full + 8 * stage, static_cast<uint32_t>(n_mine * box_rows) * (kEntry * 2));
+            mbar_expect(k_full + 8 * stage, static_cast<uint32_t>(n_mine * box_rows) * ((kPieces + 1) * 128));
           }
           __syncwarp();
 #pragma unroll 1
@@ -266,30 +294,30 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
               const uint32_t dst = k_at + s * box_rows * 128, bar = k_full + 8 * stage;
               if (box_rows == kKeys) {
                 tma_load_4d(dst, &map, bar, 0, srow, 0, sid);
-                tma_load_4d(dst + 4 * kKPiece, &map, bar, 0, srow, 4, sid);
+                tma_load_4d(dst + kPieces / 2 * kKPiece, &map, bar, 0, srow, kPieces / 2, sid);
               } else {
 #pragma unroll 1
-                for (int c = 0; c < 8; ++c) tma_load_4d(dst + c * kKPiece, &map, bar, 0, srow, c, sid);
+                for (int c = 0; c < kPieces; ++c) tma_load_4d(dst + c * kKPiece, &map, bar, 0, srow, c, sid);
               }
-              tma_load_3d(dst + 8 * kKPiece, &rope_map, bar, kLatent, srow, sid);
+              tma_load_3d(dst + kPieces * kKPiece, &rope_map, bar, kLatent, srow, sid);
             }
             __syncwarp();
           }
         } else {
           wait(v_empty + 8 * stage, parity);
-          if (elect_one()) mbar_expect(v_full + 8 * stage, static_cast<uint32_t>(n_boxes * box_rows) * kLatent);
+          if (elect_one()) mbar_expect(v_full + 8 * stage, static_cast<uint32_t>(n_boxes * box_rows) * (kPieces / 2 * 128));
           __syncwarp();
 #pragma unroll 1
           for (int s = 0; s < n_boxes; ++s) {
             const int sid = __shfl_sync(0xffffffffu, id, s), srow = __shfl_sync(0xffffffffu, row, s);
             if (elect_one()) {
-              const uint32_t dst = v_at + (s / half) * (4 * kKPiece) + (s % half) * box_rows * 128, bar = v_full + 8 * stage;
-              const int c0 = static_cast<int>(rank) * 4;
+              const uint32_t dst = v_at + (s / half) * (kPieces / 2 * kKPiece) + (s % half) * box_rows * 128, bar = v_full + 8 * stage;
+              const int c0 = static_cast<int>(rank) * (kPieces / 2);
               if (box_rows == kKeys) {
                 tma_load_4d(dst, &map, bar, 0, srow, c0, sid);
               } else {
 #pragma unroll 1
-                for (int c = 0; c < 4; ++c) tma_load_4d(dst + c * kKPiece, &map, bar, 0, srow, c0 + c, sid);
+                for (int c = 0; c < kPieces / 2; ++c) tma_load_4d(dst + c * kKPiece, &map, bar, 0, srow, c0 + c, sid);
               }
             }
             __syncwarp();
@@ -335,15 +363,18 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
         __syncwarp();
         tmem_fence_after();
         if (elect_one()) {
-          const uint64_t pa = umma_desc(base + kPAt + stage * kP, 16, 1024);
+          const uint64_t pa = umma_desc(base + L::kPAt + stage * L::kPNext, 16, 1024);
+          const uint32_t v = base + kStageAt + stage * kStage + kK;
+          constexpr int kSteps = kFp8 ? 1 : 2, kStep = 32 / kSteps;  // products along a half's entries, entries of one
 #pragma unroll
           for (int n = 0; n < 2; ++n)
 #pragma unroll
-            for (int k = 0; k < 4; ++k) {  // 16 entries each: two of the first half, two of the second
-              const uint64_t vb = umma_desc(base + kStageAt + stage * kStage + kK + (k >> 1) * (4 * kKPiece) + n * (2 * kKPiece) +
-                                                (k & 1) * 2048,
+            for (int k = 0; k < 2 * kSteps; ++k) {
+              const uint64_t vb = umma_desc(v + k / kSteps * (kPieces / 2 * kKPiece) + n * (kPieces / 4 * kKPiece) + k % kSteps * (kStep * 128),
                                             kKPiece, 1024);
-              pair_umma(tmem + n * 128, pa + 2 * k, vb, kIdescO, !first || k > 0);
+#pragma unroll
+              for (int x = 0; x < L::kWeights; ++x)
+                pair_umma<kFp8>(tmem + n * 128, pa + 2 * k + x * (L::kPPart / 16), vb, kIdescO, !first || k > 0 || x > 0);
             }
           pair_commit(v_empty + 8 * stage);
         }
@@ -355,6 +386,9 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
 #pragma unroll 1
         for (int i = 0; i < it.n; ++i, ++t) {
           const uint32_t stage = t & 1, parity = t >> 1 & 1;
+          // (queries that the softmax warps convert come after the row tile before them, its last product too)
+          const bool early = kFp8 && i == 0;
+          if (early && t > 0) values(t - 1);
           if (i == 0) wait(smem_u32(&mi.q_full), q);
           // (the lanes wait for one barrier each: one after the other, each took 80 clocks also where it was there)
           wait((lane == 0 ? k_full : lane == 1 ? k_peer : s_free) + 8 * stage, lane < 2 ? parity : parity ^ 1);
@@ -363,18 +397,21 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
           if (elect_one()) {
             const uint32_t d = tmem + kSAt + stage * kKeys;
 #pragma unroll
-            for (int c = 0; c < 9; ++c) {
-              const uint64_t qa = umma_desc(base + kQAt + c * kQPiece, 16, 1024);
+            for (int c = 0; c <= kPieces; ++c) {
+              const uint64_t qa = umma_desc(base + c * kQPiece, 16, 1024);
               const uint64_t kb = umma_desc(base + kStageAt + stage * kStage + c * kKPiece, 16, 1024);
 #pragma unroll
-              for (int k = 0; k < 4; ++k) pair_umma(d, qa + 2 * k, kb + 2 * k, kIdescS, c > 0 || k > 0);
+              for (int k = 0; k < (kFp8 && c == kPieces ? 2 : 4); ++k)  // 32 bytes each; an e4m3 entry's rotated values are 64
+#pragma unroll
+                for (int x = 0; x < kParts; ++x)
+                  pair_umma<kFp8>(d, qa + 2 * k + x * (L::kQPart / 16), kb + 2 * k, kIdescS, c > 0 || k > 0 || x > 0);
             }
             pair_commit(k_empty + 8 * stage);
             pair_commit(s_full + 8 * stage);
             if (i + 1 == it.n) pair_commit(smem_u32(&mi.q_empty));
           }
           __syncwarp();
-          if (t > 0) values(t - 1);
+          if (!early && t > 0) values(t - 1);
           first = i == 0;
         }
       }
@@ -386,10 +423,13 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     }
   } else {
     // ---- softmax and epilogue ----
-    const float factor = p.sm_scale * kLog2e;
+    const float kv_scale = kFp8 && p.scale != nullptr ? *p.scale : 1.0f;
+    float factor = p.sm_scale * kLog2e * kv_scale;
+    const float all_rows = factor;
     constexpr bool kF16 = std::is_same<T, f16>::value;
-    constexpr float kCap = kF16 ? 15.0f : 8.0f;    // weights stay below 2^kCap
-    constexpr float kPlace = kF16 ? 8.0f : 0.0f;   // where a reference puts the largest
+    constexpr float kCap = kFp8 ? 15.5f : kF16 ? 15.0f : 8.0f;    // weights stay below 2^kCap
+    constexpr float kFirst = kFp8 ? 11.0f : kF16 ? 8.0f : 0.0f;   // where a first reference puts the largest
+    constexpr float kLater = kFp8 ? 13.0f : kF16 ? 8.0f : 0.0f;   // where a later one does
     const uint32_t lanes = static_cast<uint32_t>(warp * 32) << 16;
     const int row = tid & (kRows - 1), half = tid >> 6;  // the thread's row, and which half of its entries and latent values
     const uint32_t s_free = smem_u32(&mi.s_free[0]), p_full = smem_u32(&mi.p_full[0]);
@@ -401,7 +441,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
         else pair_arrive(bar0);
       }
     };
-    uint8_t* p_row = smem + kPAt + row * 128;
+    uint8_t* p_row = smem + L::kPAt + row * 128;
     JoinNote note{-1, 0, 0, 0};
     uint32_t t = 0;
     int item = 0;
@@ -411,6 +451,21 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     };
     for (; it.next(); ++item) {
       float ref = -INFINITY, l = 0.0f;
+      const int first_row = static_cast<int>(rank) * rpc;
+      const int n_rows = min(rpc, it.n_rows - first_row);
+      if (kFp8 && it.n > 0) {  // (all products with the queries before are done: their scores have been read)
+        load_queries<T, kParts, kRows>(
+            [&](int r) {
+              const int64_t rr = it.row0 + first_row + r, t = rr / p.H;
+              return static_cast<const T*>(p.q) + t / p.q_len * p.qr_stride + t % p.q_len * p.qt_stride + rr % p.H * p.qh_stride;
+            },
+            n_rows, smem, mi, all_rows);
+        fence_async_smem();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(smem_u32(&mi.q_full));
+        named_sync<kSoft>(1);
+        factor = mi.factor[row];
+      }
 #pragma unroll 1
       for (int i = 0; i < it.n; ++i, ++t) {
         const uint32_t stage = t & 1, parity = t >> 1 & 1;
@@ -430,7 +485,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
         alignas(8) float x[32];
         // Scores less the reference, two at a time. The first tile's reference is -inf, which raises it whatever comes; where
         // a score may be -inf too, it takes the other way.
-        const bool all = mask == 0xffffffffu && factor > 0.0f;  // (the same in a warp)
+        const bool all = mask == 0xffffffffu && factor > 0.0f;
         float2* x2 = reinterpret_cast<float2*>(x);
         float over = -INFINITY;
         if (all) {
@@ -453,7 +508,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
           for (int k = 0; k < 32; ++k) top = fmaxf(top, s[k] == -INFINITY ? -INFINITY : s[k] * factor);
           mi.tops[tid] = top;
           named_sync<kSoft>(1);
-          top = fmaxf(top, mi.tops[tid ^ kRows]) - kPlace;
+          top = fmaxf(top, mi.tops[tid ^ kRows]) - (ref == -INFINITY ? kFirst : kLater);
           named_sync<kSoft>(1);  // (before the place is written again)
           float a = 1.0f;
           if (top > ref) {
@@ -493,19 +548,40 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
         if (left < kDecodeTile) {
           wait(v_full + 8 * stage, parity);
           uint8_t* v = smem + kStageAt + stage * kStage + kK;
-          for (int y = tid; y < (kDecodeTile - left) * 32; y += kSoft) {
-            const int key = left + (y >> 5), piece = y >> 3 & 3;
-            *reinterpret_cast<uint4*>(v + (key / kKeys) * (4 * kKPiece) + piece * kKPiece + (key % kKeys) * 128 + (y & 7) * 16) =
+          constexpr int kUnits = kPieces / 2 * 8;  // of 16 bytes, of an entry
+          for (int y = tid; y < (kDecodeTile - left) * kUnits; y += kSoft) {
+            const int key = left + y / kUnits, u = y % kUnits;
+            *reinterpret_cast<uint4*>(v + (key / kKeys) * (kPieces / 2 * kKPiece) + (u >> 3) * kKPiece + (key % kKeys) * 128 + (u & 7) * 16) =
                 make_uint4(0, 0, 0, 0);
           }
         }
         // the product two tiles before has read its weights
         if (t >= 2) wait(v_empty + 8 * stage, parity ^ 1);
+        if constexpr (!kFp8) {
 #pragma unroll
-        for (int j = 0; j < 4; ++j)
-          *reinterpret_cast<uint4*>(p_row + stage * kP + (((4 * half + j) ^ (row & 7)) << 4)) =
-              make_uint4(pack2<T>(x[8 * j], x[8 * j + 1]), pack2<T>(x[8 * j + 2], x[8 * j + 3]), pack2<T>(x[8 * j + 4], x[8 * j + 5]),
-                         pack2<T>(x[8 * j + 6], x[8 * j + 7]));
+          for (int j = 0; j < 4; ++j)
+            *reinterpret_cast<uint4*>(p_row + stage * L::kPNext + (((4 * half + j) ^ (row & 7)) << 4)) =
+                make_uint4(pack2<T>(x[8 * j], x[8 * j + 1]), pack2<T>(x[8 * j + 2], x[8 * j + 3]),
+                           pack2<T>(x[8 * j + 4], x[8 * j + 5]), pack2<T>(x[8 * j + 6], x[8 * j + 7]));
+        } else {
+#pragma unroll
+          for (int j = 0; j < 2; ++j) {
+            uint32_t w[3][4];
+#pragma unroll
+            for (int k = 0; k < 4; ++k) {
+              uint32_t a = pack2<f16>(x[16 * j + 4 * k], x[16 * j + 4 * k + 1]), b = pack2<f16>(x[16 * j + 4 * k + 2], x[16 * j + 4 * k + 3]);
+#pragma unroll
+              for (int part = 0; part < 3; ++part) {
+                const uint32_t lo = part < 2 ? e5m2_cut(a) : e5m2_last(a), hi = part < 2 ? e5m2_cut(b) : e5m2_last(b);
+                w[part][k] = (lo & 0xffff) | hi << 16;
+              }
+            }
+#pragma unroll
+            for (int part = 0; part < 3; ++part)
+              *reinterpret_cast<uint4*>(p_row + part * L::kPPart + (((4 * stage + 2 * half + j) ^ (row & 7)) << 4)) =
+                  make_uint4(w[part][0], w[part][1], w[part][2], w[part][3]);
+          }
+        }
         fence_async_smem();
         __syncwarp();
         arrive(p_full + 8 * stage, p_full0 + 8 * stage);
@@ -517,8 +593,6 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
       named_sync<kSoft>(1);
       const bool whole = it.n == it.tiles;
       // where the rows go: a slot of the workspace, or the state
-      const int first_row = static_cast<int>(rank) * rpc;
-      const int n_rows = min(rpc, it.n_rows - first_row);
       float* to = p.ws.slots + (static_cast<int64_t>(unit) * 2 + (it.tile == 0 ? 1 : 0)) * p.slot_floats;
       float* ml = to + p.rows_per_group * kLatent;
       if (whole) {
@@ -545,6 +619,10 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
         } else {
 #pragma unroll
           for (int k = 0; k < 32; ++k) o[k] = 0;
+        }
+        if constexpr (kFp8) {
+#pragma unroll
+          for (int k = 0; k < 32; ++k) o[k] = __float_as_uint(__uint_as_float(o[k]) * kv_scale);
         }
         if (row < n_rows) {
 #pragma unroll
@@ -580,12 +658,12 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
   }
 }
 
-template <class T>
+template <class T, int kParts>
 int run(const DecodeParams& p, const CUtensorMap& latent, const CUtensorMap& rope, const CUtensorMap& q, int box_rows, void* stream) {
-  auto k = shared_pair_kernel<T>;
-  const int st = allow_smem(reinterpret_cast<const void*>(k), kBytes);
+  auto k = shared_pair_kernel<T, kParts>;
+  const int st = allow_smem(reinterpret_cast<const void*>(k), Lay<kParts>::kBytes);
   if (st != PMG_OK) return st;
-  return launch(k, dim3(static_cast<unsigned>(2 * p.units)), kThreads, kBytes, stream, p, latent, rope, q, box_rows);
+  return launch(k, dim3(static_cast<unsigned>(2 * p.units)), kThreads, Lay<kParts>::kBytes, stream, p, latent, rope, q, box_rows);
 }
 
 int gcd(int a, int b) { return b == 0 ? a : gcd(b, a % b); }
@@ -613,28 +691,36 @@ static QueryBox query_box(const DecodeParams& p) {
 }
 
 bool prefix_pair_takes(const DecodeParams& p, int q_dtype, int cache_dtype) {
-  return cache_dtype == q_dtype && static_cast<int64_t>(p.reqs) * p.q_len * p.H > kRows && query_box(p).rows > 0;
+  return static_cast<int64_t>(p.reqs) * p.q_len * p.H > kRows && (cache_dtype == PMG_FP8_E4M3 || query_box(p).rows > 0);
 }
 
-int prefix_pair(DecodeParams& p, int q_dtype, int sms, void* stream) {
-  const QueryBox qb = query_box(p);
+int prefix_pair(DecodeParams& p, int q_dtype, int cache_dtype, int sms, void* stream) {
+  const bool fp8 = cache_dtype == PMG_FP8_E4M3;  // whose queries the softmax warps convert, row by row
+  const QueryBox qb = fp8 ? QueryBox{kRows, 0, 0, 0, false} : query_box(p);
   p.rows_per_group = 2 * qb.rows;
   p.groups = 1;
   p.units = sms / 2;
   // a pair's slot is two CTAs'
   p.slot_floats = (static_cast<int64_t>(p.rows_per_group) * (kLatent + 2) + 7) / 8 * 8;
   static_assert(2 * kRows * (kLatent + 2) <= 2 * kSlotFloats, "fits");
-  const CUtensorMapDataType type = q_dtype == PMG_BF16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT16;
-  const int box_rows = gcd(p.B, kKeys);
+  const CUtensorMapDataType type = fp8 ? CU_TENSOR_MAP_DATA_TYPE_UINT8
+                                   : q_dtype == PMG_BF16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16
+                                                         : CU_TENSOR_MAP_DATA_TYPE_FLOAT16;
+  const int box_rows = gcd(p.B, kKeys), ec = fp8 ? 1 : 2;
   const uint64_t page = static_cast<uint64_t>(p.B), blocks = static_cast<uint64_t>(p.num_blocks);
-  const uint64_t row_stride = static_cast<uint64_t>(p.tok_stride) * 2, blk_stride = static_cast<uint64_t>(p.blk_stride) * 2;
-  const uint32_t box = static_cast<uint32_t>(box_rows);
+  const uint64_t row_stride = static_cast<uint64_t>(p.tok_stride) * ec, blk_stride = static_cast<uint64_t>(p.blk_stride) * ec;
+  const uint32_t piece = 128 / ec, pieces = kLatent / piece, box = static_cast<uint32_t>(box_rows);
   CUtensorMap latent, rope, q;
-  // the latent part as pieces of 64 values; the rotated part from the whole row
-  int st = tensor_map<4>(&latent, type, p.cache, {64, page, kLatent / 64, blocks}, {row_stride, 128, blk_stride},
-                         {64, box, box_rows == kKeys ? 4u : 1u, 1});
-  if (st == PMG_OK) st = tensor_map<3>(&rope, type, p.cache, {kEntry, page, blocks}, {row_stride, blk_stride}, {64, box, 1});
+  // the latent part as pieces of 128 bytes; the rotated part from the whole row (an e4m3 one is half a piece, and what lies
+  // past the row reads as 0)
+  int st = tensor_map<4>(&latent, type, p.cache, {piece, page, pieces, blocks}, {row_stride, 128, blk_stride},
+                         {piece, box, box_rows == kKeys ? pieces / 2 : 1, 1});
+  if (st == PMG_OK) st = tensor_map<3>(&rope, type, p.cache, {kEntry, page, blocks}, {row_stride, blk_stride}, {piece, box, 1});
   if (st != PMG_OK) return st;
+  q = rope;
+  p.q_tma = 0;
+  if (fp8)
+    return q_dtype == PMG_BF16 ? run<bf16, 2>(p, latent, rope, q, box_rows, stream) : run<f16, 3>(p, latent, rope, q, box_rows, stream);
   const uint64_t reqs = static_cast<uint64_t>(p.reqs), tokens = static_cast<uint64_t>(p.q_len) * (qb.flat ? reqs : 1);
   p.q_tma = qb.flat ? INT32_MAX : p.q_len;  // new tokens of the dimension before the last
   // (the stride of a dimension of one is not used; it has to be a valid one all the same)
@@ -643,7 +729,7 @@ int prefix_pair(DecodeParams& p, int q_dtype, int sms, void* stream) {
                       !qb.flat && reqs > 1 ? p.qr_stride * 2ull : kEntry * 2ull},
                      {64, qb.heads, qb.tokens, qb.reqs});
   if (st != PMG_OK) return st;
-  return q_dtype == PMG_BF16 ? run<bf16>(p, latent, rope, q, box_rows, stream) : run<f16>(p, latent, rope, q, box_rows, stream);
+  return q_dtype == PMG_BF16 ? run<bf16, 1>(p, latent, rope, q, box_rows, stream) : run<f16, 1>(p, latent, rope, q, box_rows, stream);
 }
 
 }  // namespace pmg_mla
