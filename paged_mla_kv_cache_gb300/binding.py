@@ -561,21 +561,25 @@ def latent_decode(q: torch.Tensor, cache: torch.Tensor, block_table: torch.Tenso
               sets what is latent and what is rope
     lse       fp32 [num_reqs, q_len, heads], contiguous, or None
     """
-    shape, qs = _unit_last("q", 4, q)
-    (blocks, block_size, cached), bs = _unit_last("cache", 3, cache)
-    oshape, os_ = _unit_last("out", 4, out)
+    shape, qs, cshape, bs, oshape, os_ = q.shape, q.stride(), cache.shape, cache.stride(), out.shape, out.stride()
+    if not (len(qs) == 4 and len(bs) == 3 and len(os_) == 4 and qs[3] == 1 and bs[2] == 1 and os_[3] == 1):
+        _unit_last("q", 4, q)
+        _unit_last("cache", 3, cache)
+        _unit_last("out", 4, out)
     r, q_len, heads, entry = shape
-    dv = oshape[3]
-    if oshape[:3] != shape[:3] or cached != entry or not 1 <= dv <= entry:
-        raise ValueError(f"q {list(shape)}, cache {list(cache.shape)} and out {list(oshape)} do not fit")
+    blocks, block_size, cached = cshape
+    out_r, out_len, out_heads, dv = oshape
+    if out_r != r or out_len != q_len or out_heads != heads or cached != entry or not 1 <= dv <= entry:
+        raise ValueError(f"q {list(shape)}, cache {list(cshape)} and out {list(oshape)} do not fit")
     qd, cd = TORCH_DTYPE_CODES.get(q.dtype), TORCH_DTYPE_CODES.get(cache.dtype)
     if qd is None or cd is None or out.dtype is not q.dtype:
         raise ValueError(f"unsupported dtypes {q.dtype}, {cache.dtype} -> {out.dtype}")
-    if not (_is_vector(seq_lens, _I32, r) and (lse is None or _is_vector(lse, _F32, r * q_len * heads))):
+    if not (seq_lens.dtype is _I32 and seq_lens.numel() == r and seq_lens.is_contiguous()
+            and (lse is None or lse.dtype is _F32 and lse.numel() == r * q_len * heads and lse.is_contiguous())):
         _vector(seq_lens, _I32, r, "seq_lens")
         _vector(lse, _F32, r * q_len * heads, "lse", True)
-    width, factor = _table(block_table, r), _scalar(scale, _F32, "scale")
-    flag = _scalar(error_flag, _I32, "error_flag")
+    width, factor = _table(block_table, r), 0 if scale is None else _scalar(scale, _F32, "scale")
+    flag = 0 if error_flag is None else _scalar(error_flag, _I32, "error_flag")
     if not workspace.is_contiguous():
         raise ValueError("workspace must be contiguous")
     device = 0
@@ -744,7 +748,11 @@ def block_scores(q: torch.Tensor, bounds: torch.Tensor, block_table: torch.Tenso
     width, factor = _table(block_table, r), _scalar(scale, _F32, "scale")
     if scores.shape != (r, q_len, width):
         raise ValueError(f"scores {list(scores.shape)} must be [{r}, {q_len}, {width}]")
-    step, flag = _token_rows("scores", scores), _scalar(error_flag, _I32, "error_flag")
+    cs = scores.stride()
+    if cs[2] != 1:
+        _unit_last("scores", 3, scores)
+    step = cs[0] if q_len == 1 and r > 1 else _token_rows("scores", scores)
+    flag = 0 if error_flag is None else _scalar(error_flag, _I32, "error_flag")
     device = 0
     if not (_one_device and q.is_cuda and bounds.is_cuda and block_table.is_cuda and seq_lens.is_cuda and scores.is_cuda
             and (scale is None or scale.is_cuda) and (lse is None or lse.is_cuda)
@@ -776,20 +784,25 @@ def select_blocks(scores: torch.Tensor, block_table: torch.Tensor, seq_lens: tor
     latent_decode(q.view(-1, 1, heads, entry), cache, selected, selected_lens,
     ...) attends to them.
     """
-    (r, q_len, width), _ = _unit_last("scores", 3, scores)
-    (tokens, keep), ss = _unit_last("selected", 2, selected)
+    shape, cs, sshape, ss = scores.shape, scores.stride(), selected.shape, selected.stride()
+    if not (len(cs) == 3 and len(ss) == 2 and cs[2] == 1 and ss[1] == 1):
+        _unit_last("scores", 3, scores)
+        _unit_last("selected", 2, selected)
+    (r, q_len, width), (tokens, keep) = shape, sshape
     if scores.dtype is not _F32 or selected.dtype is not _I32:
         raise ValueError(f"scores must be float32 and selected int32, got {scores.dtype} and {selected.dtype}")
     if tokens != r * q_len or _table(block_table, r) != width:
         raise ValueError(f"scores {list(scores.shape)}, block_table {list(block_table.shape)} and selected "
                          f"{list(selected.shape)} do not fit")
-    if not (_is_vector(seq_lens, _I32, r) and _is_vector(selected_lens, _I32, tokens)):
+    if not (seq_lens.dtype is _I32 and seq_lens.numel() == r and seq_lens.is_contiguous()
+            and selected_lens.dtype is _I32 and selected_lens.numel() == tokens and selected_lens.is_contiguous()):
         _vector(seq_lens, _I32, r, "seq_lens")
         _vector(selected_lens, _I32, tokens, "selected_lens")
     if columns is not None and (columns.dtype is not _I32 or columns.shape != selected.shape
                                 or columns.stride() != selected.stride()):
         raise ValueError("columns must be like selected")
-    step, flag = _token_rows("scores", scores), _scalar(error_flag, _I32, "error_flag")
+    step = cs[0] if q_len == 1 and r > 1 else _token_rows("scores", scores)
+    flag = 0 if error_flag is None else _scalar(error_flag, _I32, "error_flag")
     device = 0
     if not (_one_device and scores.is_cuda and block_table.is_cuda and seq_lens.is_cuda and selected.is_cuda
             and selected_lens.is_cuda and (columns is None or columns.is_cuda)
@@ -839,13 +852,16 @@ def latent_decode_shared(q: torch.Tensor, cache: torch.Tensor, prefix_table: tor
     workspace     new_shared_workspace(device, num_reqs, q_len, heads, latent)
     The rest as in latent_decode.
     """
-    shape, qs = _unit_last("q", 4, q)
-    (blocks, block_size, cached), bs = _unit_last("cache", 3, cache)
-    oshape, os_ = _unit_last("out", 4, out)
+    shape, qs, cshape, bs, oshape, os_ = q.shape, q.stride(), cache.shape, cache.stride(), out.shape, out.stride()
+    if not (len(qs) == 4 and len(bs) == 3 and len(os_) == 4 and qs[3] == 1 and bs[2] == 1 and os_[3] == 1):
+        _unit_last("q", 4, q)
+        _unit_last("cache", 3, cache)
+        _unit_last("out", 4, out)
     r, q_len, heads, entry = shape
-    dv = oshape[3]
-    if oshape[:3] != shape[:3] or cached != entry or not 1 <= dv <= entry:
-        raise ValueError(f"q {list(shape)}, cache {list(cache.shape)} and out {list(oshape)} do not fit")
+    blocks, block_size, cached = cshape
+    out_r, out_len, out_heads, dv = oshape
+    if out_r != r or out_len != q_len or out_heads != heads or cached != entry or not 1 <= dv <= entry:
+        raise ValueError(f"q {list(shape)}, cache {list(cshape)} and out {list(oshape)} do not fit")
     qd, cd = TORCH_DTYPE_CODES.get(q.dtype), TORCH_DTYPE_CODES.get(cache.dtype)
     if qd is None or cd is None or out.dtype is not q.dtype:
         raise ValueError(f"unsupported dtypes {q.dtype}, {cache.dtype} -> {out.dtype}")
