@@ -48,7 +48,7 @@ struct JoinParams {
 template <class TQ>
 __global__ void __launch_bounds__(kJoinThreads, kJoinCtasPerSm) shared_join_kernel(const __grid_constant__ JoinParams p) {
   __shared__ float4 sums[kJoinThreads];
-  __shared__ float sums_l[kJoinWarps];
+  __shared__ float sums_l[kJoinWarps], tops[kJoinWarps];
   pdl_entry();
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const int dv = p.dv, quarters = (dv + 127) / 128, per_req = p.q_len * p.H;
@@ -133,17 +133,15 @@ __global__ void __launch_bounds__(kJoinThreads, kJoinCtasPerSm) shared_join_kern
     for (int k = 0; k < 4; ++k)
       if (d + k < dv) out[k] = from_f<TQ>(y[k]);
   };
-  for (int64_t x = static_cast<int64_t>(blockIdx.x) * kJoinWarps + warp; x < static_cast<int64_t>(p.rows) * quarters;
-       x += gridDim.x * kJoinWarps) {
-    const int row = static_cast<int>(x / quarters), d = static_cast<int>(x % quarters) * 128 + lane * 4;
-    const Row r = row_of(row);
-    if (r.n[0] > few || r.n[1] > few) continue;
-    // so many parts at a time, all of their loads before any is used; every lane has the references and sums
-    float4 a = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-    float l = 0.0f, top = -INFINITY;
+  // Sums of parts i0, i0 + step, ... of a row, kAhead at a time, all of their loads before any is used; every lane has the
+  // references and sums.
+  constexpr int kAhead = 4;
+  auto sum = [&](const Row& r, int row, int d, int i0, int step, float4& a, float& l, float& top) {
+    a = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+    l = 0.0f;
+    top = -INFINITY;
     const int parts = r.n[0] + r.n[1];
-    constexpr int kAhead = 4;
-    for (int i0 = 0; i0 < parts; i0 += kAhead) {
+    for (; i0 < parts; i0 += kAhead * step) {
       float4 o[kAhead];
       float m[kAhead], part_l[kAhead];
 #pragma unroll
@@ -151,9 +149,9 @@ __global__ void __launch_bounds__(kJoinThreads, kJoinCtasPerSm) shared_join_kern
         m[k] = -INFINITY;
         part_l[k] = 0.0f;
         o[k] = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-        if (i0 + k < parts) {
+        if (i0 + k * step < parts) {
           const float* ml;
-          const float* from = place(r, row, i0 + k, ml);
+          const float* from = place(r, row, i0 + k * step, ml);
           m[k] = ml[0];  // (slots of odd rows and columns: not aligned to two)
           part_l[k] = ml[1];
           o[k] = values(from, d);
@@ -170,6 +168,15 @@ __global__ void __launch_bounds__(kJoinThreads, kJoinCtasPerSm) shared_join_kern
       for (int k = 0; k < kAhead; ++k)
         if (part_l[k] != 0.0f) add(a, l, exp2f(m[k] - top), o[k], part_l[k]);
     }
+  };
+  for (int64_t x = static_cast<int64_t>(blockIdx.x) * kJoinWarps + warp; x < static_cast<int64_t>(p.rows) * quarters;
+       x += gridDim.x * kJoinWarps) {
+    const int row = static_cast<int>(x / quarters), d = static_cast<int>(x % quarters) * 128 + lane * 4;
+    const Row r = row_of(row);
+    if (r.n[0] > few || r.n[1] > few) continue;
+    float4 a;
+    float l, top;
+    sum(r, row, d, 0, 1, a, l, top);
     emit(row, d, a, top, l);
   }
   // rows in many parts, if there are any (all of this is the same for a whole CTA)
@@ -201,32 +208,26 @@ __global__ void __launch_bounds__(kJoinThreads, kJoinCtasPerSm) shared_join_kern
       const int row = note.head + x / quarters, d = x % quarters * 128 + lane * 4;
       const Row r = row_of(row);
       if (k == 1 && r.n[0] > few) continue;  // done with its prefix's
-      const int parts = r.n[0] + r.n[1];
-      float top = -INFINITY;
-      for (int y = lane; y < parts; y += 32) {
-        const float* ml;
-        place(r, row, y, ml);
-        if (ml[1] != 0.0f) top = fmaxf(top, ml[0]);
-      }
-#pragma unroll
-      for (int o = 16; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
-      float4 a = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-      float l = 0.0f;
-#pragma unroll 4
-      for (int y = warp; y < parts; y += kJoinWarps) {
-        const float* ml;
-        const float* from = place(r, row, y, ml);
-        const float m = ml[0], part_l = ml[1];
-        const float4 o = values(from, d);
-        if (part_l != 0.0f) add(a, l, exp2f(m - top), o, part_l);
-      }
+      float4 a;
+      float l, top;
+      sum(r, row, d, warp, kJoinWarps, a, l, top);
       sums[tid] = a;
-      if (lane == 0) sums_l[warp] = l;
+      if (lane == 0) {
+        sums_l[warp] = l;
+        tops[warp] = top;
+      }
       __syncthreads();
       if (warp == 0) {
+        float all = -INFINITY;
 #pragma unroll
-        for (int w = 1; w < kJoinWarps; ++w) add(a, l, 1.0f, sums[w * 32 + lane], sums_l[w]);
-        emit(row, d, a, top, l);
+        for (int w = 0; w < kJoinWarps; ++w)
+          if (sums_l[w] != 0.0f) all = fmaxf(all, tops[w]);
+        a = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+        l = 0.0f;
+#pragma unroll
+        for (int w = 0; w < kJoinWarps; ++w)
+          if (sums_l[w] != 0.0f) add(a, l, exp2f(tops[w] - all), sums[w * 32 + lane], sums_l[w]);
+        emit(row, d, a, all, l);
       }
       __syncthreads();
     }
