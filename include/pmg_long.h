@@ -47,8 +47,8 @@ extern "C" {
  *             It must not overlap the cache.
  *  block_table int32 [num_reqs, block_table_stride]. A page outside [0,
  *             num_blocks) is skipped (PMG_FLAG_PHYS_BLOCK), places past the row
- *             too (PMG_FLAG_LOGICAL_BLOCK). A page that two places in the table
- *             name and both change gets the bounds of one of them.
+ *             too (PMG_FLAG_LOGICAL_BLOCK). The bounds of a page that two places
+ *             in the table name, and both change, are undefined.
  *  ctx_lens   int32 [num_reqs]: places of which the bounds know, or NULL (none).
  *             Negative counts as 0 (PMG_FLAG_LENGTH).
  *  seq_lens   int32 [num_reqs]; negative counts as 0 (PMG_FLAG_LENGTH).
@@ -141,7 +141,7 @@ int pmg_select_blocks(const float* scores, int64_t score_stride, const int32_t* 
  *             group no requests (PMG_FLAG_CU_ORDER, for a negative value too);
  *             requests before cu_groups[0] have no prefix, and the rows of one
  *             that such an order puts in two groups are undefined.
- *  workspace  pmg_shared_workspace() bytes, 16-byte aligned; its content does
+ *  workspace  pmg_shared_workspace() bytes, 256-byte aligned; its content does
  *             not matter. Calls that may overlap need one each.
  * The rest as in pmg_latent_decode, its kernels' limits, choice and rounding
  * too. num_groups <= PMG_MAX_REQS, num_reqs * q_len * heads <= INT32_MAX.

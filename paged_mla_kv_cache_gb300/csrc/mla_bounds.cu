@@ -148,8 +148,9 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) bounds_kernel(const __gr
       ++r;
       enter();
     }
-    const uint32_t y = static_cast<uint32_t>(at - base), in = y / columns, column = y - in * columns;  // (2^31 pages of 256 units are not there)
-    const uint32_t page = static_cast<uint32_t>(j.from) / B + in;
+    const int64_t y = at - base;
+    const uint32_t in = static_cast<uint32_t>(y <= UINT32_MAX ? static_cast<uint32_t>(y) / columns : y / columns);
+    const uint32_t column = static_cast<uint32_t>(y - static_cast<int64_t>(in) * columns), page = static_cast<uint32_t>(j.from) / B + in;
     const int32_t id = p.bt[static_cast<int64_t>(r) * p.bt_stride + page];
     if (id < 0 || id >= p.num_blocks) {
       bad |= PMG_FLAG_PHYS_BLOCK;

@@ -289,7 +289,8 @@ extern "C" int pmg_latent_decode_shared(
   if (rows > INT32_MAX) return PMG_ERR_UNSUPPORTED;
   if (num_groups > 0 && (prefix_lens == nullptr || cu_groups == nullptr || (prefix_table == nullptr && prefix_table_stride > 0)))
     return PMG_ERR_NULL;
-  if (!aligned(prefix_table, 4) || !aligned(prefix_lens, 4) || !aligned(cu_groups, 4)) return PMG_ERR_ALIGN;
+  if (!aligned(prefix_table, 4) || !aligned(prefix_lens, 4) || !aligned(cu_groups, 4) || !aligned(workspace, 256))
+    return PMG_ERR_ALIGN;
   int sms = 0;
   st = sm_count(&sms);
   if (st != PMG_OK) return st;

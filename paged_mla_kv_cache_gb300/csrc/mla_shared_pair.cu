@@ -483,8 +483,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
         arrive(s_free + 8 * stage, s_free0 + 8 * stage);
         float* s = reinterpret_cast<float*>(raw_s);
         alignas(8) float x[32];
-        // Scores less the reference, two at a time. The first tile's reference is -inf, which raises it whatever comes; where
-        // a score may be -inf too, it takes the other way.
+        // Scores less the reference, two at a time. A reference of -inf makes +inf of what it meets, which raises it; where a
+        // score may be -inf too, it takes the other way.
         const bool all = mask == 0xffffffffu && factor > 0.0f;
         float2* x2 = reinterpret_cast<float2*>(x);
         float over = -INFINITY;
@@ -502,7 +502,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
             over = fmaxf(over, x[k]);
           }
         }
-        if (named_any<kSoft>(2, over > kCap || ref == -INFINITY)) {
+        if (named_any<kSoft>(2, over > kCap)) {
           float top = -INFINITY;
 #pragma unroll
           for (int k = 0; k < 32; ++k) top = fmaxf(top, s[k] == -INFINITY ? -INFINITY : s[k] * factor);
@@ -536,6 +536,9 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
           const float from = ref == -INFINITY ? 0.0f : ref;  // (nothing but -inf so far)
 #pragma unroll
           for (int k = 0; k < 32; ++k) x[k] = s[k] == -INFINITY ? -INFINITY : fmaf(s[k], factor, -from);
+        } else if (ref == -INFINITY) {  // nothing but -inf and NaN so far
+#pragma unroll
+          for (int k = 0; k < 32; ++k) x[k] = s[k];
         }
 #pragma unroll
         for (int k = 0; k < 32; ++k) x[k] = ex2(x[k]);

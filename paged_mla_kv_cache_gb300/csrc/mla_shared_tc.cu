@@ -11,13 +11,13 @@ int prefix_tc(DecodeParams& p, int q_dtype, int cache_dtype, int sms, void* stre
   p.units = sms;
   // Small calls, where one wave holds every tile of keys (as many as the table has room for) of every 16 or 32 rows: their
   // CTAs take half as long as one of 64 rows.
-  const int64_t tiles = (p.bt_stride * p.B + kDecodeTile - 1) / kDecodeTile * p.R;
+  const int64_t tiles = std::min<int64_t>((p.bt_stride * p.B + kDecodeTile - 1) / kDecodeTile, sms) * p.R;
   for (const int n : {16, 32})
     if ((rows + n - 1) / n * tiles <= sms) {
       p.rows_per_group = static_cast<int32_t>(std::min<int64_t>(rows, p.H <= n ? n / p.H * p.H : n));
       return launch_tc<true>(p, q_dtype, cache_dtype, stream);
     }
-  if (prefix_pair_takes(p, q_dtype, cache_dtype)) return prefix_pair(p, q_dtype, cache_dtype, sms, stream);
+  if (sms >= 2 && prefix_pair_takes(p, q_dtype, cache_dtype)) return prefix_pair(p, q_dtype, cache_dtype, sms, stream);
   // whole tokens in a row tile, where that leaves at most an eighth of it empty: its queries are then one box of the copy
   // engine (an e4m3 cache's are converted by the softmax warps anyhow)
   const int whole = p.H <= 64 ? 64 / p.H * p.H : 64;

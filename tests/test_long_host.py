@@ -79,8 +79,8 @@ def test_select_refusals(cuda_lib, over, status):
     (dict(sm=-1.0), 2), (dict(opt=8), 2), *[({k: -1}, 2) for k in ("qr", "qt", "qh", "bs", "ts", "orr", "ot", "oh")],
     (dict(G=(1 << 20) + 1), 5), (dict(pts=2 ** 31), 5), (dict(dr=1000), 5), (dict(R=1 << 20, n=1 << 6, H=1 << 6), 5), (dict(q=4097), 4),
     (dict(cache=4097), 4), (dict(pt=4098), 4), (dict(pl=4098), 4), (dict(cu=4098), 4), (dict(bt=4098), 4), (dict(lens=4098), 4),
-    (dict(scale=4098), 4), (dict(out=4097), 4), (dict(lse=4098), 4), (dict(ws=4104), 4), (dict(err=4098), 4), (dict(R=0), 0),
-    (dict(n=0, q=0), 0), (dict(H=0), 0)])
+    (dict(scale=4098), 4), (dict(out=4097), 4), (dict(lse=4098), 4), (dict(ws=4104), 4), (dict(ws=4096 + 128), 4), (dict(err=4098), 4),
+    (dict(R=0), 0), (dict(n=0, q=0), 0), (dict(H=0), 0)])
 def test_shared_refusals(cuda_lib, over, status):
     assert cuda_lib.pmg_call_packed(7, binding.SHARED_ARGS.pack(*{**SHARED, **over}.values())) == status
 
