@@ -145,8 +145,10 @@ __device__ __forceinline__ void note_covered(const DecodeParams& p, int tid, int
   }
 }
 
-__device__ __forceinline__ int64_t group_tiles(const DecodeParams& p, const Group& x) {
-  return (static_cast<int64_t>(x.to - x.from) * p.q_len * p.H + p.rows_per_group - 1) / p.rows_per_group;
+// (rows of a call go up to INT32_MAX: 32-bit divisions, which cost a tenth of those of 64 bits)
+__device__ __forceinline__ uint32_t group_tiles(const DecodeParams& p, const Group& x) {
+  const uint32_t rows = static_cast<uint32_t>((x.to - x.from) * p.q_len * p.H), n = static_cast<uint32_t>(p.rows_per_group);
+  return (rows + n - 1) / n;
 }
 template <int kCost>
 __device__ __forceinline__ int64_t prefix_pieces(const DecodeParams& p, int g) {
@@ -165,14 +167,15 @@ struct PrefixItems {
   int64_t first;        // the row tile's first piece
   int b;                // group
   int row_tile;
-  int64_t row0;         // the row tile's first row, of all rows of the call
-  int64_t group_row0, group_rows;
+  int row0;             // the row tile's first row, of all rows of the call
+  int group_row0, group_rows;
   int n_rows;           // its rows
   int tile, tiles;      // first tile of keys of this share, tiles of the prefix
   int n;                // tiles of this share
   int len, full_len;
   __device__ PrefixItems(const DecodeParams& p_, const Share& s) : p(&p_), at(s.begin), end(s.end), b(s.item - 1) {
-    off = total = first = row0 = group_row0 = group_rows = 0;
+    off = total = first = 0;
+    row0 = group_row0 = group_rows = 0;
     row_tile = n_rows = tile = tiles = n = len = full_len = 0;
     skip = s.offset;
   }
@@ -185,22 +188,22 @@ struct PrefixItems {
         const Group x = group_of(*p, b);
         const DecodeLen l = decode_len(*p, b);
         len = full_len = l.use;
-        group_row0 = static_cast<int64_t>(x.from) * p->q_len * p->H;
-        group_rows = static_cast<int64_t>(x.to - x.from) * p->q_len * p->H;
-        total = group_tiles(*p, x) * pieces_of<kCost>(len);
+        group_row0 = x.from * p->q_len * p->H;
+        group_rows = (x.to - x.from) * p->q_len * p->H;
+        total = static_cast<int64_t>(group_tiles(*p, x)) * pieces_of<kCost>(len);
         off = skip;
         skip = 0;
       }
       const int per = pieces_of<kCost>(len);
-      row_tile = static_cast<int>(off / per);
+      row_tile = static_cast<int>(off <= UINT32_MAX ? static_cast<uint32_t>(off) / static_cast<uint32_t>(per) : off / per);
       const int in = static_cast<int>(off - static_cast<int64_t>(row_tile) * per);
       const int take = static_cast<int>(min(static_cast<int64_t>(per - in), end - at));
       tiles = tiles_of(len);
       tile = max(0, in - kCost);
       n = max(0, in + take - kCost) - tile;
       first = at - in;
-      row0 = group_row0 + static_cast<int64_t>(row_tile) * p->rows_per_group;
-      n_rows = static_cast<int>(min(static_cast<int64_t>(p->rows_per_group), group_row0 + group_rows - row0));
+      row0 = group_row0 + row_tile * p->rows_per_group;
+      n_rows = min(p->rows_per_group, group_row0 + group_rows - row0);
       at += take;
       off += take;
     } while (n == 0 && len > 0);

@@ -132,7 +132,7 @@ struct Items {
   int full_len;
   int skip;         // pieces of the request before this share
   DecodeLen ahead;
-  static constexpr int64_t row0 = 0;  // (PrefixItems: the first row of the item's row tile)
+  static constexpr int row0 = 0;  // (PrefixItems: the first row of the item's row tile)
   static constexpr int n_rows = 0;    // (PrefixItems: its rows)
   __device__ Items(const DecodeParams& p_, const Share& s) : p(&p_), at(s.begin), end(s.end), b(s.item - 1) {
     tile = tiles = n = len = full_len = 0;
@@ -341,8 +341,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           ++items;
           if (elect_one()) {
             // (a prefix's requests lie behind each other: one dimension of new tokens)
-            const int head = kPrefix ? static_cast<int>(it.row0 % p.H) : group * p.rows_per_group % p.H;
-            const int token = kPrefix ? static_cast<int>(it.row0 / p.H) : group * p.rows_per_group / p.H;
+            const int row = kPrefix ? it.row0 : group * p.rows_per_group, head = row % p.H, token = row / p.H;
             const uint32_t bar = smem_u32(&mi.q_full);
             mbar_expect(bar, static_cast<uint32_t>(p.rows_per_group) * kEntry * 2);
 #pragma unroll 1
@@ -513,7 +512,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         load_queries<TQ, kParts, N>(
             [&](int r) {
               if constexpr (kPrefix) {
-                const int64_t rr = it.row0 + r, t = rr / p.H;
+                const int rr = it.row0 + r, t = rr / p.H;
                 return static_cast<const TQ*>(p.q) + t / p.q_len * p.qr_stride + t % p.q_len * p.qt_stride + rr % p.H * p.qh_stride;
               } else {
                 const int rr = g0 + r;

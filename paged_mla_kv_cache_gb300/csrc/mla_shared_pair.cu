@@ -267,13 +267,12 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
             if (items > 0) wait(smem_u32(&mi.q_empty), (items - 1) & 1);
             ++items;
             if (elect_one()) {
-              const int64_t r0 = it.row0 + static_cast<int64_t>(rank) * rpc;
-              const int token = static_cast<int>(r0 / p.H);
+              const int r0 = it.row0 + static_cast<int>(rank) * rpc, token = r0 / p.H;
               const uint32_t bar = smem_u32(&mi.q_full);
               mbar_expect(bar, static_cast<uint32_t>(rpc) * kEntry * 2);
 #pragma unroll 1
               for (int c = 0; c < 9; ++c)
-                tma_load_4d(base + c * kQPiece, &q_map, bar, 64 * c, static_cast<int>(r0 % p.H), token % p.q_tma, token / p.q_tma);
+                tma_load_4d(base + c * kQPiece, &q_map, bar, 64 * c, r0 % p.H, token % p.q_tma, token / p.q_tma);
             }
             __syncwarp();
           }
@@ -456,7 +455,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
       if (kFp8 && it.n > 0) {  // (all products with the queries before are done: their scores have been read)
         load_queries<T, kParts, kRows>(
             [&](int r) {
-              const int64_t rr = it.row0 + first_row + r, t = rr / p.H;
+              const int rr = it.row0 + first_row + r, t = rr / p.H;
               return static_cast<const T*>(p.q) + t / p.q_len * p.qr_stride + t % p.q_len * p.qt_stride + rr % p.H * p.qh_stride;
             },
             n_rows, smem, mi, all_rows);
@@ -599,8 +598,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
       float* to = p.ws.slots + (static_cast<int64_t>(unit) * 2 + (it.tile == 0 ? 1 : 0)) * p.slot_floats;
       float* ml = to + p.rows_per_group * kLatent;
       if (whole) {
-        to = p.state + it.row0 * kLatent;
-        ml = p.state_ml + 2 * it.row0;
+        to = p.state + static_cast<int64_t>(it.row0) * kLatent;
+        ml = p.state_ml + 2 * static_cast<int64_t>(it.row0);
       }
       if (half == 0 && row < n_rows) *reinterpret_cast<float2*>(ml + 2 * (first_row + row)) = make_float2(ref, sum);
       if (it.n > 0) product_done();
@@ -637,7 +636,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
         const int parts = whole ? 0 : unit_of(it.last_piece(), share.total, share.units) - unit + 1;
         if (half == 0 && row < n_rows)
           p.row_notes[it.row0 + first_row + row] = {static_cast<uint16_t>(whole ? 0 : unit), static_cast<uint16_t>(parts), first_row + row};
-        if (!whole && tid == 0) note = {it.b, parts, static_cast<int32_t>(it.row0), it.n_rows};
+        if (!whole && tid == 0) note = {it.b, parts, it.row0, it.n_rows};
       }
     }
     if (tid == 0 && rank == 0) p.ws.notes[unit] = note;
@@ -653,7 +652,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     for (int item = 0; again.next(); ++item) {
       const int first_row = static_cast<int>(rank) * rpc;
       if (item < mi.bad_from || tid >= min(rpc, again.n_rows - first_row)) continue;
-      float* ml = again.n == again.tiles ? p.state_ml + 2 * again.row0
+      float* ml = again.n == again.tiles ? p.state_ml + 2 * static_cast<int64_t>(again.row0)
                                          : p.ws.slots + (static_cast<int64_t>(unit) * 2 + (again.tile == 0 ? 1 : 0)) * p.slot_floats +
                                                p.rows_per_group * kLatent;
       ml[2 * (first_row + tid) + 1] = __uint_as_float(0x7fffffffu);
