@@ -12,12 +12,12 @@
 // on. A tile's bounds (147 KB) come by asynchronous copies, page by page
 // through the block table, and stay in shared memory while the rows pass in
 // chunks of N: the rows' pieces of 64 columns are split by sign on their way
-// from registers into a ring of four stages. A piece of the next tile's bounds is
-// asked for as soon as the last product with the one in its place is done, five
-// steps (pieces) before it is multiplied.
+// from registers into a ring of two to four stages. A piece of the next tile's
+// bounds is asked for as soon as the last product with the one in its place is
+// done.
 //
-// Roles: warps 0-7 load and split, warps 8-11 take the largest over the heads,
-// warp 12 issues products. The flat list of tiles of all requests is cut into equal
+// Roles: warps 0-7 load and split queries, warps 8-11 take the largest over the
+// heads, warps 12-15 copy bounds, warp 16 issues products. The flat list of tiles of all requests is cut into equal
 // shares, a CTA each.
 #include <algorithm>
 
@@ -27,9 +27,9 @@
 namespace pmg_mla {
 namespace {
 
-constexpr int kLoaders = 256, kReaders = 128;
-constexpr int kThreads = kLoaders + kReaders + 32;
-constexpr int kLoadWarps = kLoaders / 32, kIssuer = kThreads / 32 - 1;
+constexpr int kLoaders = 256, kReaders = 128, kCopiers = 128;
+constexpr int kThreads = kLoaders + kReaders + kCopiers + 32;
+constexpr int kLoadWarps = kLoaders / 32, kCopyWarp = kLoadWarps + kReaders / 32, kIssuer = kThreads / 32 - 1;
 constexpr int kEntry = 576;
 constexpr int kPieces = kEntry / 64;        // of 128 bytes
 constexpr int kPiece = kScoreTile * 128;    // 64 pages of one piece
@@ -40,7 +40,6 @@ constexpr int kHalfway = 5;
 template <int N>
 struct Lay {
   static constexpr int kStages = N == 128 ? 2 : 4;  // of queries: 64 KB
-  static constexpr int kLead = kPieces - kStages;   // steps between a piece's copy and its product
   // Accumulators of a row and page: hi and lo, and of each the first kHalfway pieces and the others, as far as tensor
   // memory reaches twice. The tensor core cuts a sum at every addition, and all of these have one sign: one sum of 72
   // additions was off by 1.2e-6 of the score, four of 16 or 20 by 3e-7.
@@ -52,7 +51,7 @@ struct Lay {
 };
 
 struct Misc {
-  uint64_t page_full[kPieces], full[4], empty[4], s_full[2], s_free[2], end;
+  uint64_t page_full[kPieces], page_empty[kPieces], full[4], empty[4], s_full[2], s_free[2], end;
   int64_t scratch[33], found[2];
   float shift[kReaders / 32][128];  // of a chunk's rows, each reading warp's own
   uint32_t tmem;
@@ -97,7 +96,7 @@ __device__ __forceinline__ void copy16(uint32_t dst, const void* src, bool there
 template <class T, int N>
 __global__ void __launch_bounds__(kThreads, 1) scores_tc_kernel(const __grid_constant__ ScoreParams p) {
   using L = Lay<N>;
-  constexpr int kStages = L::kStages, kLead = L::kLead, kSums = L::kSums;
+  constexpr int kStages = L::kStages, kSums = L::kSums;
   extern __shared__ uint8_t raw[];
   __shared__ Misc mi;
   uint8_t* smem = raw + ((1024 - (smem_u32(raw) & 1023)) & 1023);
@@ -105,7 +104,10 @@ __global__ void __launch_bounds__(kThreads, 1) scores_tc_kernel(const __grid_con
   const int tid = threadIdx.x, warp = __shfl_sync(0xffffffffu, tid >> 5, 0), lane = tid & 31;
   constexpr int kColumns = 2 * kSums * N;
   if (tid == 0) {
-    for (int i = 0; i < kPieces; ++i) mbar_init(smem_u32(&mi.page_full[i]), kLoaders);
+    for (int i = 0; i < kPieces; ++i) {
+      mbar_init(smem_u32(&mi.page_full[i]), kCopiers);
+      mbar_init(smem_u32(&mi.page_empty[i]), 1);
+    }
     for (int i = 0; i < kStages; ++i) {
       mbar_init(smem_u32(&mi.full[i]), kLoadWarps);
       mbar_init(smem_u32(&mi.empty[i]), 1);
@@ -143,10 +145,11 @@ __global__ void __launch_bounds__(kThreads, 1) scores_tc_kernel(const __grid_con
 #pragma unroll 1
         for (int k = 0; k < kPieces; ++k, ++step) {
           const uint32_t stage = step % kStages;
-          if (c == 0) mbar_wait(smem_u32(&mi.page_full[k]), tile & 1, stop);
-          mbar_wait(full + 8 * stage, step / kStages & 1, stop);
-          fence_async_smem();  // (the barriers order the loading warps' writes before it)
+          // (a barrier a lane; a tile's bounds are the same phase in all of its chunks)
+          mbar_wait(lane == 0 ? smem_u32(&mi.page_full[k]) : full + 8 * stage, lane == 0 ? tile & 1 : step / kStages & 1, stop);
           __syncwarp();
+          fence_async_smem();  // (the barriers order the loading warps' writes before it)
+
           tmem_fence_after();
           if (elect_one()) {
 #pragma unroll
@@ -159,6 +162,7 @@ __global__ void __launch_bounds__(kThreads, 1) scores_tc_kernel(const __grid_con
                                (k > 0 && (kSums == 2 || k != kHalfway)) || x > 0);
             }
             umma_commit(empty + 8 * stage);
+            if (c + 1 == chunks) umma_commit(smem_u32(&mi.page_empty[k]));
             if (k + 1 == kPieces) umma_commit(s_full + 8 * buf);
           }
           __syncwarp();
@@ -171,37 +175,7 @@ __global__ void __launch_bounds__(kThreads, 1) scores_tc_kernel(const __grid_con
   } else if (warp < kLoadWarps) {
     // ---- loads ----
     const int unit = tid & 7, row0 = tid >> 3;  // a 16-byte unit of every kApart-th row of a piece
-    // bounds: of the tile `ahead`, whose pages this thread knows
-    constexpr int kApart = kLoaders / 8, kPageRows = kScoreTile / kApart;
-    Tiles ahead(p, share);
-    const T* page[kPageRows];
-    bool there[kPageRows];
-    auto look = [&]() {
-      const bool more = ahead.next();
-      const int32_t* table = p.bt + static_cast<int64_t>(more ? ahead.r : 0) * p.bt_stride;
-#pragma unroll
-      for (int k = 0; k < kPageRows; ++k) {
-        const int64_t c = ahead.tile * kScoreTile + row0 + kApart * k;
-        const int32_t id = more && c < ahead.pages ? table[c] : -1;
-        there[k] = id >= 0 && id < p.num_blocks;
-        page[k] = reinterpret_cast<const T*>(p.bounds) + (there[k] ? id : 0) * p.bb_stride + unit * 8;
-      }
-      return more;
-    };
-    auto copy = [&](int piece) {
-#pragma unroll
-      for (int k = 0; k < kPageRows; ++k) {
-        const int row = row0 + kApart * k;
-        const uint32_t dst = base + 2 * piece * kPiece + row * 128 + ((unit ^ (row & 7)) << 4);
-        copy16(dst, page[k] + piece * 64, there[k]);
-        copy16(dst + kPiece, page[k] + p.br_stride + piece * 64, there[k]);
-      }
-      // arrives when this thread's copies have
-      asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" ::"r"(smem_u32(&mi.page_full[piece])) : "memory");
-    };
-    bool ahead_more = look();
-    for (int k = 0; k < kLead; ++k)
-      if (ahead_more) copy(k);
+    constexpr int kApart = kLoaders / 8;
     // queries: units of 16 bytes of this thread's rows of a chunk, kTurn steps ahead
     constexpr int kRows = N < kApart ? 1 : N / kApart;
     const bool splits = N >= kApart || row0 < N;
@@ -231,7 +205,6 @@ __global__ void __launch_bounds__(kThreads, 1) scores_tc_kernel(const __grid_con
 #pragma unroll
       for (int k = 0; k < kTurn; ++k) load(x[k], k);
     }
-    int drop = kLead;  // the next piece of `ahead` to be copied
     while (more) {
 #pragma unroll 1
       for (int c = 0; c < chunks; ++c) {
@@ -242,16 +215,6 @@ __global__ void __launch_bounds__(kThreads, 1) scores_tc_kernel(const __grid_con
             const int k = k0 + turn;
             const uint32_t stage = step % kStages;
             if (step >= kStages) mbar_wait(empty + 8 * stage, (step / kStages + 1) & 1, stop);
-            // the piece that was multiplied kStages steps ago makes room in a tile's last chunk (the first tile's rest
-            // has room from the start)
-            if (k >= kStages ? c + 1 == chunks : c == 0) {
-              if (drop == kPieces) {
-                drop = 0;
-                ahead_more = look();
-              }
-              if (ahead_more) copy(drop);
-              ++drop;
-            }
             // queries by sign
             uint8_t* at = smem + L::kStageAt + stage * L::kStage;
 #pragma unroll
@@ -286,6 +249,37 @@ __global__ void __launch_bounds__(kThreads, 1) scores_tc_kernel(const __grid_con
       more = next_more;
       r = next.r;
       if (more) next_more = next.next();
+    }
+  } else if (warp >= kCopyWarp) {
+    // ---- bounds ----
+    const int at0 = tid - kCopyWarp * 32, unit = at0 & 7, row0 = at0 >> 3;  // a 16-byte unit of every kApart-th row of a piece
+    constexpr int kApart = kCopiers / 8, kPageRows = kScoreTile / kApart;
+    uint32_t tile = 0;
+    for (Tiles it(p, share); it.next(); ++tile) {
+      const int32_t* table = p.bt + static_cast<int64_t>(it.r) * p.bt_stride;
+      const T* page[kPageRows];
+      bool there[kPageRows];
+#pragma unroll
+      for (int k = 0; k < kPageRows; ++k) {
+        const int64_t c = it.tile * kScoreTile + row0 + kApart * k;
+        const int32_t id = c < it.pages ? table[c] : -1;
+        there[k] = id >= 0 && id < p.num_blocks;
+        page[k] = reinterpret_cast<const T*>(p.bounds) + (there[k] ? id : 0) * p.bb_stride + unit * 8;
+      }
+#pragma unroll 1
+      for (int piece = 0; piece < kPieces; ++piece) {
+        // where the tile before has had its last product with the piece in this place
+        if (tile > 0) mbar_wait(smem_u32(&mi.page_empty[piece]), (tile - 1) & 1, stop);
+#pragma unroll
+        for (int k = 0; k < kPageRows; ++k) {
+          const int row = row0 + kApart * k;
+          const uint32_t dst = base + 2 * piece * kPiece + row * 128 + ((unit ^ (row & 7)) << 4);
+          copy16(dst, page[k] + piece * 64, there[k]);
+          copy16(dst + kPiece, page[k] + p.br_stride + piece * 64, there[k]);
+        }
+        // arrives when this thread's copies have
+        asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" ::"r"(smem_u32(&mi.page_full[piece])) : "memory");
+      }
     }
     asm volatile("cp.async.wait_all;" ::: "memory");
   } else {
