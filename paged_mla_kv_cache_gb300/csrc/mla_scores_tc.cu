@@ -234,6 +234,8 @@ __global__ void __launch_bounds__(kThreads, 1) scores_tc_kernel(const __grid_con
                 *reinterpret_cast<uint4*>(at + N * 128 + place) = make_uint4(d[0], d[1], d[2], d[3]);
               }
             }
+            __syncwarp();
+            if (lane == 0) mbar_arrive(full + 8 * stage);
             // the queries of the step kTurn further on their way
             if (k + kTurn < kPieces) {
               load(x[turn], k + kTurn);
@@ -241,8 +243,6 @@ __global__ void __launch_bounds__(kThreads, 1) scores_tc_kernel(const __grid_con
               if (k + kTurn == kPieces) begin(c + 1 < chunks ? r : next.r, c + 1 < chunks ? c + 1 : 0);
               load(x[turn], k + kTurn - kPieces);
             }
-            __syncwarp();
-            if (lane == 0) mbar_arrive(full + 8 * stage);
           }
         }
       }
