@@ -680,18 +680,22 @@ def block_bounds(cache: torch.Tensor, bounds: torch.Tensor, block_table: torch.T
     seq_lens  int32 [num_reqs]: places up to which it shall know. plan_step has
               both: one call a step, after append.
     """
-    (blocks, block_size, entry), cs = _unit_last("cache", 3, cache)
-    bshape, bs = _unit_last("bounds", 3, bounds)
+    shape, cs, bshape, bs = cache.shape, cache.stride(), bounds.shape, bounds.stride()
+    if not (len(cs) == 3 and len(bs) == 3 and cs[2] == 1 and bs[2] == 1):
+        _unit_last("cache", 3, cache)
+        _unit_last("bounds", 3, bounds)
+    blocks, block_size, entry = shape
     if bshape != (blocks, 2, entry):
         raise ValueError(f"bounds {list(bshape)} must be [{blocks}, 2, {entry}]")
     cd, bd = TORCH_DTYPE_CODES.get(cache.dtype), TORCH_DTYPE_CODES.get(bounds.dtype)
     if cd is None or bd is None:
         raise ValueError(f"unsupported dtypes {cache.dtype} -> {bounds.dtype}")
     r = seq_lens.numel()
-    if not (_is_vector(seq_lens, _I32, r) and (ctx_lens is None or _is_vector(ctx_lens, _I32, r))):
+    if not (seq_lens.dtype is _I32 and seq_lens.is_contiguous()
+            and (ctx_lens is None or ctx_lens.dtype is _I32 and ctx_lens.numel() == r and ctx_lens.is_contiguous())):
         _vector(seq_lens, _I32, r, "seq_lens")
         _vector(ctx_lens, _I32, r, "ctx_lens", True)
-    width, flag = _table(block_table, r), _scalar(error_flag, _I32, "error_flag")
+    width, flag = _table(block_table, r), 0 if error_flag is None else _scalar(error_flag, _I32, "error_flag")
     device = 0
     if not (_one_device and cache.is_cuda and bounds.is_cuda and block_table.is_cuda and seq_lens.is_cuda
             and (ctx_lens is None or ctx_lens.is_cuda) and (error_flag is None or error_flag.is_cuda)):
@@ -733,8 +737,10 @@ def block_scores(q: torch.Tensor, bounds: torch.Tensor, block_table: torch.Tenso
               a head's scores; the log sums of an earlier step make them bounds of
               the logarithms of weights, comparable over the heads
     """
-    shape, qs = _unit_last("q", 4, q)
-    bshape, bs = _unit_last("bounds", 3, bounds)
+    shape, qs, bshape, bs = q.shape, q.stride(), bounds.shape, bounds.stride()
+    if not (len(qs) == 4 and len(bs) == 3 and qs[3] == 1 and bs[2] == 1):
+        _unit_last("q", 4, q)
+        _unit_last("bounds", 3, bounds)
     r, q_len, heads, entry = shape
     blocks = bshape[0]
     if bshape[1] != 2 or bshape[2] != entry:
@@ -742,10 +748,11 @@ def block_scores(q: torch.Tensor, bounds: torch.Tensor, block_table: torch.Tenso
     code = TORCH_DTYPE_CODES.get(q.dtype)
     if code is None or bounds.dtype is not q.dtype or scores.dtype is not _F32:
         raise ValueError(f"unsupported dtypes {q.dtype}, {bounds.dtype} -> {scores.dtype}")
-    if not (_is_vector(seq_lens, _I32, r) and (lse is None or _is_vector(lse, _F32, r * q_len * heads))):
+    if not (seq_lens.dtype is _I32 and seq_lens.numel() == r and seq_lens.is_contiguous()
+            and (lse is None or lse.dtype is _F32 and lse.numel() == r * q_len * heads and lse.is_contiguous())):
         _vector(seq_lens, _I32, r, "seq_lens")
         _vector(lse, _F32, r * q_len * heads, "lse", True)
-    width, factor = _table(block_table, r), _scalar(scale, _F32, "scale")
+    width, factor = _table(block_table, r), 0 if scale is None else _scalar(scale, _F32, "scale")
     if scores.shape != (r, q_len, width):
         raise ValueError(f"scores {list(scores.shape)} must be [{r}, {q_len}, {width}]")
     cs = scores.stride()

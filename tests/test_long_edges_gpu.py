@@ -226,6 +226,20 @@ def test_a_step_behind_a_prefix_follows_its_inputs(cdt, heads):
         check_shared(dict(q=q, cache=cache, ptable=ptable, plens=plens, cu=groups, table=table, lens=lens, scale=scale, dv=512), out, lse)
 
 
+def test_shared_refuses_a_small_workspace():
+    c = shared_case([2], [100], [5, 6], 16, 1, BF16, BF16, 64)
+    out = torch.empty(2, 1, 16, 512, dtype=BF16, device=DEV)
+    full = new_ws(c)
+    for ws, status in ((binding.new_attention_workspace(DEV), 2), (full[:-256], 2), (full[128:], 4)):
+        with pytest.raises(binding.PmgError) as e:
+            call_shared(c, out, None, SM, ws)
+        assert e.value.status == status
+    call_shared(c, out, None, SM, full)  # (no log sums)
+    check_shared(c, out, run_shared(c)[1])
+    with pytest.raises(binding.PmgError):
+        binding.shared_workspace_bytes(2, 1, 16, 2000)
+
+
 def test_calls_of_nothing():
     """No requests, no tokens, no heads, an empty table."""
     i0 = i32([])
