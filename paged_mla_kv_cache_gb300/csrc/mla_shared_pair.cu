@@ -448,11 +448,16 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     auto product_done = [&]() {
       if (t > 0) wait(v_empty + 8 * ((t - 1) & 1), (t - 1) >> 1 & 1);
     };
-    for (; it.next(); ++item) {
+    // For each item: its queries, then the sums of the item before (whose last product runs meanwhile), then its tiles.
+    const int first_row = static_cast<int>(rank) * rpc;
+    bool more = it.next();
+    float* prev_out = nullptr;  // where this thread's half of its row goes
+    int prev_n = -1;            // tiles of the item before
+    bool prev_row = false;      // whether the row exists
+    for (;; ++item) {
       float ref = -INFINITY, l = 0.0f;
-      const int first_row = static_cast<int>(rank) * rpc;
-      const int n_rows = min(rpc, it.n_rows - first_row);
-      if (kFp8 && it.n > 0) {  // (all products with the queries before are done: their scores have been read)
+      const int n_rows = more ? min(rpc, it.n_rows - first_row) : 0;
+      if (kFp8 && more && it.n > 0) {  // (all products with the queries before are done: their scores have been read)
         load_queries<T, kParts, kRows>(
             [&](int r) {
               const int rr = it.row0 + first_row + r, t = rr / p.H;
@@ -462,6 +467,40 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
         fence_async_smem();
         __syncwarp();
         if (lane == 0) mbar_arrive(smem_u32(&mi.q_full));
+      }
+      if (prev_n >= 0) {
+        if (prev_n > 0) product_done();
+        __syncwarp();
+        tmem_fence_after();
+        if (stopped(stop) && tid == 0) {
+          const uint32_t at = smem_u32(&mi.bad_from);
+          for (uint32_t r = 0; r < 2; ++r)
+            asm volatile("red.relaxed.cluster.shared::cluster.min.s32 [%0], %1;" ::"r"(at_rank(at, r)), "r"(item - 1) : "memory");
+        }
+#pragma unroll 1
+        for (int c = 0; c < 256; c += 32) {
+          uint32_t o[32];
+          if (prev_n > 0) {
+            tmem_ld32(tmem + c + lanes, o);
+            tmem_wait_ld();
+            tmem_pin<32>(o);
+          } else {
+#pragma unroll
+            for (int k = 0; k < 32; ++k) o[k] = 0;
+          }
+          if constexpr (kFp8) {
+#pragma unroll
+            for (int k = 0; k < 32; ++k) o[k] = __float_as_uint(__uint_as_float(o[k]) * kv_scale);
+          }
+          if (prev_row) {
+#pragma unroll
+            for (int k = 0; k < 32; k += 8) store32(prev_out + c + k, o + k);
+          }
+        }
+        tmem_fence_before();
+      }
+      if (!more) break;
+      if (kFp8 && it.n > 0) {
         named_sync<kSoft>(1);
         factor = mi.factor[row];
       }
@@ -602,42 +641,16 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
         ml = p.state_ml + 2 * static_cast<int64_t>(it.row0);
       }
       if (half == 0 && row < n_rows) *reinterpret_cast<float2*>(ml + 2 * (first_row + row)) = make_float2(ref, sum);
-      if (it.n > 0) product_done();
-      __syncwarp();
-      tmem_fence_after();
-      if (stopped(stop) && tid == 0) {
-        const uint32_t at = smem_u32(&mi.bad_from);
-        for (uint32_t r = 0; r < 2; ++r)
-          asm volatile("red.relaxed.cluster.shared::cluster.min.s32 [%0], %1;" ::"r"(at_rank(at, r)), "r"(item) : "memory");
-      }
-      float* out = to + static_cast<int64_t>(first_row + row) * kLatent + half * 256;
-#pragma unroll 1
-      for (int c = 0; c < 256; c += 32) {
-        uint32_t o[32];
-        if (it.n > 0) {
-          tmem_ld32(tmem + c + lanes, o);
-          tmem_wait_ld();
-          tmem_pin<32>(o);
-        } else {
-#pragma unroll
-          for (int k = 0; k < 32; ++k) o[k] = 0;
-        }
-        if constexpr (kFp8) {
-#pragma unroll
-          for (int k = 0; k < 32; ++k) o[k] = __float_as_uint(__uint_as_float(o[k]) * kv_scale);
-        }
-        if (row < n_rows) {
-#pragma unroll
-          for (int k = 0; k < 32; k += 8) store32(out + c + k, o + k);
-        }
-      }
-      tmem_fence_before();
       if (whole || it.tile == 0) {
         const int parts = whole ? 0 : unit_of(it.last_piece(), share.total, share.units) - unit + 1;
         if (half == 0 && row < n_rows)
           p.row_notes[it.row0 + first_row + row] = {static_cast<uint16_t>(whole ? 0 : unit), static_cast<uint16_t>(parts), first_row + row};
         if (!whole && tid == 0) note = {it.b, parts, it.row0, it.n_rows};
       }
+      prev_out = to + static_cast<int64_t>(first_row + row) * kLatent + half * 256;
+      prev_n = it.n;
+      prev_row = row < n_rows;
+      more = it.next();
     }
     if (tid == 0 && rank == 0) p.ws.notes[unit] = note;
     if (stopped(stop) && tid == 0) set_flag(p.err, PMG_FLAG_TIMEOUT);
