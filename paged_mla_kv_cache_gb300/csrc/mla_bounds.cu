@@ -9,9 +9,10 @@
 // one 16-byte column unit of a touched page through all of its entries, kAhead of
 // them on their way at once, so neighbours read neighbouring units and nothing
 // has to meet; the units of all requests' pages are a flat list, cut into equal
-// shares, a CTA each. (A CTA a page, with groups of threads over its entries that
-// meet in shared memory, took 44 us at best for 300000 e4m3 entries.) Rows that
-// are not whole aligned units take the same threads element by element.
+// shares, a CTA each. 300000 e4m3 entries take 34 us, 5.4 TB/s of entries and bounds
+// (a CTA a page, with groups of threads over its entries that meet in shared
+// memory: 44 us at best); a step of 64 requests 3.4 us, one launch. Rows that are
+// not whole aligned units take the same threads element by element.
 #include <algorithm>
 
 #include "mla_attn.cuh"

@@ -17,8 +17,12 @@
 // done.
 //
 // Roles: warps 0-7 load and split queries, warps 8-11 take the largest over the
-// heads, warps 12-15 copy bounds, warp 16 issues products. The flat list of tiles of all requests is cut into equal
-// shares, a CTA each.
+// heads, warps 12-15 copy bounds, warp 16 issues products. The flat list of tiles
+// of all requests is cut into equal shares, a CTA each.
+//
+// Measured: 43 us for 256 requests of 128 heads and 1024 to 32768 entries on
+// pages of 64 (the bytes alone are 18), 6.7 us for 1875 pages of one request, 6.3 us for a
+// few pages, which is three loads one after the other (lengths, page ids, bounds).
 #include <algorithm>
 
 #include "mla_scores.cuh"
@@ -149,7 +153,6 @@ __global__ void __launch_bounds__(kThreads, 1) scores_tc_kernel(const __grid_con
           mbar_wait(lane == 0 ? smem_u32(&mi.page_full[k]) : full + 8 * stage, lane == 0 ? tile & 1 : step / kStages & 1, stop);
           __syncwarp();
           fence_async_smem();  // (the barriers order the loading warps' writes before it)
-
           tmem_fence_after();
           if (elect_one()) {
 #pragma unroll
