@@ -150,7 +150,7 @@ int pmg_append(const void* c_kv, int64_t c_kv_stride, const void* k_pe, int64_t 
  * q, strides below 2^38 elements; the general kernel, many times slower on long
  * requests, for everything else. Scores, sums and accumulators are 32-bit in
  * both. For the second product the tensor-core kernel rounds weights to the
- * type of a 16-bit cache (2^-8 of each, fp16 2^-11); over an e4m3 cache to 2^-9
+ * type of a 16-bit cache (2^-8 of each, fp16 2^-11); over an e4m3 cache to 2^-11
  * of each, or to 2^-28 of the row's largest where that is more. Over an e4m3
  * cache it takes query values to within 2^-17 of the row's largest.
  */

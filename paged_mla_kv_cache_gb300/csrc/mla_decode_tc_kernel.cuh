@@ -46,11 +46,11 @@
 // three for an fp16 query's 11, after a scaling by a power of two for each row
 // that puts its largest value in [224, 448); what is lost is below a step of
 // 2^-9, 2^-16.8 of the largest.
-// Weights: rounded to fp16, then three e5m2 parts of 3 significant bits, which
-// holds them to 2^-9 of their value, as bf16 would, down to half a step of
-// 2^-17. They are kept below 2^15.5 (fp16 ends at 2^16): a request's first
-// tile sets its largest weights to 2^11, which leaves room for the maximum to
-// grow as more entries come, later corrections to 2^13. So one strong key
+// Weights: rounded to fp16 (2^-11 of each), which three e5m2 parts of 3
+// significant bits, each the nearest to what is left, hold exactly, down to half
+// a step of 2^-17. They are kept below 2^15.5 (fp16 ends at 2^16): a request's
+// first tile sets its largest weights to 2^11, which leaves room for the maximum
+// to grow as more entries come, later corrections to 2^13. So one strong key
 // among n weak ones costs them at most n 2^-28 of its weight. (Two e4m3 parts,
 // one product less, end at 2^-10 with the largest at 2^4: of a tail of 16384
 // keys that together weigh as much as a strong first one a quarter was lost.)
@@ -744,7 +744,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             } else {
               uint8_t* at = row + (((g >> 1) ^ (tok & 7)) << 4) + (g & 1) * 8 + 2 * c;
               uint32_t two = pack2<f16>(a, b);
-              const uint32_t part0 = e5m2_cut(two), part1 = e5m2_cut(two);
+              const uint32_t part0 = e5m2_part(two), part1 = e5m2_part(two);
               reinterpret_cast<uint16_t*>(at)[0] = static_cast<uint16_t>(part0);
               reinterpret_cast<uint16_t*>(at + L::kPiece)[0] = static_cast<uint16_t>(part1);
               reinterpret_cast<uint16_t*>(at + 2 * L::kPiece)[0] = static_cast<uint16_t>(e5m2_last(two));

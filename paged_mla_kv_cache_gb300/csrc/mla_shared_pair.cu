@@ -615,7 +615,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
               uint32_t a = pack2<f16>(x[16 * j + 4 * k], x[16 * j + 4 * k + 1]), b = pack2<f16>(x[16 * j + 4 * k + 2], x[16 * j + 4 * k + 3]);
 #pragma unroll
               for (int part = 0; part < 3; ++part) {
-                const uint32_t lo = part < 2 ? e5m2_cut(a) : e5m2_last(a), hi = part < 2 ? e5m2_cut(b) : e5m2_last(b);
+                const uint32_t lo = part < 2 ? e5m2_part(a) : e5m2_last(a), hi = part < 2 ? e5m2_part(b) : e5m2_last(b);
                 w[part][k] = (lo & 0xffff) | hi << 16;
               }
             }

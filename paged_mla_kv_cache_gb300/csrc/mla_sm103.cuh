@@ -390,10 +390,13 @@ __device__ __forceinline__ uint32_t e4m3_part(uint32_t& x) {
 }
 
 // Parts of two values held as f16x2, packed low first, in e5m2: the upper byte
-// of an fp16 value is an e5m2 value, cut. What is left, exactly, stays in x;
-// the last part is rounded.
-__device__ __forceinline__ uint32_t e5m2_cut(uint32_t& x) {
-  const uint32_t top = x & 0xff00ff00u;
+// of an fp16 value is an e5m2 value, cut; with half a step added first it is the
+// nearest one (no value here is so large that this passes its type). What is
+// left, exactly and with a sign, stays in x: of 11 significant bits at most 7
+// after one part, 3 after two, so a third holds the rest. (Cut instead, three
+// parts hold 9 bits.) A NaN stays in x to the last part.
+__device__ __forceinline__ uint32_t e5m2_part(uint32_t& x) {
+  const uint32_t top = (x + 0x00800080u) & 0xff00ff00u;
   asm("sub.rn.f16x2 %0, %0, %1;" : "+r"(x) : "r"(top));
   return __byte_perm(top, 0, 0x4431);
 }
