@@ -66,12 +66,12 @@ int pmg_block_bounds(const void* cache, int64_t cache_block_stride, int64_t cach
  * For token i of the q_len new tokens of request r and column c of its block
  * table, with the bounds hi, lo of page block_table[r, c]:
  *   scores[r, i, c] = max_h (sm_scale * scale * s_h - lse[r, i, h]),
- *   s_h = sum_d (max(q[r, i, h, d], 0) hi[d] + min(q[r, i, h, d], 0) lo[d])
+ *   s_h = sum_d max(q[r, i, h, d] hi[d], q[r, i, h, d] lo[d])
  * which no score of an entry of the page passes; with the log sums of an
  * earlier step, no logarithm of a weight. -INFINITY for a page of which token i
  * sees no entry (it sees the first seq_lens[r] - q_len + 1 + i entries, as in
- * pmg_latent_decode) and for a page outside the cache. NaN where a term is NaN.
- * Every column of the table is written.
+ * pmg_latent_decode) and for a page outside the cache. NaN where a term is NaN
+ * (0 times an infinite bound is). Every column of the table is written.
  *
  *  q          [num_reqs, q_len, heads, entry_dim] of dtype (bf16, fp16, fp32)
  *  bounds     [num_blocks, 2, entry_dim] of dtype

@@ -2,8 +2,10 @@
 // for any sizes and the C entry.
 //
 // Mathematics: over the entries e of a page, lo <= e <= hi column by column, so
-// q . e = sum_d q_d e_d <= sum_d (max(q_d, 0) hi_d + min(q_d, 0) lo_d), and the
-// largest of these over the heads bounds every score that the page can have.
+// q . e = sum_d q_d e_d <= sum_d max(q_d hi_d, q_d lo_d) = sum_d (max(q_d, 0) hi_d
+// + min(q_d, 0) lo_d) for finite bounds, and the largest of these over the heads
+// bounds every score that the page can have. An infinite bound's product with 0
+// would be NaN: where a sum is, it is taken again as the first form.
 #include <algorithm>
 
 #include "mla_scores.cuh"
@@ -62,6 +64,7 @@ __global__ void __launch_bounds__(kGeneralThreads) scores_general_kernel(const _
               }
 #pragma unroll
             for (int o = 16; o > 0; o >>= 1) x += __shfl_xor_sync(0xffffffffu, x, o);
+            if (isnan(x)) x = score_sum_odd<T, 1>(q, row, row + p.br_stride, p.E);
             const int64_t rr = (static_cast<int64_t>(r) * p.q_len + i) * p.H + h;
             best = max_nan(best, x * factor - score_shift(p, rr));
           }

@@ -44,6 +44,26 @@ __device__ __forceinline__ float score_shift(const ScoreParams& p, int64_t row) 
   return isfinite(x) ? x : 0.0f;
 }
 
+// One row's sum as it is defined, by a warp; a lane takes N values at a time. The
+// kernels add max(q, 0) hi and min(q, 0) lo, of which one is a product with 0: NaN
+// where that bound is infinite, although the other one bounds the page. They come
+// here only with a sum of NaN.
+template <class T, int N>
+__device__ __forceinline__ float score_sum_odd(const T* q, const T* hi, const T* lo, int E) {
+  float x = 0.0f;
+  for (int d = (threadIdx.x & 31) * N; d < E; d += 32 * N) {
+    Values<T, N> y, a, b;
+    y.load(q + d);
+    a.load(hi + d);
+    b.load(lo + d);
+#pragma unroll
+    for (int k = 0; k < N; ++k) x += max_nan(to_f(y.v[k]) * to_f(a.v[k]), to_f(y.v[k]) * to_f(b.v[k]));
+  }
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) x += __shfl_xor_sync(0xffffffffu, x, o);
+  return x;
+}
+
 // Columns [from, width) of a request that no token sees anything of.
 __device__ __forceinline__ void score_rest(const ScoreParams& p, int r, int64_t from, int tid, int threads) {
   for (int i = 0; i < p.q_len; ++i) {

@@ -5,7 +5,9 @@
 // row of queries is q+ . hi + q- . lo. For a tile of 64 pages and N rows that
 // is one product of 64 x 1152 and 1152 x N values (S = HI Q+^T + LO Q-^T) with
 // the pages on the M side, so that a lane of tensor memory holds all rows'
-// bounds of its page and the largest over the heads needs no other lane.
+// bounds of its page and the largest over the heads needs no other lane. A NaN
+// there may be an infinite bound's product with the 0 of the other half: such
+// scores are taken again at the share's end, each by a warp (score_sum_odd).
 //
 // Bound by the bounds' bytes (2304 a page) as long as there are few rows; by the
 // rate of the products of 64 lanes, half of the full one, from about 64 heads
@@ -290,6 +292,7 @@ __global__ void __launch_bounds__(kThreads, 1) scores_tc_kernel(const __grid_con
     const float factor = p.sm_scale * (p.scale != nullptr ? *p.scale : 1.0f);
     const int part = warp - kLoadWarps;  // of the lanes
     int bad = 0;
+    bool odd = false;  // a score of this lane is NaN
     uint32_t chunk = 0;
     for (Tiles it(p, share); it.next();) {
       const int64_t c = it.tile * kScoreTile + part * 16 + lane;  // the page of this lane (of the first 16)
@@ -305,6 +308,7 @@ __global__ void __launch_bounds__(kThreads, 1) scores_tc_kernel(const __grid_con
         const bool seen = place < sparse_seen(it.len, token, p.q_len);
         const bool lost = stopped(stop);  // (by all lanes)
         if (in) *out = lost ? __uint_as_float(0x7fffffffu) : good && seen ? best : -INFINITY;
+        odd |= isnan(best);
         out += p.s_stride;
         best = -INFINITY;
         head = 0;
@@ -354,6 +358,26 @@ __global__ void __launch_bounds__(kThreads, 1) scores_tc_kernel(const __grid_con
         tmem_fence_before();
         __syncwarp();  // (the shifts are read too)
         if (lane == 0) mbar_arrive(s_free + 8 * buf);
+      }
+    }
+    if (__any_sync(0xffffffffu, odd) && !stopped(stop)) {  // (scores whose wait ran out stay NaN)
+      for (Tiles it(p, share); it.next();) {
+        const int64_t c = it.tile * kScoreTile + part * 16 + lane;
+        const bool in = lane < 16 && c < it.pages;
+        const int32_t id = in ? p.bt[static_cast<int64_t>(it.r) * p.bt_stride + c] : -1;
+        float* out = p.scores + static_cast<int64_t>(it.r) * p.q_len * p.s_stride + c;
+        const T* q = reinterpret_cast<const T*>(p.q) + it.r * p.qr_stride;
+        int64_t row = static_cast<int64_t>(it.r) * rows;
+        for (int token = 0; token < p.q_len; ++token, out += p.s_stride, q += p.qt_stride, row += p.H)
+          for (uint32_t left = __ballot_sync(0xffffffffu, in && isnan(*out)); left != 0; left &= left - 1) {
+            const int at = __ffs(left) - 1;  // whose page it is (one in the cache: others are -inf)
+            const T* hi = reinterpret_cast<const T*>(p.bounds) + __shfl_sync(0xffffffffu, id, at) * p.bb_stride;
+            float best = -INFINITY;
+            for (int h = 0; h < p.H && !isnan(best); ++h)
+              best = max_nan(best, score_sum_odd<T, 8>(q + h * p.qh_stride, hi, hi + p.br_stride, kEntry) * factor -
+                                       score_shift(p, row + h));
+            if (lane == at) *out = best;
+          }
       }
     }
     // columns that no token sees anything of, and what is wrong with a length: with a request's last piece
