@@ -44,7 +44,10 @@ extern "C" {
  *             fp32 or e4m3)
  *  bounds     [num_blocks, 2, entry_dim] of bounds_dtype: cache_dtype, or for an
  *             e4m3 cache bf16, fp16 or fp32 (as the queries that will meet it).
- *             It must not overlap the cache.
+ *             It must not overlap the cache. Its rows must not overlap: pages lie
+ *             behind each other (block stride >= row stride + entry_dim), or all
+ *             largest values before all smallest ones (row stride >=
+ *             (num_blocks - 1) * block stride + entry_dim).
  *  block_table int32 [num_reqs, block_table_stride]. A page outside [0,
  *             num_blocks) is skipped (PMG_FLAG_PHYS_BLOCK), places past the row
  *             too (PMG_FLAG_LOGICAL_BLOCK). The bounds of a page that two places

@@ -675,7 +675,8 @@ def block_bounds(cache: torch.Tensor, bounds: torch.Tensor, block_table: torch.T
 
     cache     [num_blocks, block_size, entry] (bf16, fp16, fp32 or e4m3)
     bounds    [num_blocks, 2, entry]: largest, then smallest; of cache's dtype, or
-              for an e4m3 cache of the queries' (its values without the scale)
+              for an e4m3 cache of the queries' (its values without the scale).
+              Pages behind each other, or all largest before all smallest
     ctx_lens  int32 [num_reqs]: places that bounds knows of already, or None
     seq_lens  int32 [num_reqs]: places up to which it shall know. plan_step has
               both: one call a step, after append.

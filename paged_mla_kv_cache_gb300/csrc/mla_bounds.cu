@@ -230,8 +230,11 @@ extern "C" int pmg_block_bounds(const void* cache, int64_t cache_block_stride, i
   if (!aligned(cache, ec) || !aligned(bounds, eb) || !aligned(block_table, 4) || !aligned(ctx_lens, 4) ||
       !aligned(seq_lens, 4) || !aligned(error_flag, 4))
     return PMG_ERR_ALIGN;
-  // the two rows of a page, and pages, lie beside each other
-  if (num_blocks > 0 && (bounds_row_stride < entry_dim || (num_blocks > 1 && bounds_block_stride < entry_dim)))
+  // no two rows that are written overlap: pages lie behind each other, or all largest values before all smallest ones
+  // (other threads write them, in no order)
+  if (num_blocks > 0 && bounds_row_stride < entry_dim) return PMG_ERR_ARG;
+  if (num_blocks > 1 && bounds_block_stride < bounds_row_stride + entry_dim &&
+      (bounds_block_stride < entry_dim || (bounds_row_stride - entry_dim) / (num_blocks - 1) < bounds_block_stride))
     return PMG_ERR_ARG;
   int sms = 0;
   const int st = sm_count(&sms);
