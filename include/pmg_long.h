@@ -70,7 +70,9 @@ int pmg_block_bounds(const void* cache, int64_t cache_block_stride, int64_t cach
  * table, with the bounds hi, lo of page block_table[r, c]:
  *   scores[r, i, c] = max_h (sm_scale * scale * s_h - lse[r, i, h]),
  *   s_h = sum_d max(q[r, i, h, d] hi[d], q[r, i, h, d] lo[d])
- * which no score of an entry of the page passes; with the log sums of an
+ * which no score of an entry of the page passes by more than the rounding of the
+ * sum (2 entry_dim products in 32 bits: at most (2 entry_dim + 72) 2^-24 of
+ * sm_scale * scale * sum_d max(|q hi|, |q lo|) + |lse|); with the log sums of an
  * earlier step, no logarithm of a weight. -INFINITY for a page of which token i
  * sees no entry (it sees the first seq_lens[r] - q_len + 1 + i entries, as in
  * pmg_latent_decode) and for a page outside the cache. NaN where a term is NaN

@@ -1,4 +1,5 @@
-"""Page scores where their terms are odd: infinite bounds of either sign under queries of either sign."""
+"""Page scores where their terms are odd or leave no room: infinite bounds
+pages of equal entries."""
 import math
 
 import pytest
@@ -95,3 +96,27 @@ def test_scores_of_nothing_but_infinities(dtype, heads):
     q[..., 100], q[..., 101] = 1.0 + normal(gen(1), 5, 4, heads).abs().to(dtype), -1.0
     got, want = score(case, 0.07, 0), largest(case, 0.07)[0]
     assert torch.equal(got, want) and (got == -math.inf).all()
+
+
+@pytest.mark.parametrize("options", [0, GENERAL])
+@pytest.mark.parametrize("heads,dtype", [(16, BF16), (128, F16), (128, BF16), (5, F16), (16, F32)])
+@pytest.mark.parametrize("block", [1, 64])
+@pytest.mark.parametrize("one_sign", [True, False])
+def test_scores_of_equal_entries(options, heads, dtype, block, one_sign):
+    """Where a page's entries are one, its score is theirs: the bound has no room to hide a lost part of the sum in."""
+    pages = 70
+    entry = normal(gen(1), pages, 1, 576)
+    q = normal(gen(2), 1, 1, heads, 576)
+    if one_sign:
+        entry, q = entry.abs(), q.abs()
+    entry, q = entry.to(dtype), q.to(dtype)
+    cache = entry.expand(pages, block, 576).contiguous()
+    bound = torch.full((pages, 2, 576), 7.0, dtype=dtype, device=DEV)
+    table, lens = torch.randperm(pages, generator=gen(3), device=DEV).to(torch.int32).view(1, pages), i32([pages * block])
+    binding.block_bounds(cache, bound, table, lens)
+    assert torch.equal(bound, entry.expand(pages, 2, 576))
+    case = (q, bound, table, lens, block, None, None)
+    got = score(case, 0.07, options)[0, 0]
+    terms = q[0, 0].double()[:, None] * entry[table[0].long(), 0].double() * 0.07
+    want, mag = terms.sum(2).amax(0), terms.abs().sum(2).amax(0)
+    assert ((got - want).abs() <= (2 * 576 + 72) * 2.0 ** -24 * mag).all(), f"off by {((got - want).abs() / mag).max():.3g}"
