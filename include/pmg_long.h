@@ -38,7 +38,9 @@ extern "C" {
  * and, where the page holds places before ctx_lens[r] too, over the bounds that
  * it has as well. Exact: values as they are in the cache, an e4m3 one's
  * without its scale. A NaN makes NaN of its column. Other pages are not
- * touched.
+ * touched. Entries that joined and were taken back (drafted tokens that were
+ * refused) stay in the bounds of a begun page, which bound those that take their
+ * places all the same, until a call has the page from its first place on.
  *
  *  cache      [num_blocks, block_size, entry_dim] of cache_dtype (bf16, fp16,
  *             fp32 or e4m3)

@@ -1,5 +1,4 @@
-"""Page scores where their terms are odd or leave no room: infinite bounds
-pages of equal entries."""
+"""Page scores where their terms are odd or leave no room: infinite bounds, pages of equal entries, entries taken back."""
 import math
 
 import pytest
@@ -7,7 +6,8 @@ import torch
 
 from paged_mla_kv_cache_gb300 import binding
 
-from test_long_ops_gpu import score_case
+import long_reference as ref
+from test_long_ops_gpu import same, score_case
 from test_mla_ops_gpu import BF16, DEV, F16, F32, GENERAL, gen, i32, normal
 
 pytestmark = pytest.mark.gpu
@@ -120,3 +120,22 @@ def test_scores_of_equal_entries(options, heads, dtype, block, one_sign):
     terms = q[0, 0].double()[:, None] * entry[table[0].long(), 0].double() * 0.07
     want, mag = terms.sum(2).amax(0), terms.abs().sum(2).amax(0)
     assert ((got - want).abs() <= (2 * 576 + 72) * 2.0 ** -24 * mag).all(), f"off by {((got - want).abs() / mag).max():.3g}"
+
+
+def test_bounds_after_entries_were_taken_back():
+    """Refused drafts widen a begun page's bounds, and leave with the page's first place."""
+    cache = normal(gen(1), 3, 64, 576, dtype=BF16)
+    bound, table = torch.zeros(3, 2, 576, dtype=BF16, device=DEV), i32([[2, 0, 1]])
+    binding.block_bounds(cache, bound, table, i32([60]))
+    drafts = cache.clone()
+    drafts[2, 61:64], drafts[0, :2] = 50.0, -50.0
+    binding.block_bounds(drafts, bound, table, i32([66]), i32([60]))   # six tokens drafted
+    assert (bound[2, 0] == 50).all() and (bound[0, 1] == -50).all()
+    binding.block_bounds(cache, bound, table, i32([63]), i32([61]))    # one kept, two of the next step
+    assert (bound[2, 0] == 50).all() and torch.equal(bound[2, 1], torch.minimum(cache[2, :63].amin(0), drafts[2, 60]))
+    binding.block_bounds(cache, bound, table, i32([66]), i32([63]))
+    whole = ref.bounds(cache, torch.zeros_like(bound), table, i32([66]))
+    assert torch.equal(bound[0], whole[0])                             # begun anew
+    assert (bound[2, 0] >= whole[2, 0]).all() and (bound[2, 1] <= whole[2, 1]).all()
+    binding.block_bounds(cache, bound, table, i32([64]), i32([0]))
+    assert same(bound, whole)
