@@ -17,7 +17,9 @@ namespace {
 // tiles of 32 keys held in shared memory in 32 bits; scores are dot products
 // of a lane, values are summed by columns of a thread. It is bound by shared
 // memory reads of the scores (one 4-byte word a multiply), far above the
-// cache's bytes: it exists for what the tensor-core kernel does not take.
+// cache's bytes: it exists for what the tensor-core kernel does not take. As a
+// prefix pass it takes 16 requests of 16 heads behind 4096 entries in 1.05 ms with
+// their own 100 entries and the join (on the tensor core 36 us).
 template <class TQ, class TC, bool kPrefix>
 __global__ void __launch_bounds__(kGenThreads) decode_general_kernel(const __grid_constant__ DecodeParams p) {
   extern __shared__ __align__(16) uint8_t smem[];

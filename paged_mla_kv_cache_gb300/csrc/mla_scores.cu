@@ -16,7 +16,9 @@ namespace {
 // Any sizes and types. A warp takes a page of a request, keeps its bounds in
 // registers (a lane every 32nd column) and meets every row of queries with
 // them; the sum over the lanes costs more than the products. It exists for what
-// the tensor-core kernel does not take.
+// the tensor-core kernel does not take: 938 pages and 16 heads in fp32 take 95 us
+// (in 16 bits 107, on the tensor core 6.8), 64 requests of 64 pages and 128 heads
+// 1.3 ms (11 us).
 constexpr int kGeneralThreads = 256;
 constexpr int kLaneColumns = PMG_MAX_ENTRY / 32;
 

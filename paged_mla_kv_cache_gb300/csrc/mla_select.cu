@@ -197,7 +197,9 @@ extern "C" int pmg_select_blocks(const float* scores, int64_t score_stride, cons
   const int st = sm_count(&sms);
   if (st != PMG_OK) return st;
   // Long rows in a larger CTA, and shorter ones while each has an SM for itself: 2 rows of 938 pages 4.3 us instead of 6.3,
-  // one of 8000 10.1 instead of 23; but 256 rows of 938 pages 9.4 instead of 8.2, 1000 of 512 27 instead of 9.
+  // one of 8000 10.1 instead of 23; but 256 rows of 938 pages 9.4 instead of 8.2, 1000 of 512 27 instead of 9. The host does
+  // not know the lengths: a row is as long as the table is wide, and many short rows in a table of more than 2048 columns
+  // take those 27.
   const int64_t rows = static_cast<int64_t>(num_reqs) * q_len;
   const dim3 grid(static_cast<unsigned>(rows));
   return block_table_stride > 2048 || (block_table_stride > 512 && rows <= sms) ? launch(select_kernel<1024>, grid, 1024, 0, stream, p)
